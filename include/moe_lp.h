@@ -365,6 +365,119 @@ moe_status moe_lm_head_logprob(int32_t T, int32_t H, int32_t V, const void* h_bf
                                const int32_t* targets, float* logprob, void* ws, size_t ws_bytes,
                                void* stream);
 
+/* ---- Training losses -------------------------------------------------------
+ * The objectives an adapter on the frozen base is trained with, each with its
+ * gradient: cross entropy and distillation through the LM head (their d_h is
+ * what the layers below take as d_out), and the router's balance loss (its
+ * gradient joins moe_expert_backward's d_logits). */
+
+/* An LM head (host memory).  logits[t][v] = logit_scale * <z_t, W_v> with
+ * z_t = h_t / sqrt(mean(h_t^2) + norm_eps), the parameter-free RMSNorm of
+ * moe_lm_head_logprob, or z_t = h_t for norm_eps = 0. */
+typedef struct {
+  int32_t num_tokens; /* T: 0..2^20                                              */
+  int32_t hidden;     /* H: multiple of 8, at most 32768                         */
+  int32_t vocab;      /* V: 1..2^20                                              */
+  float norm_eps;     /* finite, >= 0; 0: no norm                                */
+  float logit_scale;  /* finite, > 0 (an inverse temperature)                    */
+  int64_t h_stride;   /* elements between rows of h: 0 (= H), or a multiple of 8, >= H */
+  int64_t w_stride;   /* the same for W                                          */
+} moe_lm_head;
+
+/* Largest number of teacher logits per token. */
+#define MOE_DISTILL_MAX_TOP 256
+
+/* Workspace bytes of the loss entries below: top = 0 for cross entropy, else
+ * the teacher logits per token; backward != 0 for the *_backward entry.
+ * Returns 0 for an invalid or unsupported descriptor.  The logits are never
+ * held: the forward keeps two floats per token and block of vocabulary rows,
+ * the backward the scaled softmax gradient (bf16) of one piece of the
+ * vocabulary at a time (at most about 256 MB, or 256 columns where more
+ * tokens need more), and dL/dz [T][H] fp32. */
+size_t moe_lm_head_loss_workspace_bytes(const moe_lm_head* head, int32_t top, int32_t backward);
+
+/* Cross entropy of target ids: lse[t] = log sum_v exp(logits[t][v]),
+ * loss[t] = lse[t] - logits[t][y_t] (the negative log-prob).
+ * h: [T][H] bf16 (h_stride); w_lm: [V][H] bf16 (w_stride); targets: [T] int32;
+ * loss, lse: [T] fp32.  A negative target marks a token that does not count:
+ * loss = lse = 0, its row of h is not read and no product is spent on it.  A
+ * target >= V gives loss = NaN, lse = 0, and is otherwise the same. */
+moe_status moe_lm_head_loss(const moe_lm_head* head, const void* h_bf16, const void* w_lm_bf16,
+                            const int32_t* targets, float* loss, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradient for given d_loss = dL/dloss [T] fp32, with loss and lse from
+ * moe_lm_head_loss of the same inputs (the logits are formed again, one piece
+ * of the vocabulary at a time):
+ *   d_h [T][H] bf16 (contiguous)       dL/dh; 0 for tokens that do not count
+ *   d_w [V][H] bf16 (contiguous)       dL/dW; NULL: not formed (frozen head)
+ * With p = softmax(logits), r = 1/sqrt(mean(h^2) + norm_eps) (1 without a norm):
+ *   G[t][v] = logit_scale * r_t * d_loss[t] * (p[t][v] - [v = y_t])
+ *   u = G W,  d_h = u - r^2 h mean(h u) (without a norm: u),  d_W = G^T h.
+ * G is rounded to bf16 once, as the operand of the two products; sums, u and
+ * the norm's terms are fp32.  d_h and d_w must not overlap the inputs.
+ * T = 0 writes zeros to d_w. */
+moe_status moe_lm_head_loss_backward(const moe_lm_head* head, const void* h_bf16, const void* w_lm_bf16,
+                                     const int32_t* targets, const float* loss, const float* lse,
+                                     const float* d_loss, void* d_h_bf16, void* d_w_bf16, void* ws, size_t ws_bytes,
+                                     void* stream);
+
+/* Distillation from a teacher's top logits: per token the teacher gives `top`
+ * (1..MOE_DISTILL_MAX_TOP) vocabulary ids and logits; q = softmax of
+ * teacher_scale * teacher_logits over the slots that are there (id in [0, V),
+ * logit not -infinity), and
+ *   logp[t][j] = logits[t][id_j] - lse[t]      (0 for absent slots)
+ *   loss[t] = sum_j q_j (log q_j - logp[t][j]) (KL divergence; q = 0 elsewhere).
+ * teacher_ids: [T][top] int32; teacher_logits: [T][top] fp32; loss, lse: [T]
+ * fp32; logp: [T][top] fp32.  A token with no slot there does not count (as a
+ * negative target above).  Slots may repeat an id; their q add up in the
+ * gradient.  The student's softmax runs over the whole vocabulary. */
+moe_status moe_lm_head_distill(const moe_lm_head* head, int32_t top, float teacher_scale, const void* h_bf16,
+                               const void* w_lm_bf16, const int32_t* teacher_ids, const float* teacher_logits,
+                               float* loss, float* lse, float* logp, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradient: as moe_lm_head_loss_backward with
+ *   G[t][v] = logit_scale * r_t * d_loss[t] * (p[t][v] - sum_j q_j [id_j = v]);
+ * lse and logp from moe_lm_head_distill.  None for the teacher. */
+moe_status moe_lm_head_distill_backward(const moe_lm_head* head, int32_t top, float teacher_scale,
+                                        const void* h_bf16, const void* w_lm_bf16, const int32_t* teacher_ids,
+                                        const float* teacher_logits, const float* lse, const float* logp,
+                                        const float* d_loss, void* d_h_bf16, void* d_w_bf16, void* ws,
+                                        size_t ws_bytes, void* stream);
+
+/* Workspace bytes of moe_balance_loss; 0 for an invalid layer or num_segs < 1. */
+size_t moe_balance_loss_workspace_bytes(const moe_layer* layer, int32_t num_segs);
+
+/* Router balance loss and per-expert counts, per segment of consecutive
+ * tokens (a packed sequence; one segment: the whole batch).  With
+ * p_t = softmax(logits[t]) over all E experts (an expert at -infinity has
+ * p = 0; a row of them counts with p = 0):
+ *   tokens[s]    tokens of segment s that count (token_mask != 0)
+ *   counts[s][e] their routed slots: pairs (t, j) with topk_ids[t][j] = e
+ *   probs[s][e]  mean of p_t[e] over them
+ *   loss[s]      E / (k tokens[s]) * sum_e counts[s][e] probs[s][e]
+ *                (1 for uniform routing; 0 for a segment without tokens)
+ * logits: [T][E] fp32; topk_ids: [T][k] int32 (ids outside [0, E) are not
+ * counted); token_mask: NULL (all tokens count) or [T] bytes (rows of tokens
+ * that do not count are not used); seg_offsets: NULL (num_segs = 1, all
+ * tokens), or [num_segs + 1] int32, non-decreasing; tokens outside
+ * [seg_offsets[0], seg_offsets[num_segs]) belong to no segment.
+ * loss: [S] fp32; counts: [S][E] int32; tokens: [S] int32; probs: [S][E] fp32.
+ * Deterministic (no floating-point atomics).  num_segs at most 65536. */
+moe_status moe_balance_loss(const moe_layer* layer, const float* logits, const int32_t* topk_ids,
+                            const uint8_t* token_mask, const int32_t* seg_offsets, int32_t num_segs, float* loss,
+                            int32_t* counts, int32_t* tokens, float* probs, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradient for given d_loss = dL/dloss [S] fp32 (the counts are constants):
+ *   dL/dlogits[t][e] = p_t[e] (a_e - sum_i p_t[i] a_i),
+ *   a_e = d_loss[s] E counts[s][e] / (k tokens[s]^2)
+ * for the tokens that count, 0 for the others.  d_logits: [T][E] fp32, written,
+ * or with accumulate != 0 added to what it holds (moe_expert_backward's
+ * d_logits). */
+moe_status moe_balance_loss_backward(const moe_layer* layer, const float* logits, const uint8_t* token_mask,
+                                     const int32_t* seg_offsets, int32_t num_segs, const int32_t* counts,
+                                     const int32_t* tokens, const float* d_loss, int32_t accumulate,
+                                     float* d_logits, void* stream);
+
 /* ---- Allocation-free forward -------------------------------------------
  * For callers that cannot allocate device memory or pass a workspace: code
  * under HIP graph capture, tight serving loops, harnesses that forbid

@@ -23,7 +23,9 @@ EXPORTED = ("moe_abi_version", "moe_status_str", "moe_workspace_bytes", "moe_rou
             "moe_lm_head_workspace_bytes", "moe_lm_head_logprob", "moe_materialized_workspace_bytes",
             "moe_expert_forward_materialized", "moe_backward_weights_bytes", "moe_prepare_backward_weights",
             "moe_backward_workspace_bytes", "moe_expert_backward", "moe_pack_weights_kblocked",
-            "moe_quantize_activations", "moe_expert_forward_noalloc")
+            "moe_quantize_activations", "moe_expert_forward_noalloc", "moe_lm_head_loss_workspace_bytes",
+            "moe_lm_head_loss", "moe_lm_head_loss_backward", "moe_lm_head_distill", "moe_lm_head_distill_backward",
+            "moe_balance_loss_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # MOE_NOALLOC_SCRATCH_BYTES
 STAGES = ("route", "permute", "act", "gemm1", "gemm2", "combine", "dequant")
 
@@ -47,6 +49,12 @@ class MoeRouteOut(ctypes.Structure):
     _fields_ = [("topk_ids", ctypes.c_void_p), ("topk_w", ctypes.c_void_p), ("expert_offsets", ctypes.c_void_p),
                 ("sorted_rows", ctypes.c_void_p), ("row_of", ctypes.c_void_p), ("active_experts", ctypes.c_void_p),
                 ("num_active", ctypes.c_void_p)]
+
+
+class MoeLmHead(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("hidden", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("norm_eps", ctypes.c_float), ("logit_scale", ctypes.c_float), ("h_stride", ctypes.c_int64),
+                ("w_stride", ctypes.c_int64)]
 
 
 class MoeError(RuntimeError):
@@ -123,6 +131,25 @@ def lib() -> ctypes.CDLL:
         L.moe_lm_head_logprob.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                           ctypes.c_size_t, ctypes.c_void_p]
+        head, vp, i32, f32, sz = ctypes.POINTER(MoeLmHead), ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, \
+            ctypes.c_size_t
+        L.moe_lm_head_loss_workspace_bytes.restype = sz
+        L.moe_lm_head_loss_workspace_bytes.argtypes = [head, i32, i32]
+        L.moe_lm_head_loss.restype = ctypes.c_int
+        L.moe_lm_head_loss.argtypes = [head] + [vp] * 6 + [sz, vp]
+        L.moe_lm_head_loss_backward.restype = ctypes.c_int
+        L.moe_lm_head_loss_backward.argtypes = [head] + [vp] * 9 + [sz, vp]
+        L.moe_lm_head_distill.restype = ctypes.c_int
+        L.moe_lm_head_distill.argtypes = [head, i32, f32] + [vp] * 8 + [sz, vp]
+        L.moe_lm_head_distill_backward.restype = ctypes.c_int
+        L.moe_lm_head_distill_backward.argtypes = [head, i32, f32] + [vp] * 10 + [sz, vp]
+        L.moe_balance_loss_workspace_bytes.restype = sz
+        L.moe_balance_loss_workspace_bytes.argtypes = [ctypes.POINTER(MoeLayer), i32]
+        L.moe_balance_loss.restype = ctypes.c_int
+        L.moe_balance_loss.argtypes = [ctypes.POINTER(MoeLayer)] + [vp] * 4 + [i32] + [vp] * 5 + [sz, vp]
+        L.moe_balance_loss_backward.restype = ctypes.c_int
+        L.moe_balance_loss_backward.argtypes = [ctypes.POINTER(MoeLayer)] + [vp] * 3 + [i32] + [vp] * 3 + [i32, vp,
+                                                                                                          vp]
         _lib = L
     return _lib
 
@@ -403,3 +430,204 @@ def lm_head_logprob(h: torch.Tensor, w_lm: torch.Tensor, targets: torch.Tensor, 
     _check(lib().moe_lm_head_logprob(T, H, V, _ptr(h), _ptr(w_lm), _ptr(targets), _ptr(lp), _ptr(ws), ws.numel(),
                                      _stream()), "moe_lm_head_logprob")
     return lp
+
+
+# ---- training losses ----
+
+def _typed(t, name: str, dtype, shape, device):
+    """A contiguous tensor of this type and shape on the call's device."""
+    if t is None or t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} tensor of shape {tuple(shape)} on {device} expected, got "
+                         + ("None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}"))
+    return t.data_ptr()
+
+
+def _rows(t, name: str, device):
+    """A bf16 matrix whose rows are contiguous; (pointer, row stride for the descriptor: 0 = contiguous)."""
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.device != device or not t.is_cuda:
+        raise ValueError(f"{name}: bf16 device matrix expected, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    if t.stride(1) != 1 or t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap, got strides {t.stride()}")
+    return t.data_ptr(), t.stride(0)
+
+
+class _On:
+    """The device of the call's tensors, made current where it is not."""
+
+    def __init__(self, device):
+        if device.type != "cuda":
+            raise ValueError("device tensors expected")
+        self._d = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._d is not None:
+            self._d.__enter__()
+
+    def __exit__(self, *e):
+        if self._d is not None:
+            self._d.__exit__(*e)
+
+
+def _head(h, w_lm, norm_eps, logit_scale):
+    """(descriptor, pointer of h, pointer of W) of a call on h [T][H] and W [V][H]."""
+    hp, hs = _rows(h, "h", h.device)
+    wp, ws = _rows(w_lm, "w_lm", h.device)
+    if h.shape[1] != w_lm.shape[1]:
+        raise ValueError(f"h has {h.shape[1]} columns, w_lm {w_lm.shape[1]}")
+    return MoeLmHead(h.shape[0], h.shape[1], w_lm.shape[0], norm_eps, logit_scale, hs, ws), hp, wp
+
+
+def _head_ws(head, top: int, backward: bool, ws, device):
+    if ws is None:
+        ws = torch.empty(max(lib().moe_lm_head_loss_workspace_bytes(ctypes.byref(head), top, backward), 256),
+                         dtype=torch.uint8, device=device)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError("ws: contiguous tensor on the call's device expected")
+    return ws, ws.numel() * ws.element_size()
+
+
+def lm_head_loss_workspace_bytes(T: int, H: int, V: int, top: int = 0, backward: bool = False) -> int:
+    """Workspace of the head's losses: top = 0 for cross entropy, else the teacher logits per token."""
+    return lib().moe_lm_head_loss_workspace_bytes(ctypes.byref(MoeLmHead(T, H, V, 0.0, 1.0, 0, 0)), top, backward)
+
+
+def lm_head_loss(h: torch.Tensor, w_lm: torch.Tensor, targets: torch.Tensor, norm_eps: float = 1e-6,
+                 logit_scale: float = 1.0, ws: torch.Tensor | None = None):
+    """moe_lm_head_loss: cross entropy of targets [T] int32 (negative: the token
+    does not count) under the head w_lm [V][H] on h [T][H]; rows of h and w_lm
+    may be strided.  Returns (loss [T], lse [T]) fp32."""
+    dev = h.device
+    with _On(dev):
+        head, hp, wp = _head(h, w_lm, norm_eps, logit_scale)
+        T = head.num_tokens
+        y = _typed(targets, "targets", torch.int32, (T,), dev)
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        ws, nb = _head_ws(head, 0, False, ws, dev)
+        _check(lib().moe_lm_head_loss(ctypes.byref(head), hp, wp, y, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                      nb, _stream()), "moe_lm_head_loss")
+    return loss, lse
+
+
+def lm_head_loss_backward(h, w_lm, targets, loss, lse, d_loss, weight_grad: bool = False, norm_eps: float = 1e-6,
+                          logit_scale: float = 1.0, ws: torch.Tensor | None = None):
+    """moe_lm_head_loss_backward: (d_h [T][H] bf16, d_w [V][H] bf16 or None) for
+    d_loss [T] fp32, with loss and lse from lm_head_loss on the same arguments."""
+    dev = h.device
+    with _On(dev):
+        head, hp, wp = _head(h, w_lm, norm_eps, logit_scale)
+        T = head.num_tokens
+        y = _typed(targets, "targets", torch.int32, (T,), dev)
+        lo = _typed(loss, "loss", torch.float32, (T,), dev)
+        ls = _typed(lse, "lse", torch.float32, (T,), dev)
+        dl = _typed(d_loss, "d_loss", torch.float32, (T,), dev)
+        d_h = torch.empty((T, head.hidden), dtype=torch.bfloat16, device=dev)
+        d_w = torch.empty((head.vocab, head.hidden), dtype=torch.bfloat16, device=dev) if weight_grad else None
+        ws, nb = _head_ws(head, 0, True, ws, dev)
+        _check(lib().moe_lm_head_loss_backward(ctypes.byref(head), hp, wp, y, lo, ls, dl, d_h.data_ptr(), _ptr(d_w),
+                                               ws.data_ptr(), nb, _stream()), "moe_lm_head_loss_backward")
+    return d_h, d_w
+
+
+def lm_head_distill(h, w_lm, teacher_ids, teacher_logits, teacher_scale: float = 1.0, norm_eps: float = 1e-6,
+                    logit_scale: float = 1.0, ws: torch.Tensor | None = None):
+    """moe_lm_head_distill: KL divergence from the softmax over a teacher's top
+    logits (teacher_ids [T][K] int32, absent where negative; teacher_logits
+    [T][K] fp32) to the head's softmax.  Returns (loss [T], lse [T],
+    logp [T][K]) fp32."""
+    dev = h.device
+    with _On(dev):
+        head, hp, wp = _head(h, w_lm, norm_eps, logit_scale)
+        T, K = head.num_tokens, teacher_ids.shape[-1]
+        ip = _typed(teacher_ids, "teacher_ids", torch.int32, (T, K), dev)
+        tp = _typed(teacher_logits, "teacher_logits", torch.float32, (T, K), dev)
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        logp = torch.empty((T, K), dtype=torch.float32, device=dev)
+        ws, nb = _head_ws(head, K, False, ws, dev)
+        _check(lib().moe_lm_head_distill(ctypes.byref(head), K, teacher_scale, hp, wp, ip, tp, loss.data_ptr(),
+                                         lse.data_ptr(), logp.data_ptr(), ws.data_ptr(), nb, _stream()),
+               "moe_lm_head_distill")
+    return loss, lse, logp
+
+
+def lm_head_distill_backward(h, w_lm, teacher_ids, teacher_logits, lse, logp, d_loss, weight_grad: bool = False,
+                             teacher_scale: float = 1.0, norm_eps: float = 1e-6, logit_scale: float = 1.0,
+                             ws: torch.Tensor | None = None):
+    """moe_lm_head_distill_backward: (d_h, d_w or None) as lm_head_loss_backward,
+    with lse and logp from lm_head_distill on the same arguments."""
+    dev = h.device
+    with _On(dev):
+        head, hp, wp = _head(h, w_lm, norm_eps, logit_scale)
+        T, K = head.num_tokens, teacher_ids.shape[-1]
+        ip = _typed(teacher_ids, "teacher_ids", torch.int32, (T, K), dev)
+        tp = _typed(teacher_logits, "teacher_logits", torch.float32, (T, K), dev)
+        ls = _typed(lse, "lse", torch.float32, (T,), dev)
+        lp = _typed(logp, "logp", torch.float32, (T, K), dev)
+        dl = _typed(d_loss, "d_loss", torch.float32, (T,), dev)
+        d_h = torch.empty((T, head.hidden), dtype=torch.bfloat16, device=dev)
+        d_w = torch.empty((head.vocab, head.hidden), dtype=torch.bfloat16, device=dev) if weight_grad else None
+        ws, nb = _head_ws(head, K, True, ws, dev)
+        _check(lib().moe_lm_head_distill_backward(ctypes.byref(head), K, teacher_scale, hp, wp, ip, tp, ls, lp, dl,
+                                                  d_h.data_ptr(), _ptr(d_w), ws.data_ptr(), nb, _stream()),
+               "moe_lm_head_distill_backward")
+    return d_h, d_w
+
+
+def _segments(layer, token_mask, seg_offsets, dev):
+    """(segments, mask pointer, offsets pointer) of the balance calls."""
+    S = 1 if seg_offsets is None else seg_offsets.numel() - 1
+    if S < 1:
+        raise ValueError("seg_offsets: at least two entries expected")
+    if token_mask is not None and token_mask.dtype == torch.bool:
+        token_mask = token_mask.view(torch.uint8)
+    mp = None if token_mask is None else _typed(token_mask, "token_mask", torch.uint8, (layer.num_tokens,), dev)
+    return S, mp, None if seg_offsets is None else _typed(seg_offsets, "seg_offsets", torch.int32, (S + 1,), dev)
+
+
+def balance_loss(layer: MoeLayer, logits, topk_ids, token_mask=None, seg_offsets=None, ws=None):
+    """moe_balance_loss on router logits [T][E] fp32 and topk_ids [T][k] int32
+    (route_permute's), per segment of seg_offsets [S+1] int32 (None: one
+    segment), over the tokens where token_mask [T] (bool or uint8) is set.
+    Returns (loss [S], counts [S][E] int32, tokens [S] int32, probs [S][E])."""
+    dev, T, E = logits.device, layer.num_tokens, layer.num_experts
+    with _On(dev):
+        S, mp, op = _segments(layer, token_mask, seg_offsets, dev)
+        lp = _typed(logits, "logits", torch.float32, (T, E), dev)
+        ip = _typed(topk_ids, "topk_ids", torch.int32, (T, layer.top_k), dev)
+        loss = torch.empty(S, dtype=torch.float32, device=dev)
+        counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+        tokens = torch.empty(S, dtype=torch.int32, device=dev)
+        probs = torch.empty((S, E), dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = torch.empty(max(lib().moe_balance_loss_workspace_bytes(ctypes.byref(layer), S), 256),
+                             dtype=torch.uint8, device=dev)
+        elif ws.device != dev or not ws.is_contiguous():
+            raise ValueError("ws: contiguous tensor on the call's device expected")
+        _check(lib().moe_balance_loss(ctypes.byref(layer), lp, ip, mp, op, S, loss.data_ptr(), counts.data_ptr(),
+                                      tokens.data_ptr(), probs.data_ptr(), ws.data_ptr(),
+                                      ws.numel() * ws.element_size(), _stream()), "moe_balance_loss")
+    return loss, counts, tokens, probs
+
+
+def balance_loss_backward(layer: MoeLayer, logits, counts, tokens, d_loss, token_mask=None, seg_offsets=None,
+                          d_logits: torch.Tensor | None = None):
+    """moe_balance_loss_backward: dL/dlogits [T][E] fp32 for d_loss [S] fp32, with
+    counts and tokens from balance_loss.  Where d_logits is given (the one of
+    expert_backward), the gradient is added to it."""
+    dev, T, E = logits.device, layer.num_tokens, layer.num_experts
+    with _On(dev):
+        S, mp, op = _segments(layer, token_mask, seg_offsets, dev)
+        lp = _typed(logits, "logits", torch.float32, (T, E), dev)
+        cp = _typed(counts, "counts", torch.int32, (S, E), dev)
+        np_ = _typed(tokens, "tokens", torch.int32, (S,), dev)
+        dl = _typed(d_loss, "d_loss", torch.float32, (S,), dev)
+        add = d_logits is not None
+        if not add:
+            d_logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        dp = _typed(d_logits, "d_logits", torch.float32, (T, E), dev)
+        _check(lib().moe_balance_loss_backward(ctypes.byref(layer), lp, mp, op, S, cp, np_, dl, add, dp, _stream()),
+               "moe_balance_loss_backward")
+    return d_logits

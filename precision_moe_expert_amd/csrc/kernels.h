@@ -190,4 +190,43 @@ int lm_head_blocks(int V);
 void launch_lm_head(const uint16_t* h, const uint16_t* wlm, const int32_t* targets, int T, int H, int V,
                     float* stats_ws, float* tz_ws, float* logprob, hipStream_t s);
 
+// Training losses through the LM head (cross entropy: top = 1, ids = the
+// targets, tlogits null; distillation: top teacher slots per token).  A plan
+// fixes the workspace and the launches from the sizes alone.
+struct HeadPlan {
+  int T, H, V, top;       // top: sparse entries per token (1 for cross entropy)
+  bool distill, bwd;
+  int piece, npieces;     // backward: columns of G per piece (multiple of 256), pieces
+  // byte offsets into the workspace
+  size_t r, flag, rows, cidx, count, lq, zt, stats, u, g, total;
+};
+struct HeadArgs {
+  const uint16_t* h;
+  const uint16_t* w;
+  int64_t h_stride, w_stride;
+  float eps, scale, teacher_scale;
+  const int32_t* ids;     // [T][top]
+  const float* tlogits;   // [T][top], null for cross entropy
+  // forward outputs (inputs of the backward)
+  float* loss;            // [T]; backward: cross entropy's loss
+  float* lse;             // [T]
+  float* logp;            // [T][top], distillation only
+  const float* dloss;     // backward
+  uint16_t* dh;
+  uint16_t* dw;           // null: not formed
+  char* ws;
+};
+HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd);
+void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s);
+void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s);
+
+// Router balance loss.  psum / csum: [slots][E], tsum: [slots].
+int64_t balance_slots(int T, int S);
+void launch_balance(const float* logits, const int32_t* ids, const uint8_t* mask, const int32_t* off, int S, int T,
+                    int E, int k, float* psum, int32_t* csum, int32_t* tsum, float* loss, int32_t* counts,
+                    int32_t* tokens, float* probs, hipStream_t s);
+void launch_balance_bwd(const float* logits, const uint8_t* mask, const int32_t* off, int S, int T, int E, int k,
+                        const int32_t* counts, const int32_t* tokens, const float* dloss, int accumulate,
+                        float* dlogits, hipStream_t s);
+
 }  // namespace moe

@@ -1054,6 +1054,228 @@ moe_status moe_expert_forward_materialized(const moe_layer* layer, const void* x
 
 }  // extern "C"
 
+// ------------------------------------------------------- training losses
+
+namespace {
+
+// Validates the head's descriptor; top = 0: cross entropy.
+moe_status check_head(const moe_lm_head* hd, int32_t top) {
+  if (hd == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (hd->num_tokens < 0 || hd->hidden <= 0 || hd->vocab <= 0 || top < 0) return MOE_ERR_INVALID_ARGUMENT;
+  // written so that a NaN fails
+  if (!(hd->norm_eps >= 0.0f && hd->norm_eps <= 3.0e38f)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!(hd->logit_scale > 0.0f && hd->logit_scale <= 3.0e38f)) return MOE_ERR_INVALID_ARGUMENT;
+  for (int64_t st : {hd->h_stride, hd->w_stride}) {
+    if (st < 0 || (st != 0 && st < hd->hidden)) return MOE_ERR_INVALID_ARGUMENT;
+    if (st % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  }
+  if (hd->hidden % 8 != 0 || hd->hidden > (1 << 15) || hd->vocab > (1 << 20) || hd->num_tokens > (1 << 20) ||
+      top > MOE_DISTILL_MAX_TOP)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+HeadArgs head_args(const moe_lm_head* hd, const void* h, const void* w, const int32_t* ids, void* ws) {
+  HeadArgs a{};
+  a.h = static_cast<const uint16_t*>(h);
+  a.w = static_cast<const uint16_t*>(w);
+  a.h_stride = hd->h_stride ? hd->h_stride : hd->hidden;
+  a.w_stride = hd->w_stride ? hd->w_stride : hd->hidden;
+  a.eps = hd->norm_eps;
+  a.scale = hd->logit_scale;
+  a.teacher_scale = 1.0f;
+  a.ids = ids;
+  a.ws = static_cast<char*>(ws);
+  return a;
+}
+
+HeadPlan plan_of(const moe_lm_head* hd, int32_t top, bool bwd) {
+  return head_plan(hd->num_tokens, hd->hidden, hd->vocab, top ? top : 1, top != 0, bwd);
+}
+
+template <size_t N>
+bool all_aligned16(const void* const (&ptrs)[N]) {
+  for (const void* p : ptrs)
+    if (p == nullptr || !aligned16(p)) return false;
+  return true;
+}
+
+moe_status check_teacher(const moe_lm_head* hd, int32_t top, float teacher_scale) {
+  const moe_status st = check_head(hd, top);
+  if (st != MOE_OK) return st;
+  if (top < 1 || !(teacher_scale > 0.0f && teacher_scale <= 3.0e38f)) return MOE_ERR_INVALID_ARGUMENT;
+  return MOE_OK;
+}
+
+// Zeros d_w when there are no tokens (V*H is even: H is a multiple of 8).
+moe_status zero_dw(const moe_lm_head* hd, void* d_w, void* stream) {
+  if (d_w == nullptr) return MOE_OK;
+  if (!aligned16(d_w)) return MOE_ERR_INVALID_ARGUMENT;
+  launch_zero_f32(static_cast<float*>(d_w), (int64_t)hd->vocab * hd->hidden / 2, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+constexpr int kMaxSegs = 65536;
+
+// Validates the layer and the segment arguments of the balance entries.
+moe_status check_balance(const moe_layer* layer, int32_t num_segs, Dims* d) {
+  const moe_status st = check_layer(layer, d);
+  if (st != MOE_OK) return st;
+  if (num_segs < 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (num_segs > kMaxSegs) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+struct BalanceWs {
+  size_t psum, csum, tsum, total;
+};
+BalanceWs balance_ws(const Dims& d, int32_t num_segs) {
+  const size_t slots = (size_t)balance_slots(d.T, num_segs);
+  BalanceWs w;
+  w.psum = 0;
+  w.csum = align_up(slots * d.E * 4);
+  w.tsum = w.csum + align_up(slots * d.E * 4);
+  w.total = w.tsum + align_up(slots * 4);
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_lm_head_loss_workspace_bytes(const moe_lm_head* head, int32_t top, int32_t backward) {
+  if (check_head(head, top) != MOE_OK) return 0;
+  return plan_of(head, top, backward != 0).total;
+}
+
+moe_status moe_lm_head_loss(const moe_lm_head* head, const void* h_bf16, const void* w_lm_bf16,
+                            const int32_t* targets, float* loss, float* lse, void* ws, size_t ws_bytes,
+                            void* stream) {
+  const moe_status st = check_head(head, 0);
+  if (st != MOE_OK) return st;
+  if (head->num_tokens == 0) return MOE_OK;
+  const void* ptrs[] = {h_bf16, w_lm_bf16, targets, loss, lse, ws};
+  if (!all_aligned16(ptrs)) return MOE_ERR_INVALID_ARGUMENT;
+  const HeadPlan p = plan_of(head, 0, false);
+  if (ws_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  HeadArgs a = head_args(head, h_bf16, w_lm_bf16, targets, ws);
+  a.loss = loss;
+  a.lse = lse;
+  launch_head_loss(p, a, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+moe_status moe_lm_head_loss_backward(const moe_lm_head* head, const void* h_bf16, const void* w_lm_bf16,
+                                     const int32_t* targets, const float* loss, const float* lse,
+                                     const float* d_loss, void* d_h_bf16, void* d_w_bf16, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  const moe_status st = check_head(head, 0);
+  if (st != MOE_OK) return st;
+  if (head->num_tokens == 0) return zero_dw(head, d_w_bf16, stream);
+  const void* ptrs[] = {h_bf16, w_lm_bf16, targets, loss, lse, d_loss, d_h_bf16, ws};
+  if (!all_aligned16(ptrs) || !aligned16(d_w_bf16)) return MOE_ERR_INVALID_ARGUMENT;
+  const HeadPlan p = plan_of(head, 0, true);
+  if (ws_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  HeadArgs a = head_args(head, h_bf16, w_lm_bf16, targets, ws);
+  a.loss = const_cast<float*>(loss);
+  a.lse = const_cast<float*>(lse);
+  a.dloss = d_loss;
+  a.dh = static_cast<uint16_t*>(d_h_bf16);
+  a.dw = static_cast<uint16_t*>(d_w_bf16);
+  launch_head_loss_bwd(p, a, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+moe_status moe_lm_head_distill(const moe_lm_head* head, int32_t top, float teacher_scale, const void* h_bf16,
+                               const void* w_lm_bf16, const int32_t* teacher_ids, const float* teacher_logits,
+                               float* loss, float* lse, float* logp, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status st = check_teacher(head, top, teacher_scale);
+  if (st != MOE_OK) return st;
+  if (head->num_tokens == 0) return MOE_OK;
+  const void* ptrs[] = {h_bf16, w_lm_bf16, teacher_ids, teacher_logits, loss, lse, logp, ws};
+  if (!all_aligned16(ptrs)) return MOE_ERR_INVALID_ARGUMENT;
+  const HeadPlan p = plan_of(head, top, false);
+  if (ws_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  HeadArgs a = head_args(head, h_bf16, w_lm_bf16, teacher_ids, ws);
+  a.tlogits = teacher_logits;
+  a.teacher_scale = teacher_scale;
+  a.loss = loss;
+  a.lse = lse;
+  a.logp = logp;
+  launch_head_loss(p, a, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+moe_status moe_lm_head_distill_backward(const moe_lm_head* head, int32_t top, float teacher_scale,
+                                        const void* h_bf16, const void* w_lm_bf16, const int32_t* teacher_ids,
+                                        const float* teacher_logits, const float* lse, const float* logp,
+                                        const float* d_loss, void* d_h_bf16, void* d_w_bf16, void* ws,
+                                        size_t ws_bytes, void* stream) {
+  const moe_status st = check_teacher(head, top, teacher_scale);
+  if (st != MOE_OK) return st;
+  if (head->num_tokens == 0) return zero_dw(head, d_w_bf16, stream);
+  const void* ptrs[] = {h_bf16, w_lm_bf16, teacher_ids, teacher_logits, lse, logp, d_loss, d_h_bf16, ws};
+  if (!all_aligned16(ptrs) || !aligned16(d_w_bf16)) return MOE_ERR_INVALID_ARGUMENT;
+  const HeadPlan p = plan_of(head, top, true);
+  if (ws_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  HeadArgs a = head_args(head, h_bf16, w_lm_bf16, teacher_ids, ws);
+  a.tlogits = teacher_logits;
+  a.teacher_scale = teacher_scale;
+  a.lse = const_cast<float*>(lse);
+  a.logp = const_cast<float*>(logp);
+  a.dloss = d_loss;
+  a.dh = static_cast<uint16_t*>(d_h_bf16);
+  a.dw = static_cast<uint16_t*>(d_w_bf16);
+  launch_head_loss_bwd(p, a, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+size_t moe_balance_loss_workspace_bytes(const moe_layer* layer, int32_t num_segs) {
+  Dims d;
+  if (check_balance(layer, num_segs, &d) != MOE_OK) return 0;
+  return balance_ws(d, num_segs).total;
+}
+
+moe_status moe_balance_loss(const moe_layer* layer, const float* logits, const int32_t* topk_ids,
+                            const uint8_t* token_mask, const int32_t* seg_offsets, int32_t num_segs, float* loss,
+                            int32_t* counts, int32_t* tokens, float* probs, void* ws, size_t ws_bytes,
+                            void* stream) {
+  Dims d;
+  const moe_status st = check_balance(layer, num_segs, &d);
+  if (st != MOE_OK) return st;
+  if (seg_offsets == nullptr && num_segs != 1) return MOE_ERR_INVALID_ARGUMENT;
+  const void* ptrs[] = {loss, counts, tokens, probs, ws};
+  if (!all_aligned16(ptrs) || !aligned16(logits) || !aligned16(topk_ids) || !aligned16(token_mask) ||
+      !aligned16(seg_offsets) || (d.T > 0 && (logits == nullptr || topk_ids == nullptr)))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const BalanceWs w = balance_ws(d, num_segs);
+  if (ws_bytes < w.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  char* base = static_cast<char*>(ws);
+  launch_balance(logits, topk_ids, token_mask, seg_offsets, num_segs, d.T, d.E, d.k,
+                 reinterpret_cast<float*>(base + w.psum), reinterpret_cast<int32_t*>(base + w.csum),
+                 reinterpret_cast<int32_t*>(base + w.tsum), loss, counts, tokens, probs,
+                 static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+moe_status moe_balance_loss_backward(const moe_layer* layer, const float* logits, const uint8_t* token_mask,
+                                     const int32_t* seg_offsets, int32_t num_segs, const int32_t* counts,
+                                     const int32_t* tokens, const float* d_loss, int32_t accumulate,
+                                     float* d_logits, void* stream) {
+  Dims d;
+  const moe_status st = check_balance(layer, num_segs, &d);
+  if (st != MOE_OK) return st;
+  if (seg_offsets == nullptr && num_segs != 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (d.T == 0) return MOE_OK;
+  const void* ptrs[] = {logits, counts, tokens, d_loss, d_logits};
+  if (!all_aligned16(ptrs) || !aligned16(token_mask) || !aligned16(seg_offsets)) return MOE_ERR_INVALID_ARGUMENT;
+  launch_balance_bwd(logits, token_mask, seg_offsets, num_segs, d.T, d.E, d.k, counts, tokens, d_loss, accumulate,
+                     d_logits, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+}  // extern "C"
+
 // ---------------------------------------------------------------------------
 // Allocation-free forward: the workspace is a file-scope device array, one
 // copy per GPU the library runs on, alive until the process ends.
