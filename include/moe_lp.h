@@ -380,7 +380,7 @@ typedef struct {
   int32_t vocab;      /* V: 1..2^20                                              */
   float norm_eps;     /* finite, >= 0; 0: no norm                                */
   float logit_scale;  /* finite, > 0 (an inverse temperature)                    */
-  int64_t h_stride;   /* elements between rows of h: 0 (= H), or a multiple of 8, >= H */
+  int64_t h_stride;   /* elements between rows of h: 0 (= H), or a multiple of 8, H..2^22 */
   int64_t w_stride;   /* the same for W                                          */
 } moe_lm_head;
 

@@ -21,9 +21,7 @@ namespace moe {
 
 namespace {
 
-constexpr int HB = 128;       // rows and columns of a product's tile
-constexpr int HK = 32;        // K per step
-constexpr int HS = HK + 8;    // LDS row stride of a staged operand (elements)
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 MOE_DEV float hl_sum64(float v) {
 #pragma unroll
@@ -35,94 +33,73 @@ MOE_DEV float hl_max64(float v) {
   for (int x = 32; x > 0; x >>= 1) v = fmaxf(v, shfl_xor(v, x));
   return v;
 }
+MOE_DEV float hl_exp2(float v) { return __builtin_amdgcn_exp2f(v); }  // one instruction, 1 ulp
+// Joins two (maximum, sum of 2^(y - maximum)) pairs; an empty one has sum 0.
 MOE_DEV void hl_merge(float& m, float& s, float m2, float s2) {
-  if (s2 == 0.0f) return;  // an empty part changes nothing
+  if (s2 == 0.0f) return;
   if (s == 0.0f) {
     m = m2;
     s = s2;
     return;
   }
   const float M = fmaxf(m, m2);
-  s = s * expf(m - M) + s2 * expf(m2 - M);
+  s = s * hl_exp2(m - M) + s2 * hl_exp2(m2 - M);
   m = M;
 }
 
 }  // namespace
 
-// Per token (one wave): whether it counts, 1/rms of its row, and for
-// distillation the log of the teacher's probabilities (-infinity for slots
-// that are not there).
-__global__ __launch_bounds__(256) void k_head_rows(const uint16_t* __restrict__ h, int64_t h_stride, int T, int H, int V,
-                                                   float eps, const int32_t* __restrict__ ids, int top,
-                                                   const float* __restrict__ tlogits, float tscale,
-                                                   float* __restrict__ r, uint8_t* __restrict__ flag,
-                                                   float* __restrict__ lq) {
+// ---- which tokens count -----------------------------------------------------
+
+// Distillation, one wave per token: the log of the teacher's probabilities
+// (-infinity for slots that are not there) and whether there is any.
+__global__ __launch_bounds__(256) void k_head_teacher(const int32_t* __restrict__ ids, const float* __restrict__ tlogits,
+                                                      int T, int V, int top, float tscale, float* __restrict__ lq,
+                                                      uint8_t* __restrict__ flag) {
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (t >= T) return;
-  bool counts;
-  if (tlogits == nullptr) {
-    const int y = ids[t];
-    counts = y >= 0 && y < V;
-  } else {
-    float x[4], m = -INFINITY;
-    bool have[4], any = false;
+  float x[4], m = -INFINITY;
+  bool have[4], any = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = i * 64 + lane;
-      have[i] = false;
-      x[i] = -INFINITY;
-      if (j < top) {
-        const int id = ids[(int64_t)t * top + j];
-        if (id >= 0 && id < V) {
-          x[i] = tlogits[(int64_t)t * top + j];
-          have[i] = !(x[i] == -INFINITY);
-          x[i] *= tscale;
-        }
-      }
-      any |= have[i];
-      if (have[i]) m = fmaxf(m, x[i]);
-    }
-    m = hl_max64(m);
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (have[i]) s += expf(x[i] - m);
-    const float ls = logf(hl_sum64(s));
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i * 64 + lane < top) lq[(int64_t)t * top + i * 64 + lane] = have[i] ? x[i] - m - ls : -INFINITY;
-    counts = __any(any);
-  }
-  float rr = 1.0f;
-  if (counts && eps > 0.0f) {
-    float ss = 0.0f;
-    const uint16_t* row = h + (int64_t)t * h_stride;
-    for (int c = lane; c < H / 8; c += 64) {
-      const u32x4 q = *reinterpret_cast<const u32x4*>(row + c * 8);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = bf16_bits_to_f32(q[i] & 0xFFFFu), b = bf16_bits_to_f32(q[i] >> 16);
-        ss = fmaf(a, a, ss);
-        ss = fmaf(b, b, ss);
+  for (int i = 0; i < 4; ++i) {
+    const int j = i * 64 + lane;
+    have[i] = false;
+    x[i] = -INFINITY;
+    if (j < top) {
+      const int id = ids[(int64_t)t * top + j];
+      if (id >= 0 && id < V) {
+        x[i] = tlogits[(int64_t)t * top + j];
+        have[i] = !(x[i] == -INFINITY);
+        x[i] *= tscale;
       }
     }
-    rr = 1.0f / sqrtf(hl_sum64(ss) / (float)H + eps);
+    any |= have[i];
+    if (have[i]) m = fmaxf(m, x[i]);
   }
-  if (lane == 0) {
-    r[t] = rr;
-    flag[t] = counts;
-  }
+  m = hl_max64(m);
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (have[i]) s += expf(x[i] - m);
+  const float ls = logf(hl_sum64(s));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i * 64 + lane < top) lq[(int64_t)t * top + i * 64 + lane] = have[i] ? x[i] - m - ls : -INFINITY;
+  const bool counts = __any(any);
+  if (lane == 0) flag[t] = counts;
 }
 
 // The list of tokens that count, in order, and each token's place in it (-1).
-__global__ __launch_bounds__(1024) void k_head_compact(const uint8_t* __restrict__ flag, int T,
-                                                       int32_t* __restrict__ rows, int32_t* __restrict__ cidx,
-                                                       int32_t* __restrict__ count) {
+// flag null: a token counts if its id is in [0, V).
+__global__ __launch_bounds__(1024) void k_head_compact(const uint8_t* __restrict__ flag, const int32_t* __restrict__ ids,
+                                                       int T, int V, int32_t* __restrict__ rows,
+                                                       int32_t* __restrict__ cidx, int32_t* __restrict__ count) {
   __shared__ int part[1024];
   const int tid = threadIdx.x, per = (T + 1023) / 1024;
   const int t0 = min(T, tid * per), t1 = min(T, t0 + per);
+  auto on = [&](int t) { return flag != nullptr ? flag[t] != 0 : ids[t] >= 0 && ids[t] < V; };
   int n = 0;
-  for (int t = t0; t < t1; ++t) n += flag[t];
+  for (int t = t0; t < t1; ++t) n += on(t);
   part[tid] = n;
   __syncthreads();
   for (int d = 1; d < 1024; d <<= 1) {
@@ -133,7 +110,7 @@ __global__ __launch_bounds__(1024) void k_head_compact(const uint8_t* __restrict
   }
   int c = part[tid] - n;
   for (int t = t0; t < t1; ++t) {
-    if (flag[t]) {
+    if (on(t)) {
       rows[c] = t;
       cidx[t] = c++;
     } else {
@@ -143,184 +120,452 @@ __global__ __launch_bounds__(1024) void k_head_compact(const uint8_t* __restrict
   if (tid == 1023) *count = part[1023];
 }
 
-// One product of the head; what its operands are and what becomes of the
-// accumulators:
-//   STATS  h W^T -> (max, sum of exponentials) per row and column block, and
-//          the logits at the target's ids
-//   GRAD   h W^T -> G, columns [v0, v0 + piece)
-//   DZ     G W   -> u, added up over the pieces
-//   DW     G^T h -> d_w rows [v0, v0 + piece)
-enum { HP_STATS, HP_GRAD, HP_DZ, HP_DW };
+// The rows that count, one after the other, as the products read them: hc
+// [..][Hp] with zeros in columns H..Hp and in the rows up to the next multiple
+// of 64 (the K of a product runs over either in steps of 64); r[c] = 1/rms of
+// row c.  One block per row.
+__global__ __launch_bounds__(256) void k_head_gather(const uint16_t* __restrict__ h, int64_t h_stride, int H, int Hp,
+                                                     float eps, const int32_t* __restrict__ rows,
+                                                     const int32_t* __restrict__ count, uint16_t* __restrict__ hc,
+                                                     float* __restrict__ r) {
+  __shared__ float part[4];
+  const int c = blockIdx.x, n = *count;
+  if (c >= (n + 63) / 64 * 64) return;
+  uint16_t* o = hc + (int64_t)c * Hp;
+  const uint16_t* row = c < n ? h + (int64_t)rows[c] * h_stride : nullptr;
+  float ss = 0.0f;
+  for (int i = threadIdx.x; i < Hp / 8; i += 256) {
+    u32x4 q = {0, 0, 0, 0};
+    if (c < n && i < H / 8) q = *reinterpret_cast<const u32x4*>(row + i * 8);
+    *reinterpret_cast<u32x4*>(o + i * 8) = q;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = bf16_bits_to_f32(q[j] & 0xFFFFu), b = bf16_bits_to_f32(q[j] >> 16);
+      ss = fmaf(a, a, ss);
+      ss = fmaf(b, b, ss);
+    }
+  }
+  if (c >= n) return;
+  ss = hl_sum64(ss);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = ss;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    r[c] = eps > 0.0f ? 1.0f / sqrtf(((part[0] + part[1]) + (part[2] + part[3])) / (float)H + eps) : 1.0f;
+}
+
+// ---- the products -----------------------------------------------------------
+//
+// C[m][n] = sum_k A[m][k] B[n][k] on 16x16x32 bf16 MFMAs, tiles of BM x BN by 8
+// waves, K in steps of 64.  Each operand lies in memory either with K
+// contiguous (rows m) or with m contiguous (rows k): the head's forward
+// product, G W and G^T h need both kinds, and no transposed copy is made.
+//
+// Stages of 64 K go to an LDS ring by DMA; a wave reads its fragments of the
+// next 32 K into registers while the MFMAs of the current 32 run (two MFMA
+// rows per LDS read), so that only the barrier of every 64 K shows.
+// K-contiguous rows (128 bytes per stage) keep 16-byte part p at slot
+// p ^ ((row >> 1) & 7): the 16 rows of a fragment cover all banks once.
+// m-contiguous rows (2 BM bytes) are read by the transposing 8-byte LDS read,
+// 4 rows x 32 bytes per 16 lanes; 32-byte piece c of row k lies at
+// c ^ (k & 3 | (k >> 1 & 4)), so the 8 rows that 32 lanes touch at once cover
+// all banks.
+//
+// The accumulators are formed transposed (B's fragment first): a lane then
+// holds 4 consecutive columns of one row.
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// An operand tile: p its first element, ld bytes between rows, `mn` valid rows
+// (K contiguous) or columns from there, `k` valid K.  Loads past either are
+// redirected to the last valid piece: rows and columns past the end belong to
+// outputs that are not kept, and past the end of K the other operand holds
+// zeros.
+struct HeadSrc {
+  const char* p;
+  uint32_t ld;
+  int mn;
+  int k;
+};
+
+// global_load_lds with a uniform base and a 32-bit lane offset.
+MOE_DEV void hl_dma(const char* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+
+// One operand of a tile: R rows (or columns) by 64 K per stage.
+template <int R, bool KM>
+struct HeadOperand {
+  static constexpr int BYTES = R * 128;
+  static constexpr int ND = R / 64;  // DMAs per wave and stage
+  static constexpr int RB = KM ? R * 2 : 128;
+  static constexpr int LPR = RB / 16;     // lanes per row of a DMA
+  static_assert(R % 64 == 0 && (!KM || R >= 128), "tile");
+  HeadSrc s;
+  uint32_t off[ND];
+  MOE_DEV static int row_of(int wave, int lane, int j) { return (wave * ND + j) * (64 / LPR) + lane / LPR; }
+  MOE_DEV void init(const HeadSrc& src, int wave, int lane) {
+    s = src;
+#pragma unroll
+    for (int j = 0; j < ND; ++j) {
+      const int row = row_of(wave, lane, j), q = lane % LPR;
+      if (KM) {
+        const int f = (row & 3) | ((row >> 1) & 4);
+        const int col = min((((q >> 1) ^ f) << 4) + (q & 1) * 8, s.mn - 8);
+        off[j] = (uint32_t)row * s.ld + col * 2;
+      } else {
+        off[j] = (uint32_t)min(row, s.mn - 1) * s.ld + ((q ^ ((row >> 1) & 7)) << 4);
+      }
+    }
+  }
+  // DMA j of stage kt into the stage at LDS address lds.
+  MOE_DEV void issue(int j, int kt, uint32_t lds, int wave, int lane) const {
+    uint32_t o = off[j];
+    const int over = kt * 64 + 64 - s.k;  // K past the end (uniform)
+    if (over > 0) {
+      const int row = row_of(wave, lane, j);
+      if (KM) {
+        const int last = 63 - over;
+        if (row > last) o -= (uint32_t)(row - last) * s.ld;
+      } else {
+        const int k = ((lane % LPR) ^ ((row >> 1) & 7)) * 8, last = 56 - over;
+        if (k > last) o -= (k - last) * 2;
+      }
+    }
+    hl_dma(s.p + (KM ? (int64_t)kt * 64 * s.ld : (int64_t)kt * 128), o,
+           __builtin_amdgcn_readfirstlane(lds + (wave * ND + j) * 1024));
+  }
+  // Fragment of rows r0 + 16 i .. (r0 a multiple of 16 i's range), K half s.
+  // base: lane_base(r0, lane).
+  MOE_DEV static int lane_base(int r0, int lane) {
+    const int ln = lane & 15, lg = lane >> 4;
+    if (KM) {
+      const int f = (ln >> 2) | ((lg & 1) << 2);
+      return (8 * lg + (ln >> 2)) * RB + (((r0 >> 4) ^ f) << 5) + (ln & 3) * 8;
+    }
+    return (r0 + ln) * 128 + ((lg ^ (ln >> 1)) << 4);
+  }
+  MOE_DEV static bf16x8 frag(const uint8_t* st, int base, int i, int half) {
+    if (KM) {
+      const uint8_t* a = st + (base ^ (i << 5)) + half * 32 * RB;
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * RB));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    return *reinterpret_cast<const bf16x8*>(st + (base ^ (half << 6)) + i * 2048);
+  }
+};
+
+// The tile of a workgroup: BM x BN, WM x WN waves, S stages.
+template <int BM_, int BN_, int WM_, int WN_, int S_>
+struct HeadTile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
+  static constexpr int MI = BM / WM / 16, NJ = BN / WN / 16;  // 16-row and 16-column pieces per wave
+  static constexpr int STAGE = (BM + BN) * 128;
+  static_assert(WM * WN == 8, "eight waves");
+};
+
+template <class C, bool KMA, bool KMB>
+MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[C::MI][C::NJ], uint8_t* smem) {
+  using OA = HeadOperand<C::BM, KMA>;
+  using OB = HeadOperand<C::BN, KMB>;
+  constexpr int S = C::S, MI = C::MI, NJ = C::NJ, NPER = OA::ND + OB::ND;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  OA oa;
+  OB ob;
+  oa.init(sa, wave, lane);
+  ob.init(sb, wave, lane);
+  const uint32_t smem0 = lds_u32(smem);
+  auto issue1 = [&](int j, int kt, int slot) {
+    if (j < OA::ND) oa.issue(j, kt, smem0 + slot * C::STAGE, wave, lane);
+    else if (j < NPER) ob.issue(j - OA::ND, kt, smem0 + slot * C::STAGE + OA::BYTES, wave, lane);
+  };
+  const int ba = OA::lane_base((wave / C::WN) * MI * 16, lane);
+  const int bb = OB::lane_base((wave % C::WN) * NJ * 16, lane);
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    if (s < KT)
+#pragma unroll
+      for (int j = 0; j < NPER; ++j) issue1(j, s, s);
+  wait_stages<NPER>(min(S, KT) - 1);
+  lds_barrier();
+  bf16x8 a[2][MI], b[2][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) a[0][i] = OA::frag(smem, ba, i, 0);
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) b[0][j] = OB::frag(smem + OA::BYTES, bb, j, 0);
+  int slot = 0;
+#pragma unroll 1
+  for (int kt = 0; kt < KT; ++kt) {
+    const uint8_t* st = smem + slot * C::STAGE;
+    const int nslot = slot + 1 == S ? 0 : slot + 1;
+    // first half: its MFMAs, and the second half's fragments
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      a[1][i] = OA::frag(st, ba, i, 1);
+#pragma unroll
+      for (int j = i * NJ / MI; j < (i + 1) * NJ / MI; ++j) b[1][j] = OB::frag(st + OA::BYTES, bb, j, 1);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_bf16_16x16x32(b[0][j], a[0][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // every wave holds the rest of this stage in registers after the barrier:
+    // its slot is free; the next stage has landed
+    if (kt + 1 < KT) wait_stages<NPER>(min(S - 2, KT - 2 - kt));
+    lds_barrier();
+    const uint8_t* nst = smem + nslot * C::STAGE;
+    const bool more = kt + S < KT;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      a[0][i] = OA::frag(nst, ba, i, 0);
+#pragma unroll
+      for (int j = i * NJ / MI; j < (i + 1) * NJ / MI; ++j) b[0][j] = OB::frag(nst + OA::BYTES, bb, j, 0);
+      if (more) {
+#pragma unroll
+        for (int j = i * NPER / MI; j < (i + 1) * NPER / MI; ++j) issue1(j, kt + S, slot);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_bf16_16x16x32(b[1][j], a[1][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    slot = nslot;
+  }
+  lds_barrier();  // the stages are free
+}
+
+// Workgroup -> tile.  Workgroups go round the 8 XCDs; each XCD takes a
+// contiguous range of tiles, ordered in bands of GM tile rows, so the tiles
+// it works on at one time share few row and column panels in its L2.
+constexpr int HEAD_GM = 4;
+MOE_DEV bool head_tile(int bid, int nm, int nn, int& m, int& n) {
+  const int nt = nm * nn, per = (nt + 7) >> 3, at = bid >> 3, idx = (bid & 7) * per + at;
+  if (at >= per || idx >= nt) return false;
+  const int band = idx / (HEAD_GM * nn), rem = idx - band * HEAD_GM * nn;
+  const int gm = min(HEAD_GM, nm - band * HEAD_GM);
+  n = rem / gm;
+  m = band * HEAD_GM + rem - n * gm;
+  return true;
+}
 
 struct HeadGemm {
-  const uint16_t* h;
+  const uint16_t* hc;     // [..][Hp]
   const uint16_t* w;
-  int64_t h_stride, w_stride;
-  int H, V, top;
+  int64_t w_stride;
+  int H, Hp, V, top;
   const int32_t* rows;
   const int32_t* count;
-  const float* r;
-  const float* lse;
-  const float* dloss;
+  const float* r;         // [count]
+  const float* lse;       // [T]
+  const float* dloss;     // [T]
   float scale;
   const int32_t* ids;
   float* stats;   // [count][nvb][2]
   float* zt;      // [T][top]
-  uint16_t* g;    // [count][piece]
+  uint16_t* g;    // [..][piece]
   float* u;       // [count][H]
   uint16_t* dw;   // [V][H]
   int v0, piece;
 };
 
-template <int MODE>
-__global__ __launch_bounds__(256) void k_head_gemm(HeadGemm p) {
-  __shared__ __align__(16) uint16_t sa[HB * HS], sb[HB * HS];
-  __shared__ float zs[MODE == HP_STATS ? HB * (HB + 1) : 1];
-  __shared__ float rm[2][HB], rs[2][HB];
-  const int n = *p.count;
-  const int m0 = blockIdx.y * HB, n0 = blockIdx.x * HB;
-  const int M = MODE == HP_DW ? min(p.piece, p.V - p.v0) : n;
-  if (m0 >= M) return;
-  const int N = (MODE == HP_STATS || MODE == HP_GRAD) ? p.V : p.H;
-  const int K = (MODE == HP_STATS || MODE == HP_GRAD) ? p.H : MODE == HP_DZ ? min(p.piece, p.V - p.v0) : n;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int ln = lane & 15, lg = lane >> 4;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-  f32x4 acc[4][4];
+// Forward: per row and block of BN columns the maximum of y = l log2 e and the
+// sum of 2^(y - maximum), and the logits at the target's ids (the tile goes
+// through LDS for those).
+template <class C>
+__global__ __launch_bounds__(512, 2) void k_head_stats(HeadGemm p) {
+  constexpr int SMEM = C::S * C::STAGE;
+  __shared__ __align__(16) uint8_t smem[SMEM];
+  __shared__ float rm[C::WN][C::BM], rs[C::WN][C::BM];
+  const int n = *p.count, nvb = (p.V + C::BN - 1) / C::BN;
+  int mt, nt;
+  if (!head_tile(blockIdx.x, (n + C::BM - 1) / C::BM, nvb, mt, nt)) return;
+  const int m0 = mt * C::BM, n0 = nt * C::BN;
+  const HeadSrc sa = {reinterpret_cast<const char*>(p.hc + (int64_t)m0 * p.Hp), (uint32_t)p.Hp * 2, C::BM, p.Hp};
+  const HeadSrc sb = {reinterpret_cast<const char*>(p.w + (int64_t)n0 * p.w_stride), (uint32_t)p.w_stride * 2,
+                      p.V - n0, p.H};
+  f32x4 acc[C::MI][C::NJ];
+  head_mm<C, false, false>(sa, sb, p.Hp / 64, acc, smem);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
+  const int wm = wave / C::WN * C::MI * 16, wn = wave % C::WN * C::NJ * 16;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < C::MI; ++i) {
+    const int row = wm + i * 16 + ln;
+    const float f = m0 + row < n ? p.scale * p.r[m0 + row] : 0.0f;
+    float mx = -INFINITY, s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-  const u32x4 zero = {0, 0, 0, 0};
-  for (int k0 = 0; k0 < K; k0 += HK) {
-    __syncthreads();
-    if (MODE == HP_STATS || MODE == HP_GRAD || MODE == HP_DZ) {  // A rows hold K contiguously
-      for (int c = threadIdx.x; c < HB * HK / 8; c += 256) {
-        const int m = m0 + c / (HK / 8), k = k0 + c % (HK / 8) * 8;
-        u32x4 q = zero;
-        if (m < M && k < K) {
-          const uint16_t* src = MODE == HP_DZ ? p.g + (int64_t)m * p.piece + k
-                                              : p.h + (int64_t)p.rows[m] * p.h_stride + k;
-          q = *reinterpret_cast<const u32x4*>(src);
-        }
-        *reinterpret_cast<u32x4*>(sa + (c / (HK / 8)) * HS + c % (HK / 8) * 8) = q;
+    for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[i][j][e] *= f;
+        if (n0 + wn + j * 16 + lg * 4 + e < p.V) mx = fmaxf(mx, acc[i][j][e]);
       }
-    } else {
-      for (int c = threadIdx.x; c < HB * HK / 8; c += 256) {
-        const int k = c / (HB / 8), m = c % (HB / 8) * 8;
-        u32x4 q = zero;
-        if (k0 + k < K) q = *reinterpret_cast<const u32x4*>(p.g + (int64_t)(k0 + k) * p.piece + m0 + m);
+    mx = fmaxf(mx, shfl_xor(mx, 16));
+    mx = fmaxf(mx, shfl_xor(mx, 32)) * kLog2e;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sa[(m + 2 * i) * HS + k] = (uint16_t)(q[i] & 0xFFFFu);
-          sa[(m + 2 * i + 1) * HS + k] = (uint16_t)(q[i] >> 16);
-        }
-      }
+    for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n0 + wn + j * 16 + lg * 4 + e < p.V) s += hl_exp2(fmaf(acc[i][j][e], kLog2e, -mx));
+    s += shfl_xor(s, 16);
+    s += shfl_xor(s, 32);
+    if (lg == 0) {
+      rm[wave % C::WN][row] = mx;
+      rs[wave % C::WN][row] = s;
     }
-    if (MODE == HP_STATS || MODE == HP_GRAD) {
-      for (int c = threadIdx.x; c < HB * HK / 8; c += 256) {
-        const int v = p.v0 + n0 + c / (HK / 8), k = k0 + c % (HK / 8) * 8;
-        u32x4 q = zero;
-        if (v < N && k < K) q = *reinterpret_cast<const u32x4*>(p.w + (int64_t)v * p.w_stride + k);
-        *reinterpret_cast<u32x4*>(sb + (c / (HK / 8)) * HS + c % (HK / 8) * 8) = q;
-      }
-    } else {
-      for (int c = threadIdx.x; c < HB * HK / 8; c += 256) {
-        const int k = c / (HB / 8), m = c % (HB / 8) * 8;
-        u32x4 q = zero;
-        if (k0 + k < K && n0 + m < N)
-          q = *reinterpret_cast<const u32x4*>(
-              (MODE == HP_DZ ? p.w + (int64_t)(p.v0 + k0 + k) * p.w_stride
-                             : p.h + (int64_t)p.rows[k0 + k] * p.h_stride) + n0 + m);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sb[(m + 2 * i) * HS + k] = (uint16_t)(q[i] & 0xFFFFu);
-          sb[(m + 2 * i + 1) * HS + k] = (uint16_t)(q[i] >> 16);
-        }
-      }
-    }
-    __syncthreads();
-    bf16x8 a[4], b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = *reinterpret_cast<const bf16x8*>(sa + (wm + i * 16 + ln) * HS + lg * 8);
-      b[i] = *reinterpret_cast<const bf16x8*>(sb + (wn + i * 16 + ln) * HS + lg * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = mfma_bf16_16x16x32(a[i], b[j], acc[i][j]);
   }
-  // accumulator [i][j][e]: row wm + 16 i + 4 lg + e, column wn + 16 j + ln
+  // logits at the ids: ZR rows of the tile at a time, 16-byte piece q of a row at q ^ (row & 15)
+  constexpr int ZR = C::BM * C::BN * 4 <= SMEM ? C::BM : C::BM / C::WM;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int z0 = 0; z0 < C::BM; z0 += ZR) {
+    if (z0) lds_barrier();
+    if (ZR == C::BM || wm == z0) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int lr = wm + i * 16 + lg * 4 + e, c = m0 + lr;
-      const bool in = c < M;
-      if (MODE == HP_STATS) {
-        const float f = in ? p.scale * p.r[p.rows[c]] : 0.0f;
-        float z[4], mx = -INFINITY, s = 0.0f;
+      for (int i = 0; i < C::MI; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          z[j] = n0 + wn + j * 16 + ln < N ? acc[i][j][e] * f : -INFINITY;
-          zs[lr * (HB + 1) + wn + j * 16 + ln] = z[j];
-          mx = fmaxf(mx, z[j]);
+        for (int j = 0; j < C::NJ; ++j) {
+          const int row = wm + i * 16 + ln, q = (wn + j * 16) / 4 + lg;
+          *reinterpret_cast<f32x4*>(smem + (row - z0) * C::BN * 4 + ((q ^ (row & 15)) << 4)) = acc[i][j];
         }
-#pragma unroll
-        for (int x = 1; x < 16; x <<= 1) mx = fmaxf(mx, shfl_xor(mx, x));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s += n0 + wn + j * 16 + ln < N ? expf(z[j] - mx) : 0.0f;
-#pragma unroll
-        for (int x = 1; x < 16; x <<= 1) s += shfl_xor(s, x);
-        if (ln == 0) {
-          rm[wave & 1][lr] = mx;
-          rs[wave & 1][lr] = s;
-        }
-      } else if (in) {
-        if (MODE == HP_GRAD) {
-          const int t = p.rows[c];
-          const float f = p.scale * p.r[t], l = p.lse[t], cf = f * p.dloss[t];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int v = n0 + wn + j * 16 + ln;
-            if (v < p.piece)
-              p.g[(int64_t)c * p.piece + v] =
-                  p.v0 + v < N ? (uint16_t)f32_to_bf16_bits(cf * expf(acc[i][j][e] * f - l)) : 0;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int v = n0 + wn + j * 16 + ln;
-            if (v >= N) continue;
-            if (MODE == HP_DZ) {
-              float* o = p.u + (int64_t)c * p.H + v;
-              *o = p.v0 == 0 ? acc[i][j][e] : *o + acc[i][j][e];
-            } else {
-              p.dw[(int64_t)(p.v0 + c) * p.H + v] = (uint16_t)f32_to_bf16_bits(acc[i][j][e]);
-            }
-          }
-        }
-      }
     }
-  if (MODE == HP_STATS) {
-    __syncthreads();
-    if (threadIdx.x < HB && m0 + (int)threadIdx.x < M) {
-      const int lr = threadIdx.x;
-      float m = rm[0][lr], s = rs[0][lr];
-      hl_merge(m, s, rm[1][lr], rs[1][lr]);
-      float* o = p.stats + ((int64_t)(m0 + lr) * gridDim.x + blockIdx.x) * 2;
-      o[0] = m;
-      o[1] = s;
-    }
-    for (int q = threadIdx.x; q < HB * p.top; q += 256) {
-      const int lr = q / p.top;
-      if (m0 + lr >= M) break;
-      const int64_t at = (int64_t)p.rows[m0 + lr] * p.top + q % p.top;
+    lds_barrier();
+    for (int x = threadIdx.x; x < ZR * p.top; x += 512) {
+      const int row = z0 + x / p.top;
+      if (m0 + row >= n) break;
+      const int64_t at = (int64_t)p.rows[m0 + row] * p.top + x % p.top;
       const int v = p.ids[at] - n0;
-      if (v >= 0 && v < HB && n0 + v < N) p.zt[at] = zs[lr * (HB + 1) + v];
+      if (v >= 0 && v < C::BN && n0 + v < p.V)
+        p.zt[at] = *reinterpret_cast<const float*>(smem + (row - z0) * C::BN * 4 + (((v >> 2) ^ (row & 15)) << 4) +
+                                                   (v & 3) * 4);
     }
   }
+  for (int row = threadIdx.x; row < C::BM && m0 + row < n; row += 512) {
+    float m = rm[0][row], s = rs[0][row];
+#pragma unroll
+    for (int w = 1; w < C::WN; ++w) hl_merge(m, s, rm[w][row], rs[w][row]);
+    float* o = p.stats + ((int64_t)(m0 + row) * nvb + nt) * 2;
+    o[0] = m;
+    o[1] = s;
+  }
+}
+
+// Backward: G, columns [v0, v0 + piece), of every row of the tiles (zeros
+// behind the last row and past the vocabulary).
+template <class C>
+__global__ __launch_bounds__(512, 2) void k_head_grad(HeadGemm p) {
+  __shared__ __align__(16) uint8_t smem[C::S * C::STAGE];
+  const int n = *p.count;
+  int mt, nt;
+  if (!head_tile(blockIdx.x, (n + C::BM - 1) / C::BM, p.piece / C::BN, mt, nt)) return;
+  const int m0 = mt * C::BM, n0 = p.v0 + nt * C::BN;
+  const HeadSrc sa = {reinterpret_cast<const char*>(p.hc + (int64_t)m0 * p.Hp), (uint32_t)p.Hp * 2, C::BM, p.Hp};
+  // a piece's last tiles may lie past the vocabulary: they read its last row and write zeros
+  const int nb = min(n0, p.V - 1);
+  const HeadSrc sb = {reinterpret_cast<const char*>(p.w + (int64_t)nb * p.w_stride), (uint32_t)p.w_stride * 2,
+                      p.V - nb, p.H};
+  f32x4 acc[C::MI][C::NJ];
+  head_mm<C, false, false>(sa, sb, p.Hp / 64, acc, smem);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
+  const int wm = wave / C::WN * C::MI * 16, wn = wave % C::WN * C::NJ * 16;
+#pragma unroll
+  for (int i = 0; i < C::MI; ++i) {
+    const int c = m0 + wm + i * 16 + ln;
+    float f = 0.0f, l = 0.0f, cf = 0.0f;
+    if (c < n) {
+      const int t = p.rows[c];
+      const float sr = p.scale * p.r[c];
+      f = sr * kLog2e;
+      l = p.lse[t] * kLog2e;
+      cf = sr * p.dloss[t];
+    }
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool in = c < n && n0 + wn + j * 16 + lg * 4 + e < p.V;
+        x[e] = in ? cf * hl_exp2(fmaf(acc[i][j][e], f, -l)) : 0.0f;
+      }
+      const u32x2 q = {bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3])};
+      *reinterpret_cast<u32x2*>(p.g + (int64_t)c * p.piece + (n0 - p.v0) + wn + j * 16 + lg * 4) = q;
+    }
+  }
+}
+
+// u += G W over a piece.
+template <class C>
+MOE_DEV void head_dz(const HeadGemm& p, int bid, uint8_t* smem) {
+  const int n = *p.count;
+  int mt, nt;
+  if (!head_tile(bid, (n + C::BM - 1) / C::BM, (p.H + C::BN - 1) / C::BN, mt, nt)) return;
+  const int m0 = mt * C::BM, n0 = nt * C::BN, K = min(p.piece, p.V - p.v0);
+  const HeadSrc sa = {reinterpret_cast<const char*>(p.g + (int64_t)m0 * p.piece), (uint32_t)p.piece * 2, C::BM,
+                      p.piece};
+  const HeadSrc sb = {reinterpret_cast<const char*>(p.w + (int64_t)p.v0 * p.w_stride + n0), (uint32_t)p.w_stride * 2,
+                      p.H - n0, K};
+  f32x4 acc[C::MI][C::NJ];
+  head_mm<C, false, true>(sa, sb, (K + 63) / 64, acc, smem);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
+  const int wm = wave / C::WN * C::MI * 16, wn = wave % C::WN * C::NJ * 16;
+#pragma unroll
+  for (int i = 0; i < C::MI; ++i) {
+    const int c = m0 + wm + i * 16 + ln;
+    if (c >= n) continue;
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j) {
+      const int col = n0 + wn + j * 16 + lg * 4;
+      if (col >= p.H) continue;
+      f32x4* o = reinterpret_cast<f32x4*>(p.u + (int64_t)c * p.H + col);
+      *o = p.v0 == 0 ? acc[i][j] : *o + acc[i][j];
+    }
+  }
+}
+
+// d_w rows [v0, v0 + piece) = G^T h.
+template <class C>
+MOE_DEV void head_dw(const HeadGemm& p, int bid, uint8_t* smem) {
+  const int n = *p.count, M = min(p.piece, p.V - p.v0);
+  int mt, nt;
+  if (!head_tile(bid, (M + C::BM - 1) / C::BM, (p.H + C::BN - 1) / C::BN, mt, nt)) return;
+  const int m0 = mt * C::BM, n0 = nt * C::BN, KT = (n + 63) / 64;
+  const HeadSrc sa = {reinterpret_cast<const char*>(p.g + m0), (uint32_t)p.piece * 2, p.piece - m0, KT * 64};
+  const HeadSrc sb = {reinterpret_cast<const char*>(p.hc + n0), (uint32_t)p.Hp * 2, p.Hp - n0, KT * 64};
+  f32x4 acc[C::MI][C::NJ];
+  if (KT > 0) {
+    head_mm<C, true, true>(sa, sb, KT, acc, smem);
+  } else {
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+      for (int j = 0; j < C::NJ; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
+  const int wm = wave / C::WN * C::MI * 16, wn = wave % C::WN * C::NJ * 16;
+#pragma unroll
+  for (int i = 0; i < C::MI; ++i) {
+    const int v = m0 + wm + i * 16 + ln;
+    if (v >= M) continue;
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j) {
+      const int col = n0 + wn + j * 16 + lg * 4;
+      if (col >= p.H) continue;
+      const u32x2 q = {bf16x2_bits(acc[i][j][0], acc[i][j][1]), bf16x2_bits(acc[i][j][2], acc[i][j][3])};
+      *reinterpret_cast<u32x2*>(p.dw + (int64_t)(p.v0 + v) * p.H + col) = q;
+    }
+  }
+}
+
+template <class C>
+__global__ __launch_bounds__(512, 2) void k_head_dz(HeadGemm p) {
+  __shared__ __align__(16) uint8_t smem[C::S * C::STAGE];
+  head_dz<C>(p, blockIdx.x, smem);
+}
+template <class C>
+__global__ __launch_bounds__(512, 2) void k_head_dw(HeadGemm p) {
+  __shared__ __align__(16) uint8_t smem[C::S * C::STAGE];
+  head_dw<C>(p, blockIdx.x, smem);
 }
 
 // Per token (one wave): joins its blocks' statistics and forms the outputs.
@@ -352,7 +597,7 @@ __global__ __launch_bounds__(256) void k_head_finish(const float* __restrict__ s
     const float m2 = shfl_xor(m, x), s2 = shfl_xor(s, x);
     hl_merge(m, s, m2, s2);
   }
-  const float l = m + logf(s);
+  const float l = m * kLn2 + logf(s);
   float kl;
   if (distill) {
     kl = 0.0f;
@@ -389,7 +634,7 @@ __global__ __launch_bounds__(256) void k_head_targets(const int32_t* __restrict_
   const int c = blockIdx.x * 4 + wave;
   if (c >= *count) return;
   const int t = rows[c];
-  const float cf = scale * r[t] * dloss[t];
+  const float cf = scale * r[c] * dloss[t];
   if (lq == nullptr) {  // cross entropy: p - 1 = exp(-loss) - 1
     const int v = ids[t] - v0;
     if (lane == 0 && v >= 0 && v < piece)
@@ -440,7 +685,7 @@ __global__ __launch_bounds__(256) void k_head_dh(const float* __restrict__ u, co
     dot = hl_sum64(dot);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
     __syncthreads();
-    f = r[t] * r[t] * ((part[0] + part[1]) + (part[2] + part[3])) / (float)H;
+    f = r[c] * r[c] * ((part[0] + part[1]) + (part[2] + part[3])) / (float)H;
   }
   for (int i = threadIdx.x; i < H / 8; i += 256) {
     const f32x4 a = *reinterpret_cast<const f32x4*>(ur + i * 8), b = *reinterpret_cast<const f32x4*>(ur + i * 8 + 4);
@@ -458,6 +703,7 @@ __global__ __launch_bounds__(256) void k_head_dh(const float* __restrict__ u, co
 
 namespace {
 inline int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+using HeadBig = HeadTile<256, 256, 2, 4, 2>;
 }  // namespace
 
 HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
@@ -474,24 +720,26 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
     o = (o + bytes + 255) / 256 * 256;
     return at;
   };
-  const size_t t = (size_t)T;
-  p.r = take(t * 4);
-  p.flag = take(t);
+  const size_t t = (size_t)T, rows = (t + 255) / 256 * 256;  // rows of the largest tiles
+  p.Hp = (H + 63) / 64 * 64;
+  p.r = take(rows * 4);
+  p.flag = take(distill ? t : 0);
   p.rows = take(t * 4);
   p.cidx = take(t * 4);
   p.count = take(4);
+  p.hc = take(rows * p.Hp * 2);
   p.lq = take(distill ? t * top * 4 : 0);
   if (!bwd) {
     p.zt = take(t * top * 4);
-    p.stats = take(t * cdiv(V, HB) * 8);
+    p.stats = take(t * cdiv(V, HeadBig::BN) * 8);
   } else {
     // columns of G per piece: 256 MB of G, at least 256 columns
-    const int64_t most = T > 0 ? ((int64_t)128 << 20) / T / 256 * 256 : V;
+    const int64_t most = T > 0 ? ((int64_t)128 << 20) / (int64_t)rows / 256 * 256 : V;
     p.npieces = cdiv(V, most > 256 ? most : 256);
     p.piece = cdiv(cdiv(V, p.npieces), 256) * 256;
     p.npieces = cdiv(V, p.piece);
     p.u = take(t * H * 4);
-    p.g = take(t * p.piece * 2);
+    p.g = take(rows * p.piece * 2);
   }
   p.total = o;
   return p;
@@ -500,20 +748,23 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
 static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
   char* ws = a.ws;
   float* r = reinterpret_cast<float*>(ws + p.r);
-  uint8_t* flag = reinterpret_cast<uint8_t*>(ws + p.flag);
+  uint8_t* flag = p.distill ? reinterpret_cast<uint8_t*>(ws + p.flag) : nullptr;
   int32_t* rows = reinterpret_cast<int32_t*>(ws + p.rows);
   int32_t* cidx = reinterpret_cast<int32_t*>(ws + p.cidx);
   int32_t* count = reinterpret_cast<int32_t*>(ws + p.count);
-  float* lq = p.distill ? reinterpret_cast<float*>(ws + p.lq) : nullptr;
-  hipLaunchKernelGGL(k_head_rows, dim3(cdiv(p.T, 4)), dim3(256), 0, s, a.h, a.h_stride, p.T, p.H, p.V, a.eps, a.ids,
-                     p.top, a.tlogits, a.teacher_scale, r, flag, lq);
-  hipLaunchKernelGGL(k_head_compact, dim3(1), dim3(1024), 0, s, flag, p.T, rows, cidx, count);
+  uint16_t* hc = reinterpret_cast<uint16_t*>(ws + p.hc);
+  if (p.distill)
+    hipLaunchKernelGGL(k_head_teacher, dim3(cdiv(p.T, 4)), dim3(256), 0, s, a.ids, a.tlogits, p.T, p.V, p.top,
+                       a.teacher_scale, reinterpret_cast<float*>(ws + p.lq), flag);
+  hipLaunchKernelGGL(k_head_compact, dim3(1), dim3(1024), 0, s, flag, a.ids, p.T, p.V, rows, cidx, count);
+  hipLaunchKernelGGL(k_head_gather, dim3(cdiv(p.T, 64) * 64), dim3(256), 0, s, a.h, a.h_stride, p.H, p.Hp, a.eps, rows,
+                     count, hc, r);
   HeadGemm g{};
-  g.h = a.h;
+  g.hc = hc;
   g.w = a.w;
-  g.h_stride = a.h_stride;
   g.w_stride = a.w_stride;
   g.H = p.H;
+  g.Hp = p.Hp;
   g.V = p.V;
   g.top = p.top;
   g.rows = rows;
@@ -527,12 +778,16 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
   return g;
 }
 
+// Workgroups for nm x nn tiles (a multiple of the 8 XCDs).
+static int head_grid(int nm, int nn) { return cdiv((int64_t)nm * nn, 8) * 8; }
+
 void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
+  using C = HeadBig;
   HeadGemm g = head_common(p, a, s);
-  const int nvb = cdiv(p.V, HB);
+  const int nvb = cdiv(p.V, C::BN);
   g.stats = reinterpret_cast<float*>(a.ws + p.stats);
   g.zt = reinterpret_cast<float*>(a.ws + p.zt);
-  hipLaunchKernelGGL(k_head_gemm<HP_STATS>, dim3(nvb, cdiv(p.T, HB)), dim3(256), 0, s, g);
+  hipLaunchKernelGGL(k_head_stats<C>, dim3(head_grid(cdiv(p.T, C::BM), nvb)), dim3(512), 0, s, g);
   hipLaunchKernelGGL(k_head_finish, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.stats, g.zt,
                      reinterpret_cast<const int32_t*>(a.ws + p.cidx), a.ids,
                      reinterpret_cast<const float*>(a.ws + p.lq), p.T, p.V, nvb, p.top, p.distill, a.loss, a.lse,
@@ -540,19 +795,21 @@ void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
 }
 
 void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
+  using C = HeadBig;
   HeadGemm g = head_common(p, a, s);
   g.u = reinterpret_cast<float*>(a.ws + p.u);
   g.g = reinterpret_cast<uint16_t*>(a.ws + p.g);
   g.piece = p.piece;
-  const int mb = cdiv(p.T, HB), hb = cdiv(p.H, HB);
+  const int mb = cdiv(p.T, C::BM), hb = cdiv(p.H, C::BN);
   for (int i = 0; i < p.npieces; ++i) {
     g.v0 = i * p.piece;
-    hipLaunchKernelGGL(k_head_gemm<HP_GRAD>, dim3(p.piece / HB, mb), dim3(256), 0, s, g);
+    hipLaunchKernelGGL(k_head_grad<C>, dim3(head_grid(mb, p.piece / C::BN)), dim3(512), 0, s, g);
     hipLaunchKernelGGL(k_head_targets, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.rows, g.count, a.ids,
                        p.distill ? reinterpret_cast<const float*>(a.ws + p.lq) : nullptr, a.logp, a.loss, g.r,
                        a.dloss, a.scale, p.V, p.top, g.v0, p.piece, g.g);
-    hipLaunchKernelGGL(k_head_gemm<HP_DZ>, dim3(hb, mb), dim3(256), 0, s, g);
-    if (a.dw != nullptr) hipLaunchKernelGGL(k_head_gemm<HP_DW>, dim3(hb, p.piece / HB), dim3(256), 0, s, g);
+    hipLaunchKernelGGL(k_head_dz<C>, dim3(head_grid(mb, hb)), dim3(512), 0, s, g);
+    if (a.dw != nullptr)
+      hipLaunchKernelGGL(k_head_dw<C>, dim3(head_grid(p.piece / C::BM, hb)), dim3(512), 0, s, g);
   }
   hipLaunchKernelGGL(k_head_dh, dim3(p.T), dim3(256), 0, s, g.u, a.h, a.h_stride,
                      reinterpret_cast<const int32_t*>(a.ws + p.cidx), g.r, p.H, a.eps > 0.0f, a.dh);

@@ -198,7 +198,8 @@ struct HeadPlan {
   bool distill, bwd;
   int piece, npieces;     // backward: columns of G per piece (multiple of 256), pieces
   // byte offsets into the workspace
-  size_t r, flag, rows, cidx, count, lq, zt, stats, u, g, total;
+  int Hp;                 // H rounded up to the products' K step
+  size_t r, flag, rows, cidx, count, hc, lq, zt, stats, u, g, total;
 };
 struct HeadArgs {
   const uint16_t* h;

@@ -1067,7 +1067,7 @@ moe_status check_head(const moe_lm_head* hd, int32_t top) {
   if (!(hd->logit_scale > 0.0f && hd->logit_scale <= 3.0e38f)) return MOE_ERR_INVALID_ARGUMENT;
   for (int64_t st : {hd->h_stride, hd->w_stride}) {
     if (st < 0 || (st != 0 && st < hd->hidden)) return MOE_ERR_INVALID_ARGUMENT;
-    if (st % 8 != 0) return MOE_ERR_UNSUPPORTED;
+    if (st % 8 != 0 || st > (1 << 22)) return MOE_ERR_UNSUPPORTED;
   }
   if (hd->hidden % 8 != 0 || hd->hidden > (1 << 15) || hd->vocab > (1 << 20) || hd->num_tokens > (1 << 20) ||
       top > MOE_DISTILL_MAX_TOP)

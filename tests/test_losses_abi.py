@@ -49,7 +49,7 @@ def _distill_bwd(hd, top=4, ts=1.0, ptrs=None, nb=BIG):
     (dict(T=-1), INV), (dict(H=0), INV), (dict(V=0), INV), (dict(eps=-1.0), INV), (dict(eps=math.nan), INV),
     (dict(eps=math.inf), INV), (dict(scale=0.0), INV), (dict(scale=-1.0), INV), (dict(scale=math.nan), INV),
     (dict(scale=math.inf), INV), (dict(hs=-8), INV), (dict(hs=248), INV), (dict(ws=128), INV), (dict(H=252), UNS),
-    (dict(hs=260), UNS), (dict(ws=257), UNS), (dict(H=1 << 16), UNS), (dict(V=(1 << 20) + 1), UNS),
+    (dict(hs=260), UNS), (dict(ws=257), UNS), (dict(ws=(1 << 22) + 8), UNS), (dict(H=1 << 16), UNS), (dict(V=(1 << 20) + 1), UNS),
     (dict(T=(1 << 20) + 1), UNS)])
 def test_head_descriptor(change, status):
     hd = _head(**change)
