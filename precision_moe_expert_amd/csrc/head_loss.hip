@@ -17,6 +17,8 @@
 #include "common.h"
 #include "kernels.h"
 
+#include <type_traits>
+
 namespace moe {
 
 namespace {
@@ -123,18 +125,64 @@ __global__ __launch_bounds__(1024) void k_head_compact(const uint8_t* __restrict
 // The rows that count, one after the other, as the products read them: hc
 // [..][Hp] with zeros in columns H..Hp and in the rows up to the next multiple
 // of 64 (the K of a product runs over either in steps of 64); r[c] = 1/rms of
-// row c.  One block per row.
+// row c.  One block per row.  FEW (at most 1024 tokens): every block finds its
+// own token among the flags, and block 0 writes the lists, so that no launch
+// is spent on k_head_compact.
+template <bool FEW>
 __global__ __launch_bounds__(256) void k_head_gather(const uint16_t* __restrict__ h, int64_t h_stride, int H, int Hp,
-                                                     float eps, const int32_t* __restrict__ rows,
-                                                     const int32_t* __restrict__ count, uint16_t* __restrict__ hc,
+                                                     float eps, const uint8_t* __restrict__ flag,
+                                                     const int32_t* __restrict__ ids, int T, int V,
+                                                     int32_t* __restrict__ rows, int32_t* __restrict__ cidx,
+                                                     int32_t* __restrict__ count, uint16_t* __restrict__ hc,
                                                      float* __restrict__ r) {
   __shared__ float part[4];
-  const int c = blockIdx.x, n = *count;
+  __shared__ int wsum[4], found;
+  const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  int n, t = 0;
+  if (FEW) {
+    // thread i looks at tokens 4 i .. 4 i + 3
+    int on[4], k = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int u = tid * 4 + i;
+      on[i] = u < T && (flag != nullptr ? flag[u] != 0 : ids[u] >= 0 && ids[u] < V);
+      k += on[i];
+    }
+    int before = k;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(before, d, 64);
+      if (lane >= d) before += v;
+    }
+    if (lane == 63) wsum[tid >> 6] = before;
+    __syncthreads();
+    before -= k;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      if (w < (tid >> 6)) before += wsum[w];
+    n = wsum[0] + wsum[1] + wsum[2] + wsum[3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int u = tid * 4 + i;
+      if (on[i] && before == c) found = u;
+      if (c == 0 && u < T) {
+        cidx[u] = on[i] ? before : -1;
+        if (on[i]) rows[before] = u;
+      }
+      before += on[i];
+    }
+    if (c == 0 && tid == 0) *count = n;
+    __syncthreads();
+    if (c < n) t = found;
+  } else {
+    n = *count;
+    if (c < n) t = rows[c];
+  }
   if (c >= (n + 63) / 64 * 64) return;
   uint16_t* o = hc + (int64_t)c * Hp;
-  const uint16_t* row = c < n ? h + (int64_t)rows[c] * h_stride : nullptr;
+  const uint16_t* row = h + (int64_t)t * h_stride;
   float ss = 0.0f;
-  for (int i = threadIdx.x; i < Hp / 8; i += 256) {
+  for (int i = tid; i < Hp / 8; i += 256) {
     u32x4 q = {0, 0, 0, 0};
     if (c < n && i < H / 8) q = *reinterpret_cast<const u32x4*>(row + i * 8);
     *reinterpret_cast<u32x4*>(o + i * 8) = q;
@@ -147,9 +195,9 @@ __global__ __launch_bounds__(256) void k_head_gather(const uint16_t* __restrict_
   }
   if (c >= n) return;
   ss = hl_sum64(ss);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = ss;
+  if (lane == 0) part[tid >> 6] = ss;
   __syncthreads();
-  if (threadIdx.x == 0)
+  if (tid == 0)
     r[c] = eps > 0.0f ? 1.0f / sqrtf(((part[0] + part[1]) + (part[2] + part[3])) / (float)H + eps) : 1.0f;
 }
 
@@ -217,11 +265,13 @@ struct HeadOperand {
       }
     }
   }
-  // DMA j of stage kt into the stage at LDS address lds.
+  // DMA j of stage kt into the stage at LDS address lds.  LAST: the stage may
+  // reach past the end of K.
+  template <bool LAST>
   MOE_DEV void issue(int j, int kt, uint32_t lds, int wave, int lane) const {
     uint32_t o = off[j];
     const int over = kt * 64 + 64 - s.k;  // K past the end (uniform)
-    if (over > 0) {
+    if (LAST && over > 0) {
       const int row = row_of(wave, lane, j);
       if (KM) {
         const int last = 63 - over;
@@ -256,12 +306,19 @@ struct HeadOperand {
   }
 };
 
-// The tile of a workgroup: BM x BN, WM x WN waves, S stages.
-template <int BM_, int BN_, int WM_, int WN_, int S_>
+// The tile of a workgroup: BM x BN, WM x WN waves, S stages; WPS waves per
+// SIMD in flight (2 per resident workgroup).
+template <int BM_, int BN_, int WM_, int WN_, int S_, int WPS_>
 struct HeadTile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, WPS = WPS_;
   static constexpr int MI = BM / WM / 16, NJ = BN / WN / 16;  // 16-row and 16-column pieces per wave
   static constexpr int STAGE = (BM + BN) * 128;
+  // Tiles with two stages keep a fifth half-stage buffer: A and B pieces of the
+  // stages take turns in a ring of five, and A's of the stage after the next are
+  // requested half a step before B's.
+  static constexpr bool FIVE = S == 2;
+  static_assert(!FIVE || BM == BN, "buffers of one size");
+  static constexpr int SMEM = FIVE ? 5 * BM * 128 : S * STAGE;
   static_assert(WM * WN == 8, "eight waves");
 };
 
@@ -276,9 +333,17 @@ MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[
   oa.init(sa, wave, lane);
   ob.init(sb, wave, lane);
   const uint32_t smem0 = lds_u32(smem);
-  auto issue1 = [&](int j, int kt, int slot) {
-    if (j < OA::ND) oa.issue(j, kt, smem0 + slot * C::STAGE, wave, lane);
-    else if (j < NPER) ob.issue(j - OA::ND, kt, smem0 + slot * C::STAGE + OA::BYTES, wave, lane);
+  // a stage's place: its slot of the ring, or (FIVE) the buffer of its A piece,
+  // B's piece in the next one
+  auto off_a = [](int slot) { return C::FIVE ? slot * OA::BYTES : slot * C::STAGE; };
+  auto off_b = [](int slot) {
+    return C::FIVE ? (slot == 4 ? 0 : slot + 1) * OA::BYTES : slot * C::STAGE + OA::BYTES;
+  };
+  auto next = [](int slot) { return C::FIVE ? (slot >= 3 ? slot - 3 : slot + 2) : slot + 1 == S ? 0 : slot + 1; };
+  auto issue1 = [&](auto last, int j, int kt, int slot) {
+    constexpr bool LAST = decltype(last)::value;
+    if (j < OA::ND) oa.template issue<LAST>(j, kt, smem0 + off_a(slot), wave, lane);
+    else ob.template issue<LAST>(j - OA::ND, kt, smem0 + off_b(slot), wave, lane);
   };
   const int ba = OA::lane_base((wave / C::WN) * MI * 16, lane);
   const int bb = OB::lane_base((wave % C::WN) * NJ * 16, lane);
@@ -290,50 +355,70 @@ MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[
   for (int s = 0; s < S; ++s)
     if (s < KT)
 #pragma unroll
-      for (int j = 0; j < NPER; ++j) issue1(j, s, s);
+      for (int j = 0; j < NPER; ++j) issue1(std::true_type(), j, s, C::FIVE ? 2 * s : s);
   wait_stages<NPER>(min(S, KT) - 1);
   lds_barrier();
-  bf16x8 a[2][MI], b[2][NJ];
+  // fragments of the current and of the next 32 K: B's, then A's
+  bf16x8 f[2][NJ + MI];
+  auto read = [&](int x, int slot, int i, int half) {
+    f[x][i] = i < NJ ? OB::frag(smem + off_b(slot), bb, i, half) : OA::frag(smem + off_a(slot), ba, i - NJ, half);
+  };
 #pragma unroll
-  for (int i = 0; i < MI; ++i) a[0][i] = OA::frag(smem, ba, i, 0);
+  for (int i = 0; i < NJ + MI; ++i) read(0, 0, i, 0);
+  // The MFMAs of fragments f[x], and the next fragments into f[1 - x] over the
+  // first of them (so that they have arrived when they are wanted); dma(i)
+  // issues the i-th part of a stage.  A fixed order: MFMAs lead each group.
+  constexpr int RG = MI > 2 ? MI - 2 : MI;  // groups that read
+  auto phase = [&](auto x, int rslot, int half, auto dma) {
+    constexpr int X = decltype(x)::value;
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) b[0][j] = OB::frag(smem + OA::BYTES, bb, j, 0);
+    for (int i = 0; i < MI; ++i) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_bf16_16x16x32(f[X][j], f[X][NJ + i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int r = i * (NJ + MI) / RG; r < (i + 1) * (NJ + MI) / RG && r < NJ + MI; ++r) read(1 - X, rslot, r, half);
+      dma(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  using X0 = std::integral_constant<int, 0>;
+  using X1 = std::integral_constant<int, 1>;
   int slot = 0;
-#pragma unroll 1
-  for (int kt = 0; kt < KT; ++kt) {
-    const uint8_t* st = smem + slot * C::STAGE;
-    const int nslot = slot + 1 == S ? 0 : slot + 1;
-    // first half: its MFMAs, and the second half's fragments
+  // ISSUE: 0 no stage left to issue, 1 stage kt + S, 2 the same and it is the last
+  auto step = [&](auto issue, int kt) {
+    constexpr int ISSUE = decltype(issue)::value;
+    const int nslot = next(slot);
+    using Last = std::integral_constant<bool, ISSUE == 2>;
+    phase(X0(), slot, 1, [&](int i) {
+      if (C::FIVE && ISSUE) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      a[1][i] = OA::frag(st, ba, i, 1);
-#pragma unroll
-      for (int j = i * NJ / MI; j < (i + 1) * NJ / MI; ++j) b[1][j] = OB::frag(st + OA::BYTES, bb, j, 1);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_bf16_16x16x32(b[0][j], a[0][i], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    // every wave holds the rest of this stage in registers after the barrier:
-    // its slot is free; the next stage has landed
-    if (kt + 1 < KT) wait_stages<NPER>(min(S - 2, KT - 2 - kt));
-    lds_barrier();
-    const uint8_t* nst = smem + nslot * C::STAGE;
-    const bool more = kt + S < KT;
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      a[0][i] = OA::frag(nst, ba, i, 0);
-#pragma unroll
-      for (int j = i * NJ / MI; j < (i + 1) * NJ / MI; ++j) b[0][j] = OB::frag(nst + OA::BYTES, bb, j, 0);
-      if (more) {
-#pragma unroll
-        for (int j = i * NPER / MI; j < (i + 1) * NPER / MI; ++j) issue1(j, kt + S, slot);
+        for (int j = i * OA::ND / MI; j < (i + 1) * OA::ND / MI; ++j) issue1(Last(), j, kt + S, next(nslot));
       }
+    });
+    // after the barrier every wave holds the rest of this stage in registers
+    // (its place is free), and the next stage has landed
+    if (ISSUE) wait_vmcnt_clamped<C::FIVE ? OA::ND : (S - 2) * NPER>();
+    else if (kt + 1 < KT) wait_stages<NPER>(KT - 2 - kt);
+    lds_barrier();
+    phase(X1(), nslot, 0, [&](int i) {
+      if (C::FIVE && ISSUE) {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_bf16_16x16x32(b[1][j], a[1][i], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+        for (int j = i * 2 * OB::ND / MI; j < (i + 1) * 2 * OB::ND / MI && j < OB::ND; ++j)
+          issue1(Last(), OA::ND + j, kt + S, next(nslot));
+      } else if (ISSUE) {
+#pragma unroll
+        for (int j = i * NPER / MI; j < (i + 1) * NPER / MI; ++j) issue1(Last(), j, kt + S, slot);
+      }
+    });
     slot = nslot;
-  }
+  };
+  int kt = 0;
+#pragma unroll 1
+  for (; kt < KT - S - 1; ++kt) step(std::integral_constant<int, 1>(), kt);
+  if (kt < KT - S) step(std::integral_constant<int, 2>(), kt++);
+#pragma unroll 1
+  for (; kt < KT; ++kt) step(std::integral_constant<int, 0>(), kt);
   lds_barrier();  // the stages are free
 }
 
@@ -369,16 +454,22 @@ struct HeadGemm {
   float* u;       // [count][H]
   uint16_t* dw;   // [V][H]
   int v0, piece;
+  int cus, dz_max;        // compute units; most workgroups of the G W product
 };
 
 // Forward: per row and block of BN columns the maximum of y = l log2 e and the
 // sum of 2^(y - maximum), and the logits at the target's ids (the tile goes
 // through LDS for those).
 template <class C>
-__global__ __launch_bounds__(512, 2) void k_head_stats(HeadGemm p) {
-  constexpr int SMEM = C::S * C::STAGE;
+__global__ __launch_bounds__(512, C::WPS) void k_head_stats(HeadGemm p) {
+  constexpr int RED = C::WN * C::BM * 4;  // bytes of the rows' maxima, and of their sums
+  // the tile of logits, or a part of it, and the rows' statistics behind it
+  constexpr int ZR = C::BM * C::BN * 4 + 2 * RED <= C::SMEM ? C::BM : C::BM / C::WM;
+  constexpr int ZB = ZR * C::BN * 4;
+  constexpr int SMEM = ZB + 2 * RED > C::SMEM ? ZB + 2 * RED : C::SMEM;
   __shared__ __align__(16) uint8_t smem[SMEM];
-  __shared__ float rm[C::WN][C::BM], rs[C::WN][C::BM];
+  float(*rm)[C::BM] = reinterpret_cast<float(*)[C::BM]>(smem + ZB);
+  float(*rs)[C::BM] = reinterpret_cast<float(*)[C::BM]>(smem + ZB + RED);
   const int n = *p.count, nvb = (p.V + C::BN - 1) / C::BN;
   int mt, nt;
   if (!head_tile(blockIdx.x, (n + C::BM - 1) / C::BM, nvb, mt, nt)) return;
@@ -417,7 +508,6 @@ __global__ __launch_bounds__(512, 2) void k_head_stats(HeadGemm p) {
     }
   }
   // logits at the ids: ZR rows of the tile at a time, 16-byte piece q of a row at q ^ (row & 15)
-  constexpr int ZR = C::BM * C::BN * 4 <= SMEM ? C::BM : C::BM / C::WM;
 #pragma unroll
   for (int z0 = 0; z0 < C::BM; z0 += ZR) {
     if (z0) lds_barrier();
@@ -454,8 +544,8 @@ __global__ __launch_bounds__(512, 2) void k_head_stats(HeadGemm p) {
 // Backward: G, columns [v0, v0 + piece), of every row of the tiles (zeros
 // behind the last row and past the vocabulary).
 template <class C>
-__global__ __launch_bounds__(512, 2) void k_head_grad(HeadGemm p) {
-  __shared__ __align__(16) uint8_t smem[C::S * C::STAGE];
+__global__ __launch_bounds__(512, C::WPS) void k_head_grad(HeadGemm p) {
+  __shared__ __align__(16) uint8_t smem[C::SMEM];
   const int n = *p.count;
   int mt, nt;
   if (!head_tile(blockIdx.x, (n + C::BM - 1) / C::BM, p.piece / C::BN, mt, nt)) return;
@@ -494,19 +584,61 @@ __global__ __launch_bounds__(512, 2) void k_head_grad(HeadGemm p) {
   }
 }
 
-// u += G W over a piece.
+// G W has few tiles for few rows or a narrow h, and a long K: its K is split
+// over `splits` workgroups per tile, which add to separate slabs of u (added
+// up in order by k_head_dh, so results do not depend on the order of
+// execution).  The number follows from the rows that count: the least
+//   rounds of workgroups x (K steps each + HEAD_STEP0) + splits x (steps that
+//   writing and reading a slab costs)
+// where a K step of a 256 x 256 tile takes about a microsecond and memory
+// moves about 5 MB in that time.
+constexpr int HEAD_STEP0 = 10;
+constexpr int HEAD_SPLITS = 16;
+MOE_DEV int head_splits(int n, int H, int K, int bm, int bn, int cus, int most) {
+  const int tiles = ((n + bm - 1) / bm) * ((H + bn - 1) / bn), steps = (K + 63) / 64;
+  const int slab = (int)((int64_t)n * H * 8 / 5000000);
+  int best = 1;
+  int64_t least = -1;
+  for (int s = 1; s <= HEAD_SPLITS && (s == 1 || (tiles * s <= most && s <= steps)); ++s) {
+    const int64_t rounds = (tiles * s + cus - 1) / cus;
+    const int64_t cost = rounds * ((steps + s - 1) / s + HEAD_STEP0) + (int64_t)s * slab;
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+// u (slab of this workgroup's share of K) += G W over a piece.
 template <class C>
 MOE_DEV void head_dz(const HeadGemm& p, int bid, uint8_t* smem) {
-  const int n = *p.count;
+  const int n = *p.count, nm = (n + C::BM - 1) / C::BM, nn = (p.H + C::BN - 1) / C::BN;
+  if (n == 0) return;
+  // the shares are those of the first piece, so every piece adds to the same slabs
+  const int splits = head_splits(n, p.H, min(p.piece, p.V), C::BM, C::BN, p.cus, p.dz_max);
   int mt, nt;
-  if (!head_tile(bid, (n + C::BM - 1) / C::BM, (p.H + C::BN - 1) / C::BN, mt, nt)) return;
-  const int m0 = mt * C::BM, n0 = nt * C::BN, K = min(p.piece, p.V - p.v0);
-  const HeadSrc sa = {reinterpret_cast<const char*>(p.g + (int64_t)m0 * p.piece), (uint32_t)p.piece * 2, C::BM,
-                      p.piece};
-  const HeadSrc sb = {reinterpret_cast<const char*>(p.w + (int64_t)p.v0 * p.w_stride + n0), (uint32_t)p.w_stride * 2,
-                      p.H - n0, K};
+  if (!head_tile(bid, nm * splits, nn, mt, nt)) return;
+  const int sp = mt / nm;
+  mt -= sp * nm;
+  const int Kp = min(p.piece, p.V - p.v0), steps = (Kp + 63) / 64;
+  const int k0 = (int)((int64_t)steps * sp / splits) * 64, k1 = (int)((int64_t)steps * (sp + 1) / splits) * 64;
+  const int m0 = mt * C::BM, n0 = nt * C::BN, K = min(k1, Kp) - k0;
   f32x4 acc[C::MI][C::NJ];
-  head_mm<C, false, true>(sa, sb, (K + 63) / 64, acc, smem);
+  if (K > 0) {
+    const HeadSrc sa = {reinterpret_cast<const char*>(p.g + (int64_t)m0 * p.piece + k0), (uint32_t)p.piece * 2, C::BM,
+                        p.piece - k0};
+    const HeadSrc sb = {reinterpret_cast<const char*>(p.w + (int64_t)(p.v0 + k0) * p.w_stride + n0),
+                        (uint32_t)p.w_stride * 2, p.H - n0, K};
+    head_mm<C, false, true>(sa, sb, (K + 63) / 64, acc, smem);
+  } else if (p.v0 != 0) {
+    return;
+  } else {
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+      for (int j = 0; j < C::NJ; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  }
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
   const int wm = wave / C::WN * C::MI * 16, wn = wave % C::WN * C::NJ * 16;
 #pragma unroll
@@ -517,7 +649,7 @@ MOE_DEV void head_dz(const HeadGemm& p, int bid, uint8_t* smem) {
     for (int j = 0; j < C::NJ; ++j) {
       const int col = n0 + wn + j * 16 + lg * 4;
       if (col >= p.H) continue;
-      f32x4* o = reinterpret_cast<f32x4*>(p.u + (int64_t)c * p.H + col);
+      f32x4* o = reinterpret_cast<f32x4*>(p.u + ((int64_t)sp * n + c) * p.H + col);
       *o = p.v0 == 0 ? acc[i][j] : *o + acc[i][j];
     }
   }
@@ -558,13 +690,13 @@ MOE_DEV void head_dw(const HeadGemm& p, int bid, uint8_t* smem) {
 }
 
 template <class C>
-__global__ __launch_bounds__(512, 2) void k_head_dz(HeadGemm p) {
-  __shared__ __align__(16) uint8_t smem[C::S * C::STAGE];
+__global__ __launch_bounds__(512, C::WPS) void k_head_dz(HeadGemm p) {
+  __shared__ __align__(16) uint8_t smem[C::SMEM];
   head_dz<C>(p, blockIdx.x, smem);
 }
 template <class C>
-__global__ __launch_bounds__(512, 2) void k_head_dw(HeadGemm p) {
-  __shared__ __align__(16) uint8_t smem[C::S * C::STAGE];
+__global__ __launch_bounds__(512, C::WPS) void k_head_dw(HeadGemm p) {
+  __shared__ __align__(16) uint8_t smem[C::SMEM];
   head_dw<C>(p, blockIdx.x, smem);
 }
 
@@ -663,29 +795,50 @@ __global__ __launch_bounds__(256) void k_head_targets(const int32_t* __restrict_
   }
 }
 
-// d_h = u - r^2 h mean(h u), or u without a norm; zeros for tokens that do
-// not count.  One block per token.
-__global__ __launch_bounds__(256) void k_head_dh(const float* __restrict__ u, const uint16_t* __restrict__ h,
-                                                 int64_t h_stride, const int32_t* __restrict__ cidx,
-                                                 const float* __restrict__ r, int H, bool norm,
+// d_h = u - r^2 h mean(h u), or u without a norm, u the sum of its slabs;
+// zeros for tokens that do not count.  One block per token.
+__global__ __launch_bounds__(256) void k_head_dh(HeadGemm p, const uint16_t* __restrict__ h, int64_t h_stride,
+                                                 const int32_t* __restrict__ cidx, bool norm, int bm, int bn,
                                                  uint16_t* __restrict__ dh) {
   __shared__ float part[4];
-  const int t = blockIdx.x, c = cidx[t];
+  const int t = blockIdx.x, c = cidx[t], H = p.H;
   uint16_t* o = dh + (int64_t)t * H;
   if (c < 0) {
     for (int i = threadIdx.x; i < H / 8; i += 256) *reinterpret_cast<u32x4*>(o + i * 8) = (u32x4){0, 0, 0, 0};
     return;
   }
-  const float* ur = u + (int64_t)c * H;
+  const int n = *p.count, splits = head_splits(n, H, min(p.piece, p.V), bm, bn, p.cus, p.dz_max);
+  const int64_t slab = (int64_t)n * H;
+  float* ur = p.u + (int64_t)c * H;
   const uint16_t* hr = h + (int64_t)t * h_stride;
   float f = 0.0f;
-  if (norm) {
+  if (norm || splits > 1) {
     float dot = 0.0f;
-    for (int i = threadIdx.x; i < H; i += 256) dot = fmaf(ur[i], bf16_bits_to_f32(hr[i]), dot);
-    dot = hl_sum64(dot);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
-    __syncthreads();
-    f = r[c] * r[c] * ((part[0] + part[1]) + (part[2] + part[3])) / (float)H;
+    for (int i = threadIdx.x; i < H / 8; i += 256) {
+      f32x4 a = *reinterpret_cast<const f32x4*>(ur + i * 8), b = *reinterpret_cast<const f32x4*>(ur + i * 8 + 4);
+      for (int s = 1; s < splits; ++s) {
+        a += *reinterpret_cast<const f32x4*>(ur + s * slab + i * 8);
+        b += *reinterpret_cast<const f32x4*>(ur + s * slab + i * 8 + 4);
+      }
+      if (splits > 1) {  // this thread's own pieces again below
+        *reinterpret_cast<f32x4*>(ur + i * 8) = a;
+        *reinterpret_cast<f32x4*>(ur + i * 8 + 4) = b;
+      }
+      if (norm) {
+        const u32x4 q = *reinterpret_cast<const u32x4*>(hr + i * 8);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          dot = fmaf(j < 2 ? a[2 * j] : b[2 * j - 4], bf16_bits_to_f32(q[j] & 0xFFFFu), dot);
+          dot = fmaf(j < 2 ? a[2 * j + 1] : b[2 * j - 3], bf16_bits_to_f32(q[j] >> 16), dot);
+        }
+      }
+    }
+    if (norm) {
+      dot = hl_sum64(dot);
+      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+      __syncthreads();
+      f = p.r[c] * p.r[c] * ((part[0] + part[1]) + (part[2] + part[3])) / (float)H;
+    }
   }
   for (int i = threadIdx.x; i < H / 8; i += 256) {
     const f32x4 a = *reinterpret_cast<const f32x4*>(ur + i * 8), b = *reinterpret_cast<const f32x4*>(ur + i * 8 + 4);
@@ -703,7 +856,33 @@ __global__ __launch_bounds__(256) void k_head_dh(const float* __restrict__ u, co
 
 namespace {
 inline int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-using HeadBig = HeadTile<256, 256, 2, 4, 2>;
+// Tiles by the number of rows.  Up to about 500 rows the products are bound by
+// reading W once (a 256-row tile needs as long for its MFMAs as its share of W
+// takes from memory), so narrow tiles of the vocabulary fill the CUs.
+using HeadBig = HeadTile<256, 256, 2, 4, 2, 2>;
+using Head256 = HeadTile<256, 128, 4, 2, 3, 2>;
+using Head128 = HeadTile<128, 128, 2, 4, 4, 2>;
+using Head64 = HeadTile<64, 128, 1, 8, 3, 4>;
+// f(tile) for at most T rows.
+template <typename F>
+void head_dispatch(int T, F f) {
+  if (T <= 64) f(Head64());
+  else if (T <= 128) f(Head128());
+  else if (T <= 256) f(Head256());
+  else f(HeadBig());
+}
+// Workgroups for nm x nn tiles (a multiple of the 8 XCDs).
+int head_grid(int64_t nm, int64_t nn) { return cdiv(nm * nn, 8) * 8; }
+int head_cus() {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) dev = 0;
+  return device_cus(dev);
+}
+// Most workgroups of the G W product: room for a second round's splits.
+int head_dz_max(int T, int H, int bm, int bn) {
+  const int64_t tiles = (int64_t)cdiv(T, bm) * cdiv(H, bn);
+  return (int)(tiles > 2048 ? tiles : tiles * 2 > 1024 ? tiles * 2 : 1024);
+}
 }  // namespace
 
 HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
@@ -720,8 +899,13 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
     o = (o + bytes + 255) / 256 * 256;
     return at;
   };
-  const size_t t = (size_t)T, rows = (t + 255) / 256 * 256;  // rows of the largest tiles
+  const size_t t = (size_t)T, rows = (t + 255) / 256 * 256;  // whole tiles
   p.Hp = (H + 63) / 64 * 64;
+  int bm = 0, bn = 0;
+  head_dispatch(T, [&](auto c) {
+    bm = decltype(c)::BM;
+    bn = decltype(c)::BN;
+  });
   p.r = take(rows * 4);
   p.flag = take(distill ? t : 0);
   p.rows = take(t * 4);
@@ -731,14 +915,18 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
   p.lq = take(distill ? t * top * 4 : 0);
   if (!bwd) {
     p.zt = take(t * top * 4);
-    p.stats = take(t * cdiv(V, HeadBig::BN) * 8);
+    p.stats = take(t * cdiv(V, bn) * 8);
   } else {
     // columns of G per piece: 256 MB of G, at least 256 columns
     const int64_t most = T > 0 ? ((int64_t)128 << 20) / (int64_t)rows / 256 * 256 : V;
     p.npieces = cdiv(V, most > 256 ? most : 256);
     p.piece = cdiv(cdiv(V, p.npieces), 256) * 256;
     p.npieces = cdiv(V, p.piece);
-    p.u = take(t * H * 4);
+    // slabs of u: the splits of a tile times the tiles stay below dz_max (or are 1)
+    size_t u = (size_t)head_dz_max(T, H, bm, bn) * bm * bn;
+    if (u > t * H * HEAD_SPLITS) u = t * H * HEAD_SPLITS;
+    if (u < t * H) u = t * H;
+    p.u = take(u * 4);
     p.g = take(rows * p.piece * 2);
   }
   p.total = o;
@@ -756,9 +944,15 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
   if (p.distill)
     hipLaunchKernelGGL(k_head_teacher, dim3(cdiv(p.T, 4)), dim3(256), 0, s, a.ids, a.tlogits, p.T, p.V, p.top,
                        a.teacher_scale, reinterpret_cast<float*>(ws + p.lq), flag);
-  hipLaunchKernelGGL(k_head_compact, dim3(1), dim3(1024), 0, s, flag, a.ids, p.T, p.V, rows, cidx, count);
-  hipLaunchKernelGGL(k_head_gather, dim3(cdiv(p.T, 64) * 64), dim3(256), 0, s, a.h, a.h_stride, p.H, p.Hp, a.eps, rows,
-                     count, hc, r);
+  const dim3 grid(cdiv(p.T, 64) * 64);
+  if (p.T <= 1024) {
+    hipLaunchKernelGGL(k_head_gather<true>, grid, dim3(256), 0, s, a.h, a.h_stride, p.H, p.Hp, a.eps, flag, a.ids, p.T,
+                       p.V, rows, cidx, count, hc, r);
+  } else {
+    hipLaunchKernelGGL(k_head_compact, dim3(1), dim3(1024), 0, s, flag, a.ids, p.T, p.V, rows, cidx, count);
+    hipLaunchKernelGGL(k_head_gather<false>, grid, dim3(256), 0, s, a.h, a.h_stride, p.H, p.Hp, a.eps, flag, a.ids,
+                       p.T, p.V, rows, cidx, count, hc, r);
+  }
   HeadGemm g{};
   g.hc = hc;
   g.w = a.w;
@@ -778,16 +972,16 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
   return g;
 }
 
-// Workgroups for nm x nn tiles (a multiple of the 8 XCDs).
-static int head_grid(int nm, int nn) { return cdiv((int64_t)nm * nn, 8) * 8; }
-
 void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
-  using C = HeadBig;
   HeadGemm g = head_common(p, a, s);
-  const int nvb = cdiv(p.V, C::BN);
   g.stats = reinterpret_cast<float*>(a.ws + p.stats);
   g.zt = reinterpret_cast<float*>(a.ws + p.zt);
-  hipLaunchKernelGGL(k_head_stats<C>, dim3(head_grid(cdiv(p.T, C::BM), nvb)), dim3(512), 0, s, g);
+  int nvb = 0;
+  head_dispatch(p.T, [&](auto c) {
+    using C = decltype(c);
+    nvb = cdiv(p.V, C::BN);
+    hipLaunchKernelGGL(k_head_stats<C>, dim3(head_grid(cdiv(p.T, C::BM), nvb)), dim3(512), 0, s, g);
+  });
   hipLaunchKernelGGL(k_head_finish, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.stats, g.zt,
                      reinterpret_cast<const int32_t*>(a.ws + p.cidx), a.ids,
                      reinterpret_cast<const float*>(a.ws + p.lq), p.T, p.V, nvb, p.top, p.distill, a.loss, a.lse,
@@ -795,24 +989,29 @@ void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
 }
 
 void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
-  using C = HeadBig;
   HeadGemm g = head_common(p, a, s);
   g.u = reinterpret_cast<float*>(a.ws + p.u);
   g.g = reinterpret_cast<uint16_t*>(a.ws + p.g);
   g.piece = p.piece;
-  const int mb = cdiv(p.T, C::BM), hb = cdiv(p.H, C::BN);
-  for (int i = 0; i < p.npieces; ++i) {
-    g.v0 = i * p.piece;
-    hipLaunchKernelGGL(k_head_grad<C>, dim3(head_grid(mb, p.piece / C::BN)), dim3(512), 0, s, g);
-    hipLaunchKernelGGL(k_head_targets, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.rows, g.count, a.ids,
-                       p.distill ? reinterpret_cast<const float*>(a.ws + p.lq) : nullptr, a.logp, a.loss, g.r,
-                       a.dloss, a.scale, p.V, p.top, g.v0, p.piece, g.g);
-    hipLaunchKernelGGL(k_head_dz<C>, dim3(head_grid(mb, hb)), dim3(512), 0, s, g);
-    if (a.dw != nullptr)
-      hipLaunchKernelGGL(k_head_dw<C>, dim3(head_grid(p.piece / C::BM, hb)), dim3(512), 0, s, g);
-  }
-  hipLaunchKernelGGL(k_head_dh, dim3(p.T), dim3(256), 0, s, g.u, a.h, a.h_stride,
-                     reinterpret_cast<const int32_t*>(a.ws + p.cidx), g.r, p.H, a.eps > 0.0f, a.dh);
+  g.cus = head_cus();
+  head_dispatch(p.T, [&](auto c) {
+    using C = decltype(c);
+    const int mb = cdiv(p.T, C::BM);
+    g.dz_max = head_dz_max(p.T, p.H, C::BM, C::BN);
+    for (int i = 0; i < p.npieces; ++i) {
+      g.v0 = i * p.piece;
+      hipLaunchKernelGGL(k_head_grad<C>, dim3(head_grid(mb, p.piece / C::BN)), dim3(512), 0, s, g);
+      hipLaunchKernelGGL(k_head_targets, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.rows, g.count, a.ids,
+                         p.distill ? reinterpret_cast<const float*>(a.ws + p.lq) : nullptr, a.logp, a.loss, g.r,
+                         a.dloss, a.scale, p.V, p.top, g.v0, p.piece, g.g);
+      hipLaunchKernelGGL(k_head_dz<C>, dim3(head_grid(g.dz_max, 1)), dim3(512), 0, s, g);
+      if (a.dw != nullptr)
+        hipLaunchKernelGGL(k_head_dw<HeadBig>, dim3(head_grid(p.piece / HeadBig::BM, cdiv(p.H, HeadBig::BN))),
+                           dim3(512), 0, s, g);
+    }
+    hipLaunchKernelGGL(k_head_dh, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride,
+                       reinterpret_cast<const int32_t*>(a.ws + p.cidx), a.eps > 0.0f, C::BM, C::BN, a.dh);
+  });
 }
 
 }  // namespace moe
