@@ -122,19 +122,30 @@ __global__ __launch_bounds__(1024) void k_head_compact(const uint8_t* __restrict
   if (tid == 1023) *count = part[1023];
 }
 
+// What a product's epilogue needs of its row c (16 bytes, one load).
+struct HeadRow {
+  float f2;   // logit_scale / rms * log2 e
+  float f;    // forward: logit_scale / rms; backward: that times dL/dloss
+  float l2;   // backward: lse log2 e
+  int tgt;    // cross entropy: the target's id
+};
+
 // The rows that count, one after the other, as the products read them: hc
-// [..][Hp] with zeros in columns H..Hp and in the rows up to the next multiple
-// of 64 (the K of a product runs over either in steps of 64); r[c] = 1/rms of
-// row c.  One block per row.  FEW (at most 1024 tokens): every block finds its
-// own token among the flags, and block 0 writes the lists, so that no launch
-// is spent on k_head_compact.
+// [..][Hp] with zeros in columns H..Hp (the K of the products goes in steps of
+// 64) and in the rows up to the next multiple of a tile's BM rows, with
+// r[c] = 1/rms of row c and its HeadRow (zeros behind the last row).  One block
+// per row.  FEW (at most 1024 tokens): every block finds its own token among
+// the flags, and block 0 writes the lists, so that no launch is spent on
+// k_head_compact.
 template <bool FEW>
 __global__ __launch_bounds__(256) void k_head_gather(const uint16_t* __restrict__ h, int64_t h_stride, int H, int Hp,
                                                      float eps, const uint8_t* __restrict__ flag,
                                                      const int32_t* __restrict__ ids, int T, int V,
                                                      int32_t* __restrict__ rows, int32_t* __restrict__ cidx,
-                                                     int32_t* __restrict__ count, uint16_t* __restrict__ hc,
-                                                     float* __restrict__ r) {
+                                                     int32_t* __restrict__ count, int bm, float scale,
+                                                     const float* __restrict__ lse, const float* __restrict__ dloss,
+                                                     uint16_t* __restrict__ hc, float* __restrict__ r,
+                                                     HeadRow* __restrict__ info) {
   __shared__ float part[4];
   __shared__ int wsum[4], found;
   const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
@@ -178,7 +189,7 @@ __global__ __launch_bounds__(256) void k_head_gather(const uint16_t* __restrict_
     n = *count;
     if (c < n) t = rows[c];
   }
-  if (c >= (n + 63) / 64 * 64) return;
+  if (c >= (n + bm - 1) / bm * bm) return;
   uint16_t* o = hc + (int64_t)c * Hp;
   const uint16_t* row = h + (int64_t)t * h_stride;
   float ss = 0.0f;
@@ -193,12 +204,20 @@ __global__ __launch_bounds__(256) void k_head_gather(const uint16_t* __restrict_
       ss = fmaf(b, b, ss);
     }
   }
-  if (c >= n) return;
+  if (c >= n) {
+    if (tid == 0) info[c] = HeadRow{0.0f, 0.0f, 0.0f, -1};
+    return;
+  }
   ss = hl_sum64(ss);
   if (lane == 0) part[tid >> 6] = ss;
   __syncthreads();
-  if (tid == 0)
-    r[c] = eps > 0.0f ? 1.0f / sqrtf(((part[0] + part[1]) + (part[2] + part[3])) / (float)H + eps) : 1.0f;
+  if (tid == 0) {
+    const float rr = eps > 0.0f ? 1.0f / sqrtf(((part[0] + part[1]) + (part[2] + part[3])) / (float)H + eps) : 1.0f;
+    const float f = scale * rr;
+    r[c] = rr;
+    info[c] = HeadRow{f * kLog2e, dloss != nullptr ? f * dloss[t] : f, dloss != nullptr ? lse[t] * kLog2e : 0.0f,
+                      flag == nullptr ? ids[t] : -1};
+  }
 }
 
 // ---- the products -----------------------------------------------------------
@@ -241,13 +260,13 @@ MOE_DEV void hl_dma(const char* base, uint32_t off, uint32_t lds) {
 }
 
 // One operand of a tile: R rows (or columns) by 64 K per stage.
-template <int R, bool KM>
+template <int R, bool KM, int NW>
 struct HeadOperand {
   static constexpr int BYTES = R * 128;
-  static constexpr int ND = R / 64;  // DMAs per wave and stage
+  static constexpr int ND = R / 8 / NW;  // DMAs per wave and stage
   static constexpr int RB = KM ? R * 2 : 128;
   static constexpr int LPR = RB / 16;     // lanes per row of a DMA
-  static_assert(R % 64 == 0 && (!KM || R >= 128), "tile");
+  static_assert(R % (8 * NW) == 0 && (!KM || R >= 128), "tile");
   HeadSrc s;
   uint32_t off[ND];
   MOE_DEV static int row_of(int wave, int lane, int j) { return (wave * ND + j) * (64 / LPR) + lane / LPR; }
@@ -319,13 +338,13 @@ struct HeadTile {
   static constexpr bool FIVE = S == 2;
   static_assert(!FIVE || BM == BN, "buffers of one size");
   static constexpr int SMEM = FIVE ? 5 * BM * 128 : S * STAGE;
-  static_assert(WM * WN == 8, "eight waves");
+  static constexpr int NW = WM * WN, NT = NW * 64;
 };
 
 template <class C, bool KMA, bool KMB>
 MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[C::MI][C::NJ], uint8_t* smem) {
-  using OA = HeadOperand<C::BM, KMA>;
-  using OB = HeadOperand<C::BN, KMB>;
+  using OA = HeadOperand<C::BM, KMA, C::NW>;
+  using OB = HeadOperand<C::BN, KMB, C::NW>;
   constexpr int S = C::S, MI = C::MI, NJ = C::NJ, NPER = OA::ND + OB::ND;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   OA oa;
@@ -365,21 +384,28 @@ MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[
   };
 #pragma unroll
   for (int i = 0; i < NJ + MI; ++i) read(0, 0, i, 0);
-  // The MFMAs of fragments f[x], and the next fragments into f[1 - x] over the
-  // first of them (so that they have arrived when they are wanted); dma(i)
-  // issues the i-th part of a stage.  A fixed order: MFMAs lead each group.
-  constexpr int RG = MI > 2 ? MI - 2 : MI;  // groups that read
+  // The MFMAs of fragments f[x], with the reads of the next fragments into
+  // f[1 - x] spread over the first three quarters of them (so that they have
+  // arrived when they are wanted) and the parts dma(i) of a stage in between: a
+  // wave's MFMAs then never wait behind a run of other instructions.
+  constexpr int NR = NJ + MI, RM = MI * NJ * 3 / 4;  // fragments, MFMAs that lead their reads
   auto phase = [&](auto x, int rslot, int half, auto dma) {
     constexpr int X = decltype(x)::value;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
+    for (int m = 0; m < MI * NJ; ++m) {
+      const int i = m / NJ, j = m % NJ;
+      acc[i][j] = mfma_bf16_16x16x32(f[X][j], f[X][NJ + i], acc[i][j]);
+      if (m < RM) {
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_bf16_16x16x32(f[X][j], f[X][NJ + i], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int r = i * (NJ + MI) / RG; r < (i + 1) * (NJ + MI) / RG && r < NJ + MI; ++r) read(1 - X, rslot, r, half);
-      dma(i);
-      __builtin_amdgcn_sched_barrier(0);
+        for (int r = m * NR / RM; r < (m + 1) * NR / RM; ++r) read(1 - X, rslot, r, half);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (m % NJ == NJ / 2) {
+        __builtin_amdgcn_sched_barrier(0);
+        dma(i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   };
   using X0 = std::integral_constant<int, 0>;
@@ -444,12 +470,12 @@ struct HeadGemm {
   const int32_t* rows;
   const int32_t* count;
   const float* r;         // [count]
-  const float* lse;       // [T]
-  const float* dloss;     // [T]
+  const HeadRow* info;    // [..]
   float scale;
   const int32_t* ids;
+  bool distill;
   float* stats;   // [count][nvb][2]
-  float* zt;      // [T][top]
+  float* zt;      // [count][top]
   uint16_t* g;    // [..][piece]
   float* u;       // [count][H]
   uint16_t* dw;   // [V][H]
@@ -461,7 +487,8 @@ struct HeadGemm {
 // sum of 2^(y - maximum), and the logits at the target's ids (the tile goes
 // through LDS for those).
 template <class C>
-__global__ __launch_bounds__(512, C::WPS) void k_head_stats(HeadGemm p) {
+__global__ __launch_bounds__(C::NT, C::WPS) void k_head_stats(HeadGemm p) {
+  static_assert(C::NT % C::BM == 0 || C::NT % (C::BM / C::WM) == 0, "rows per thread");
   constexpr int RED = C::WN * C::BM * 4;  // bytes of the rows' maxima, and of their sums
   // the tile of logits, or a part of it, and the rows' statistics behind it
   constexpr int ZR = C::BM * C::BN * 4 + 2 * RED <= C::SMEM ? C::BM : C::BM / C::WM;
@@ -481,57 +508,83 @@ __global__ __launch_bounds__(512, C::WPS) void k_head_stats(HeadGemm p) {
   head_mm<C, false, false>(sa, sb, p.Hp / 64, acc, smem);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
   const int wm = wave / C::WN * C::MI * 16, wn = wave % C::WN * C::NJ * 16;
+  const bool full = n0 + C::BN <= p.V;  // uniform: no column of the tile is past the vocabulary
+  HeadRow info[C::MI];
 #pragma unroll
-  for (int i = 0; i < C::MI; ++i) {
-    const int row = wm + i * 16 + ln;
-    const float f = m0 + row < n ? p.scale * p.r[m0 + row] : 0.0f;
-    float mx = -INFINITY, s = 0.0f;
+  for (int i = 0; i < C::MI; ++i) info[i] = p.info[m0 + wm + i * 16 + ln];
+  auto rows_stats = [&](auto all) {
+    constexpr bool ALL = decltype(all)::value;
 #pragma unroll
-    for (int j = 0; j < C::NJ; ++j)
+    for (int i = 0; i < C::MI; ++i) {
+      const int row = wm + i * 16 + ln;
+      float mx = -INFINITY, s = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[i][j][e] *= f;
-        if (n0 + wn + j * 16 + lg * 4 + e < p.V) mx = fmaxf(mx, acc[i][j][e]);
+      for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (ALL || n0 + wn + j * 16 + lg * 4 + e < p.V) mx = fmaxf(mx, acc[i][j][e]);
+      mx = fmaxf(mx, shfl_xor(mx, 16));
+      mx = fmaxf(mx, shfl_xor(mx, 32)) * info[i].f2;
+#pragma unroll
+      for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (ALL || n0 + wn + j * 16 + lg * 4 + e < p.V) s += hl_exp2(fmaf(acc[i][j][e], info[i].f2, -mx));
+      s += shfl_xor(s, 16);
+      s += shfl_xor(s, 32);
+      if (lg == 0) {
+        rm[wave % C::WN][row] = mx;
+        rs[wave % C::WN][row] = s;
       }
-    mx = fmaxf(mx, shfl_xor(mx, 16));
-    mx = fmaxf(mx, shfl_xor(mx, 32)) * kLog2e;
-#pragma unroll
-    for (int j = 0; j < C::NJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n0 + wn + j * 16 + lg * 4 + e < p.V) s += hl_exp2(fmaf(acc[i][j][e], kLog2e, -mx));
-    s += shfl_xor(s, 16);
-    s += shfl_xor(s, 32);
-    if (lg == 0) {
-      rm[wave % C::WN][row] = mx;
-      rs[wave % C::WN][row] = s;
     }
-  }
-  // logits at the ids: ZR rows of the tile at a time, 16-byte piece q of a row at q ^ (row & 15)
+  };
+  if (full) rows_stats(std::true_type());
+  else rows_stats(std::false_type());
+  if (!p.distill) {
+    // the one lane that holds a row's target picks it out
 #pragma unroll
-  for (int z0 = 0; z0 < C::BM; z0 += ZR) {
-    if (z0) lds_barrier();
-    if (ZR == C::BM || wm == z0) {
+    for (int i = 0; i < C::MI; ++i) {
+      const int tc = info[i].tgt - n0 - wn;
+      const bool hit = tc >= 0 && tc < C::NJ * 16 && ((tc >> 2) & 3) == lg;
+      if (!__any(hit)) continue;
+      float z = 0.0f;
 #pragma unroll
-      for (int i = 0; i < C::MI; ++i)
+      for (int j = 0; j < C::NJ; ++j)
 #pragma unroll
-        for (int j = 0; j < C::NJ; ++j) {
-          const int row = wm + i * 16 + ln, q = (wn + j * 16) / 4 + lg;
-          *reinterpret_cast<f32x4*>(smem + (row - z0) * C::BN * 4 + ((q ^ (row & 15)) << 4)) = acc[i][j];
-        }
+        for (int e = 0; e < 4; ++e) z = tc == j * 16 + lg * 4 + e ? acc[i][j][e] : z;
+      if (hit) p.zt[m0 + wm + i * 16 + ln] = z * info[i].f;
     }
     lds_barrier();
-    for (int x = threadIdx.x; x < ZR * p.top; x += 512) {
-      const int row = z0 + x / p.top;
-      if (m0 + row >= n) break;
-      const int64_t at = (int64_t)p.rows[m0 + row] * p.top + x % p.top;
-      const int v = p.ids[at] - n0;
-      if (v >= 0 && v < C::BN && n0 + v < p.V)
-        p.zt[at] = *reinterpret_cast<const float*>(smem + (row - z0) * C::BN * 4 + (((v >> 2) ^ (row & 15)) << 4) +
-                                                   (v & 3) * 4);
+  } else {
+    // the logits go through LDS, ZR rows of the tile at a time, 16-byte piece q
+    // of a row at q ^ (row & 15); NT / ZR threads look up a row's ids
+#pragma unroll
+    for (int z0 = 0; z0 < C::BM; z0 += ZR) {
+      if (z0) lds_barrier();
+      if (ZR == C::BM || wm == z0) {
+#pragma unroll
+        for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+          for (int j = 0; j < C::NJ; ++j) {
+            const int row = wm + i * 16 + ln, q = (wn + j * 16) / 4 + lg;
+            *reinterpret_cast<f32x4*>(smem + (row - z0) * C::BN * 4 + ((q ^ (row & 15)) << 4)) = acc[i][j] * info[i].f;
+          }
+      }
+      lds_barrier();
+      constexpr int TPR = C::NT / ZR > 0 ? C::NT / ZR : 1;
+      const int row = z0 + (int)threadIdx.x / TPR, c = m0 + row;
+      if (threadIdx.x < ZR * TPR && c < n) {
+        const int32_t* id = p.ids + (int64_t)p.rows[c] * p.top;
+        for (int k = threadIdx.x % TPR; k < p.top; k += TPR) {
+          const int v = id[k] - n0;
+          if (v >= 0 && v < C::BN && n0 + v < p.V)
+            p.zt[(int64_t)c * p.top + k] = *reinterpret_cast<const float*>(
+                smem + (row - z0) * C::BN * 4 + (((v >> 2) ^ (row & 15)) << 4) + (v & 3) * 4);
+        }
+      }
     }
   }
-  for (int row = threadIdx.x; row < C::BM && m0 + row < n; row += 512) {
+  for (int row = threadIdx.x; row < C::BM && m0 + row < n; row += C::NT) {
     float m = rm[0][row], s = rs[0][row];
 #pragma unroll
     for (int w = 1; w < C::WN; ++w) hl_merge(m, s, rm[w][row], rs[w][row]);
@@ -544,7 +597,7 @@ __global__ __launch_bounds__(512, C::WPS) void k_head_stats(HeadGemm p) {
 // Backward: G, columns [v0, v0 + piece), of every row of the tiles (zeros
 // behind the last row and past the vocabulary).
 template <class C>
-__global__ __launch_bounds__(512, C::WPS) void k_head_grad(HeadGemm p) {
+__global__ __launch_bounds__(C::NT, C::WPS) void k_head_grad(HeadGemm p) {
   __shared__ __align__(16) uint8_t smem[C::SMEM];
   const int n = *p.count;
   int mt, nt;
@@ -559,29 +612,29 @@ __global__ __launch_bounds__(512, C::WPS) void k_head_grad(HeadGemm p) {
   head_mm<C, false, false>(sa, sb, p.Hp / 64, acc, smem);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
   const int wm = wave / C::WN * C::MI * 16, wn = wave % C::WN * C::NJ * 16;
+  const bool full = n0 + C::BN <= p.V;
+  HeadRow info[C::MI];
 #pragma unroll
-  for (int i = 0; i < C::MI; ++i) {
-    const int c = m0 + wm + i * 16 + ln;
-    float f = 0.0f, l = 0.0f, cf = 0.0f;
-    if (c < n) {
-      const int t = p.rows[c];
-      const float sr = p.scale * p.r[c];
-      f = sr * kLog2e;
-      l = p.lse[t] * kLog2e;
-      cf = sr * p.dloss[t];
-    }
+  for (int i = 0; i < C::MI; ++i) info[i] = p.info[m0 + wm + i * 16 + ln];
+  auto write = [&](auto all) {
+    constexpr bool ALL = decltype(all)::value;
 #pragma unroll
-    for (int j = 0; j < C::NJ; ++j) {
-      float x[4];
+    for (int i = 0; i < C::MI; ++i) {
+      uint16_t* o = p.g + (int64_t)(m0 + wm + i * 16 + ln) * p.piece + (n0 - p.v0) + wn + lg * 4;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool in = c < n && n0 + wn + j * 16 + lg * 4 + e < p.V;
-        x[e] = in ? cf * hl_exp2(fmaf(acc[i][j][e], f, -l)) : 0.0f;
+      for (int j = 0; j < C::NJ; ++j) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = info[i].f * hl_exp2(fmaf(acc[i][j][e], info[i].f2, -info[i].l2));
+          if (!ALL && n0 + wn + j * 16 + lg * 4 + e >= p.V) x[e] = 0.0f;
+        }
+        *reinterpret_cast<u32x2*>(o + j * 16) = (u32x2){bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3])};
       }
-      const u32x2 q = {bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3])};
-      *reinterpret_cast<u32x2*>(p.g + (int64_t)c * p.piece + (n0 - p.v0) + wn + j * 16 + lg * 4) = q;
     }
-  }
+  };
+  if (full) write(std::true_type());
+  else write(std::false_type());
 }
 
 // G W has few tiles for few rows or a narrow h, and a long K: its K is split
@@ -690,12 +743,12 @@ MOE_DEV void head_dw(const HeadGemm& p, int bid, uint8_t* smem) {
 }
 
 template <class C>
-__global__ __launch_bounds__(512, C::WPS) void k_head_dz(HeadGemm p) {
+__global__ __launch_bounds__(C::NT, C::WPS) void k_head_dz(HeadGemm p) {
   __shared__ __align__(16) uint8_t smem[C::SMEM];
   head_dz<C>(p, blockIdx.x, smem);
 }
 template <class C>
-__global__ __launch_bounds__(512, C::WPS) void k_head_dw(HeadGemm p) {
+__global__ __launch_bounds__(C::NT, C::WPS) void k_head_dw(HeadGemm p) {
   __shared__ __align__(16) uint8_t smem[C::SMEM];
   head_dw<C>(p, blockIdx.x, smem);
 }
@@ -737,13 +790,13 @@ __global__ __launch_bounds__(256) void k_head_finish(const float* __restrict__ s
       const int64_t at = (int64_t)t * top + j;
       const float q = lq[at];
       const bool have = !(q == -INFINITY);
-      const float lp = have ? zt[at] - l : 0.0f;
+      const float lp = have ? zt[(int64_t)c * top + j] - l : 0.0f;
       logp[at] = lp;
       if (have) kl = fmaf(expf(q), q - lp, kl);
     }
     kl = hl_sum64(kl);
   } else {
-    kl = l - zt[t];
+    kl = l - zt[c];
   }
   if (lane == 0) {
     loss[t] = kl;
@@ -906,7 +959,9 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
     bm = decltype(c)::BM;
     bn = decltype(c)::BN;
   });
+  p.bm = bm;
   p.r = take(rows * 4);
+  p.info = take(rows * sizeof(HeadRow));
   p.flag = take(distill ? t : 0);
   p.rows = take(t * 4);
   p.cidx = take(t * 4);
@@ -944,14 +999,16 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
   if (p.distill)
     hipLaunchKernelGGL(k_head_teacher, dim3(cdiv(p.T, 4)), dim3(256), 0, s, a.ids, a.tlogits, p.T, p.V, p.top,
                        a.teacher_scale, reinterpret_cast<float*>(ws + p.lq), flag);
-  const dim3 grid(cdiv(p.T, 64) * 64);
+  const dim3 grid(cdiv(p.T, p.bm) * p.bm);
+  HeadRow* info = reinterpret_cast<HeadRow*>(ws + p.info);
+  const float *lse = p.bwd ? a.lse : nullptr, *dloss = p.bwd ? a.dloss : nullptr;
   if (p.T <= 1024) {
     hipLaunchKernelGGL(k_head_gather<true>, grid, dim3(256), 0, s, a.h, a.h_stride, p.H, p.Hp, a.eps, flag, a.ids, p.T,
-                       p.V, rows, cidx, count, hc, r);
+                       p.V, rows, cidx, count, p.bm, a.scale, lse, dloss, hc, r, info);
   } else {
     hipLaunchKernelGGL(k_head_compact, dim3(1), dim3(1024), 0, s, flag, a.ids, p.T, p.V, rows, cidx, count);
     hipLaunchKernelGGL(k_head_gather<false>, grid, dim3(256), 0, s, a.h, a.h_stride, p.H, p.Hp, a.eps, flag, a.ids,
-                       p.T, p.V, rows, cidx, count, hc, r);
+                       p.T, p.V, rows, cidx, count, p.bm, a.scale, lse, dloss, hc, r, info);
   }
   HeadGemm g{};
   g.hc = hc;
@@ -964,8 +1021,8 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
   g.rows = rows;
   g.count = count;
   g.r = r;
-  g.lse = a.lse;
-  g.dloss = a.dloss;
+  g.info = info;
+  g.distill = p.distill;
   g.scale = a.scale;
   g.ids = a.ids;
   g.dw = a.dw;
@@ -980,7 +1037,7 @@ void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
   head_dispatch(p.T, [&](auto c) {
     using C = decltype(c);
     nvb = cdiv(p.V, C::BN);
-    hipLaunchKernelGGL(k_head_stats<C>, dim3(head_grid(cdiv(p.T, C::BM), nvb)), dim3(512), 0, s, g);
+    hipLaunchKernelGGL(k_head_stats<C>, dim3(head_grid(cdiv(p.T, C::BM), nvb)), dim3(C::NT), 0, s, g);
   });
   hipLaunchKernelGGL(k_head_finish, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.stats, g.zt,
                      reinterpret_cast<const int32_t*>(a.ws + p.cidx), a.ids,
@@ -1000,14 +1057,14 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
     g.dz_max = head_dz_max(p.T, p.H, C::BM, C::BN);
     for (int i = 0; i < p.npieces; ++i) {
       g.v0 = i * p.piece;
-      hipLaunchKernelGGL(k_head_grad<C>, dim3(head_grid(mb, p.piece / C::BN)), dim3(512), 0, s, g);
+      hipLaunchKernelGGL(k_head_grad<C>, dim3(head_grid(mb, p.piece / C::BN)), dim3(C::NT), 0, s, g);
       hipLaunchKernelGGL(k_head_targets, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.rows, g.count, a.ids,
                          p.distill ? reinterpret_cast<const float*>(a.ws + p.lq) : nullptr, a.logp, a.loss, g.r,
                          a.dloss, a.scale, p.V, p.top, g.v0, p.piece, g.g);
-      hipLaunchKernelGGL(k_head_dz<C>, dim3(head_grid(g.dz_max, 1)), dim3(512), 0, s, g);
+      hipLaunchKernelGGL(k_head_dz<C>, dim3(head_grid(g.dz_max, 1)), dim3(C::NT), 0, s, g);
       if (a.dw != nullptr)
         hipLaunchKernelGGL(k_head_dw<HeadBig>, dim3(head_grid(p.piece / HeadBig::BM, cdiv(p.H, HeadBig::BN))),
-                           dim3(512), 0, s, g);
+                           dim3(HeadBig::NT), 0, s, g);
     }
     hipLaunchKernelGGL(k_head_dh, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride,
                        reinterpret_cast<const int32_t*>(a.ws + p.cidx), a.eps > 0.0f, C::BM, C::BN, a.dh);

@@ -199,7 +199,8 @@ struct HeadPlan {
   int piece, npieces;     // backward: columns of G per piece (multiple of 256), pieces
   // byte offsets into the workspace
   int Hp;                 // H rounded up to the products' K step
-  size_t r, flag, rows, cidx, count, hc, lq, zt, stats, u, g, total;
+  int bm;                 // rows of a tile
+  size_t r, info, flag, rows, cidx, count, hc, lq, zt, stats, u, g, total;
 };
 struct HeadArgs {
   const uint16_t* h;
