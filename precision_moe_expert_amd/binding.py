@@ -453,6 +453,11 @@ def _rows(t, name: str, device):
     return t.data_ptr(), t.stride(0)
 
 
+def _raw_stream(device) -> int:
+    """The current stream of the device as a handle (torch.cuda.current_stream builds an object first)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 class _On:
     """The device of the call's tensors, made current where it is not."""
 
@@ -507,7 +512,7 @@ def lm_head_loss(h: torch.Tensor, w_lm: torch.Tensor, targets: torch.Tensor, nor
         lse = torch.empty(T, dtype=torch.float32, device=dev)
         ws, nb = _head_ws(head, 0, False, ws, dev)
         _check(lib().moe_lm_head_loss(ctypes.byref(head), hp, wp, y, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                                      nb, _stream()), "moe_lm_head_loss")
+                                      nb, _raw_stream(dev)), "moe_lm_head_loss")
     return loss, lse
 
 
@@ -527,7 +532,7 @@ def lm_head_loss_backward(h, w_lm, targets, loss, lse, d_loss, weight_grad: bool
         d_w = torch.empty((head.vocab, head.hidden), dtype=torch.bfloat16, device=dev) if weight_grad else None
         ws, nb = _head_ws(head, 0, True, ws, dev)
         _check(lib().moe_lm_head_loss_backward(ctypes.byref(head), hp, wp, y, lo, ls, dl, d_h.data_ptr(), _ptr(d_w),
-                                               ws.data_ptr(), nb, _stream()), "moe_lm_head_loss_backward")
+                                               ws.data_ptr(), nb, _raw_stream(dev)), "moe_lm_head_loss_backward")
     return d_h, d_w
 
 
@@ -548,7 +553,7 @@ def lm_head_distill(h, w_lm, teacher_ids, teacher_logits, teacher_scale: float =
         logp = torch.empty((T, K), dtype=torch.float32, device=dev)
         ws, nb = _head_ws(head, K, False, ws, dev)
         _check(lib().moe_lm_head_distill(ctypes.byref(head), K, teacher_scale, hp, wp, ip, tp, loss.data_ptr(),
-                                         lse.data_ptr(), logp.data_ptr(), ws.data_ptr(), nb, _stream()),
+                                         lse.data_ptr(), logp.data_ptr(), ws.data_ptr(), nb, _raw_stream(dev)),
                "moe_lm_head_distill")
     return loss, lse, logp
 
@@ -571,7 +576,7 @@ def lm_head_distill_backward(h, w_lm, teacher_ids, teacher_logits, lse, logp, d_
         d_w = torch.empty((head.vocab, head.hidden), dtype=torch.bfloat16, device=dev) if weight_grad else None
         ws, nb = _head_ws(head, K, True, ws, dev)
         _check(lib().moe_lm_head_distill_backward(ctypes.byref(head), K, teacher_scale, hp, wp, ip, tp, ls, lp, dl,
-                                                  d_h.data_ptr(), _ptr(d_w), ws.data_ptr(), nb, _stream()),
+                                                  d_h.data_ptr(), _ptr(d_w), ws.data_ptr(), nb, _raw_stream(dev)),
                "moe_lm_head_distill_backward")
     return d_h, d_w
 
@@ -608,7 +613,7 @@ def balance_loss(layer: MoeLayer, logits, topk_ids, token_mask=None, seg_offsets
             raise ValueError("ws: contiguous tensor on the call's device expected")
         _check(lib().moe_balance_loss(ctypes.byref(layer), lp, ip, mp, op, S, loss.data_ptr(), counts.data_ptr(),
                                       tokens.data_ptr(), probs.data_ptr(), ws.data_ptr(),
-                                      ws.numel() * ws.element_size(), _stream()), "moe_balance_loss")
+                                      ws.numel() * ws.element_size(), _raw_stream(dev)), "moe_balance_loss")
     return loss, counts, tokens, probs
 
 
@@ -628,6 +633,6 @@ def balance_loss_backward(layer: MoeLayer, logits, counts, tokens, d_loss, token
         if not add:
             d_logits = torch.empty((T, E), dtype=torch.float32, device=dev)
         dp = _typed(d_logits, "d_logits", torch.float32, (T, E), dev)
-        _check(lib().moe_balance_loss_backward(ctypes.byref(layer), lp, mp, op, S, cp, np_, dl, add, dp, _stream()),
+        _check(lib().moe_balance_loss_backward(ctypes.byref(layer), lp, mp, op, S, cp, np_, dl, add, dp, _raw_stream(dev)),
                "moe_balance_loss_backward")
     return d_logits

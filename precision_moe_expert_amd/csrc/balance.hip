@@ -59,18 +59,21 @@ MOE_DEV void bl_load(const float* __restrict__ row, int E, int ln, float (&v)[NV
   }
 }
 
-// v <- softmax of the row; a row of -infinities gives zeros.
+// v <- softmax of the row; a row of -infinities gives zeros.  2^(x log2 e - c)
+// in one fused operation: c's own rounding is the same for the whole row and
+// drops out.
 template <int N>
 MOE_DEV void bl_softmax(float (&v)[N]) {
+  constexpr float kLog2e = 1.44269504088896340736f;
   float m = v[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
   m = bl_max16(m);
-  if (m == -INFINITY) m = 0.0f;
+  const float c = m == -INFINITY ? 0.0f : m * kLog2e;
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    v[i] = expf(v[i] - m);
+    v[i] = __builtin_amdgcn_exp2f(fmaf(v[i], kLog2e, -c));
     s += v[i];
   }
   s = bl_sum16(s);
@@ -91,37 +94,82 @@ MOE_DEV int bl_count_le(const int32_t* off, int n, int t) {
   return lo;
 }
 
+// A thread's share of a run of tokens [t, tend): sums of softmax rows into acc
+// (16 lanes per token, `stride` tokens apart), routed slots into the LDS
+// counts, tokens into mine.
+template <int NV, bool VEC>
+MOE_DEV void bl_run(const float* __restrict__ logits, const int32_t* __restrict__ ids,
+                    const uint8_t* __restrict__ mask, int t, int tend, int stride, int E, int k, int ln, int* cnt,
+                    float (&acc)[NV * 4], int& mine) {
+  for (int u = t; u < tend; u += stride) {
+    if (mask != nullptr && mask[u] == 0) continue;
+    ++mine;
+    float v[NV * 4];
+    bl_load<NV, VEC>(logits + (int64_t)u * E, E, ln, v);
+    if (ln < k) {
+      const int e = ids[(int64_t)u * k + ln];
+      if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
+    }
+    bl_softmax(v);
+#pragma unroll
+    for (int i = 0; i < NV * 4; ++i) acc[i] += v[i];
+  }
+}
+
+// Adds the four tokens' lanes of a wave and writes the wave's sums.
+template <int NV>
+MOE_DEV void bl_wave_sums(float (&acc)[NV * 4], int lane, float* out) {
+#pragma unroll
+  for (int i = 0; i < NV * 4; ++i) {
+    acc[i] += shfl_xor(acc[i], 16);
+    acc[i] += shfl_xor(acc[i], 32);
+  }
+  if (lane < 16)
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      *reinterpret_cast<f32x4*>(out + bl_expert(i, lane, 0)) =
+          (f32x4){acc[i * 4], acc[i * 4 + 1], acc[i * 4 + 2], acc[i * 4 + 3]};
+}
+
+constexpr int BL_OFF = 1024;  // segment offsets that fit the LDS copy
+
 }  // namespace
 
 // A block sums one slab of `slab` consecutive tokens.  Where segments meet
 // inside a slab it leaves one partial sum per segment: slab b and segment s
 // share slot b + s (both only grow along the tokens, so slots are distinct;
-// at most slabs + S - 1 of them).
+// at most slabs + S - 1 of them).  Also clears the finish's tickets.
 template <int NV, bool VEC>
 __global__ __launch_bounds__(256) void k_balance_sums(const float* __restrict__ logits, const int32_t* __restrict__ ids,
                                                       const uint8_t* __restrict__ mask,
                                                       const int32_t* __restrict__ off, int S, int T, int E, int k,
                                                       int slab, float* __restrict__ psum, int32_t* __restrict__ csum,
-                                                      int32_t* __restrict__ tsum) {
+                                                      int32_t* __restrict__ tsum, int32_t* __restrict__ ticket) {
   constexpr int NE = NV * 64;
-  __shared__ float red[16][NE];
-  __shared__ int cnt[NE];
+  __shared__ __align__(16) float red[4][NE];
+  __shared__ int cnt[NE], loff[BL_OFF];
   __shared__ int ntok;
-  const int tid = threadIdx.x, row = tid >> 4, ln = tid & 15;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = tid >> 4, ln = tid & 15;
   const int b = blockIdx.x;
+  for (int i = b * 256 + tid; i < S; i += gridDim.x * 256) ticket[i] = 0;
   int t = b * slab;
   const int tend = min(T, t + slab);
   int s = 0;
   if (off != nullptr) {
-    // the segment of t: the last one that starts at or before it
-    s = bl_count_le(off, S, t) - 1;
+    if (S < BL_OFF) {  // the search's dependent reads go to LDS
+      for (int i = tid; i <= S; i += 256) loff[i] = off[i];
+      __syncthreads();
+      s = bl_count_le(loff, S, t) - 1;
+    } else {
+      s = bl_count_le(off, S, t) - 1;
+    }
     if (s < 0) {  // tokens before the first segment
       s = 0;
       t = max(t, off[0]);
     }
   }
   while (t < tend && s < S) {
-    const int send = off != nullptr ? min(tend, max(off[s + 1], t)) : tend;
+    const int send = off != nullptr ? min(tend, max(S < BL_OFF ? loff[s + 1] : off[s + 1], t)) : tend;
     if (send > t) {
       for (int e = tid; e < NE; e += 256) cnt[e] = 0;
       if (tid == 0) ntok = 0;
@@ -130,31 +178,13 @@ __global__ __launch_bounds__(256) void k_balance_sums(const float* __restrict__ 
 #pragma unroll
       for (int i = 0; i < NV * 4; ++i) acc[i] = 0.0f;
       int mine = 0;
-      for (int u = t + row; u < send; u += 16) {
-        if (mask != nullptr && mask[u] == 0) continue;
-        ++mine;
-        float v[NV * 4];
-        bl_load<NV, VEC>(logits + (int64_t)u * E, E, ln, v);
-        bl_softmax(v);
-#pragma unroll
-        for (int i = 0; i < NV * 4; ++i) acc[i] += v[i];
-        if (ln < k) {
-          const int e = ids[(int64_t)u * k + ln];
-          if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
-        }
-      }
+      bl_run<NV, VEC>(logits, ids, mask, t + row, send, 16, E, k, ln, cnt, acc, mine);
       if (ln == 0 && mine) atomicAdd(&ntok, mine);
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) red[row][bl_expert(i, ln, j)] = acc[i * 4 + j];
+      bl_wave_sums<NV>(acc, lane, red[wave]);
       __syncthreads();
       const int64_t slot = b + s;
       for (int e = tid; e < E; e += 256) {
-        float a = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) a += red[r][e];
-        psum[slot * E + e] = a;
+        psum[slot * E + e] = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
         csum[slot * E + e] = cnt[e];
       }
       if (tid == 0) tsum[slot] = ntok;
@@ -165,63 +195,135 @@ __global__ __launch_bounds__(256) void k_balance_sums(const float* __restrict__ 
   }
 }
 
-// One block per segment: adds its slots in order and forms the outputs.
+// Block (s, j) adds the slots of segment s for experts 64 j .. 64 j + 63, 16
+// groups of 64 threads each taking every 16th slot; the last block of the
+// segment to arrive (a ticket) adds the loss's parts in the order of j, so
+// results do not depend on which one it is.
 __global__ __launch_bounds__(1024) void k_balance_finish(const float* __restrict__ psum,
                                                          const int32_t* __restrict__ csum,
                                                          const int32_t* __restrict__ tsum,
                                                          const int32_t* __restrict__ off, int T, int E, int k,
-                                                         int slab, float* __restrict__ loss,
+                                                         int slab, int32_t* __restrict__ ticket,
+                                                         float* __restrict__ part, float* __restrict__ loss,
                                                          int32_t* __restrict__ counts, int32_t* __restrict__ tokens,
                                                          float* __restrict__ probs) {
-  __shared__ float rp[1024];
-  __shared__ int rc[1024];
-  __shared__ float wsum[16];
-  const int s = blockIdx.x, tid = threadIdx.x;
+  __shared__ float rp[16][64];
+  __shared__ int rc[16][64], rn[16];
+  const int s = blockIdx.x, tid = threadIdx.x, g = tid >> 6, lane = tid & 63, e = blockIdx.y * 64 + lane;
   const int t0 = off != nullptr ? min(max(off[s], 0), T) : 0;
   const int t1 = off != nullptr ? min(max(off[s + 1], t0), T) : T;
   const int b0 = t0 / slab, nb = t1 > t0 ? (t1 - 1) / slab - b0 + 1 : 0;
-  // tokens of the segment
+  const int64_t first = b0 + s;
   int n = 0;
-  for (int b = tid; b < nb; b += 1024) n += tsum[b0 + b + s];
-  rc[tid] = n;
-  __syncthreads();
-  for (int d = 512; d > 0; d >>= 1) {
-    if (tid < d) rc[tid] += rc[tid + d];
-    __syncthreads();
-  }
-  n = rc[0];
-  __syncthreads();
-  const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
-  // G groups of threads share the slots of an expert (E <= 1024)
-  const int W = (E + 63) / 64 * 64, G = 1024 / W;
-  const int g = tid / W, e = tid - g * W;
+  for (int b = tid; b < nb; b += 1024) n += tsum[first + b];
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) n += shfl_xor(n, x);
+  if (lane == 0) rn[g] = n;
   float a = 0.0f;
   int c = 0;
-  if (g < G && e < E)
-    for (int b = g; b < nb; b += G) {
-      a += psum[(int64_t)(b0 + b + s) * E + e];
-      c += csum[(int64_t)(b0 + b + s) * E + e];
+  if (e < E)
+    for (int b = g; b < nb; b += 128) {
+      // up to 8 slots' loads in flight
+      float x[8];
+      int y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool in = b + i * 16 < nb;
+        x[i] = in ? psum[(first + b + i * 16) * E + e] : 0.0f;
+        y[i] = in ? csum[(first + b + i * 16) * E + e] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a += x[i];
+        c += y[i];
+      }
     }
-  rp[tid] = a;
-  rc[tid] = c;
+  rp[g][lane] = a;
+  rc[g][lane] = c;
   __syncthreads();
-  float part = 0.0f;
-  if (tid < E) {
-    for (int j = 1; j < G; ++j) {
-      a += rp[j * W + tid];
-      c += rc[j * W + tid];
+  if (g != 0) return;
+  n = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) n += rn[i];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) {
+    a += rp[i][lane];
+    c += rc[i][lane];
+  }
+  const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
+  const float p = a * inv;
+  if (e < E) {
+    probs[(int64_t)s * E + e] = p;
+    counts[(int64_t)s * E + e] = c;
+  }
+  float l = e < E ? (float)c * p : 0.0f;
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) l += shfl_xor(l, x);
+  if (lane == 0) {
+    int last = 1;
+    if (gridDim.y > 1) {
+      // agent scope: other XCDs' parts are in memory before their ticket is
+      __hip_atomic_store(&part[(int64_t)s * gridDim.y + blockIdx.y], l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      last = __hip_atomic_fetch_add(&ticket[s], 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.y - 1;
+      if (last) {
+        l = 0.0f;
+        for (unsigned j = 0; j < gridDim.y; ++j)
+          l += __hip_atomic_load(&part[(int64_t)s * gridDim.y + j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
     }
+    if (last) {
+      loss[s] = l * inv * ((float)E / (float)k);
+      tokens[s] = n;
+    }
+  }
+}
+
+// Up to BALANCE_ONE tokens: one launch, a block of 64 tokens' lanes per segment
+// that forms the outputs itself.
+template <int NV, bool VEC>
+__global__ __launch_bounds__(1024) void k_balance_one(const float* __restrict__ logits, const int32_t* __restrict__ ids,
+                                                      const uint8_t* __restrict__ mask,
+                                                      const int32_t* __restrict__ off, int T, int E, int k,
+                                                      float* __restrict__ loss, int32_t* __restrict__ counts,
+                                                      int32_t* __restrict__ tokens, float* __restrict__ probs) {
+  constexpr int NE = NV * 64;
+  __shared__ __align__(16) float red[16][NE];
+  __shared__ int cnt[NE];
+  __shared__ float wsum[16];
+  __shared__ int ntok;
+  const int s = blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = tid >> 4, ln = tid & 15;
+  const int t0 = off != nullptr ? min(max(off[s], 0), T) : 0;
+  const int t1 = off != nullptr ? min(max(off[s + 1], t0), T) : T;
+  if (tid < NE) cnt[tid] = 0;
+  if (tid == 0) ntok = 0;
+  __syncthreads();
+  float acc[NV * 4];
+#pragma unroll
+  for (int i = 0; i < NV * 4; ++i) acc[i] = 0.0f;
+  int mine = 0;
+  bl_run<NV, VEC>(logits, ids, mask, t0 + row, t1, 64, E, k, ln, cnt, acc, mine);
+  if (ln == 0 && mine) atomicAdd(&ntok, mine);
+  bl_wave_sums<NV>(acc, lane, red[wave]);
+  __syncthreads();
+  const int n = ntok;
+  const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
+  float l = 0.0f;
+  if (tid < E) {
+    float a = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) a += red[w][tid];
     const float p = a * inv;
+    const int c = cnt[tid];
     probs[(int64_t)s * E + tid] = p;
     counts[(int64_t)s * E + tid] = c;
-    part = (float)c * p;
+    l = (float)c * p;
   }
 #pragma unroll
-  for (int x = 32; x > 0; x >>= 1) part += shfl_xor(part, x);
-  if ((tid & 63) == 0) wsum[tid >> 6] = part;
+  for (int x = 32; x > 0; x >>= 1) l += shfl_xor(l, x);
+  if (lane == 0) wsum[wave] = l;
   __syncthreads();
   if (tid == 0) {
-    float l = 0.0f;
+    l = 0.0f;
     for (int i = 0; i < 16; ++i) l += wsum[i];
     loss[s] = l * inv * ((float)E / (float)k);
     tokens[s] = n;
@@ -238,8 +340,13 @@ __global__ __launch_bounds__(256) void k_balance_bwd(const float* __restrict__ l
                                                      const int32_t* __restrict__ tokens,
                                                      const float* __restrict__ dloss, int accumulate, int slab,
                                                      float* __restrict__ dlogits) {
+  __shared__ int loff[BL_OFF];
   const int row = threadIdx.x >> 4, ln = threadIdx.x & 15;
   const int tend = min(T, ((int)blockIdx.x + 1) * slab);
+  if (off != nullptr && S < BL_OFF) {
+    for (int i = threadIdx.x; i <= S; i += 256) loff[i] = off[i];
+    __syncthreads();
+  }
   int shi = -1;  // end of the segment whose a is held
   float a[NV * 4];
   bool none = false;
@@ -248,8 +355,8 @@ __global__ __launch_bounds__(256) void k_balance_bwd(const float* __restrict__ l
       int s = 0;
       shi = T;
       if (off != nullptr) {
-        s = bl_count_le(off, S + 1, t) - 1;  // -1 or S: no segment
-        shi = s >= S ? T : off[s + 1];
+        s = (S < BL_OFF ? bl_count_le(loff, S + 1, t) : bl_count_le(off, S + 1, t)) - 1;  // -1 or S: no segment
+        shi = s >= S ? T : S < BL_OFF ? loff[s + 1] : off[s + 1];
       }
       none = s < 0 || s >= S || tokens[s] <= 0;
       if (!none) {
@@ -304,10 +411,13 @@ __global__ __launch_bounds__(256) void k_balance_bwd(const float* __restrict__ l
   }
 }
 
-// Tokens per block: 16 rows of lanes take them 16 at a time.
-int balance_slab(int T) {
+constexpr int BALANCE_ONE = 1024;
+
+// Tokens per block: 16 rows of lanes take them 16 at a time, and two blocks
+// per CU hide the reads' latency.
+int balance_slab(int T, int most = 512) {
   int slab = 16;
-  while (slab < 1024 && (T + slab - 1) / slab > 512) slab *= 2;
+  while (slab < 1024 && (T + slab - 1) / slab > most) slab *= 2;
   return slab;
 }
 int64_t balance_slots(int T, int S) { return (T + balance_slab(T) - 1) / balance_slab(T) + (int64_t)S; }
@@ -331,23 +441,29 @@ static void balance_dispatch(int E, F f) {
 }
 
 void launch_balance(const float* logits, const int32_t* ids, const uint8_t* mask, const int32_t* off, int S, int T,
-                    int E, int k, float* psum, int32_t* csum, int32_t* tsum, float* loss, int32_t* counts,
-                    int32_t* tokens, float* probs, hipStream_t s) {
+                    int E, int k, float* psum, int32_t* csum, int32_t* tsum, int32_t* ticket, float* part, float* loss,
+                    int32_t* counts, int32_t* tokens, float* probs, hipStream_t s) {
   const int slab = balance_slab(T);
-  if (T > 0)
+  if (T <= BALANCE_ONE) {
     balance_dispatch(E, [&](auto nv, auto vec) {
-      hipLaunchKernelGGL((k_balance_sums<decltype(nv)::value, decltype(vec)::value>), dim3((T + slab - 1) / slab),
-                         dim3(256), 0, s, logits, ids, mask, off, S, T, E, k, slab, psum, csum, tsum);
+      hipLaunchKernelGGL((k_balance_one<decltype(nv)::value, decltype(vec)::value>), dim3(S), dim3(1024), 0, s, logits,
+                         ids, mask, off, T, E, k, loss, counts, tokens, probs);
     });
-  hipLaunchKernelGGL(k_balance_finish, dim3(S), dim3(1024), 0, s, psum, csum, tsum, off, T, E, k, slab, loss, counts,
-                     tokens, probs);
+    return;
+  }
+  balance_dispatch(E, [&](auto nv, auto vec) {
+    hipLaunchKernelGGL((k_balance_sums<decltype(nv)::value, decltype(vec)::value>), dim3((T + slab - 1) / slab),
+                       dim3(256), 0, s, logits, ids, mask, off, S, T, E, k, slab, psum, csum, tsum, ticket);
+  });
+  hipLaunchKernelGGL(k_balance_finish, dim3(S, (E + 63) / 64), dim3(1024), 0, s, psum, csum, tsum, off, T, E, k, slab,
+                     ticket, part, loss, counts, tokens, probs);
 }
 
 void launch_balance_bwd(const float* logits, const uint8_t* mask, const int32_t* off, int S, int T, int E, int k,
                         const int32_t* counts, const int32_t* tokens, const float* dloss, int accumulate,
                         float* dlogits, hipStream_t s) {
   if (T == 0) return;
-  const int slab = balance_slab(T);
+  const int slab = balance_slab(T, 1024);
   balance_dispatch(E, [&](auto nv, auto vec) {
     hipLaunchKernelGGL((k_balance_bwd<decltype(nv)::value, decltype(vec)::value>), dim3((T + slab - 1) / slab),
                        dim3(256), 0, s, logits, mask, off, S, T, E, k, counts, tokens, dloss, accumulate, slab,

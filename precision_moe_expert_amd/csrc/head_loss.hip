@@ -92,34 +92,55 @@ __global__ __launch_bounds__(256) void k_head_teacher(const int32_t* __restrict_
 }
 
 // The list of tokens that count, in order, and each token's place in it (-1).
-// flag null: a token counts if its id is in [0, V).
+// flag null: a token counts if its id is in [0, V).  One block, 8192 tokens at a
+// time, 8 consecutive ones per thread.
 __global__ __launch_bounds__(1024) void k_head_compact(const uint8_t* __restrict__ flag, const int32_t* __restrict__ ids,
                                                        int T, int V, int32_t* __restrict__ rows,
                                                        int32_t* __restrict__ cidx, int32_t* __restrict__ count) {
-  __shared__ int part[1024];
-  const int tid = threadIdx.x, per = (T + 1023) / 1024;
-  const int t0 = min(T, tid * per), t1 = min(T, t0 + per);
-  auto on = [&](int t) { return flag != nullptr ? flag[t] != 0 : ids[t] >= 0 && ids[t] < V; };
-  int n = 0;
-  for (int t = t0; t < t1; ++t) n += on(t);
-  part[tid] = n;
-  __syncthreads();
-  for (int d = 1; d < 1024; d <<= 1) {
-    const int v = tid >= d ? part[tid - d] : 0;
-    __syncthreads();
-    part[tid] += v;
-    __syncthreads();
-  }
-  int c = part[tid] - n;
-  for (int t = t0; t < t1; ++t) {
-    if (on(t)) {
-      rows[c] = t;
-      cidx[t] = c++;
-    } else {
-      cidx[t] = -1;
+  __shared__ int wsum[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int base = 0;
+  for (int t0 = 0; t0 < T; t0 += 8192) {
+    const int t = t0 + tid * 8;
+    int on = 0;  // bit i: token t + i
+    if (t < T) {
+      if (flag != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) on |= (t + i < T && flag[t + i] != 0) << i;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int y = t + i < T ? ids[t + i] : -1;
+          on |= (y >= 0 && y < V) << i;
+        }
+      }
     }
+    const int k = __popc(on);
+    int before = k;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(before, d, 64);
+      if (lane >= d) before += v;
+    }
+    __syncthreads();  // the previous round's sums have been read
+    if (lane == 63) wsum[wave] = before;
+    __syncthreads();
+    before += base - k;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      const int v = wsum[w];
+      if (w < wave) before += v;
+      base += v;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (t + i < T) {
+        const bool o = (on >> i) & 1;
+        cidx[t + i] = o ? before : -1;
+        if (o) rows[before++] = t + i;
+      }
   }
-  if (tid == 1023) *count = part[1023];
+  if (tid == 0) *count = base;
 }
 
 // What a product's epilogue needs of its row c (16 bytes, one load).
@@ -849,61 +870,72 @@ __global__ __launch_bounds__(256) void k_head_targets(const int32_t* __restrict_
 }
 
 // d_h = u - r^2 h mean(h u), or u without a norm, u the sum of its slabs;
-// zeros for tokens that do not count.  One block per token.
+// zeros for tokens that do not count.  One block per token; a thread keeps its
+// NP pieces of 8 columns of u and h in registers between the sum and the
+// result (NP = 4: H <= 8192, 16: any).
+template <int NP>
 __global__ __launch_bounds__(256) void k_head_dh(HeadGemm p, const uint16_t* __restrict__ h, int64_t h_stride,
                                                  const int32_t* __restrict__ cidx, bool norm, int bm, int bn,
                                                  uint16_t* __restrict__ dh) {
   __shared__ float part[4];
-  const int t = blockIdx.x, c = cidx[t], H = p.H;
+  const int t = blockIdx.x, c = cidx[t], H = p.H, np = H / 8;
   uint16_t* o = dh + (int64_t)t * H;
   if (c < 0) {
-    for (int i = threadIdx.x; i < H / 8; i += 256) *reinterpret_cast<u32x4*>(o + i * 8) = (u32x4){0, 0, 0, 0};
+    for (int i = threadIdx.x; i < np; i += 256) *reinterpret_cast<u32x4*>(o + i * 8) = (u32x4){0, 0, 0, 0};
     return;
   }
   const int n = *p.count, splits = head_splits(n, H, min(p.piece, p.V), bm, bn, p.cus, p.dz_max);
   const int64_t slab = (int64_t)n * H;
-  float* ur = p.u + (int64_t)c * H;
+  const float* ur = p.u + (int64_t)c * H;
   const uint16_t* hr = h + (int64_t)t * h_stride;
-  float f = 0.0f;
-  if (norm || splits > 1) {
-    float dot = 0.0f;
-    for (int i = threadIdx.x; i < H / 8; i += 256) {
-      f32x4 a = *reinterpret_cast<const f32x4*>(ur + i * 8), b = *reinterpret_cast<const f32x4*>(ur + i * 8 + 4);
-      for (int s = 1; s < splits; ++s) {
-        a += *reinterpret_cast<const f32x4*>(ur + s * slab + i * 8);
-        b += *reinterpret_cast<const f32x4*>(ur + s * slab + i * 8 + 4);
-      }
-      if (splits > 1) {  // this thread's own pieces again below
-        *reinterpret_cast<f32x4*>(ur + i * 8) = a;
-        *reinterpret_cast<f32x4*>(ur + i * 8 + 4) = b;
-      }
-      if (norm) {
-        const u32x4 q = *reinterpret_cast<const u32x4*>(hr + i * 8);
+  f32x4 a[NP], b[NP];
+  u32x4 q[NP];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          dot = fmaf(j < 2 ? a[2 * j] : b[2 * j - 4], bf16_bits_to_f32(q[j] & 0xFFFFu), dot);
-          dot = fmaf(j < 2 ? a[2 * j + 1] : b[2 * j - 3], bf16_bits_to_f32(q[j] >> 16), dot);
-        }
-      }
-    }
-    if (norm) {
-      dot = hl_sum64(dot);
-      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
-      __syncthreads();
-      f = p.r[c] * p.r[c] * ((part[0] + part[1]) + (part[2] + part[3])) / (float)H;
+  for (int k = 0; k < NP; ++k) {
+    const int i = threadIdx.x + k * 256;
+    a[k] = b[k] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    q[k] = (u32x4){0, 0, 0, 0};
+    if (i < np) {
+      a[k] = *reinterpret_cast<const f32x4*>(ur + i * 8);
+      b[k] = *reinterpret_cast<const f32x4*>(ur + i * 8 + 4);
+      if (norm) q[k] = *reinterpret_cast<const u32x4*>(hr + i * 8);  // without a norm h is not read
     }
   }
-  for (int i = threadIdx.x; i < H / 8; i += 256) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(ur + i * 8), b = *reinterpret_cast<const f32x4*>(ur + i * 8 + 4);
-    u32x4 q = {0, 0, 0, 0};
-    if (norm) q = *reinterpret_cast<const u32x4*>(hr + i * 8);  // without a norm f = 0 and h is not read
+  for (int s = 1; s < splits; ++s)
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int i = threadIdx.x + k * 256;
+      if (i < np) {
+        a[k] += *reinterpret_cast<const f32x4*>(ur + s * slab + i * 8);
+        b[k] += *reinterpret_cast<const f32x4*>(ur + s * slab + i * 8 + 4);
+      }
+    }
+  float f = 0.0f;
+  if (norm) {
+    float dot = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        dot = fmaf(j < 2 ? a[k][2 * j] : b[k][2 * j - 4], bf16_bits_to_f32(q[k][j] & 0xFFFFu), dot);
+        dot = fmaf(j < 2 ? a[k][2 * j + 1] : b[k][2 * j - 3], bf16_bits_to_f32(q[k][j] >> 16), dot);
+      }
+    dot = hl_sum64(dot);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+    __syncthreads();
+    f = p.r[c] * p.r[c] * ((part[0] + part[1]) + (part[2] + part[3])) / (float)H;
+  }
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int i = threadIdx.x + k * 256;
     u32x4 x;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float lo = j < 2 ? a[2 * j] : b[2 * j - 4], hi = j < 2 ? a[2 * j + 1] : b[2 * j - 3];
-      x[j] = bf16x2_bits(fmaf(-f, bf16_bits_to_f32(q[j] & 0xFFFFu), lo), fmaf(-f, bf16_bits_to_f32(q[j] >> 16), hi));
+      const float lo = j < 2 ? a[k][2 * j] : b[k][2 * j - 4], hi = j < 2 ? a[k][2 * j + 1] : b[k][2 * j - 3];
+      x[j] = bf16x2_bits(fmaf(-f, bf16_bits_to_f32(q[k][j] & 0xFFFFu), lo),
+                         fmaf(-f, bf16_bits_to_f32(q[k][j] >> 16), hi));
     }
-    *reinterpret_cast<u32x4*>(o + i * 8) = x;
+    if (i < np) *reinterpret_cast<u32x4*>(o + i * 8) = x;
   }
 }
 
@@ -1066,8 +1098,13 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
         hipLaunchKernelGGL(k_head_dw<HeadBig>, dim3(head_grid(p.piece / HeadBig::BM, cdiv(p.H, HeadBig::BN))),
                            dim3(HeadBig::NT), 0, s, g);
     }
-    hipLaunchKernelGGL(k_head_dh, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride,
-                       reinterpret_cast<const int32_t*>(a.ws + p.cidx), a.eps > 0.0f, C::BM, C::BN, a.dh);
+    const int32_t* cidx = reinterpret_cast<const int32_t*>(a.ws + p.cidx);
+    if (p.H <= 8192)
+      hipLaunchKernelGGL(k_head_dh<4>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f, C::BM, C::BN,
+                         a.dh);
+    else
+      hipLaunchKernelGGL(k_head_dh<16>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f, C::BM,
+                         C::BN, a.dh);
   });
 }
 

@@ -222,11 +222,12 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd);
 void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s);
 void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s);
 
-// Router balance loss.  psum / csum: [slots][E], tsum: [slots].
+// Router balance loss.  psum / csum: [slots][E], tsum: [slots], ticket: [S],
+// part: [S][ceil(E/64)].
 int64_t balance_slots(int T, int S);
 void launch_balance(const float* logits, const int32_t* ids, const uint8_t* mask, const int32_t* off, int S, int T,
-                    int E, int k, float* psum, int32_t* csum, int32_t* tsum, float* loss, int32_t* counts,
-                    int32_t* tokens, float* probs, hipStream_t s);
+                    int E, int k, float* psum, int32_t* csum, int32_t* tsum, int32_t* ticket, float* part, float* loss,
+                    int32_t* counts, int32_t* tokens, float* probs, hipStream_t s);
 void launch_balance_bwd(const float* logits, const uint8_t* mask, const int32_t* off, int S, int T, int E, int k,
                         const int32_t* counts, const int32_t* tokens, const float* dloss, int accumulate,
                         float* dlogits, hipStream_t s);

@@ -1127,7 +1127,7 @@ moe_status check_balance(const moe_layer* layer, int32_t num_segs, Dims* d) {
 }
 
 struct BalanceWs {
-  size_t psum, csum, tsum, total;
+  size_t psum, csum, tsum, ticket, part, total;
 };
 BalanceWs balance_ws(const Dims& d, int32_t num_segs) {
   const size_t slots = (size_t)balance_slots(d.T, num_segs);
@@ -1135,7 +1135,9 @@ BalanceWs balance_ws(const Dims& d, int32_t num_segs) {
   w.psum = 0;
   w.csum = align_up(slots * d.E * 4);
   w.tsum = w.csum + align_up(slots * d.E * 4);
-  w.total = w.tsum + align_up(slots * 4);
+  w.ticket = w.tsum + align_up(slots * 4);
+  w.part = w.ticket + align_up((size_t)num_segs * 4);
+  w.total = w.part + align_up((size_t)num_segs * ((d.E + 63) / 64) * 4);
   return w;
 }
 
@@ -1253,7 +1255,8 @@ moe_status moe_balance_loss(const moe_layer* layer, const float* logits, const i
   char* base = static_cast<char*>(ws);
   launch_balance(logits, topk_ids, token_mask, seg_offsets, num_segs, d.T, d.E, d.k,
                  reinterpret_cast<float*>(base + w.psum), reinterpret_cast<int32_t*>(base + w.csum),
-                 reinterpret_cast<int32_t*>(base + w.tsum), loss, counts, tokens, probs,
+                 reinterpret_cast<int32_t*>(base + w.tsum), reinterpret_cast<int32_t*>(base + w.ticket),
+                 reinterpret_cast<float*>(base + w.part), loss, counts, tokens, probs,
                  static_cast<hipStream_t>(stream));
   return launch_status();
 }

@@ -180,7 +180,8 @@ def test_head_without_tokens(torch_gpu):
 
 
 BALANCE = [(1, 1, 1), (1, 8, 2), (15, 5, 2), (16, 64, 4), (17, 65, 3), (33, 130, 8), (300, 128, 8), (1000, 256, 8),
-           (700, 384, 6), (130, 385, 1), (90, 1000, 16), (70, 1024, 16), (20000, 60, 4)]
+           (700, 384, 6), (130, 385, 1), (90, 1000, 16), (70, 1024, 16), (20000, 60, 4), (1024, 33, 2), (1025, 64, 2),
+           (2100, 1024, 8), (1500, 390, 7)]
 
 
 @pytest.mark.parametrize("packed", [False, True])
@@ -223,13 +224,14 @@ def test_balance(torch_gpu, T, E, k, packed):
     assert all(torch.equal(a, b) for a, b in zip((loss, counts, tokens, probs), again))
 
 
-def test_balance_many_segments(torch_gpu):
-    """More segments than slabs: one to three tokens each, empty ones among them."""
-    T, E, k = 900, 48, 3
+@pytest.mark.parametrize("T,E,k,most", [(900, 48, 3, 4), (1100, 385, 2, 4), (3000, 48, 3, 3), (5000, 130, 4, 40)])
+def test_balance_many_segments(torch_gpu, T, E, k, most):
+    """More segments than slabs, up to `most` - 1 tokens each, empty ones among them (3000 tokens: more than 1024
+    segments)."""
     torch.manual_seed(1)
     off = [0]
     while off[-1] < T:
-        off.append(min(T, off[-1] + int(torch.randint(0, 4, (1,)))))
+        off.append(min(T, off[-1] + int(torch.randint(0, most, (1,)))))
     off = torch.tensor(off + [T]).int()
     logits = torch.randn(T, E)
     ids = torch.topk(logits, k, 1).indices.int()
