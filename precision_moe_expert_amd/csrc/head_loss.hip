@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256) void k_head_teacher(const int32_t* __restrict_
 
 // The list of tokens that count, in order, and each token's place in it (-1).
 // flag null: a token counts if its id is in [0, V).  One block, 8192 tokens at a
-// time, 8 consecutive ones per thread.
+// time: a wave takes 512 in steps of 64 (one per lane).
 __global__ __launch_bounds__(1024) void k_head_compact(const uint8_t* __restrict__ flag, const int32_t* __restrict__ ids,
                                                        int T, int V, int32_t* __restrict__ rows,
                                                        int32_t* __restrict__ cidx, int32_t* __restrict__ count) {
@@ -101,44 +101,38 @@ __global__ __launch_bounds__(1024) void k_head_compact(const uint8_t* __restrict
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int base = 0;
   for (int t0 = 0; t0 < T; t0 += 8192) {
-    const int t = t0 + tid * 8;
-    int on = 0;  // bit i: token t + i
-    if (t < T) {
-      if (flag != nullptr) {
+    const int t = t0 + wave * 512 + lane;
+    int x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) on |= (t + i < T && flag[t + i] != 0) << i;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int y = t + i < T ? ids[t + i] : -1;
-          on |= (y >= 0 && y < V) << i;
-        }
-      }
+    for (int i = 0; i < 8; ++i) {
+      const int u = min(t + i * 64, T - 1);
+      x[i] = flag != nullptr ? (int)flag[u] - 1 : ids[u];  // counts: in [0, V)
     }
-    const int k = __popc(on);
-    int before = k;
+    uint64_t on[8];
+    int k = 0;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(before, d, 64);
-      if (lane >= d) before += v;
+    for (int i = 0; i < 8; ++i) {
+      on[i] = __ballot(t + i * 64 < T && x[i] >= 0 && x[i] < V);
+      k += __popcll(on[i]);
     }
     __syncthreads();  // the previous round's sums have been read
-    if (lane == 63) wsum[wave] = before;
+    if (lane == 0) wsum[wave] = k;
     __syncthreads();
-    before += base - k;
+    int at = base;
 #pragma unroll
     for (int w = 0; w < 16; ++w) {
       const int v = wsum[w];
-      if (w < wave) before += v;
+      if (w < wave) at += v;
       base += v;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (t + i < T) {
-        const bool o = (on >> i) & 1;
-        cidx[t + i] = o ? before : -1;
-        if (o) rows[before++] = t + i;
-      }
+    for (int i = 0; i < 8; ++i) {
+      const int u = t + i * 64, c = at + __popcll(on[i] & ((1ull << lane) - 1));
+      const bool o = (on[i] >> lane) & 1;
+      if (u < T) cidx[u] = o ? c : -1;
+      if (o) rows[c] = u;
+      at += __popcll(on[i]);
+    }
   }
   if (tid == 0) *count = base;
 }
@@ -773,6 +767,14 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_head_dw(HeadGemm p) {
   __shared__ __align__(16) uint8_t smem[C::SMEM];
   head_dw<C>(p, blockIdx.x, smem);
 }
+// Both of a piece in one launch, the longer G W tiles first: the G^T h tiles
+// fill the CUs that its last round leaves idle.
+template <class C>
+__global__ __launch_bounds__(C::NT, C::WPS) void k_head_dz_dw(HeadGemm p, int ndz) {
+  __shared__ __align__(16) uint8_t smem[C::SMEM];
+  if ((int)blockIdx.x < ndz) head_dz<C>(p, blockIdx.x, smem);
+  else head_dw<C>(p, blockIdx.x - ndz, smem);
+}
 
 // Per token (one wave): joins its blocks' statistics and forms the outputs.
 __global__ __launch_bounds__(256) void k_head_finish(const float* __restrict__ stats, const float* __restrict__ zt,
@@ -1093,10 +1095,15 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
       hipLaunchKernelGGL(k_head_targets, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.rows, g.count, a.ids,
                          p.distill ? reinterpret_cast<const float*>(a.ws + p.lq) : nullptr, a.logp, a.loss, g.r,
                          a.dloss, a.scale, p.V, p.top, g.v0, p.piece, g.g);
-      hipLaunchKernelGGL(k_head_dz<C>, dim3(head_grid(g.dz_max, 1)), dim3(C::NT), 0, s, g);
-      if (a.dw != nullptr)
-        hipLaunchKernelGGL(k_head_dw<HeadBig>, dim3(head_grid(p.piece / HeadBig::BM, cdiv(p.H, HeadBig::BN))),
-                           dim3(HeadBig::NT), 0, s, g);
+      const int ndz = head_grid(g.dz_max, 1), ndw = head_grid(p.piece / HeadBig::BM, cdiv(p.H, HeadBig::BN));
+      if constexpr (C::BM == HeadBig::BM && C::BN == HeadBig::BN) {
+        if (a.dw != nullptr) {
+          hipLaunchKernelGGL(k_head_dz_dw<C>, dim3(ndz + ndw), dim3(C::NT), 0, s, g, ndz);
+          continue;
+        }
+      }
+      hipLaunchKernelGGL(k_head_dz<C>, dim3(ndz), dim3(C::NT), 0, s, g);
+      if (a.dw != nullptr) hipLaunchKernelGGL(k_head_dw<HeadBig>, dim3(ndw), dim3(HeadBig::NT), 0, s, g);
     }
     const int32_t* cidx = reinterpret_cast<const int32_t*>(a.ws + p.cidx);
     if (p.H <= 8192)
