@@ -51,6 +51,31 @@ MOE_DEV void hl_merge(float& m, float& s, float m2, float s2) {
 
 }  // namespace
 
+// G W (dL/dz) has few tiles for few rows or a narrow h, and a long K: its K is
+// split over `splits` workgroups per tile, which add to separate slabs of u
+// (added up in order by k_head_dh, so results do not depend on the order of
+// execution).  The number follows from the rows that count, when they are
+// known: the least
+//   rounds of workgroups x (K steps each + HEAD_STEP0) + splits x (steps that
+//   writing and reading a slab costs)
+// where a K step takes about a microsecond, memory moves about 5 MB in that
+// time, and a slab more costs k_head_dh about an eighth of it.
+constexpr int HEAD_STEP0 = 8;
+constexpr int HEAD_SPLITS = 64;  // one per lane of the wave that chooses
+struct HeadSplit {
+  int H, K, bm, bn;  // of the first piece, so every piece adds to the same slabs
+  int slots, most;   // workgroups that run at a time; most workgroups
+};
+MOE_DEV int head_splits(const HeadSplit& q, int n, int lane) {
+  const int tiles = ((n + q.bm - 1) / q.bm) * ((q.H + q.bn - 1) / q.bn), steps = (q.K + 63) / 64, s = lane + 1;
+  float cost = INFINITY;
+  if (s == 1 || (tiles * s <= q.most && s <= steps))
+    cost = (float)((tiles * s + q.slots - 1) / q.slots) * (float)((steps + s - 1) / s + HEAD_STEP0) +
+           (float)s * ((float)n * (float)q.H * (8.0f / 5e6f) + 0.125f);
+  const float least = -hl_max64(-cost);
+  return __ffsll(__ballot(cost == least));  // the first of them
+}
+
 // ---- which tokens count -----------------------------------------------------
 
 // Distillation, one wave per token: the log of the teacher's probabilities
@@ -95,7 +120,7 @@ __global__ __launch_bounds__(256) void k_head_teacher(const int32_t* __restrict_
 // flag null: a token counts if its id is in [0, V).  One block, 8192 tokens at a
 // time: a wave takes 512 in steps of 64 (one per lane).
 __global__ __launch_bounds__(1024) void k_head_compact(const uint8_t* __restrict__ flag, const int32_t* __restrict__ ids,
-                                                       int T, int V, int32_t* __restrict__ rows,
+                                                       int T, int V, HeadSplit q, int32_t* __restrict__ rows,
                                                        int32_t* __restrict__ cidx, int32_t* __restrict__ count) {
   __shared__ int wsum[16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -134,7 +159,13 @@ __global__ __launch_bounds__(1024) void k_head_compact(const uint8_t* __restrict
       at += __popcll(on[i]);
     }
   }
-  if (tid == 0) *count = base;
+  if (wave == 0) {
+    const int splits = head_splits(q, base, lane);
+    if (lane == 0) {
+      count[0] = base;
+      count[1] = splits;
+    }
+  }
 }
 
 // What a product's epilogue needs of its row c (16 bytes, one load).
@@ -145,33 +176,88 @@ struct HeadRow {
   int tgt;    // cross entropy: the target's id
 };
 
+// How the rows that count are found: from k_head_compact's list; by every block
+// itself among at most 1024 flags (block 0 writes the lists, no launch is spent
+// on them); or, up to HEAD_SAME tokens, not at all: row c is token c, rows of
+// tokens that do not count are zeros, and the teacher's probabilities are
+// formed here too.
+enum { HR_LIST, HR_FEW, HR_SAME };
+constexpr int HEAD_FEW = 1024, HEAD_SAME = 256;
+
+struct HeadRowsArgs {
+  const uint16_t* h;
+  int64_t h_stride;
+  int T, H, Hp, V, top, bm;
+  float eps, scale, tscale;
+  const int32_t* ids;
+  const float* tlogits;  // null: cross entropy
+  const uint8_t* flag;   // distillation, HR_LIST and HR_FEW
+  const float* loss;     // backward (cross entropy)
+  const float* lse;      // backward
+  const float* dloss;    // backward
+  HeadSplit split;
+  int32_t* rows;
+  int32_t* cidx;
+  int32_t* count;        // rows, splits of G W
+  uint16_t* hc;
+  float* r;
+  HeadRow* info;
+  float* gt;             // backward, cross entropy: G at the row's target
+  float* lq;
+};
+
 // The rows that count, one after the other, as the products read them: hc
 // [..][Hp] with zeros in columns H..Hp (the K of the products goes in steps of
-// 64) and in the rows up to the next multiple of a tile's BM rows, with
+// 64) and in the rows up to the next multiple of a tile's bm rows, with
 // r[c] = 1/rms of row c and its HeadRow (zeros behind the last row).  One block
-// per row.  FEW (at most 1024 tokens): every block finds its own token among
-// the flags, and block 0 writes the lists, so that no launch is spent on
-// k_head_compact.
-template <bool FEW>
-__global__ __launch_bounds__(256) void k_head_gather(const uint16_t* __restrict__ h, int64_t h_stride, int H, int Hp,
-                                                     float eps, const uint8_t* __restrict__ flag,
-                                                     const int32_t* __restrict__ ids, int T, int V,
-                                                     int32_t* __restrict__ rows, int32_t* __restrict__ cidx,
-                                                     int32_t* __restrict__ count, int bm, float scale,
-                                                     const float* __restrict__ lse, const float* __restrict__ dloss,
-                                                     uint16_t* __restrict__ hc, float* __restrict__ r,
-                                                     HeadRow* __restrict__ info) {
-  __shared__ float part[4];
+// per row.
+template <int MODE>
+__global__ __launch_bounds__(256) void k_head_gather(HeadRowsArgs p) {
+  __shared__ float part[4], part2[4];
   __shared__ int wsum[4], found;
-  const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
-  int n, t = 0;
-  if (FEW) {
+  const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int n, t = c;
+  bool live;  // row c holds a token that counts
+  if (MODE == HR_SAME) {
+    n = p.T;
+    if (p.tlogits == nullptr) {
+      const int y = c < n ? p.ids[c] : -1;
+      live = y >= 0 && y < p.V;
+    } else {
+      // thread j has slot j (top <= 256)
+      float x = -INFINITY;
+      if (c < n && tid < p.top) {
+        const int id = p.ids[(int64_t)c * p.top + tid];
+        if (id >= 0 && id < p.V) x = p.tlogits[(int64_t)c * p.top + tid];
+      }
+      const bool have = !(x == -INFINITY);
+      x *= p.tscale;
+      const float m4 = hl_max64(have ? x : -INFINITY);
+      const bool any4 = __any(have);
+      if (lane == 0) {
+        part[wave] = m4;
+        wsum[wave] = any4;
+      }
+      __syncthreads();
+      const float m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+      live = wsum[0] | wsum[1] | wsum[2] | wsum[3];
+      const float s4 = hl_sum64(have ? expf(x - m) : 0.0f);
+      if (lane == 0) part2[wave] = s4;
+      __syncthreads();
+      const float ls = logf((part2[0] + part2[1]) + (part2[2] + part2[3]));
+      if (c < n && tid < p.top) p.lq[(int64_t)c * p.top + tid] = have ? x - m - ls : -INFINITY;
+    }
+    if (c < n && tid == 0) {
+      p.rows[c] = c;
+      p.cidx[c] = live ? c : -1;
+    }
+  } else if (MODE == HR_FEW) {
     // thread i looks at tokens 4 i .. 4 i + 3
     int on[4], k = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int u = tid * 4 + i;
-      on[i] = u < T && (flag != nullptr ? flag[u] != 0 : ids[u] >= 0 && ids[u] < V);
+      on[i] = u < p.T && (p.flag != nullptr ? p.flag[u] != 0 : p.ids[u] >= 0 && p.ids[u] < p.V);
       k += on[i];
     }
     int before = k;
@@ -180,37 +266,45 @@ __global__ __launch_bounds__(256) void k_head_gather(const uint16_t* __restrict_
       const int v = __shfl_up(before, d, 64);
       if (lane >= d) before += v;
     }
-    if (lane == 63) wsum[tid >> 6] = before;
+    if (lane == 63) wsum[wave] = before;
     __syncthreads();
     before -= k;
 #pragma unroll
     for (int w = 0; w < 4; ++w)
-      if (w < (tid >> 6)) before += wsum[w];
+      if (w < wave) before += wsum[w];
     n = wsum[0] + wsum[1] + wsum[2] + wsum[3];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int u = tid * 4 + i;
       if (on[i] && before == c) found = u;
-      if (c == 0 && u < T) {
-        cidx[u] = on[i] ? before : -1;
-        if (on[i]) rows[before] = u;
+      if (c == 0 && u < p.T) {
+        p.cidx[u] = on[i] ? before : -1;
+        if (on[i]) p.rows[before] = u;
       }
       before += on[i];
     }
-    if (c == 0 && tid == 0) *count = n;
     __syncthreads();
-    if (c < n) t = found;
+    live = c < n;
+    if (live) t = found;
   } else {
-    n = *count;
-    if (c < n) t = rows[c];
+    n = p.count[0];
+    live = c < n;
+    if (live) t = p.rows[c];
   }
-  if (c >= (n + bm - 1) / bm * bm) return;
-  uint16_t* o = hc + (int64_t)c * Hp;
-  const uint16_t* row = h + (int64_t)t * h_stride;
+  if (MODE != HR_LIST && c == 0 && wave == 0) {
+    const int splits = head_splits(p.split, n, lane);
+    if (lane == 0) {
+      p.count[0] = n;
+      p.count[1] = splits;
+    }
+  }
+  if (c >= (n + p.bm - 1) / p.bm * p.bm) return;
+  uint16_t* o = p.hc + (int64_t)c * p.Hp;
+  const uint16_t* row = p.h + (int64_t)t * p.h_stride;
   float ss = 0.0f;
-  for (int i = tid; i < Hp / 8; i += 256) {
+  for (int i = tid; i < p.Hp / 8; i += 256) {
     u32x4 q = {0, 0, 0, 0};
-    if (c < n && i < H / 8) q = *reinterpret_cast<const u32x4*>(row + i * 8);
+    if (live && i < p.H / 8) q = *reinterpret_cast<const u32x4*>(row + i * 8);
     *reinterpret_cast<u32x4*>(o + i * 8) = q;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -219,19 +313,26 @@ __global__ __launch_bounds__(256) void k_head_gather(const uint16_t* __restrict_
       ss = fmaf(b, b, ss);
     }
   }
-  if (c >= n) {
-    if (tid == 0) info[c] = HeadRow{0.0f, 0.0f, 0.0f, -1};
+  if (!live) {
+    if (tid == 0) p.info[c] = HeadRow{0.0f, 0.0f, 0.0f, -1};
     return;
   }
   ss = hl_sum64(ss);
-  if (lane == 0) part[tid >> 6] = ss;
+  __syncthreads();  // part has been read
+  if (lane == 0) part[wave] = ss;
   __syncthreads();
   if (tid == 0) {
-    const float rr = eps > 0.0f ? 1.0f / sqrtf(((part[0] + part[1]) + (part[2] + part[3])) / (float)H + eps) : 1.0f;
-    const float f = scale * rr;
-    r[c] = rr;
-    info[c] = HeadRow{f * kLog2e, dloss != nullptr ? f * dloss[t] : f, dloss != nullptr ? lse[t] * kLog2e : 0.0f,
-                      flag == nullptr ? ids[t] : -1};
+    const float rr =
+        p.eps > 0.0f ? 1.0f / sqrtf(((part[0] + part[1]) + (part[2] + part[3])) / (float)p.H + p.eps) : 1.0f;
+    const float f = p.scale * rr;
+    p.r[c] = rr;
+    HeadRow w = {f * kLog2e, f, 0.0f, p.tlogits == nullptr ? p.ids[t] : -1};
+    if (p.dloss != nullptr) {
+      w.f = f * p.dloss[t];
+      w.l2 = p.lse[t] * kLog2e;
+      if (p.loss != nullptr) p.gt[c] = w.f * expm1f(-p.loss[t]);  // p - 1 = exp(-loss) - 1
+    }
+    p.info[c] = w;
   }
 }
 
@@ -483,8 +584,9 @@ struct HeadGemm {
   int64_t w_stride;
   int H, Hp, V, top;
   const int32_t* rows;
-  const int32_t* count;
+  const int32_t* count;   // rows, splits of G W
   const float* r;         // [count]
+  const float* gt;        // [count], cross entropy: G at the row's target
   const HeadRow* info;    // [..]
   float scale;
   const int32_t* ids;
@@ -495,7 +597,6 @@ struct HeadGemm {
   float* u;       // [count][H]
   uint16_t* dw;   // [V][H]
   int v0, piece;
-  int cus, dz_max;        // compute units; most workgroups of the G W product
 };
 
 // Forward: per row and block of BN columns the maximum of y = l log2 e and the
@@ -650,32 +751,17 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_head_grad(HeadGemm p) {
   };
   if (full) write(std::true_type());
   else write(std::false_type());
-}
-
-// G W has few tiles for few rows or a narrow h, and a long K: its K is split
-// over `splits` workgroups per tile, which add to separate slabs of u (added
-// up in order by k_head_dh, so results do not depend on the order of
-// execution).  The number follows from the rows that count: the least
-//   rounds of workgroups x (K steps each + HEAD_STEP0) + splits x (steps that
-//   writing and reading a slab costs)
-// where a K step of a 256 x 256 tile takes about a microsecond and memory
-// moves about 5 MB in that time.
-constexpr int HEAD_STEP0 = 10;
-constexpr int HEAD_SPLITS = 16;
-MOE_DEV int head_splits(int n, int H, int K, int bm, int bn, int cus, int most) {
-  const int tiles = ((n + bm - 1) / bm) * ((H + bn - 1) / bn), steps = (K + 63) / 64;
-  const int slab = (int)((int64_t)n * H * 8 / 5000000);
-  int best = 1;
-  int64_t least = -1;
-  for (int s = 1; s <= HEAD_SPLITS && (s == 1 || (tiles * s <= most && s <= steps)); ++s) {
-    const int64_t rounds = (tiles * s + cus - 1) / cus;
-    const int64_t cost = rounds * ((steps + s - 1) / s + HEAD_STEP0) + (int64_t)s * slab;
-    if (least < 0 || cost < least) {
-      least = cost;
-      best = s;
+  if (!p.distill) {
+    // the lane that wrote a row's target puts s r g (p - 1) over it
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i) {
+      const int tc = info[i].tgt - n0 - wn;
+      if (tc >= 0 && tc < C::NJ * 16 && ((tc >> 2) & 3) == lg) {
+        const int64_t c = m0 + wm + i * 16 + ln;
+        p.g[c * p.piece + (n0 - p.v0) + wn + tc] = (uint16_t)f32_to_bf16_bits(p.gt[c]);
+      }
     }
   }
-  return best;
 }
 
 // u (slab of this workgroup's share of K) += G W over a piece.
@@ -683,8 +769,7 @@ template <class C>
 MOE_DEV void head_dz(const HeadGemm& p, int bid, uint8_t* smem) {
   const int n = *p.count, nm = (n + C::BM - 1) / C::BM, nn = (p.H + C::BN - 1) / C::BN;
   if (n == 0) return;
-  // the shares are those of the first piece, so every piece adds to the same slabs
-  const int splits = head_splits(n, p.H, min(p.piece, p.V), C::BM, C::BN, p.cus, p.dz_max);
+  const int splits = p.count[1];
   int mt, nt;
   if (!head_tile(bid, nm * splits, nn, mt, nt)) return;
   const int sp = mt / nm;
@@ -827,28 +912,20 @@ __global__ __launch_bounds__(256) void k_head_finish(const float* __restrict__ s
   }
 }
 
-// Backward: G at the target's ids in [v0, v0 + piece), from the forward's
-// log-probs: s r g (p - q), one wave per counted token.  Slots that repeat an
+// Distillation's backward: G at the slots' ids in [v0, v0 + piece), from the
+// forward's log-probs: s r g (p - q), one wave per row.  Slots that repeat an
 // id add their q, and the first of them writes.
 __global__ __launch_bounds__(256) void k_head_targets(const int32_t* __restrict__ rows, const int32_t* __restrict__ count,
                                                       const int32_t* __restrict__ ids, const float* __restrict__ lq,
-                                                      const float* __restrict__ logp, const float* __restrict__ loss,
-                                                      const float* __restrict__ r, const float* __restrict__ dloss,
-                                                      float scale, int V, int top, int v0, int piece,
-                                                      uint16_t* __restrict__ g) {
+                                                      const float* __restrict__ logp, const HeadRow* __restrict__ info,
+                                                      int top, int v0, int piece, uint16_t* __restrict__ g) {
   __shared__ int sid[4][256];
   __shared__ float sq[4][256];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int c = blockIdx.x * 4 + wave;
   if (c >= *count) return;
   const int t = rows[c];
-  const float cf = scale * r[c] * dloss[t];
-  if (lq == nullptr) {  // cross entropy: p - 1 = exp(-loss) - 1
-    const int v = ids[t] - v0;
-    if (lane == 0 && v >= 0 && v < piece)
-      g[(int64_t)c * piece + v] = (uint16_t)f32_to_bf16_bits(cf * expm1f(-loss[t]));
-    return;
-  }
+  const float cf = info[c].f;
   for (int j = lane; j < top; j += 64) {
     const float q = lq[(int64_t)t * top + j];
     const bool have = !(q == -INFINITY);
@@ -877,7 +954,7 @@ __global__ __launch_bounds__(256) void k_head_targets(const int32_t* __restrict_
 // result (NP = 4: H <= 8192, 16: any).
 template <int NP>
 __global__ __launch_bounds__(256) void k_head_dh(HeadGemm p, const uint16_t* __restrict__ h, int64_t h_stride,
-                                                 const int32_t* __restrict__ cidx, bool norm, int bm, int bn,
+                                                 const int32_t* __restrict__ cidx, bool norm,
                                                  uint16_t* __restrict__ dh) {
   __shared__ float part[4];
   const int t = blockIdx.x, c = cidx[t], H = p.H, np = H / 8;
@@ -886,8 +963,8 @@ __global__ __launch_bounds__(256) void k_head_dh(HeadGemm p, const uint16_t* __r
     for (int i = threadIdx.x; i < np; i += 256) *reinterpret_cast<u32x4*>(o + i * 8) = (u32x4){0, 0, 0, 0};
     return;
   }
-  const int n = *p.count, splits = head_splits(n, H, min(p.piece, p.V), bm, bn, p.cus, p.dz_max);
-  const int64_t slab = (int64_t)n * H;
+  const int splits = p.count[1];
+  const int64_t slab = (int64_t)p.count[0] * H;
   const float* ur = p.u + (int64_t)c * H;
   const uint16_t* hr = h + (int64_t)t * h_stride;
   f32x4 a[NP], b[NP];
@@ -903,15 +980,30 @@ __global__ __launch_bounds__(256) void k_head_dh(HeadGemm p, const uint16_t* __r
       if (norm) q[k] = *reinterpret_cast<const u32x4*>(hr + i * 8);  // without a norm h is not read
     }
   }
-  for (int s = 1; s < splits; ++s)
 #pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      const int i = threadIdx.x + k * 256;
-      if (i < np) {
-        a[k] += *reinterpret_cast<const f32x4*>(ur + s * slab + i * 8);
-        b[k] += *reinterpret_cast<const f32x4*>(ur + s * slab + i * 8 + 4);
+  for (int k = 0; k < NP; ++k) {
+    const int i = threadIdx.x + k * 256;
+    if (i >= np) continue;
+    const float* us = ur + i * 8;
+    int s = 1;
+    for (; s + 4 <= splits; s += 4) {  // four slabs' loads in flight
+      f32x4 x[4], y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = *reinterpret_cast<const f32x4*>(us + (s + j) * slab);
+        y[j] = *reinterpret_cast<const f32x4*>(us + (s + j) * slab + 4);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a[k] += x[j];
+        b[k] += y[j];
       }
     }
+    for (; s < splits; ++s) {
+      a[k] += *reinterpret_cast<const f32x4*>(us + s * slab);
+      b[k] += *reinterpret_cast<const f32x4*>(us + s * slab + 4);
+    }
+  }
   float f = 0.0f;
   if (norm) {
     float dot = 0.0f;
@@ -992,14 +1084,18 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
   head_dispatch(T, [&](auto c) {
     bm = decltype(c)::BM;
     bn = decltype(c)::BN;
+    p.per_cu = decltype(c)::WPS * 4 / decltype(c)::NW;
   });
+  p.bn = bn;
+  p.dz_max = head_dz_max(T, H, bm, bn);
   p.bm = bm;
   p.r = take(rows * 4);
   p.info = take(rows * sizeof(HeadRow));
+  p.gt = take(bwd && !distill ? t * 4 : 0);
   p.flag = take(distill ? t : 0);
   p.rows = take(t * 4);
   p.cidx = take(t * 4);
-  p.count = take(4);
+  p.count = take(8);
   p.hc = take(rows * p.Hp * 2);
   p.lq = take(distill ? t * top * 4 : 0);
   if (!bwd) {
@@ -1012,7 +1108,7 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
     p.piece = cdiv(cdiv(V, p.npieces), 256) * 256;
     p.npieces = cdiv(V, p.piece);
     // slabs of u: the splits of a tile times the tiles stay below dz_max (or are 1)
-    size_t u = (size_t)head_dz_max(T, H, bm, bn) * bm * bn;
+    size_t u = (size_t)p.dz_max * bm * bn;
     if (u > t * H * HEAD_SPLITS) u = t * H * HEAD_SPLITS;
     if (u < t * H) u = t * H;
     p.u = take(u * 4);
@@ -1024,25 +1120,48 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
 
 static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
   char* ws = a.ws;
-  float* r = reinterpret_cast<float*>(ws + p.r);
-  uint8_t* flag = p.distill ? reinterpret_cast<uint8_t*>(ws + p.flag) : nullptr;
-  int32_t* rows = reinterpret_cast<int32_t*>(ws + p.rows);
-  int32_t* cidx = reinterpret_cast<int32_t*>(ws + p.cidx);
-  int32_t* count = reinterpret_cast<int32_t*>(ws + p.count);
-  uint16_t* hc = reinterpret_cast<uint16_t*>(ws + p.hc);
-  if (p.distill)
+  uint8_t* flag = p.distill && p.T > HEAD_SAME ? reinterpret_cast<uint8_t*>(ws + p.flag) : nullptr;
+  HeadRowsArgs q{};
+  q.h = a.h;
+  q.h_stride = a.h_stride;
+  q.T = p.T;
+  q.H = p.H;
+  q.Hp = p.Hp;
+  q.V = p.V;
+  q.top = p.top;
+  q.bm = p.bm;
+  q.eps = a.eps;
+  q.scale = a.scale;
+  q.tscale = a.teacher_scale;
+  q.ids = a.ids;
+  q.tlogits = a.tlogits;
+  q.flag = flag;
+  if (p.bwd) {
+    q.loss = p.distill ? nullptr : a.loss;
+    q.lse = a.lse;
+    q.dloss = a.dloss;
+  }
+  q.split = HeadSplit{p.H, p.bwd ? (p.piece < p.V ? p.piece : p.V) : 64, p.bm, p.bn, head_cus() * p.per_cu, p.dz_max};
+  q.rows = reinterpret_cast<int32_t*>(ws + p.rows);
+  q.cidx = reinterpret_cast<int32_t*>(ws + p.cidx);
+  q.count = reinterpret_cast<int32_t*>(ws + p.count);
+  uint16_t* hc = q.hc = reinterpret_cast<uint16_t*>(ws + p.hc);
+  q.r = reinterpret_cast<float*>(ws + p.r);
+  q.info = reinterpret_cast<HeadRow*>(ws + p.info);
+  q.gt = reinterpret_cast<float*>(ws + p.gt);
+  q.lq = reinterpret_cast<float*>(ws + p.lq);
+  if (flag != nullptr)
     hipLaunchKernelGGL(k_head_teacher, dim3(cdiv(p.T, 4)), dim3(256), 0, s, a.ids, a.tlogits, p.T, p.V, p.top,
-                       a.teacher_scale, reinterpret_cast<float*>(ws + p.lq), flag);
+                       a.teacher_scale, q.lq, flag);
   const dim3 grid(cdiv(p.T, p.bm) * p.bm);
-  HeadRow* info = reinterpret_cast<HeadRow*>(ws + p.info);
-  const float *lse = p.bwd ? a.lse : nullptr, *dloss = p.bwd ? a.dloss : nullptr;
-  if (p.T <= 1024) {
-    hipLaunchKernelGGL(k_head_gather<true>, grid, dim3(256), 0, s, a.h, a.h_stride, p.H, p.Hp, a.eps, flag, a.ids, p.T,
-                       p.V, rows, cidx, count, p.bm, a.scale, lse, dloss, hc, r, info);
+  if (p.T <= HEAD_SAME) {
+    hipLaunchKernelGGL(k_head_gather<HR_SAME>, grid, dim3(256), 0, s, q);
+  } else if (p.T <= HEAD_FEW) {
+    hipLaunchKernelGGL(k_head_gather<HR_FEW>, grid, dim3(256), 0, s, q);
   } else {
-    hipLaunchKernelGGL(k_head_compact, dim3(1), dim3(1024), 0, s, flag, a.ids, p.T, p.V, rows, cidx, count);
-    hipLaunchKernelGGL(k_head_gather<false>, grid, dim3(256), 0, s, a.h, a.h_stride, p.H, p.Hp, a.eps, flag, a.ids,
-                       p.T, p.V, rows, cidx, count, p.bm, a.scale, lse, dloss, hc, r, info);
+    hipLaunchKernelGGL(k_head_compact, dim3(1), dim3(1024), 0, s, flag, a.ids, p.T, p.V, q.split, q.rows, q.cidx,
+                       q.count);
+    hipLaunchKernelGGL(k_head_gather<HR_LIST>, grid, dim3(256), 0, s, q);
   }
   HeadGemm g{};
   g.hc = hc;
@@ -1052,10 +1171,11 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
   g.Hp = p.Hp;
   g.V = p.V;
   g.top = p.top;
-  g.rows = rows;
-  g.count = count;
-  g.r = r;
-  g.info = info;
+  g.rows = q.rows;
+  g.count = q.count;
+  g.r = q.r;
+  g.gt = q.gt;
+  g.info = q.info;
   g.distill = p.distill;
   g.scale = a.scale;
   g.ids = a.ids;
@@ -1084,18 +1204,16 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
   g.u = reinterpret_cast<float*>(a.ws + p.u);
   g.g = reinterpret_cast<uint16_t*>(a.ws + p.g);
   g.piece = p.piece;
-  g.cus = head_cus();
   head_dispatch(p.T, [&](auto c) {
     using C = decltype(c);
     const int mb = cdiv(p.T, C::BM);
-    g.dz_max = head_dz_max(p.T, p.H, C::BM, C::BN);
     for (int i = 0; i < p.npieces; ++i) {
       g.v0 = i * p.piece;
       hipLaunchKernelGGL(k_head_grad<C>, dim3(head_grid(mb, p.piece / C::BN)), dim3(C::NT), 0, s, g);
-      hipLaunchKernelGGL(k_head_targets, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.rows, g.count, a.ids,
-                         p.distill ? reinterpret_cast<const float*>(a.ws + p.lq) : nullptr, a.logp, a.loss, g.r,
-                         a.dloss, a.scale, p.V, p.top, g.v0, p.piece, g.g);
-      const int ndz = head_grid(g.dz_max, 1), ndw = head_grid(p.piece / HeadBig::BM, cdiv(p.H, HeadBig::BN));
+      if (p.distill)
+        hipLaunchKernelGGL(k_head_targets, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.rows, g.count, a.ids,
+                           reinterpret_cast<const float*>(a.ws + p.lq), a.logp, g.info, p.top, g.v0, p.piece, g.g);
+      const int ndz = head_grid(p.dz_max, 1), ndw = head_grid(p.piece / HeadBig::BM, cdiv(p.H, HeadBig::BN));
       if constexpr (C::BM == HeadBig::BM && C::BN == HeadBig::BN) {
         if (a.dw != nullptr) {
           hipLaunchKernelGGL(k_head_dz_dw<C>, dim3(ndz + ndw), dim3(C::NT), 0, s, g, ndz);
@@ -1107,11 +1225,11 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
     }
     const int32_t* cidx = reinterpret_cast<const int32_t*>(a.ws + p.cidx);
     if (p.H <= 8192)
-      hipLaunchKernelGGL(k_head_dh<4>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f, C::BM, C::BN,
+      hipLaunchKernelGGL(k_head_dh<4>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f,
                          a.dh);
     else
-      hipLaunchKernelGGL(k_head_dh<16>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f, C::BM,
-                         C::BN, a.dh);
+      hipLaunchKernelGGL(k_head_dh<16>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f,
+                         a.dh);
   });
 }
 

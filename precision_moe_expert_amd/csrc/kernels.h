@@ -199,8 +199,9 @@ struct HeadPlan {
   int piece, npieces;     // backward: columns of G per piece (multiple of 256), pieces
   // byte offsets into the workspace
   int Hp;                 // H rounded up to the products' K step
-  int bm;                 // rows of a tile
-  size_t r, info, flag, rows, cidx, count, hc, lq, zt, stats, u, g, total;
+  int bm, bn, per_cu;     // rows and columns of a tile, workgroups per CU
+  int dz_max;             // most workgroups of the G W product
+  size_t r, info, gt, flag, rows, cidx, count, hc, lq, zt, stats, u, g, total;
 };
 struct HeadArgs {
   const uint16_t* h;
