@@ -710,6 +710,32 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_head_stats(HeadGemm p) {
   }
 }
 
+// The tile of a wave's accumulators as bf16 rows in LDS, for stores of whole
+// rows: 8 bytes per lane straight to memory would leave 32-byte pieces of 16
+// rows per instruction.
+template <class C>
+struct HeadOut {
+  static constexpr int LS = C::BN * 2 + 16;  // LDS row stride
+  static_assert(C::BM * LS <= C::SMEM, "the tile fits the stage buffers");
+  MOE_DEV static uint8_t* at(uint8_t* smem, int row, int col) { return smem + row * LS + col * 2; }
+  // Rows [0, nrows) and bytes [0, nb) of each (a multiple of 16) to g, gs bytes apart.
+  MOE_DEV static void store(const uint8_t* smem, char* g, int64_t gs, int nrows, int nb) {
+    constexpr int PPR = C::BN / 8, RPI = C::NT / PPR;  // 16-byte pieces per row, rows per step
+    const int r0 = (int)threadIdx.x / PPR, x = (int)threadIdx.x % PPR * 16;
+    if (x >= nb) return;
+    constexpr int G = C::BM / RPI >= 4 ? 4 : 1;
+#pragma unroll 1
+    for (int r = r0; r < C::BM; r += G * RPI) {
+      u32x4 v[G];
+#pragma unroll
+      for (int i = 0; i < G; ++i) v[i] = *reinterpret_cast<const u32x4*>(smem + (r + i * RPI) * LS + x);
+#pragma unroll
+      for (int i = 0; i < G; ++i)
+        if (r + i * RPI < nrows) *reinterpret_cast<u32x4*>(g + (r + i * RPI) * gs + x) = v[i];
+    }
+  }
+};
+
 // Backward: G, columns [v0, v0 + piece), of every row of the tiles (zeros
 // behind the last row and past the vocabulary).
 template <class C>
@@ -736,7 +762,7 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_head_grad(HeadGemm p) {
     constexpr bool ALL = decltype(all)::value;
 #pragma unroll
     for (int i = 0; i < C::MI; ++i) {
-      uint16_t* o = p.g + (int64_t)(m0 + wm + i * 16 + ln) * p.piece + (n0 - p.v0) + wn + lg * 4;
+      uint8_t* o = HeadOut<C>::at(smem, wm + i * 16 + ln, wn + lg * 4);
 #pragma unroll
       for (int j = 0; j < C::NJ; ++j) {
         float x[4];
@@ -745,7 +771,7 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_head_grad(HeadGemm p) {
           x[e] = info[i].f * hl_exp2(fmaf(acc[i][j][e], info[i].f2, -info[i].l2));
           if (!ALL && n0 + wn + j * 16 + lg * 4 + e >= p.V) x[e] = 0.0f;
         }
-        *reinterpret_cast<u32x2*>(o + j * 16) = (u32x2){bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3])};
+        *reinterpret_cast<u32x2*>(o + j * 32) = (u32x2){bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3])};
       }
     }
   };
@@ -756,12 +782,14 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_head_grad(HeadGemm p) {
 #pragma unroll
     for (int i = 0; i < C::MI; ++i) {
       const int tc = info[i].tgt - n0 - wn;
-      if (tc >= 0 && tc < C::NJ * 16 && ((tc >> 2) & 3) == lg) {
-        const int64_t c = m0 + wm + i * 16 + ln;
-        p.g[c * p.piece + (n0 - p.v0) + wn + tc] = (uint16_t)f32_to_bf16_bits(p.gt[c]);
-      }
+      if (tc >= 0 && tc < C::NJ * 16 && ((tc >> 2) & 3) == lg)
+        *reinterpret_cast<uint16_t*>(HeadOut<C>::at(smem, wm + i * 16 + ln, wn + tc)) =
+            (uint16_t)f32_to_bf16_bits(p.gt[m0 + wm + i * 16 + ln]);
     }
   }
+  lds_barrier();
+  HeadOut<C>::store(smem, reinterpret_cast<char*>(p.g + (int64_t)m0 * p.piece + (n0 - p.v0)), (int64_t)p.piece * 2,
+                    C::BM, C::BN * 2);
 }
 
 // u (slab of this workgroup's share of K) += G W over a piece.
@@ -829,17 +857,14 @@ MOE_DEV void head_dw(const HeadGemm& p, int bid, uint8_t* smem) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
   const int wm = wave / C::WN * C::MI * 16, wn = wave % C::WN * C::NJ * 16;
 #pragma unroll
-  for (int i = 0; i < C::MI; ++i) {
-    const int v = m0 + wm + i * 16 + ln;
-    if (v >= M) continue;
+  for (int i = 0; i < C::MI; ++i)
 #pragma unroll
-    for (int j = 0; j < C::NJ; ++j) {
-      const int col = n0 + wn + j * 16 + lg * 4;
-      if (col >= p.H) continue;
-      const u32x2 q = {bf16x2_bits(acc[i][j][0], acc[i][j][1]), bf16x2_bits(acc[i][j][2], acc[i][j][3])};
-      *reinterpret_cast<u32x2*>(p.dw + (int64_t)(p.v0 + v) * p.H + col) = q;
-    }
-  }
+    for (int j = 0; j < C::NJ; ++j)
+      *reinterpret_cast<u32x2*>(HeadOut<C>::at(smem, wm + i * 16 + ln, wn + j * 16 + lg * 4)) =
+          (u32x2){bf16x2_bits(acc[i][j][0], acc[i][j][1]), bf16x2_bits(acc[i][j][2], acc[i][j][3])};
+  lds_barrier();
+  HeadOut<C>::store(smem, reinterpret_cast<char*>(p.dw + (int64_t)(p.v0 + m0) * p.H + n0), (int64_t)p.H * 2, M - m0,
+                    (p.H - n0) * 2);
 }
 
 template <class C>
