@@ -56,21 +56,20 @@ MOE_DEV void hl_merge(float& m, float& s, float m2, float s2) {
 // (added up in order by k_head_dh, so results do not depend on the order of
 // execution).  The number follows from the rows that count, when they are
 // known: the least
-//   rounds of workgroups x (K steps each + HEAD_STEP0) + splits x (steps that
-//   writing and reading a slab costs)
-// where a K step takes about a microsecond, memory moves about 5 MB in that
-// time, and a slab more costs k_head_dh about an eighth of it.
-constexpr int HEAD_STEP0 = 8;
+//   rounds of workgroups x (K steps each x step + over) + splits x (writing and
+//   reading a slab at 5 MB per microsecond, and an eighth of one in k_head_dh)
+// in microseconds, step and over being the tile's (HeadShape).
 constexpr int HEAD_SPLITS = 64;  // one per lane of the wave that chooses
 struct HeadSplit {
   int H, K, bm, bn;  // of the first piece, so every piece adds to the same slabs
   int slots, most;   // workgroups that run at a time; most workgroups
+  float step, over;  // microseconds per K step, and per tile besides
 };
 MOE_DEV int head_splits(const HeadSplit& q, int n, int lane) {
   const int tiles = ((n + q.bm - 1) / q.bm) * ((q.H + q.bn - 1) / q.bn), steps = (q.K + 63) / 64, s = lane + 1;
   float cost = INFINITY;
   if (s == 1 || (tiles * s <= q.most && s <= steps))
-    cost = (float)((tiles * s + q.slots - 1) / q.slots) * (float)((steps + s - 1) / s + HEAD_STEP0) +
+    cost = (float)((tiles * s + q.slots - 1) / q.slots) * ((float)((steps + s - 1) / s) * q.step + q.over) +
            (float)s * ((float)n * (float)q.H * (8.0f / 5e6f) + 0.125f);
   const float least = -hl_max64(-cost);
   return __ffsll(__ballot(cost == least));  // the first of them
@@ -1060,20 +1059,74 @@ __global__ __launch_bounds__(256) void k_head_dh(HeadGemm p, const uint16_t* __r
 
 namespace {
 inline int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-// Tiles by the number of rows.  Up to about 500 rows the products are bound by
-// reading W once (a 256-row tile needs as long for its MFMAs as its share of W
-// takes from memory), so narrow tiles of the vocabulary fill the CUs.
+// The tiles, and what each costs: microseconds per K step of 64 with every CU
+// busy, and per tile besides (start, epilogue), measured from T = 16..1500 over
+// five heads of 512 x 8000 to 7168 x 32000 and 2048 x 128000.
 using HeadBig = HeadTile<256, 256, 2, 4, 2, 2>;
-using Head256 = HeadTile<256, 128, 4, 2, 3, 2>;
-using Head128 = HeadTile<128, 128, 2, 4, 4, 2>;
-using Head64 = HeadTile<64, 128, 1, 8, 3, 4>;
-// f(tile) for at most T rows.
+struct HeadShape {
+  int bm, bn, per_cu;  // per_cu: workgroups a CU holds
+  float step, over;
+};
+constexpr HeadShape kHeadShapes[] = {
+    {256, 256, 1, 1.36f, 7.0f}, {256, 128, 1, 0.78f, 5.0f}, {128, 256, 1, 0.84f, 5.0f},
+    {128, 128, 1, 0.54f, 4.0f}, {64, 128, 2, 0.60f, 3.5f},
+};
+constexpr int kHeadShapeCount = sizeof(kHeadShapes) / sizeof(kHeadShapes[0]);
 template <typename F>
-void head_dispatch(int T, F f) {
-  if (T <= 64) f(Head64());
-  else if (T <= 128) f(Head128());
-  else if (T <= 256) f(Head256());
-  else f(HeadBig());
+void head_dispatch(int shape, F f) {
+  switch (shape) {
+    case 0: f(HeadBig()); break;
+    case 1: f(HeadTile<256, 128, 4, 2, 3, 2>()); break;
+    case 2: f(HeadTile<128, 256, 2, 4, 3, 2>()); break;
+    case 3: f(HeadTile<128, 128, 2, 4, 4, 2>()); break;
+    default: f(HeadTile<64, 128, 2, 2, 3, 2>()); break;
+  }
+}
+// Microseconds of a product of M rows, N columns and K, its K split `splits`
+// ways: rounds of workgroups, each step of which takes the longer of reading its
+// rows of W at 5 MB per microsecond (`width`: times more for narrow tiles of a
+// product that reads W in row pieces) and its MFMAs with a third of that.
+float head_cost(const HeadShape& t, int M, int N, int K, int splits, int cus, float width) {
+  const int64_t nm = (M + t.bm - 1) / t.bm, tiles = nm * ((N + t.bn - 1) / t.bn) * splits;
+  const int64_t slots = (int64_t)cus * t.per_cu, rounds = (tiles + slots - 1) / slots;
+  const int64_t steps = ((K + 63) / 64 + splits - 1) / splits, act = tiles < slots ? tiles : slots;
+  const float mfma = act > cus || t.per_cu == 1 ? t.step : 0.6f * t.step;  // alone on its CU
+  const float mem = (float)act / (float)nm * (float)(t.bn * 128) / 5e6f * (t.bn < 256 ? width : 1.0f);
+  const float both = mfma + 0.35f * mem;
+  return (float)rounds * ((float)steps * (both > mem ? both : mem) + t.over);
+}
+// The cheapest tile for h W^T.  Within 0.3% of the best tile of each of those
+// shapes on average, 10% at most (always 256 x 256: 1.6 times the best at 16
+// rows of 512 x 8000 and 1.7 at 64 rows of 7168 x 32000; always 64 x 128: 2
+// times at 1500 rows).
+int head_tile_logits(int T, int H, int V, int cus) {
+  int best = 0;
+  for (int i = 1; i < kHeadShapeCount; ++i)
+    if (head_cost(kHeadShapes[i], T, V, H, 1, cus, 1.0f) < head_cost(kHeadShapes[best], T, V, H, 1, cus, 1.0f)) best = i;
+  return best;
+}
+// Most workgroups of the G W product: room for a second round's splits.
+int head_dz_max(int T, int H, int bm, int bn) {
+  const int64_t tiles = (int64_t)((T + bm - 1) / bm) * ((H + bn - 1) / bn);
+  return (int)(tiles > 2048 ? tiles : tiles * 2 > 1024 ? tiles * 2 : 1024);
+}
+// The cheapest tile for G W with its best split (2% from the best on average).
+int head_tile_dz(int T, int H, int K, int cus) {
+  int best = 0;
+  float least = -1.0f;
+  for (int i = 0; i < kHeadShapeCount; ++i) {
+    const HeadShape& t = kHeadShapes[i];
+    const int64_t tiles = (int64_t)((T + t.bm - 1) / t.bm) * ((H + t.bn - 1) / t.bn);
+    const int64_t most = head_dz_max(T, H, t.bm, t.bn);
+    for (int s = 1; s <= HEAD_SPLITS && (s == 1 || (tiles * s <= most && s <= (K + 63) / 64)); ++s) {
+      const float c = head_cost(t, T, H, K, s, cus, 1.25f) + (float)s * ((float)T * (float)H * (8.0f / 5e6f) + 0.125f);
+      if (least < 0.0f || c < least) {
+        least = c;
+        best = i;
+      }
+    }
+  }
+  return best;
 }
 // Workgroups for nm x nn tiles (a multiple of the 8 XCDs).
 int head_grid(int64_t nm, int64_t nn) { return cdiv(nm * nn, 8) * 8; }
@@ -1081,11 +1134,6 @@ int head_cus() {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) dev = 0;
   return device_cus(dev);
-}
-// Most workgroups of the G W product: room for a second round's splits.
-int head_dz_max(int T, int H, int bm, int bn) {
-  const int64_t tiles = (int64_t)cdiv(T, bm) * cdiv(H, bn);
-  return (int)(tiles > 2048 ? tiles : tiles * 2 > 1024 ? tiles * 2 : 1024);
 }
 }  // namespace
 
@@ -1105,15 +1153,18 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
   };
   const size_t t = (size_t)T, rows = (t + 255) / 256 * 256;  // whole tiles
   p.Hp = (H + 63) / 64 * 64;
-  int bm = 0, bn = 0;
-  head_dispatch(T, [&](auto c) {
-    bm = decltype(c)::BM;
-    bn = decltype(c)::BN;
-    p.per_cu = decltype(c)::WPS * 4 / decltype(c)::NW;
-  });
-  p.bn = bn;
-  p.dz_max = head_dz_max(T, H, bm, bn);
-  p.bm = bm;
+  const int cus = head_cus();
+  p.tile_l = head_tile_logits(T, H, V, cus);
+  p.bm = kHeadShapes[p.tile_l].bm;
+  if (bwd) {
+    // columns of G per piece: 256 MB of G, at least 256 columns
+    const int64_t most = T > 0 ? ((int64_t)128 << 20) / (int64_t)rows / 256 * 256 : V;
+    p.npieces = cdiv(V, most > 256 ? most : 256);
+    p.piece = cdiv(cdiv(V, p.npieces), 256) * 256;
+    p.npieces = cdiv(V, p.piece);
+    p.tile_z = head_tile_dz(T, H, p.piece < V ? p.piece : V, cus);
+    p.dz_max = head_dz_max(T, H, kHeadShapes[p.tile_z].bm, kHeadShapes[p.tile_z].bn);
+  }
   p.r = take(rows * 4);
   p.info = take(rows * sizeof(HeadRow));
   p.gt = take(bwd && !distill ? t * 4 : 0);
@@ -1125,15 +1176,10 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
   p.lq = take(distill ? t * top * 4 : 0);
   if (!bwd) {
     p.zt = take(t * top * 4);
-    p.stats = take(t * cdiv(V, bn) * 8);
+    p.stats = take(t * cdiv(V, kHeadShapes[p.tile_l].bn) * 8);
   } else {
-    // columns of G per piece: 256 MB of G, at least 256 columns
-    const int64_t most = T > 0 ? ((int64_t)128 << 20) / (int64_t)rows / 256 * 256 : V;
-    p.npieces = cdiv(V, most > 256 ? most : 256);
-    p.piece = cdiv(cdiv(V, p.npieces), 256) * 256;
-    p.npieces = cdiv(V, p.piece);
     // slabs of u: the splits of a tile times the tiles stay below dz_max (or are 1)
-    size_t u = (size_t)p.dz_max * bm * bn;
+    size_t u = (size_t)p.dz_max * kHeadShapes[p.tile_z].bm * kHeadShapes[p.tile_z].bn;
     if (u > t * H * HEAD_SPLITS) u = t * H * HEAD_SPLITS;
     if (u < t * H) u = t * H;
     p.u = take(u * 4);
@@ -1166,7 +1212,9 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
     q.lse = a.lse;
     q.dloss = a.dloss;
   }
-  q.split = HeadSplit{p.H, p.bwd ? (p.piece < p.V ? p.piece : p.V) : 64, p.bm, p.bn, head_cus() * p.per_cu, p.dz_max};
+  const HeadShape& z = kHeadShapes[p.tile_z];
+  q.split = HeadSplit{p.H, p.bwd ? (p.piece < p.V ? p.piece : p.V) : 64, z.bm, z.bn, head_cus() * z.per_cu, p.dz_max,
+                      z.step, z.over};
   q.rows = reinterpret_cast<int32_t*>(ws + p.rows);
   q.cidx = reinterpret_cast<int32_t*>(ws + p.cidx);
   q.count = reinterpret_cast<int32_t*>(ws + p.count);
@@ -1213,7 +1261,7 @@ void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
   g.stats = reinterpret_cast<float*>(a.ws + p.stats);
   g.zt = reinterpret_cast<float*>(a.ws + p.zt);
   int nvb = 0;
-  head_dispatch(p.T, [&](auto c) {
+  head_dispatch(p.tile_l, [&](auto c) {
     using C = decltype(c);
     nvb = cdiv(p.V, C::BN);
     hipLaunchKernelGGL(k_head_stats<C>, dim3(head_grid(cdiv(p.T, C::BM), nvb)), dim3(C::NT), 0, s, g);
@@ -1229,33 +1277,31 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
   g.u = reinterpret_cast<float*>(a.ws + p.u);
   g.g = reinterpret_cast<uint16_t*>(a.ws + p.g);
   g.piece = p.piece;
-  head_dispatch(p.T, [&](auto c) {
-    using C = decltype(c);
-    const int mb = cdiv(p.T, C::BM);
-    for (int i = 0; i < p.npieces; ++i) {
-      g.v0 = i * p.piece;
-      hipLaunchKernelGGL(k_head_grad<C>, dim3(head_grid(mb, p.piece / C::BN)), dim3(C::NT), 0, s, g);
-      if (p.distill)
-        hipLaunchKernelGGL(k_head_targets, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.rows, g.count, a.ids,
-                           reinterpret_cast<const float*>(a.ws + p.lq), a.logp, g.info, p.top, g.v0, p.piece, g.g);
-      const int ndz = head_grid(p.dz_max, 1), ndw = head_grid(p.piece / HeadBig::BM, cdiv(p.H, HeadBig::BN));
-      if constexpr (C::BM == HeadBig::BM && C::BN == HeadBig::BN) {
-        if (a.dw != nullptr) {
-          hipLaunchKernelGGL(k_head_dz_dw<C>, dim3(ndz + ndw), dim3(C::NT), 0, s, g, ndz);
-          continue;
-        }
-      }
-      hipLaunchKernelGGL(k_head_dz<C>, dim3(ndz), dim3(C::NT), 0, s, g);
-      if (a.dw != nullptr) hipLaunchKernelGGL(k_head_dw<HeadBig>, dim3(ndw), dim3(HeadBig::NT), 0, s, g);
+  const int ndz = head_grid(p.dz_max, 1), ndw = head_grid(cdiv(p.piece, HeadBig::BM), cdiv(p.H, HeadBig::BN));
+  for (int i = 0; i < p.npieces; ++i) {
+    g.v0 = i * p.piece;
+    head_dispatch(p.tile_l, [&](auto c) {
+      using C = decltype(c);
+      hipLaunchKernelGGL(k_head_grad<C>, dim3(head_grid(cdiv(p.T, C::BM), p.piece / C::BN)), dim3(C::NT), 0, s, g);
+    });
+    if (p.distill)
+      hipLaunchKernelGGL(k_head_targets, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.rows, g.count, a.ids,
+                         reinterpret_cast<const float*>(a.ws + p.lq), a.logp, g.info, p.top, g.v0, p.piece, g.g);
+    if (a.dw != nullptr && p.tile_z == 0) {
+      hipLaunchKernelGGL(k_head_dz_dw<HeadBig>, dim3(ndz + ndw), dim3(HeadBig::NT), 0, s, g, ndz);
+      continue;
     }
-    const int32_t* cidx = reinterpret_cast<const int32_t*>(a.ws + p.cidx);
-    if (p.H <= 8192)
-      hipLaunchKernelGGL(k_head_dh<4>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f,
-                         a.dh);
-    else
-      hipLaunchKernelGGL(k_head_dh<16>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f,
-                         a.dh);
-  });
+    head_dispatch(p.tile_z, [&](auto c) {
+      using C = decltype(c);
+      hipLaunchKernelGGL(k_head_dz<C>, dim3(ndz), dim3(C::NT), 0, s, g);
+    });
+    if (a.dw != nullptr) hipLaunchKernelGGL(k_head_dw<HeadBig>, dim3(ndw), dim3(HeadBig::NT), 0, s, g);
+  }
+  const int32_t* cidx = reinterpret_cast<const int32_t*>(a.ws + p.cidx);
+  if (p.H <= 8192)
+    hipLaunchKernelGGL(k_head_dh<4>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f, a.dh);
+  else
+    hipLaunchKernelGGL(k_head_dh<16>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f, a.dh);
 }
 
 }  // namespace moe

@@ -199,7 +199,8 @@ struct HeadPlan {
   int piece, npieces;     // backward: columns of G per piece (multiple of 256), pieces
   // byte offsets into the workspace
   int Hp;                 // H rounded up to the products' K step
-  int bm, bn, per_cu;     // rows and columns of a tile, workgroups per CU
+  int tile_l, tile_z;     // tiles of h W^T and of G W
+  int bm;                 // rows of the former
   int dz_max;             // most workgroups of the G W product
   size_t r, info, gt, flag, rows, cidx, count, hc, lq, zt, stats, u, g, total;
 };
