@@ -392,8 +392,8 @@ typedef struct {
  * Returns 0 for an invalid or unsupported descriptor.  The logits are never
  * held: the forward keeps two floats per token and block of vocabulary rows,
  * the backward the scaled softmax gradient (bf16) of one piece of the
- * vocabulary at a time (at most about 256 MB, or 256 columns where more
- * tokens need more), and dL/dz [T][H] fp32. */
+ * vocabulary at a time (at most about 512 MB, or 256 columns where more
+ * tokens need more), and partial sums of dL/dz (fp32, up to 64 [T][H]). */
 size_t moe_lm_head_loss_workspace_bytes(const moe_lm_head* head, int32_t top, int32_t backward);
 
 /* Cross entropy of target ids: lse[t] = log sum_v exp(logits[t][v]),

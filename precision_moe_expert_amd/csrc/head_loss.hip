@@ -973,7 +973,82 @@ __global__ __launch_bounds__(256) void k_head_targets(const int32_t* __restrict_
 }
 
 // d_h = u - r^2 h mean(h u), or u without a norm, u the sum of its slabs;
-// zeros for tokens that do not count.  One block per token; a thread keeps its
+// zeros for tokens that do not count.  For H <= 2048, where u has the most
+// slabs: one block per token, its 256 threads in groups of P = the power of two
+// at or above H / 8, each of which adds every (256 / P)-th slab; the groups' sums
+// are added in order.
+__global__ __launch_bounds__(256) void k_head_dh_narrow(HeadGemm p, const uint16_t* __restrict__ h, int64_t h_stride,
+                                                        const int32_t* __restrict__ cidx, bool norm, int P,
+                                                        uint16_t* __restrict__ dh) {
+  __shared__ __align__(16) f32x4 sum[2][256];
+  __shared__ float part[4];
+  const int t = blockIdx.x, c = cidx[t], H = p.H, np = H / 8, tid = threadIdx.x;
+  const int i = tid & (P - 1), g = tid / P, groups = 256 / P;
+  uint16_t* o = dh + (int64_t)t * H + i * 8;
+  if (c < 0) {
+    if (g == 0 && i < np) *reinterpret_cast<u32x4*>(o) = (u32x4){0, 0, 0, 0};
+    return;
+  }
+  const int splits = p.count[1];
+  const int64_t slab = (int64_t)p.count[0] * H;
+  const float* us = p.u + (int64_t)c * H + i * 8;
+  u32x4 q = {0, 0, 0, 0};
+  if (norm && i < np) q = *reinterpret_cast<const u32x4*>(h + (int64_t)t * h_stride + i * 8);
+  f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
+  if (i < np) {
+    int s = g;
+    for (; s + 3 * groups < splits; s += 4 * groups) {  // four slabs' loads in flight
+      f32x4 x[4], y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = *reinterpret_cast<const f32x4*>(us + (s + j * groups) * slab);
+        y[j] = *reinterpret_cast<const f32x4*>(us + (s + j * groups) * slab + 4);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a += x[j];
+        b += y[j];
+      }
+    }
+    for (; s < splits; s += groups) {
+      a += *reinterpret_cast<const f32x4*>(us + s * slab);
+      b += *reinterpret_cast<const f32x4*>(us + s * slab + 4);
+    }
+  }
+  if (groups > 1) {
+    sum[0][tid] = a;
+    sum[1][tid] = b;
+    __syncthreads();
+    for (int k = 1; k < groups; ++k) {
+      a = k == 1 ? sum[0][i] + sum[0][P + i] : a + sum[0][k * P + i];
+      b = k == 1 ? sum[1][i] + sum[1][P + i] : b + sum[1][k * P + i];
+    }
+  }
+  float f = 0.0f;
+  if (norm) {
+    float dot = 0.0f;
+    if (g == 0)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        dot = fmaf(j < 2 ? a[2 * j] : b[2 * j - 4], bf16_bits_to_f32(q[j] & 0xFFFFu), dot);
+        dot = fmaf(j < 2 ? a[2 * j + 1] : b[2 * j - 3], bf16_bits_to_f32(q[j] >> 16), dot);
+      }
+    dot = hl_sum64(dot);
+    if ((tid & 63) == 0) part[tid >> 6] = dot;
+    __syncthreads();
+    f = p.r[c] * p.r[c] * ((part[0] + part[1]) + (part[2] + part[3])) / (float)H;
+  }
+  if (g != 0 || i >= np) return;
+  u32x4 x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float lo = j < 2 ? a[2 * j] : b[2 * j - 4], hi = j < 2 ? a[2 * j + 1] : b[2 * j - 3];
+    x[j] = bf16x2_bits(fmaf(-f, bf16_bits_to_f32(q[j] & 0xFFFFu), lo), fmaf(-f, bf16_bits_to_f32(q[j] >> 16), hi));
+  }
+  *reinterpret_cast<u32x4*>(o) = x;
+}
+
+// The same for wider h: one block per token, a thread keeps its
 // NP pieces of 8 columns of u and h in registers between the sum and the
 // result (NP = 4: H <= 8192, 16: any).
 template <int NP>
@@ -1157,8 +1232,10 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
   p.tile_l = head_tile_logits(T, H, V, cus);
   p.bm = kHeadShapes[p.tile_l].bm;
   if (bwd) {
-    // columns of G per piece: 256 MB of G, at least 256 columns
-    const int64_t most = T > 0 ? ((int64_t)128 << 20) / (int64_t)rows / 256 * 256 : V;
+    // columns of G per piece: 512 MB of G, at least 256 columns (256 MB, which
+    // the last-level cache would hold: 2% slower at 8192 x 7168 x 32000 and 14%
+    // at 8192 x 512 x 128000, where every piece reads and writes u again)
+    const int64_t most = T > 0 ? ((int64_t)256 << 20) / (int64_t)rows / 256 * 256 : V;
     p.npieces = cdiv(V, most > 256 ? most : 256);
     p.piece = cdiv(cdiv(V, p.npieces), 256) * 256;
     p.npieces = cdiv(V, p.piece);
@@ -1298,7 +1375,11 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
     if (a.dw != nullptr) hipLaunchKernelGGL(k_head_dw<HeadBig>, dim3(ndw), dim3(HeadBig::NT), 0, s, g);
   }
   const int32_t* cidx = reinterpret_cast<const int32_t*>(a.ws + p.cidx);
-  if (p.H <= 8192)
+  if (p.H <= 2048) {
+    int P = 8;
+    while (P < p.H / 8) P *= 2;
+    hipLaunchKernelGGL(k_head_dh_narrow, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f, P, a.dh);
+  } else if (p.H <= 8192)
     hipLaunchKernelGGL(k_head_dh<4>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f, a.dh);
   else
     hipLaunchKernelGGL(k_head_dh<16>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f, a.dh);

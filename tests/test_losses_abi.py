@@ -82,7 +82,7 @@ def test_head_workspace_is_bounded():
     for T in (1, 64, 8192, 65536):
         for V in (1000, 32000, 1 << 20):
             nb = binding.lm_head_loss_workspace_bytes(T, 2048, V, backward=True)
-            assert nb <= T * 2048 * 4 * 32 + max(300 << 20, T * 512) + T * 64 + (1 << 20), (T, V)
+            assert nb <= T * 2048 * 4 * 64 + max(512 << 20, (T + 256) * 512) + (T + 256) * 2048 * 2 + T * 64 + (1 << 20)
 
 
 def test_teacher_arguments():
