@@ -77,41 +77,48 @@ MOE_DEV int head_splits(const HeadSplit& q, int n, int lane) {
 
 // ---- which tokens count -----------------------------------------------------
 
-// Distillation, one wave per token: the log of the teacher's probabilities
-// (-infinity for slots that are not there) and whether there is any.
-__global__ __launch_bounds__(256) void k_head_teacher(const int32_t* __restrict__ ids, const float* __restrict__ tlogits,
-                                                      int T, int V, int top, float tscale, float* __restrict__ lq,
-                                                      uint8_t* __restrict__ flag) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (t >= T) return;
-  float x[4], m = -INFINITY;
-  bool have[4], any = false;
+// One wave, one token's slots: the log of the teacher's probabilities of slots
+// lane, lane + 64, ... (-infinity for those that are not there); whether any is.
+MOE_DEV bool head_teacher(const int32_t* __restrict__ ids, const float* __restrict__ tlogits, int V, int top,
+                          float tscale, int lane, float (&lq)[4]) {
+  float m = -INFINITY;
+  bool any = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int j = i * 64 + lane;
-    have[i] = false;
-    x[i] = -INFINITY;
+    lq[i] = -INFINITY;
     if (j < top) {
-      const int id = ids[(int64_t)t * top + j];
-      if (id >= 0 && id < V) {
-        x[i] = tlogits[(int64_t)t * top + j];
-        have[i] = !(x[i] == -INFINITY);
-        x[i] *= tscale;
-      }
+      const int id = ids[j];
+      if (id >= 0 && id < V) lq[i] = tlogits[j] * tscale;  // tscale > 0 keeps -infinity
     }
-    any |= have[i];
-    if (have[i]) m = fmaxf(m, x[i]);
+    const bool have = !(lq[i] == -INFINITY);
+    any |= have;
+    if (have) m = fmaxf(m, lq[i]);
   }
   m = hl_max64(m);
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (have[i]) s += expf(x[i] - m);
+    if (!(lq[i] == -INFINITY)) s += expf(lq[i] - m);
   const float ls = logf(hl_sum64(s));
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (i * 64 + lane < top) lq[(int64_t)t * top + i * 64 + lane] = have[i] ? x[i] - m - ls : -INFINITY;
-  const bool counts = __any(any);
+    if (!(lq[i] == -INFINITY)) lq[i] = lq[i] - m - ls;
+  return __any(any);
+}
+
+// Distillation, more than HEAD_SAME tokens, one wave each: lq and flag.
+__global__ __launch_bounds__(256) void k_head_teacher(const int32_t* __restrict__ ids, const float* __restrict__ tlogits,
+                                                      int T, int V, int top, float tscale, float* __restrict__ lq,
+                                                      uint8_t* __restrict__ flag) {
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (t >= T) return;
+  float q[4];
+  const bool counts =
+      head_teacher(ids + (int64_t)t * top, tlogits + (int64_t)t * top, V, top, tscale, lane, q);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i * 64 + lane < top) lq[(int64_t)t * top + i * 64 + lane] = q[i];
   if (lane == 0) flag[t] = counts;
 }
 
@@ -456,8 +463,12 @@ struct HeadTile {
   static constexpr int NW = WM * WN, NT = NW * 64;
 };
 
-template <class C, bool KMA, bool KMB>
-MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[C::MI][C::NJ], uint8_t* smem) {
+// SQ (64 rows of A, 256 threads): also sums into *ss the squares of the 16
+// values that thread t sees per stage of row t / 4 of A.
+template <class C, bool KMA, bool KMB, bool SQ = false>
+MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[C::MI][C::NJ], uint8_t* smem,
+                     float* ss = nullptr) {
+  static_assert(!SQ || (!KMA && C::BM == 64 && C::NT == 256 && !C::FIVE), "rows per thread");
   using OA = HeadOperand<C::BM, KMA, C::NW>;
   using OB = HeadOperand<C::BN, KMB, C::NW>;
   constexpr int S = C::S, MI = C::MI, NJ = C::NJ, NPER = OA::ND + OB::ND;
@@ -531,6 +542,20 @@ MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[
     constexpr int ISSUE = decltype(issue)::value;
     const int nslot = next(slot);
     using Last = std::integral_constant<bool, ISSUE == 2>;
+    if (SQ) {
+      const int row = threadIdx.x >> 2, part = (threadIdx.x & 3) * 2;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const u32x4 q = *reinterpret_cast<const u32x4*>(smem + off_a(slot) + row * 128 +
+                                                        (((part + j) ^ ((row >> 1) & 7)) << 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a = bf16_bits_to_f32(q[e] & 0xFFFFu), b = bf16_bits_to_f32(q[e] >> 16);
+          *ss = fmaf(a, a, *ss);
+          *ss = fmaf(b, b, *ss);
+        }
+      }
+    }
     phase(X0(), slot, 1, [&](int i) {
       if (C::FIVE && ISSUE) {
 #pragma unroll
@@ -578,6 +603,10 @@ MOE_DEV bool head_tile(int bid, int nm, int nn, int& m, int& n) {
 }
 
 struct HeadGemm {
+  const uint16_t* h;      // direct forward: the rows as they are, T of them
+  int64_t h_stride;
+  int T;
+  float eps;
   const uint16_t* hc;     // [..][Hp]
   const uint16_t* w;
   int64_t w_stride;
@@ -600,8 +629,10 @@ struct HeadGemm {
 
 // Forward: per row and block of BN columns the maximum of y = l log2 e and the
 // sum of 2^(y - maximum), and the logits at the target's ids (the tile goes
-// through LDS for those).
-template <class C>
+// through LDS for those).  DIRECT: for up to 64 rows of a width that is a
+// multiple of 64 the rows are read where they are and their 1/rms is formed
+// from the staged pieces, so nothing has to be launched before this.
+template <class C, bool DIRECT>
 __global__ __launch_bounds__(C::NT, C::WPS) void k_head_stats(HeadGemm p) {
   static_assert(C::NT % C::BM == 0 || C::NT % (C::BM / C::WM) == 0, "rows per thread");
   constexpr int RED = C::WN * C::BM * 4;  // bytes of the rows' maxima, and of their sums
@@ -612,21 +643,38 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_head_stats(HeadGemm p) {
   __shared__ __align__(16) uint8_t smem[SMEM];
   float(*rm)[C::BM] = reinterpret_cast<float(*)[C::BM]>(smem + ZB);
   float(*rs)[C::BM] = reinterpret_cast<float(*)[C::BM]>(smem + ZB + RED);
-  const int n = *p.count, nvb = (p.V + C::BN - 1) / C::BN;
+  const int n = DIRECT ? p.T : *p.count, nvb = (p.V + C::BN - 1) / C::BN;
   int mt, nt;
   if (!head_tile(blockIdx.x, (n + C::BM - 1) / C::BM, nvb, mt, nt)) return;
   const int m0 = mt * C::BM, n0 = nt * C::BN;
-  const HeadSrc sa = {reinterpret_cast<const char*>(p.hc + (int64_t)m0 * p.Hp), (uint32_t)p.Hp * 2, C::BM, p.Hp};
+  HeadSrc sa = {reinterpret_cast<const char*>(p.hc + (int64_t)m0 * p.Hp), (uint32_t)p.Hp * 2, C::BM, p.Hp};
+  if (DIRECT) sa = HeadSrc{reinterpret_cast<const char*>(p.h), (uint32_t)p.h_stride * 2, n, p.H};
   const HeadSrc sb = {reinterpret_cast<const char*>(p.w + (int64_t)n0 * p.w_stride), (uint32_t)p.w_stride * 2,
                       p.V - n0, p.H};
   f32x4 acc[C::MI][C::NJ];
-  head_mm<C, false, false>(sa, sb, p.Hp / 64, acc, smem);
+  float ss = 0.0f;
+  head_mm<C, false, false, DIRECT>(sa, sb, p.Hp / 64, acc, smem, &ss);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
   const int wm = wave / C::WN * C::MI * 16, wn = wave % C::WN * C::NJ * 16;
   const bool full = n0 + C::BN <= p.V;  // uniform: no column of the tile is past the vocabulary
   HeadRow info[C::MI];
+  if (DIRECT) {
+    ss += shfl_xor(ss, 1);
+    ss += shfl_xor(ss, 2);
+    float* rr = reinterpret_cast<float*>(smem);
+    if ((threadIdx.x & 3) == 0) rr[threadIdx.x >> 2] = p.eps > 0.0f ? 1.0f / sqrtf(ss / (float)p.H + p.eps) : 1.0f;
+    lds_barrier();
 #pragma unroll
-  for (int i = 0; i < C::MI; ++i) info[i] = p.info[m0 + wm + i * 16 + ln];
+    for (int i = 0; i < C::MI; ++i) {
+      const int row = wm + i * 16 + ln;
+      const float f = p.scale * rr[row];
+      info[i] = HeadRow{f * kLog2e, f, 0.0f, p.distill || row >= n ? -1 : p.ids[row]};
+    }
+    lds_barrier();
+  } else {
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i) info[i] = p.info[m0 + wm + i * 16 + ln];
+  }
   auto rows_stats = [&](auto all) {
     constexpr bool ALL = decltype(all)::value;
 #pragma unroll
@@ -689,7 +737,7 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_head_stats(HeadGemm p) {
       constexpr int TPR = C::NT / ZR > 0 ? C::NT / ZR : 1;
       const int row = z0 + (int)threadIdx.x / TPR, c = m0 + row;
       if (threadIdx.x < ZR * TPR && c < n) {
-        const int32_t* id = p.ids + (int64_t)p.rows[c] * p.top;
+        const int32_t* id = p.ids + (int64_t)(DIRECT ? c : p.rows[c]) * p.top;
         for (int k = threadIdx.x % TPR; k < p.top; k += TPR) {
           const int v = id[k] - n0;
           if (v >= 0 && v < C::BN && n0 + v < p.V)
@@ -886,27 +934,55 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_head_dz_dw(HeadGemm p, int nd
 }
 
 // Per token (one wave): joins its blocks' statistics and forms the outputs.
-__global__ __launch_bounds__(256) void k_head_finish(const float* __restrict__ stats, const float* __restrict__ zt,
-                                                     const int32_t* __restrict__ cidx,
-                                                     const int32_t* __restrict__ ids, const float* __restrict__ lq,
-                                                     int T, int V, int nvb, int top, bool distill,
-                                                     float* __restrict__ loss, float* __restrict__ lse,
-                                                     float* __restrict__ logp) {
+// DIRECT: row t is token t, and whether it counts and the teacher's
+// probabilities are found here.
+struct HeadFinish {
+  const float* stats;
+  const float* zt;
+  const int32_t* cidx;
+  const int32_t* ids;
+  const float* lq;
+  const float* tlogits;
+  float tscale;
+  int T, V, nvb, top;
+  float* loss;
+  float* lse;
+  float* logp;  // null: cross entropy
+};
+template <bool DIRECT>
+__global__ __launch_bounds__(256) void k_head_finish(HeadFinish p) {
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (t >= T) return;
-  const int c = cidx[t];
+  if (t >= p.T) return;
+  const bool distill = p.logp != nullptr;
+  float lq[4];  // of slots lane, lane + 64, ...
+  int c = t;
+  if (DIRECT) {
+    if (distill) {
+      c = head_teacher(p.ids + (int64_t)t * p.top, p.tlogits + (int64_t)t * p.top, p.V, p.top, p.tscale, lane, lq) ? t
+                                                                                                                  : -1;
+    } else {
+      const int y = p.ids[t];
+      c = y >= 0 && y < p.V ? t : -1;
+    }
+  } else {
+    c = p.cidx[t];
+    if (distill)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        lq[i] = i * 64 + lane < p.top ? p.lq[(int64_t)t * p.top + i * 64 + lane] : -INFINITY;
+  }
   if (c < 0) {
     if (distill)
-      for (int j = lane; j < top; j += 64) logp[(int64_t)t * top + j] = 0.0f;
+      for (int j = lane; j < p.top; j += 64) p.logp[(int64_t)t * p.top + j] = 0.0f;
     if (lane == 0) {
-      loss[t] = !distill && ids[t] >= V ? __builtin_nanf("") : 0.0f;
-      lse[t] = 0.0f;
+      p.loss[t] = !distill && p.ids[t] >= p.V ? __builtin_nanf("") : 0.0f;
+      p.lse[t] = 0.0f;
     }
     return;
   }
   float m = -INFINITY, s = 0.0f;
-  for (int b = lane; b < nvb; b += 64) {
-    const float* o = stats + ((int64_t)c * nvb + b) * 2;
+  for (int b = lane; b < p.nvb; b += 64) {
+    const float* o = p.stats + ((int64_t)c * p.nvb + b) * 2;
     hl_merge(m, s, o[0], o[1]);
   }
 #pragma unroll
@@ -918,21 +994,23 @@ __global__ __launch_bounds__(256) void k_head_finish(const float* __restrict__ s
   float kl;
   if (distill) {
     kl = 0.0f;
-    for (int j = lane; j < top; j += 64) {
-      const int64_t at = (int64_t)t * top + j;
-      const float q = lq[at];
-      const bool have = !(q == -INFINITY);
-      const float lp = have ? zt[(int64_t)c * top + j] - l : 0.0f;
-      logp[at] = lp;
-      if (have) kl = fmaf(expf(q), q - lp, kl);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = i * 64 + lane;
+      if (j < p.top) {
+        const bool have = !(lq[i] == -INFINITY);
+        const float lp = have ? p.zt[(int64_t)c * p.top + j] - l : 0.0f;
+        p.logp[(int64_t)t * p.top + j] = lp;
+        if (have) kl = fmaf(expf(lq[i]), lq[i] - lp, kl);
+      }
     }
     kl = hl_sum64(kl);
   } else {
-    kl = l - zt[c];
+    kl = l - p.zt[c];
   }
   if (lane == 0) {
-    loss[t] = kl;
-    lse[t] = l;
+    p.loss[t] = kl;
+    p.lse[t] = l;
   }
 }
 
@@ -1334,19 +1412,48 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
 }
 
 void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
-  HeadGemm g = head_common(p, a, s);
+  using Direct = HeadTile<64, 128, 2, 2, 3, 2>;
+  const bool direct = p.T <= Direct::BM && p.bm == Direct::BM && p.H % 64 == 0;
+  HeadGemm g = direct ? HeadGemm{} : head_common(p, a, s);
+  g.h = a.h;
+  g.h_stride = a.h_stride;
+  g.T = p.T;
+  g.eps = a.eps;
+  g.w = a.w;
+  g.w_stride = a.w_stride;
+  g.H = p.H;
+  g.Hp = p.Hp;
+  g.V = p.V;
+  g.top = p.top;
+  g.scale = a.scale;
+  g.ids = a.ids;
+  g.distill = p.distill;
   g.stats = reinterpret_cast<float*>(a.ws + p.stats);
   g.zt = reinterpret_cast<float*>(a.ws + p.zt);
-  int nvb = 0;
+  HeadFinish f{g.stats,
+               g.zt,
+               reinterpret_cast<const int32_t*>(a.ws + p.cidx),
+               a.ids,
+               reinterpret_cast<const float*>(a.ws + p.lq),
+               a.tlogits,
+               a.teacher_scale,
+               p.T,
+               p.V,
+               cdiv(p.V, kHeadShapes[p.tile_l].bn),
+               p.top,
+               a.loss,
+               a.lse,
+               a.logp};
+  if (direct) {
+    hipLaunchKernelGGL((k_head_stats<Direct, true>), dim3(head_grid(1, f.nvb)), dim3(Direct::NT), 0, s, g);
+    hipLaunchKernelGGL(k_head_finish<true>, dim3(cdiv(p.T, 4)), dim3(256), 0, s, f);
+    return;
+  }
   head_dispatch(p.tile_l, [&](auto c) {
     using C = decltype(c);
-    nvb = cdiv(p.V, C::BN);
-    hipLaunchKernelGGL(k_head_stats<C>, dim3(head_grid(cdiv(p.T, C::BM), nvb)), dim3(C::NT), 0, s, g);
+    hipLaunchKernelGGL((k_head_stats<C, false>), dim3(head_grid(cdiv(p.T, C::BM), f.nvb)), dim3(C::NT), 0, s, g);
   });
-  hipLaunchKernelGGL(k_head_finish, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.stats, g.zt,
-                     reinterpret_cast<const int32_t*>(a.ws + p.cidx), a.ids,
-                     reinterpret_cast<const float*>(a.ws + p.lq), p.T, p.V, nvb, p.top, p.distill, a.loss, a.lse,
-                     a.logp);
+  hipLaunchKernelGGL(k_head_finish<false>, dim3(cdiv(p.T, 4)), dim3(256), 0, s, f);
 }
 
 void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
