@@ -8,7 +8,12 @@
 //             but those
 //   backward  per piece of the vocabulary l again, G = s r g exp(l - lse) in
 //             bf16, its entries at the target's ids replaced by
-//             s r g (p - q); then u += G W (dL/dz r) and d_W = G^T h
+//             s r g (p - q); then u += G W (dL/dz r) and d_W = G^T h.  One such
+//             entry is as large as the rest of its row together, so its bf16
+//             rounding (up to 2^-8) would be the gradient's where few rows
+//             count.  Where these entries are not many they are therefore kept
+//             in fp32 beside a G that is 0 there; entry x row of W is added to
+//             u, and entry x row of h to d_W
 // with r = 1 / sqrt(mean h^2 + eps), s the logit scale and g = dL/dloss.
 // r s multiplies the fp32 accumulators: the products' operands are the bf16
 // inputs themselves, and G is the one value that is rounded on the way.
@@ -208,7 +213,9 @@ struct HeadRowsArgs {
   uint16_t* hc;
   float* r;
   HeadRow* info;
-  float* gt;             // backward, cross entropy: G at the row's target
+  int32_t* eid;          // backward, cross entropy: the row's target (-1: none) and G there
+  float* ev;
+  int32_t* uses;         // entries of each id, null: not counted
   float* lq;
 };
 
@@ -320,7 +327,10 @@ __global__ __launch_bounds__(256) void k_head_gather(HeadRowsArgs p) {
     }
   }
   if (!live) {
-    if (tid == 0) p.info[c] = HeadRow{0.0f, 0.0f, 0.0f, -1};
+    if (tid == 0) {
+      p.info[c] = HeadRow{0.0f, 0.0f, 0.0f, -1};
+      if (p.loss != nullptr && c < n) p.eid[c] = -1;
+    }
     return;
   }
   ss = hl_sum64(ss);
@@ -336,7 +346,11 @@ __global__ __launch_bounds__(256) void k_head_gather(HeadRowsArgs p) {
     if (p.dloss != nullptr) {
       w.f = f * p.dloss[t];
       w.l2 = p.lse[t] * kLog2e;
-      if (p.loss != nullptr) p.gt[c] = w.f * expm1f(-p.loss[t]);  // p - 1 = exp(-loss) - 1
+      if (p.loss != nullptr) {
+        p.eid[c] = w.tgt;
+        p.ev[c] = w.f * expm1f(-p.loss[t]);  // p - 1 = exp(-loss) - 1
+        if (p.uses != nullptr) atomicAdd(&p.uses[w.tgt], 1);
+      }
     }
     p.info[c] = w;
   }
@@ -614,7 +628,10 @@ struct HeadGemm {
   const int32_t* rows;
   const int32_t* count;   // rows, splits of G W
   const float* r;         // [count]
-  const float* gt;        // [count], cross entropy: G at the row's target
+  int32_t* eid;           // [count][top] G's entries at the target's ids: id (-1: none),
+  float* ev;              //   value (distillation: exact only)
+  bool exact;             // they are kept apart from G
+  int32_t* uses;          // [V] entries of each id, null: not counted
   const HeadRow* info;    // [..]
   float scale;
   const int32_t* ids;
@@ -825,13 +842,14 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_head_grad(HeadGemm p) {
   if (full) write(std::true_type());
   else write(std::false_type());
   if (!p.distill) {
-    // the lane that wrote a row's target puts s r g (p - 1) over it
+    // the lane that wrote a row's target puts s r g (p - 1) over it, or 0 where
+    // such entries are kept apart
 #pragma unroll
     for (int i = 0; i < C::MI; ++i) {
       const int tc = info[i].tgt - n0 - wn;
       if (tc >= 0 && tc < C::NJ * 16 && ((tc >> 2) & 3) == lg)
         *reinterpret_cast<uint16_t*>(HeadOut<C>::at(smem, wm + i * 16 + ln, wn + tc)) =
-            (uint16_t)f32_to_bf16_bits(p.gt[m0 + wm + i * 16 + ln]);
+            p.exact ? 0 : (uint16_t)f32_to_bf16_bits(p.ev[m0 + wm + i * 16 + ln]);
     }
   }
   lds_barrier();
@@ -1014,13 +1032,17 @@ __global__ __launch_bounds__(256) void k_head_finish(HeadFinish p) {
   }
 }
 
-// Distillation's backward: G at the slots' ids in [v0, v0 + piece), from the
-// forward's log-probs: s r g (p - q), one wave per row.  Slots that repeat an
-// id add their q, and the first of them writes.
+// Distillation's backward: the entries s r g (p - q) at the slots' ids, from
+// the forward's log-probs, one wave per row.  Slots that repeat an id add their
+// q, and the first of them is the entry.  ev null: into G's columns [v0, v0 +
+// piece); else 0 goes there, and with the first piece the entries to ev and
+// their ids to eid.
 __global__ __launch_bounds__(256) void k_head_targets(const int32_t* __restrict__ rows, const int32_t* __restrict__ count,
                                                       const int32_t* __restrict__ ids, const float* __restrict__ lq,
                                                       const float* __restrict__ logp, const HeadRow* __restrict__ info,
-                                                      int top, int v0, int piece, uint16_t* __restrict__ g) {
+                                                      int top, int v0, int piece, uint16_t* __restrict__ g,
+                                                      int32_t* __restrict__ eid, float* __restrict__ ev,
+                                                      int32_t* __restrict__ uses) {
   __shared__ int sid[4][256];
   __shared__ float sq[4][256];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -1038,16 +1060,130 @@ __global__ __launch_bounds__(256) void k_head_targets(const int32_t* __restrict_
   __builtin_amdgcn_wave_barrier();
   for (int j = lane; j < top; j += 64) {
     const int id = sid[wave][j], v = id - v0;
-    if (id < 0 || v < 0 || v >= piece) continue;
+    const bool here = id >= 0 && v >= 0 && v < piece;
+    if (!here && (ev == nullptr || v0 != 0)) continue;
     float q = 0.0f;
-    bool first = true;
+    bool first = id >= 0;
     for (int i = 0; i < top; ++i)
       if (sid[wave][i] == id) {
         q += sq[wave][i];
         if (i < j) first = false;
       }
-    if (first) g[(int64_t)c * piece + v] = (uint16_t)f32_to_bf16_bits(cf * (expf(logp[(int64_t)t * top + j]) - q));
+    const float x = first ? cf * (expf(logp[(int64_t)t * top + j]) - q) : 0.0f;
+    if (ev != nullptr && v0 == 0) {
+      eid[(int64_t)c * top + j] = first ? id : -1;
+      ev[(int64_t)c * top + j] = x;
+      if (first && uses != nullptr) atomicAdd(&uses[id], 1);
+    }
+    if (here && first) g[(int64_t)c * piece + v] = ev != nullptr ? 0 : (uint16_t)f32_to_bf16_bits(x);
   }
+}
+
+// Adds row c's fp32 entries [first, top) in steps of `step` times their rows of
+// W, 8 columns from col, to a and b; four rows' loads in flight.
+MOE_DEV void head_add_entries(const HeadGemm& p, int c, int first, int step, int col, f32x4& a, f32x4& b) {
+  const int32_t* id = p.eid + (int64_t)c * p.top;
+  const float* ev = p.ev + (int64_t)c * p.top;
+  for (int k = first; k < p.top; k += 4 * step) {
+    u32x4 w[4];
+    float x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = k + j * step, v = at < p.top ? id[at] : -1;
+      x[j] = v >= 0 ? ev[at] : 0.0f;
+      w[j] = (u32x4){0, 0, 0, 0};
+      if (v >= 0) w[j] = *reinterpret_cast<const u32x4*>(p.w + (int64_t)v * p.w_stride + col);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        a[2 * e] = fmaf(x[j], bf16_bits_to_f32(w[j][e] & 0xFFFFu), a[2 * e]);
+        a[2 * e + 1] = fmaf(x[j], bf16_bits_to_f32(w[j][e] >> 16), a[2 * e + 1]);
+        b[2 * e] = fmaf(x[j], bf16_bits_to_f32(w[j][e + 2] & 0xFFFFu), b[2 * e]);
+        b[2 * e + 1] = fmaf(x[j], bf16_bits_to_f32(w[j][e + 2] >> 16), b[2 * e + 1]);
+      }
+  }
+}
+
+// d_w rows at the ids of fp32 entries: += entry x row of h.  Block (e, j): entry
+// e and its columns 2048 j ..; the first entry of an id adds all of that id, in
+// their order, so results do not depend on the execution; the others' blocks
+// end.  Where there are many entries, uses[id] (how many have it) spares most of
+// them the search for others.
+__global__ __launch_bounds__(256) void k_head_dw_entries(HeadGemm p) {
+  __shared__ int at[2048];
+  __shared__ int wsum[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int total = p.count[0] * p.top, e0 = blockIdx.x;
+  const int id = e0 < total ? p.eid[e0] : -1;
+  if (id < 0) return;
+  const bool alone = p.uses != nullptr && p.uses[id] == 1;
+  // bits of the thread's 8 entries from e (a multiple of 8) on that have the id
+  auto same = [&](int e) {
+    uint32_t bits = 0;
+    if (e < total) {  // the list is padded to a multiple of 8
+      const i32x4 x = *reinterpret_cast<const i32x4*>(p.eid + e), y = *reinterpret_cast<const i32x4*>(p.eid + e + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bits |= (uint32_t)(x[i] == id && e + i < total) << i;
+        bits |= (uint32_t)(y[i] == id && e + 4 + i < total) << (4 + i);
+      }
+    }
+    return bits;
+  };
+  if (!alone) {
+    int seen = 0;
+    for (int b = 0; b < e0; b += 2048) {
+      const int e = b + tid * 8;
+      uint32_t bits = same(e);
+      if (e + 8 > e0) bits &= e < e0 ? (1u << (e0 - e)) - 1 : 0;
+      seen |= bits != 0;
+    }
+    if (__syncthreads_or(seen)) return;
+  }
+  const int col = blockIdx.y * 2048 + tid * 8;
+  const bool in = col < p.H;
+  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int b = e0 / 2048 * 2048; b < (alone ? e0 + 1 : total); b += 2048) {
+    // the entries of this id among these 2048, in order: 8 per thread (none
+    // before e0)
+    const uint32_t mine = !alone ? same(b + tid * 8) : e0 - b - tid * 8 >= 0 && e0 - b - tid * 8 < 8 ? 1u << (e0 - b - tid * 8) : 0;
+    int before = __popc(mine);
+    const int k = before;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(before, d, 64);
+      if (lane >= d) before += v;
+    }
+    __syncthreads();  // the previous list has been read
+    if (lane == 63) wsum[wave] = before;
+    __syncthreads();
+    before -= k;
+    for (int w = 0; w < wave; ++w) before += wsum[w];
+    const int n = wsum[0] + wsum[1] + wsum[2] + wsum[3];
+    for (int i = 0; i < 8; ++i)
+      if ((mine >> i) & 1) at[before++] = tid * 8 + i;
+    __syncthreads();
+    if (in)
+      for (int j = 0; j < n; ++j) {
+        const int e = b + at[j];
+        const float x = p.ev[e];
+        const u32x4 q = *reinterpret_cast<const u32x4*>(p.hc + (int64_t)(e / p.top) * p.Hp + col);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[2 * i] = fmaf(x, bf16_bits_to_f32(q[i] & 0xFFFFu), acc[2 * i]);
+          acc[2 * i + 1] = fmaf(x, bf16_bits_to_f32(q[i] >> 16), acc[2 * i + 1]);
+        }
+      }
+  }
+  if (!in) return;
+  uint16_t* o = p.dw + (int64_t)id * p.H + col;
+  u32x4 q = *reinterpret_cast<const u32x4*>(o);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    q[i] = bf16x2_bits(bf16_bits_to_f32(q[i] & 0xFFFFu) + acc[2 * i], bf16_bits_to_f32(q[i] >> 16) + acc[2 * i + 1]);
+  *reinterpret_cast<u32x4*>(o) = q;
 }
 
 // d_h = u - r^2 h mean(h u), or u without a norm, u the sum of its slabs;
@@ -1092,6 +1228,7 @@ __global__ __launch_bounds__(256) void k_head_dh_narrow(HeadGemm p, const uint16
       a += *reinterpret_cast<const f32x4*>(us + s * slab);
       b += *reinterpret_cast<const f32x4*>(us + s * slab + 4);
     }
+    if (p.exact) head_add_entries(p, c, g, groups, i * 8, a, b);
   }
   if (groups > 1) {
     sum[0][tid] = a;
@@ -1180,6 +1317,7 @@ __global__ __launch_bounds__(256) void k_head_dh(HeadGemm p, const uint16_t* __r
       a[k] += *reinterpret_cast<const f32x4*>(us + s * slab);
       b[k] += *reinterpret_cast<const f32x4*>(us + s * slab + 4);
     }
+    if (p.exact) head_add_entries(p, c, 0, 1, i * 8, a[k], b[k]);
   }
   float f = 0.0f;
   if (norm) {
@@ -1322,7 +1460,14 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
   }
   p.r = take(rows * 4);
   p.info = take(rows * sizeof(HeadRow));
-  p.gt = take(bwd && !distill ? t * 4 : 0);
+  // G's entries at the target's ids are kept apart in fp32 up to 65536 of them
+  // (beyond, their roundings average out, and finding equal ids grows with the
+  // square), for distillation while their rows of W are at most a quarter of it
+  const int64_t entries = (int64_t)T * top;
+  p.exact = bwd && entries <= 65536 && (!distill || entries <= V / 4);
+  p.eid = take(p.exact || (bwd && !distill) ? t * top * 4 + 32 : 0);
+  p.uses = take(p.exact && entries > 2048 ? (size_t)V * 4 : 0);
+  p.ev = take(p.exact || (bwd && !distill) ? t * top * 4 : 0);
   p.flag = take(distill ? t : 0);
   p.rows = take(t * 4);
   p.cidx = take(t * 4);
@@ -1376,7 +1521,12 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
   uint16_t* hc = q.hc = reinterpret_cast<uint16_t*>(ws + p.hc);
   q.r = reinterpret_cast<float*>(ws + p.r);
   q.info = reinterpret_cast<HeadRow*>(ws + p.info);
-  q.gt = reinterpret_cast<float*>(ws + p.gt);
+  q.eid = reinterpret_cast<int32_t*>(ws + p.eid);
+  q.ev = reinterpret_cast<float*>(ws + p.ev);
+  if (a.dw != nullptr && p.exact && (int64_t)p.T * p.top > 2048) {  // one search of 2048 entries costs less
+    q.uses = reinterpret_cast<int32_t*>(ws + p.uses);
+    launch_zero_f32(reinterpret_cast<float*>(q.uses), p.V, s);
+  }
   q.lq = reinterpret_cast<float*>(ws + p.lq);
   if (flag != nullptr)
     hipLaunchKernelGGL(k_head_teacher, dim3(cdiv(p.T, 4)), dim3(256), 0, s, a.ids, a.tlogits, p.T, p.V, p.top,
@@ -1402,7 +1552,10 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
   g.rows = q.rows;
   g.count = q.count;
   g.r = q.r;
-  g.gt = q.gt;
+  g.eid = q.eid;
+  g.ev = p.distill && !p.exact ? nullptr : q.ev;
+  g.exact = p.exact;
+  g.uses = q.uses;
   g.info = q.info;
   g.distill = p.distill;
   g.scale = a.scale;
@@ -1470,7 +1623,8 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
     });
     if (p.distill)
       hipLaunchKernelGGL(k_head_targets, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.rows, g.count, a.ids,
-                         reinterpret_cast<const float*>(a.ws + p.lq), a.logp, g.info, p.top, g.v0, p.piece, g.g);
+                         reinterpret_cast<const float*>(a.ws + p.lq), a.logp, g.info, p.top, g.v0, p.piece, g.g, g.eid,
+                         p.exact ? g.ev : nullptr, g.uses);
     if (a.dw != nullptr && p.tile_z == 0) {
       hipLaunchKernelGGL(k_head_dz_dw<HeadBig>, dim3(ndz + ndw), dim3(HeadBig::NT), 0, s, g, ndz);
       continue;
@@ -1481,6 +1635,8 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
     });
     if (a.dw != nullptr) hipLaunchKernelGGL(k_head_dw<HeadBig>, dim3(ndw), dim3(HeadBig::NT), 0, s, g);
   }
+  if (a.dw != nullptr && p.exact)
+    hipLaunchKernelGGL(k_head_dw_entries, dim3(p.T * p.top, cdiv(p.H, 2048)), dim3(256), 0, s, g);
   const int32_t* cidx = reinterpret_cast<const int32_t*>(a.ws + p.cidx);
   if (p.H <= 2048) {
     int P = 8;

@@ -202,7 +202,8 @@ struct HeadPlan {
   int tile_l, tile_z;     // tiles of h W^T and of G W
   int bm;                 // rows of the former
   int dz_max;             // most workgroups of the G W product
-  size_t r, info, gt, flag, rows, cidx, count, hc, lq, zt, stats, u, g, total;
+  bool exact;             // G's entries at the target's ids are kept in fp32
+  size_t r, info, eid, ev, uses, flag, rows, cidx, count, hc, lq, zt, stats, u, g, total;
 };
 struct HeadArgs {
   const uint16_t* h;

@@ -131,6 +131,48 @@ def test_cross_entropy_masks(torch_gpu):
     _close(gh, d_h, b_h, "confident d_h")
 
 
+@pytest.mark.parametrize("T,V,spread", [(40, 300, 3), (600, 129, 129), (2500, 700, 2), (2500, 3000, 3000), (5000, 90, 1)])
+def test_repeated_targets(torch_gpu, T, V, spread):
+    """Many tokens of one target: the rows of d_w that the fp32 entries go to, alone, in pairs and in thousands, the
+    same each time."""
+    H = 72
+    h, w, y, dl, g = _inputs(T, H, V, ignored=0.2)
+    y = torch.where(y >= 0, torch.randint(0, spread, (T,), generator=g, device="cuda").int() * (V // spread), y).int()
+    ref = lr.ce_ref(h, w, y)
+    loss, lse = moe.lm_head_loss(h, w, y)
+    d_h, b_h, d_w, b_w = ref.grads(dl, True)
+    got = moe.lm_head_loss_backward(h, w, y, loss, lse, dl, weight_grad=True)
+    _close(got[0], d_h, b_h, "d_h")
+    _close(got[1], d_w, b_w, "d_w")
+    again = moe.lm_head_loss_backward(h, w, y, loss, lse, dl, weight_grad=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.parametrize("T,K,V", [(20, 5, 1000), (20, 5, 300), (300, 9, 12000), (300, 9, 9000)])
+def test_entry_precision(torch_gpu, T, K, V):
+    """Where the entries at the target's ids are kept in fp32 (few of them for the vocabulary; cross entropy always),
+    the gradients of peaked rows are within 1.25 of the rounding of the results themselves; bf16 entries alone would
+    add as much again."""
+    H = 256
+    h, w, y, dl, g = _inputs(T, H, V, ignored=0.0)
+    ids = torch.randint(0, V, (T, K), generator=g, device="cuda").int()
+    tl = torch.randn(T, K, generator=g, device="cuda")
+    ref = lr.ce_ref(h, w, y)
+    loss, lse = moe.lm_head_loss(h, w, y)
+    pairs = [(ref, moe.lm_head_loss_backward(h, w, y, loss, lse, dl, weight_grad=True))]
+    if T * K <= V // 4:
+        loss, lse, logp = moe.lm_head_distill(h, w, ids, tl)
+        pairs.append((lr.distill_ref(h, w, ids, tl)[0],
+                      moe.lm_head_distill_backward(h, w, ids, tl, lse, logp, dl, weight_grad=True)))
+    for ref, got in pairs:
+        want = ref.grads(dl, True)
+        for a, b in zip(got, (want[0], want[2])):
+            rounding = torch.linalg.norm(b.bfloat16().double() - b)
+            # G's other entries are rounded too: their share of G's norm, in quadrature
+            rest = torch.linalg.norm(torch.where(ref.q > 0, 0.0, ref.p)) / torch.linalg.norm(ref.p - ref.q)
+            assert torch.linalg.norm(a.double() - b) <= rounding * (1.25 + rest)
+
+
 def test_head_rows_strided(torch_gpu):
     T, H, V = 90, 200, 700
     h, w, y, dl, _ = _inputs(T, H, V)
