@@ -551,13 +551,17 @@ MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[
   using X0 = std::integral_constant<int, 0>;
   using X1 = std::integral_constant<int, 1>;
   int slot = 0;
+  float ss_low = 0.0f;
   // ISSUE: 0 no stage left to issue, 1 stage kt + S, 2 the same and it is the last
   auto step = [&](auto issue, int kt) {
     constexpr int ISSUE = decltype(issue)::value;
     const int nslot = next(slot);
     using Last = std::integral_constant<bool, ISSUE == 2>;
     if (SQ) {
+      // a stage's 16 squares first, then one compensated addition: a plain sum
+      // over the whole row would cost 1/rms, and so every logit, a few 1e-7
       const int row = threadIdx.x >> 2, part = (threadIdx.x & 3) * 2;
+      float x[8];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const u32x4 q = *reinterpret_cast<const u32x4*>(smem + off_a(slot) + row * 128 +
@@ -565,10 +569,13 @@ MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float a = bf16_bits_to_f32(q[e] & 0xFFFFu), b = bf16_bits_to_f32(q[e] >> 16);
-          *ss = fmaf(a, a, *ss);
-          *ss = fmaf(b, b, *ss);
+          x[j * 4 + e] = fmaf(a, a, b * b);
         }
       }
+      const float y = (((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]))) - ss_low;
+      const float sum = *ss + y;
+      ss_low = (sum - *ss) - y;
+      *ss = sum;
     }
     phase(X0(), slot, 1, [&](int i) {
       if (C::FIVE && ISSUE) {
