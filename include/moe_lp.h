@@ -389,10 +389,11 @@ typedef struct {
 
 /* Workspace bytes of the loss entries below: top = 0 for cross entropy, else
  * the teacher logits per token; backward != 0 for the *_backward entry.
- * Returns 0 for an invalid or unsupported descriptor.  The logits are never
- * held: the forward keeps two floats per token and block of vocabulary rows,
- * the backward the scaled softmax gradient (bf16) of one piece of the
- * vocabulary at a time (at most about 512 MB, or 256 columns where more
+ * Returns 0 for an invalid or unsupported descriptor.  The logits are held
+ * only where there are few (parts of their sums, fp32, at most 64 MB);
+ * otherwise the forward keeps two floats per token and block of vocabulary
+ * rows.  The backward keeps the scaled softmax gradient (bf16) of one piece of
+ * the vocabulary at a time (at most about 512 MB, or 256 columns where more
  * tokens need more), and partial sums of dL/dz (fp32, up to 64 [T][H]). */
 size_t moe_lm_head_loss_workspace_bytes(const moe_lm_head* head, int32_t top, int32_t backward);
 

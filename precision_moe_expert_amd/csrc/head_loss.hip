@@ -5,7 +5,7 @@
 // or `top` ids with weights q), so they share every product:
 //   forward   l = s r h W^T, per row the log of the sum of exponentials and
 //             the few l at the target's ids; no l leaves the product's tile
-//             but those
+//             but those (few tiles apart, whose K is split: k_head_part)
 //   backward  per piece of the vocabulary l again, G = s r g exp(l - lse) in
 //             bf16, its entries at the target's ids replaced by
 //             s r g (p - q); then u += G W (dL/dz r) and d_W = G^T h.  One such
@@ -648,6 +648,9 @@ struct HeadGemm {
   uint16_t* g;    // [..][piece]
   float* u;       // [count][H]
   uint16_t* dw;   // [V][H]
+  float* lp;      // [psplits][T][Vp] partial h W^T (K split), Vp a multiple of 4
+  int psplits, Vp;
+  bool direct;    // its rows are h's as they are
   int v0, piece;
 };
 
@@ -958,6 +961,78 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_head_dz_dw(HeadGemm p, int nd
   else head_dw<C>(p, blockIdx.x - ndz, smem);
 }
 
+// Few tiles (a small vocabulary, few rows) leave CUs idle and, with each tile's
+// own requests alone in flight, most of the memory's rate unused.  There K is
+// split: partial h W^T go to slabs of fp32 (at most 64 MB), and what the
+// epilogues above do is done from their sums.
+template <class C>
+__global__ __launch_bounds__(C::NT, C::WPS) void k_head_part(HeadGemm p) {
+  __shared__ __align__(16) uint8_t smem[C::SMEM];
+  const int n = p.direct ? p.T : *p.count, nm = (n + C::BM - 1) / C::BM;
+  int mt, nt;
+  if (n == 0 || !head_tile(blockIdx.x, nm * p.psplits, (p.V + C::BN - 1) / C::BN, mt, nt)) return;
+  const int sp = mt / nm;
+  mt -= sp * nm;
+  const int steps = p.Hp / 64, s0 = steps * sp / p.psplits, s1 = steps * (sp + 1) / p.psplits;
+  const int m0 = mt * C::BM, n0 = nt * C::BN, k0 = s0 * 64;
+  HeadSrc sa = {reinterpret_cast<const char*>(p.hc + (int64_t)m0 * p.Hp + k0), (uint32_t)p.Hp * 2, C::BM, p.Hp - k0};
+  if (p.direct)
+    sa = HeadSrc{reinterpret_cast<const char*>(p.h + (int64_t)m0 * p.h_stride + k0), (uint32_t)p.h_stride * 2, n - m0,
+                 p.H - k0};
+  const HeadSrc sb = {reinterpret_cast<const char*>(p.w + (int64_t)n0 * p.w_stride + k0), (uint32_t)p.w_stride * 2,
+                      p.V - n0, p.H - k0};
+  f32x4 acc[C::MI][C::NJ];
+  head_mm<C, false, false>(sa, sb, s1 - s0, acc, smem);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
+  const int wm = wave / C::WN * C::MI * 16, wn = wave % C::WN * C::NJ * 16;
+#pragma unroll
+  for (int i = 0; i < C::MI; ++i) {
+    const int c = m0 + wm + i * 16 + ln;
+    if (c >= n) continue;
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j) {
+      const int col = n0 + wn + j * 16 + lg * 4;
+      if (col < p.V) *reinterpret_cast<f32x4*>(p.lp + ((int64_t)sp * p.T + c) * p.Vp + col) = acc[i][j];
+    }
+  }
+}
+// Columns v .. v + 3 of row c: the slabs' sum, in order.
+MOE_DEV f32x4 head_part4(const HeadGemm& p, int c, int v) {
+  const float* o = p.lp + (int64_t)c * p.Vp + v;
+  const int64_t slab = (int64_t)p.T * p.Vp;
+  f32x4 z = *reinterpret_cast<const f32x4*>(o);
+  int s = 1;
+  for (; s + 3 < p.psplits; s += 3) {  // three slabs' loads in flight
+    const f32x4 a = *reinterpret_cast<const f32x4*>(o + s * slab), b = *reinterpret_cast<const f32x4*>(o + (s + 1) * slab),
+                c3 = *reinterpret_cast<const f32x4*>(o + (s + 2) * slab);
+    z = ((z + a) + b) + c3;
+  }
+  for (; s < p.psplits; ++s) z += *reinterpret_cast<const f32x4*>(o + s * slab);
+  return z;
+}
+MOE_DEV float head_part1(const HeadGemm& p, int c, int v) { return head_part4(p, c, v & ~3)[v & 3]; }
+
+// G from the slabs: a block takes 2048 columns of a row, 8 per thread.
+__global__ __launch_bounds__(256) void k_head_part_grad(HeadGemm p, int bm) {
+  const int c = blockIdx.x, n = p.count[0], v = blockIdx.y * 2048 + (int)threadIdx.x * 8;
+  if (c >= (n + bm - 1) / bm * bm || v >= p.piece) return;
+  const HeadRow w = p.info[c];
+  float x[8];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < n && v + k * 4 < p.V) z = head_part4(p, c, v + k * 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int at = v + k * 4 + e;
+      x[k * 4 + e] = c < n && at < p.V ? w.f * hl_exp2(fmaf(z[e], w.f2, -w.l2)) : 0.0f;
+      if (!p.distill && at == w.tgt && at < p.V) x[k * 4 + e] = p.exact ? 0.0f : p.ev[c];
+    }
+  }
+  *reinterpret_cast<u32x4*>(p.g + (int64_t)c * p.piece + v) =
+      (u32x4){bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]), bf16x2_bits(x[4], x[5]), bf16x2_bits(x[6], x[7])};
+}
+
 // Per token (one wave): joins its blocks' statistics and forms the outputs.
 // DIRECT: row t is token t, and whether it counts and the teacher's
 // probabilities are found here.
@@ -1032,6 +1107,116 @@ __global__ __launch_bounds__(256) void k_head_finish(HeadFinish p) {
     kl = hl_sum64(kl);
   } else {
     kl = l - p.zt[c];
+  }
+  if (lane == 0) {
+    p.loss[t] = kl;
+    p.lse[t] = l;
+  }
+}
+
+// The same from slabs, one block per token.  p.direct: 1/rms is formed here too.
+__global__ __launch_bounds__(256) void k_head_part_finish(HeadGemm g, HeadFinish p) {
+  __shared__ float sm[4], ss[4];
+  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const bool distill = p.logp != nullptr;
+  float lq[4];
+  int c = t;
+  if (g.direct) {
+    if (distill) {
+      c = head_teacher(p.ids + (int64_t)t * p.top, p.tlogits + (int64_t)t * p.top, p.V, p.top, p.tscale, lane, lq) ? t
+                                                                                                                  : -1;
+    } else {
+      const int y = p.ids[t];
+      c = y >= 0 && y < p.V ? t : -1;
+    }
+  } else {
+    c = p.cidx[t];
+    if (distill)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        lq[i] = i * 64 + lane < p.top ? p.lq[(int64_t)t * p.top + i * 64 + lane] : -INFINITY;
+  }
+  if (c < 0) {
+    if (distill)
+      for (int j = tid; j < p.top; j += 256) p.logp[(int64_t)t * p.top + j] = 0.0f;
+    if (tid == 0) {
+      p.loss[t] = !distill && p.ids[t] >= p.V ? __builtin_nanf("") : 0.0f;
+      p.lse[t] = 0.0f;
+    }
+    return;
+  }
+  float f;
+  if (g.direct) {
+    float r = 1.0f;
+    if (g.eps > 0.0f) {
+      float sq = 0.0f;
+      const uint16_t* row = g.h + (int64_t)t * g.h_stride;
+      for (int i = tid; i < g.H / 8; i += 256) {
+        const u32x4 q = *reinterpret_cast<const u32x4*>(row + i * 8);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float a = bf16_bits_to_f32(q[j] & 0xFFFFu), b = bf16_bits_to_f32(q[j] >> 16);
+          sq = fmaf(a, a, sq);
+          sq = fmaf(b, b, sq);
+        }
+      }
+      sq = hl_sum64(sq);
+      if (lane == 0) ss[wave] = sq;
+      __syncthreads();
+      r = 1.0f / sqrtf(((ss[0] + ss[1]) + (ss[2] + ss[3])) / (float)g.H + g.eps);
+      __syncthreads();
+    }
+    f = g.scale * r;
+  } else {
+    f = g.info[c].f;
+  }
+  const float f2 = f * kLog2e;
+  float m = -INFINITY, s = 0.0f;
+  for (int v = tid * 4; v < p.V; v += 1024) {
+    const f32x4 z = head_part4(g, c, v);
+    float y[4], mx = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      y[e] = v + e < p.V ? z[e] * f2 : -INFINITY;
+      mx = fmaxf(mx, y[e]);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += hl_exp2(y[e] - mx);
+    hl_merge(m, s, mx, sum);
+  }
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) {
+    const float m2 = shfl_xor(m, x), s2 = shfl_xor(s, x);
+    hl_merge(m, s, m2, s2);
+  }
+  if (lane == 0) {
+    sm[wave] = m;
+    ss[wave] = s;
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  m = sm[0];
+  s = ss[0];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) hl_merge(m, s, sm[w], ss[w]);
+  const float l = m * kLn2 + logf(s);
+  float kl;
+  if (distill) {
+    kl = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = i * 64 + lane;
+      if (j < p.top) {
+        const bool have = !(lq[i] == -INFINITY);
+        const float lp = have ? head_part1(g, c, p.ids[(int64_t)t * p.top + j]) * f - l : 0.0f;
+        p.logp[(int64_t)t * p.top + j] = lp;
+        if (have) kl = fmaf(expf(lq[i]), lq[i] - lp, kl);
+      }
+    }
+    kl = hl_sum64(kl);
+  } else {
+    kl = l - head_part1(g, c, p.ids[t]) * f;
   }
   if (lane == 0) {
     p.loss[t] = kl;
@@ -1397,10 +1582,27 @@ float head_cost(const HeadShape& t, int M, int N, int K, int splits, int cus, fl
 // shapes on average, 10% at most (always 256 x 256: 1.6 times the best at 16
 // rows of 512 x 8000 and 1.7 at 64 rows of 7168 x 32000; always 64 x 128: 2
 // times at 1500 rows).
-int head_tile_logits(int T, int H, int V, int cus) {
+// With K split (splits > 1) the slabs are written and read at about 8 MB per
+// microsecond, the forward reads a row of them with one block and the backward
+// has a launch more.  Against unsplit: forward of 2 x 6488 x 1118 45 -> 19 us,
+// 42 x 5536 x 3619 39 -> 22, 256 x 4096 x 4096 30 -> 22; gradient of the second
+// 55 -> 38; the same from 8000 columns at 64 rows of 2048 or 300 of 3264.
+int head_tile_logits(int T, int H, int V, bool bwd, int cus, int* splits) {
   int best = 0;
-  for (int i = 1; i < kHeadShapeCount; ++i)
-    if (head_cost(kHeadShapes[i], T, V, H, 1, cus, 1.0f) < head_cost(kHeadShapes[best], T, V, H, 1, cus, 1.0f)) best = i;
+  float least = -1.0f;
+  for (int i = 0; i < kHeadShapeCount; ++i)
+    for (int s = 1; s <= 16 && (s == 1 || (s <= (H + 63) / 64 && (int64_t)T * V * s <= (16 << 20))); ++s) {
+      float c = head_cost(kHeadShapes[i], T, V, H, s, cus, 1.0f);
+      if (s > 1) {
+        const float bytes = (float)T * (float)V * (float)s * 8.0f;
+        c += bytes / 8e6f + (bwd ? 6.0f : 1.0f + (float)V * (float)s * 2.5e-4f);
+      }
+      if (least < 0.0f || c < least) {
+        least = c;
+        best = i;
+        *splits = s;
+      }
+    }
   return best;
 }
 // Most workgroups of the G W product: room for a second round's splits.
@@ -1452,7 +1654,7 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
   const size_t t = (size_t)T, rows = (t + 255) / 256 * 256;  // whole tiles
   p.Hp = (H + 63) / 64 * 64;
   const int cus = head_cus();
-  p.tile_l = head_tile_logits(T, H, V, cus);
+  p.tile_l = head_tile_logits(T, H, V, bwd, cus, &p.psplits);
   p.bm = kHeadShapes[p.tile_l].bm;
   if (bwd) {
     // columns of G per piece: 512 MB of G, at least 256 columns (256 MB, which
@@ -1462,6 +1664,7 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
     p.npieces = cdiv(V, most > 256 ? most : 256);
     p.piece = cdiv(cdiv(V, p.npieces), 256) * 256;
     p.npieces = cdiv(V, p.piece);
+    if (p.npieces > 1) p.psplits = 1;
     p.tile_z = head_tile_dz(T, H, p.piece < V ? p.piece : V, cus);
     p.dz_max = head_dz_max(T, H, kHeadShapes[p.tile_z].bm, kHeadShapes[p.tile_z].bn);
   }
@@ -1481,6 +1684,7 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
   p.count = take(8);
   p.hc = take(rows * p.Hp * 2);
   p.lq = take(distill ? t * top * 4 : 0);
+  p.lp = take(p.psplits > 1 ? t * ((V + 3) / 4 * 4) * p.psplits * 4 : 0);
   if (!bwd) {
     p.zt = take(t * top * 4);
     p.stats = take(t * cdiv(V, kHeadShapes[p.tile_l].bn) * 8);
@@ -1571,9 +1775,19 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
   return g;
 }
 
+// The partial products' launch.
+static void launch_head_part(const HeadPlan& p, const HeadGemm& g, hipStream_t s) {
+  head_dispatch(p.tile_l, [&](auto c) {
+    using C = decltype(c);
+    hipLaunchKernelGGL(k_head_part<C>, dim3(head_grid((int64_t)cdiv(p.T, C::BM) * p.psplits, cdiv(p.V, C::BN))),
+                       dim3(C::NT), 0, s, g);
+  });
+}
+
 void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
   using Direct = HeadTile<64, 128, 2, 2, 3, 2>;
-  const bool direct = p.T <= Direct::BM && p.bm == Direct::BM && p.H % 64 == 0;
+  const bool part = p.psplits > 1;
+  const bool direct = p.H % 64 == 0 && (part ? p.T <= HEAD_SAME : p.T <= Direct::BM && p.bm == Direct::BM);
   HeadGemm g = direct ? HeadGemm{} : head_common(p, a, s);
   g.h = a.h;
   g.h_stride = a.h_stride;
@@ -1604,6 +1818,15 @@ void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
                a.loss,
                a.lse,
                a.logp};
+  if (part) {
+    g.lp = reinterpret_cast<float*>(a.ws + p.lp);
+    g.psplits = p.psplits;
+    g.Vp = (p.V + 3) / 4 * 4;
+    g.direct = direct;
+    launch_head_part(p, g, s);
+    hipLaunchKernelGGL(k_head_part_finish, dim3(p.T), dim3(256), 0, s, g, f);
+    return;
+  }
   if (direct) {
     hipLaunchKernelGGL((k_head_stats<Direct, true>), dim3(head_grid(1, f.nvb)), dim3(Direct::NT), 0, s, g);
     hipLaunchKernelGGL(k_head_finish<true>, dim3(cdiv(p.T, 4)), dim3(256), 0, s, f);
@@ -1620,14 +1843,23 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
   HeadGemm g = head_common(p, a, s);
   g.u = reinterpret_cast<float*>(a.ws + p.u);
   g.g = reinterpret_cast<uint16_t*>(a.ws + p.g);
+  g.lp = reinterpret_cast<float*>(a.ws + p.lp);
+  g.T = p.T;
+  g.psplits = p.psplits;
+  g.Vp = (p.V + 3) / 4 * 4;
   g.piece = p.piece;
   const int ndz = head_grid(p.dz_max, 1), ndw = head_grid(cdiv(p.piece, HeadBig::BM), cdiv(p.H, HeadBig::BN));
   for (int i = 0; i < p.npieces; ++i) {
     g.v0 = i * p.piece;
-    head_dispatch(p.tile_l, [&](auto c) {
-      using C = decltype(c);
-      hipLaunchKernelGGL(k_head_grad<C>, dim3(head_grid(cdiv(p.T, C::BM), p.piece / C::BN)), dim3(C::NT), 0, s, g);
-    });
+    if (p.psplits > 1) {
+      launch_head_part(p, g, s);
+      hipLaunchKernelGGL(k_head_part_grad, dim3(cdiv(p.T, p.bm) * p.bm, cdiv(p.piece, 2048)), dim3(256), 0, s, g, p.bm);
+    } else {
+      head_dispatch(p.tile_l, [&](auto c) {
+        using C = decltype(c);
+        hipLaunchKernelGGL(k_head_grad<C>, dim3(head_grid(cdiv(p.T, C::BM), p.piece / C::BN)), dim3(C::NT), 0, s, g);
+      });
+    }
     if (p.distill)
       hipLaunchKernelGGL(k_head_targets, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.rows, g.count, a.ids,
                          reinterpret_cast<const float*>(a.ws + p.lq), a.logp, g.info, p.top, g.v0, p.piece, g.g, g.eid,

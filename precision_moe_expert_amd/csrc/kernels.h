@@ -201,9 +201,10 @@ struct HeadPlan {
   int Hp;                 // H rounded up to the products' K step
   int tile_l, tile_z;     // tiles of h W^T and of G W
   int bm;                 // rows of the former
+  int psplits;            // ways its K is split (1: not)
   int dz_max;             // most workgroups of the G W product
   bool exact;             // G's entries at the target's ids are kept in fp32
-  size_t r, info, eid, ev, uses, flag, rows, cidx, count, hc, lq, zt, stats, u, g, total;
+  size_t r, info, eid, ev, uses, flag, rows, cidx, count, hc, lq, lp, zt, stats, u, g, total;
 };
 struct HeadArgs {
   const uint16_t* h;

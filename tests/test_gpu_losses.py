@@ -77,6 +77,22 @@ def test_cross_entropy(torch_gpu, T, H, V, eps, scale):
     _close(gh2, d_h, b_h, "d_h of a frozen head")
 
 
+# wide rows with few columns: the sum over H is split between workgroups (each on
+# both sides of 256 rows, of whole tiles and of a multiple of 64 columns of h)
+WIDE = [(1, 4096, 3), (2, 6488, 1118), (3, 2048, 700), (64, 7168, 2049), (137, 6872, 4001), (256, 4096, 300),
+        (257, 4096, 501), (300, 1032, 257), (900, 2048, 130), (1500, 5000, 66)]
+
+
+@pytest.mark.parametrize("T,H,V", WIDE)
+def test_cross_entropy_wide_rows(torch_gpu, T, H, V):
+    test_cross_entropy(torch_gpu, T, H, V, 1e-6, 0.9)
+
+
+@pytest.mark.parametrize("T,H,V", WIDE)
+def test_distillation_wide_rows(torch_gpu, T, H, V):
+    test_distillation(torch_gpu, T, H, V, 5, True)
+
+
 @pytest.mark.parametrize("nans", [True, False])
 @pytest.mark.parametrize("K", [1, 2, 7, 64, 65, 256])
 @pytest.mark.parametrize("T,H,V", [(1, 64, 100), (5, 72, 129), (130, 136, 3001), (300, 256, 513)])
