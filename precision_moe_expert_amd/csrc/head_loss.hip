@@ -1380,16 +1380,18 @@ __global__ __launch_bounds__(256) void k_head_dw_entries(HeadGemm p) {
 
 // d_h = u - r^2 h mean(h u), or u without a norm, u the sum of its slabs;
 // zeros for tokens that do not count.  For H <= 2048, where u has the most
-// slabs: one block per token, its 256 threads in groups of P = the power of two
-// at or above H / 8, each of which adds every (256 / P)-th slab; the groups' sums
-// are added in order.
-__global__ __launch_bounds__(256) void k_head_dh_narrow(HeadGemm p, const uint16_t* __restrict__ h, int64_t h_stride,
+// slabs, and for H <= 8192 with at most two tokens per CU: one block per token,
+// its NT threads in groups of P = the power of two at or above H / 8, each of
+// which adds every (NT / P)-th slab; the groups' sums are added in order.  NT is
+// 1024 where tokens are few and adding the groups is not the longer part.
+template <int NT>
+__global__ __launch_bounds__(NT) void k_head_dh_narrow(HeadGemm p, const uint16_t* __restrict__ h, int64_t h_stride,
                                                         const int32_t* __restrict__ cidx, bool norm, int P,
                                                         uint16_t* __restrict__ dh) {
-  __shared__ __align__(16) f32x4 sum[2][256];
-  __shared__ float part[4];
+  __shared__ __align__(16) f32x4 sum[2][NT];
+  __shared__ float part[NT / 64];
   const int t = blockIdx.x, c = cidx[t], H = p.H, np = H / 8, tid = threadIdx.x;
-  const int i = tid & (P - 1), g = tid / P, groups = 256 / P;
+  const int i = tid & (P - 1), g = tid / P, groups = NT / P;
   uint16_t* o = dh + (int64_t)t * H + i * 8;
   if (c < 0) {
     if (g == 0 && i < np) *reinterpret_cast<u32x4*>(o) = (u32x4){0, 0, 0, 0};
@@ -1443,7 +1445,10 @@ __global__ __launch_bounds__(256) void k_head_dh_narrow(HeadGemm p, const uint16
     dot = hl_sum64(dot);
     if ((tid & 63) == 0) part[tid >> 6] = dot;
     __syncthreads();
-    f = p.r[c] * p.r[c] * ((part[0] + part[1]) + (part[2] + part[3])) / (float)H;
+    float all = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) all += part[w];
+    f = p.r[c] * p.r[c] * all / (float)H;
   }
   if (g != 0 || i >= np) return;
   u32x4 x;
@@ -1877,10 +1882,13 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
   if (a.dw != nullptr && p.exact)
     hipLaunchKernelGGL(k_head_dw_entries, dim3(p.T * p.top, cdiv(p.H, 2048)), dim3(256), 0, s, g);
   const int32_t* cidx = reinterpret_cast<const int32_t*>(a.ws + p.cidx);
-  if (p.H <= 2048) {
-    int P = 8;
-    while (P < p.H / 8) P *= 2;
-    hipLaunchKernelGGL(k_head_dh_narrow, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f, P, a.dh);
+  int P = 8;
+  while (P < p.H / 8) P *= 2;
+  if (p.H > 512 && p.H <= 8192 && p.T <= 2 * head_cus()) {
+    hipLaunchKernelGGL(k_head_dh_narrow<1024>, dim3(p.T), dim3(1024), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f, P,
+                       a.dh);
+  } else if (p.H <= 2048) {
+    hipLaunchKernelGGL(k_head_dh_narrow<256>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f, P, a.dh);
   } else if (p.H <= 8192)
     hipLaunchKernelGGL(k_head_dh<4>, dim3(p.T), dim3(256), 0, s, g, a.h, a.h_stride, cidx, a.eps > 0.0f, a.dh);
   else
