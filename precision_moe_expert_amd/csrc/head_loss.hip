@@ -82,6 +82,15 @@ MOE_DEV int head_splits(const HeadSplit& q, int n, int lane) {
 
 // ---- which tokens count -----------------------------------------------------
 
+// Log of a teacher's probability before its normalisation, x - m times the
+// scale: the difference first, and held above the lowest fp32 values, so that
+// logits of -3.4e38 (a mask's) stay slots that are there, at probability 0 or,
+// where all of a token's are, equal.
+MOE_DEV float hl_teacher(float x, float m, float tscale) {
+  const float y = (x - m) * tscale;
+  return y < -3.0e38f ? -3.0e38f : y;  // NaN stays
+}
+
 // One wave, one token's slots: the log of the teacher's probabilities of slots
 // lane, lane + 64, ... (-infinity for those that are not there); whether any is.
 MOE_DEV bool head_teacher(const int32_t* __restrict__ ids, const float* __restrict__ tlogits, int V, int top,
@@ -94,7 +103,7 @@ MOE_DEV bool head_teacher(const int32_t* __restrict__ ids, const float* __restri
     lq[i] = -INFINITY;
     if (j < top) {
       const int id = ids[j];
-      if (id >= 0 && id < V) lq[i] = tlogits[j] * tscale;  // tscale > 0 keeps -infinity
+      if (id >= 0 && id < V) lq[i] = tlogits[j];
     }
     const bool have = !(lq[i] == -INFINITY);
     any |= have;
@@ -104,11 +113,14 @@ MOE_DEV bool head_teacher(const int32_t* __restrict__ ids, const float* __restri
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (!(lq[i] == -INFINITY)) s += expf(lq[i] - m);
+    if (!(lq[i] == -INFINITY)) {
+      lq[i] = hl_teacher(lq[i], m, tscale);
+      s += expf(lq[i]);
+    }
   const float ls = logf(hl_sum64(s));
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (!(lq[i] == -INFINITY)) lq[i] = lq[i] - m - ls;
+    if (!(lq[i] == -INFINITY)) lq[i] -= ls;
   return __any(any);
 }
 
@@ -244,7 +256,6 @@ __global__ __launch_bounds__(256) void k_head_gather(HeadRowsArgs p) {
         if (id >= 0 && id < p.V) x = p.tlogits[(int64_t)c * p.top + tid];
       }
       const bool have = !(x == -INFINITY);
-      x *= p.tscale;
       const float m4 = hl_max64(have ? x : -INFINITY);
       const bool any4 = __any(have);
       if (lane == 0) {
@@ -254,11 +265,12 @@ __global__ __launch_bounds__(256) void k_head_gather(HeadRowsArgs p) {
       __syncthreads();
       const float m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
       live = wsum[0] | wsum[1] | wsum[2] | wsum[3];
-      const float s4 = hl_sum64(have ? expf(x - m) : 0.0f);
+      x = hl_teacher(x, m, p.tscale);  // not used where there is no slot
+      const float s4 = hl_sum64(have ? expf(x) : 0.0f);
       if (lane == 0) part2[wave] = s4;
       __syncthreads();
       const float ls = logf((part2[0] + part2[1]) + (part2[2] + part2[3]));
-      if (c < n && tid < p.top) p.lq[(int64_t)c * p.top + tid] = have ? x - m - ls : -INFINITY;
+      if (c < n && tid < p.top) p.lq[(int64_t)c * p.top + tid] = have ? x - ls : -INFINITY;
     }
     if (c < n && tid == 0) {
       p.rows[c] = c;

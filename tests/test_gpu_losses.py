@@ -116,6 +116,30 @@ def test_distillation(torch_gpu, T, H, V, K, nans):
     _close(gw, d_w, b_w, "d_w")
 
 
+@pytest.mark.parametrize("T,H,V", [(5, 64, 300), (70, 136, 301), (300, 64, 500), (1100, 64, 129), (9, 4096, 300)])
+def test_distillation_lowest_logits(torch_gpu, T, H, V):
+    """Teacher logits of the type's lowest value are slots that are there: probability 0 beside others, equal where
+    a token has no others, whatever the scale."""
+    K = 6
+    h, w, _, dl, g = _inputs(T, H, V)
+    ids = torch.stack([torch.randperm(V, generator=g, device="cuda")[:K] for _ in range(T)]).int()
+    tl = torch.randn(T, K, generator=g, device="cuda")
+    low = torch.finfo(torch.float32).min
+    tl[:, 2] = low
+    tl[::3] = low
+    tl[1, 0] = 2e38
+    ref, have, q = lr.distill_ref(h, w, ids, tl, 2.0, 1e-6, 1.0)
+    assert have.all() and (q[0] == q[0, 0]).all()
+    lse, loss, logp, b_lse, b_loss, b_logp = lr.distill_loss(ref, ids, have, q)
+    got, got_lse, got_logp = moe.lm_head_distill(h, w, ids, tl, teacher_scale=2.0)
+    _close(got_logp, logp, b_logp, "logp")
+    _close(got, loss, b_loss, "loss")
+    d_h, b_h, d_w, b_w = ref.grads(dl, True)
+    gh, gw = moe.lm_head_distill_backward(h, w, ids, tl, got_lse, got_logp, dl, weight_grad=True, teacher_scale=2.0)
+    _close(gh, d_h, b_h, "d_h")
+    _close(gw, d_w, b_w, "d_w")
+
+
 def test_cross_entropy_masks(torch_gpu):
     """No token counts; all do; ids past the vocabulary; confident rows."""
     T, H, V = 70, 128, 500
@@ -280,6 +304,30 @@ def test_balance(torch_gpu, T, E, k, packed):
     # the same sums in the same order each time
     again = moe.balance_loss(layer, lg, ids.cuda(), token_mask=None if msk is None else msk.bool(), seg_offsets=offd)
     assert all(torch.equal(a, b) for a, b in zip((loss, counts, tokens, probs), again))
+
+
+@pytest.mark.parametrize("T,E,k", [(70, 48, 3), (70, 45, 3), (1100, 200, 2)])
+def test_balance_lowest_logits(torch_gpu, T, E, k):
+    """Masks of the type's lowest value: probability 0 beside others, equal where a row has no others; so at the
+    other end of the range."""
+    torch.manual_seed(T)
+    logits = torch.randn(T, E)
+    low = torch.finfo(torch.float32).min
+    logits[:, E // 2] = low
+    logits[::3] = low
+    logits[1] = -low
+    logits[2, 3] = 3e38
+    ids = torch.topk(logits, k, 1).indices.int()
+    layer = moe.make_layer(T, 256, 128, E, k, moe.FMT_INT4)
+    g = torch.tensor([0.7])
+    ref = lr.balance_ref(logits, ids, k, d_loss=g)
+    loss, counts, tokens, probs = moe.balance_loss(layer, logits.cuda(), ids.cuda())
+    # |m - x| of a lowest value enters the reference's bound where p is 0: such rows count with their sum of p, 1
+    assert torch.allclose(probs.cpu().double(), ref["probs"], rtol=(T + 64) * 2.0 ** -24, atol=16 * 2.0 ** -24)
+    assert torch.allclose(loss.cpu().double(), ref["loss"], rtol=(T + E + 64) * 2.0 ** -24, atol=0)
+    d = moe.balance_loss_backward(layer, logits.cuda(), counts, tokens, g.cuda())
+    a = 0.7 * E / (k * T * T) * ref["counts"][0].double()
+    assert ((d.cpu().double() - ref["d_logits"]).abs() <= a.max() * (E + 64) * 2.0 ** -24).all()
 
 
 @pytest.mark.parametrize("T,E,k,most", [(900, 48, 3, 4), (1100, 385, 2, 4), (3000, 48, 3, 3), (5000, 130, 4, 40)])
