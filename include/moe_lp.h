@@ -369,7 +369,9 @@ moe_status moe_lm_head_logprob(int32_t T, int32_t H, int32_t V, const void* h_bf
  * The objectives an adapter on the frozen base is trained with, each with its
  * gradient: cross entropy and distillation through the LM head (their d_h is
  * what the layers below take as d_out), and the router's balance loss (its
- * gradient joins moe_expert_backward's d_logits). */
+ * gradient joins moe_expert_backward's d_logits).  A workspace serves one call
+ * at a time: calls that may run at once, replayed graphs among them, need one
+ * each. */
 
 /* An LM head (host memory).  logits[t][v] = logit_scale * <z_t, W_v> with
  * z_t = h_t / sqrt(mean(h_t^2) + norm_eps), the parameter-free RMSNorm of
