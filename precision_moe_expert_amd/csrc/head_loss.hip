@@ -487,6 +487,8 @@ struct HeadTile {
   static_assert(!FIVE || BM == BN, "buffers of one size");
   static constexpr int SMEM = FIVE ? 5 * BM * 128 : S * STAGE;
   static constexpr int NW = WM * WN, NT = NW * 64;
+  // what a last round of these tiles may be done with (head_tile_tail)
+  using Half = std::conditional_t<FIVE, HeadTile<BM_ / 2, BN_, WM_, WN_, 3, WPS_>, HeadTile>;
 };
 
 // SQ (64 rows of A, 256 threads): also sums into *ss the squares of the 16
@@ -625,13 +627,42 @@ MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[
 // contiguous range of tiles, ordered in bands of GM tile rows, so the tiles
 // it works on at one time share few row and column panels in its L2.
 constexpr int HEAD_GM = 4;
-MOE_DEV bool head_tile(int bid, int nm, int nn, int& m, int& n) {
-  const int nt = nm * nn, per = (nt + 7) >> 3, at = bid >> 3, idx = (bid & 7) * per + at;
-  if (at >= per || idx >= nt) return false;
+MOE_DEV void head_order(int idx, int nm, int nn, int& m, int& n) {
   const int band = idx / (HEAD_GM * nn), rem = idx - band * HEAD_GM * nn;
   const int gm = min(HEAD_GM, nm - band * HEAD_GM);
   n = rem / gm;
   m = band * HEAD_GM + rem - n * gm;
+}
+// Place of workgroup bid among `total` pieces of work, -1 past them.
+MOE_DEV int head_place(int bid, int total) {
+  const int per = (total + 7) >> 3, at = bid >> 3, idx = (bid & 7) * per + at;
+  return at >= per || idx >= total ? -1 : idx;
+}
+MOE_DEV bool head_tile(int bid, int nm, int nn, int& m, int& n) {
+  const int idx = head_place(bid, nm * nn);
+  if (idx < 0) return false;
+  head_order(idx, nm, nn, m, n);
+  return true;
+}
+// The same where the last round of tiles would leave half of the CUs idle: its
+// tiles are done as two halves of BM/2 rows each.  Halves: `half` is 0 or 1;
+// -1: a whole tile.
+MOE_DEV bool head_tile_tail(int bid, int nm, int nn, int slots, int& m, int& n, int& half) {
+  const int nt = nm * nn;
+  int whole = nt / slots * slots & ~7;
+  if ((nt - whole) * 2 > slots) whole = nt;
+  half = -1;
+  if (whole == nt) return head_tile(bid, nm, nn, m, n);
+  int idx;
+  if (bid < whole) {
+    idx = head_place(bid, whole);
+  } else {
+    idx = head_place(bid - whole, (nt - whole) * 2);
+    if (idx < 0) return false;
+    half = idx & 1;
+    idx = whole + (idx >> 1);
+  }
+  head_order(idx, nm, nn, m, n);
   return true;
 }
 
@@ -663,6 +694,7 @@ struct HeadGemm {
   float* lp;      // [psplits][T][Vp] partial h W^T (K split), Vp a multiple of 4
   int psplits, Vp;
   bool direct;    // its rows are h's as they are
+  int slots;      // CUs
   int v0, piece;
 };
 
@@ -671,21 +703,20 @@ struct HeadGemm {
 // through LDS for those).  DIRECT: for up to 64 rows of a width that is a
 // multiple of 64 the rows are read where they are and their 1/rms is formed
 // from the staged pieces, so nothing has to be launched before this.
-template <class C, bool DIRECT>
-__global__ __launch_bounds__(C::NT, C::WPS) void k_head_stats(HeadGemm p) {
-  static_assert(C::NT % C::BM == 0 || C::NT % (C::BM / C::WM) == 0, "rows per thread");
-  constexpr int RED = C::WN * C::BM * 4;  // bytes of the rows' maxima, and of their sums
+template <class C>
+struct HeadStats {
+  static constexpr int RED = C::WN * C::BM * 4;  // bytes of the rows' maxima, and of their sums
   // the tile of logits, or a part of it, and the rows' statistics behind it
-  constexpr int ZR = C::BM * C::BN * 4 + 2 * RED <= C::SMEM ? C::BM : C::BM / C::WM;
-  constexpr int ZB = ZR * C::BN * 4;
-  constexpr int SMEM = ZB + 2 * RED > C::SMEM ? ZB + 2 * RED : C::SMEM;
-  __shared__ __align__(16) uint8_t smem[SMEM];
+  static constexpr int ZR = C::BM * C::BN * 4 + 2 * RED <= C::SMEM ? C::BM : C::BM / C::WM;
+  static constexpr int ZB = ZR * C::BN * 4;
+  static constexpr int SMEM = ZB + 2 * RED > C::SMEM ? ZB + 2 * RED : C::SMEM;
+};
+template <class C, bool DIRECT>
+MOE_DEV void head_stats(const HeadGemm& p, int n, int m0, int nt, uint8_t* smem) {
+  constexpr int RED = HeadStats<C>::RED, ZR = HeadStats<C>::ZR, ZB = HeadStats<C>::ZB;
   float(*rm)[C::BM] = reinterpret_cast<float(*)[C::BM]>(smem + ZB);
   float(*rs)[C::BM] = reinterpret_cast<float(*)[C::BM]>(smem + ZB + RED);
-  const int n = DIRECT ? p.T : *p.count, nvb = (p.V + C::BN - 1) / C::BN;
-  int mt, nt;
-  if (!head_tile(blockIdx.x, (n + C::BM - 1) / C::BM, nvb, mt, nt)) return;
-  const int m0 = mt * C::BM, n0 = nt * C::BN;
+  const int n0 = nt * C::BN, nvb = (p.V + C::BN - 1) / C::BN;
   HeadSrc sa = {reinterpret_cast<const char*>(p.hc + (int64_t)m0 * p.Hp), (uint32_t)p.Hp * 2, C::BM, p.Hp};
   if (DIRECT) sa = HeadSrc{reinterpret_cast<const char*>(p.h), (uint32_t)p.h_stride * 2, n, p.H};
   const HeadSrc sb = {reinterpret_cast<const char*>(p.w + (int64_t)n0 * p.w_stride), (uint32_t)p.w_stride * 2,
@@ -795,6 +826,23 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_head_stats(HeadGemm p) {
     o[1] = s;
   }
 }
+template <class C, bool DIRECT>
+__global__ __launch_bounds__(C::NT, C::WPS) void k_head_stats(HeadGemm p) {
+  using Half = typename C::Half;
+  constexpr int SMEM = HeadStats<C>::SMEM > HeadStats<Half>::SMEM ? HeadStats<C>::SMEM : HeadStats<Half>::SMEM;
+  __shared__ __align__(16) uint8_t smem[SMEM];
+  const int n = DIRECT ? p.T : *p.count, nm = (n + C::BM - 1) / C::BM, nvb = (p.V + C::BN - 1) / C::BN;
+  int mt, nt, half = -1;
+  if (std::is_same<C, Half>::value ? !head_tile(blockIdx.x, nm, nvb, mt, nt)
+                                   : !head_tile_tail(blockIdx.x, nm, nvb, p.slots, mt, nt, half))
+    return;
+  if (half < 0) {
+    head_stats<C, DIRECT>(p, n, mt * C::BM, nt, smem);
+  } else {
+    const int m0 = mt * C::BM + half * Half::BM;
+    if (m0 < n) head_stats<Half, DIRECT>(p, n, m0, nt, smem);
+  }
+}
 
 // The tile of a wave's accumulators as bf16 rows in LDS, for stores of whole
 // rows: 8 bytes per lane straight to memory would leave 32-byte pieces of 16
@@ -825,12 +873,8 @@ struct HeadOut {
 // Backward: G, columns [v0, v0 + piece), of every row of the tiles (zeros
 // behind the last row and past the vocabulary).
 template <class C>
-__global__ __launch_bounds__(C::NT, C::WPS) void k_head_grad(HeadGemm p) {
-  __shared__ __align__(16) uint8_t smem[C::SMEM];
-  const int n = *p.count;
-  int mt, nt;
-  if (!head_tile(blockIdx.x, (n + C::BM - 1) / C::BM, p.piece / C::BN, mt, nt)) return;
-  const int m0 = mt * C::BM, n0 = p.v0 + nt * C::BN;
+MOE_DEV void head_grad(const HeadGemm& p, int m0, int nt, uint8_t* smem) {
+  const int n0 = p.v0 + nt * C::BN;
   const HeadSrc sa = {reinterpret_cast<const char*>(p.hc + (int64_t)m0 * p.Hp), (uint32_t)p.Hp * 2, C::BM, p.Hp};
   // a piece's last tiles may lie past the vocabulary: they read its last row and write zeros
   const int nb = min(n0, p.V - 1);
@@ -877,6 +921,19 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_head_grad(HeadGemm p) {
   lds_barrier();
   HeadOut<C>::store(smem, reinterpret_cast<char*>(p.g + (int64_t)m0 * p.piece + (n0 - p.v0)), (int64_t)p.piece * 2,
                     C::BM, C::BN * 2);
+}
+template <class C>
+__global__ __launch_bounds__(C::NT, C::WPS) void k_head_grad(HeadGemm p) {
+  using Half = typename C::Half;
+  __shared__ __align__(16) uint8_t smem[C::SMEM > Half::SMEM ? C::SMEM : Half::SMEM];
+  const int nm = (*p.count + C::BM - 1) / C::BM, nn = p.piece / C::BN;
+  int mt, nt, half = -1;
+  if (std::is_same<C, Half>::value ? !head_tile(blockIdx.x, nm, nn, mt, nt)
+                                   : !head_tile_tail(blockIdx.x, nm, nn, p.slots, mt, nt, half))
+    return;
+  // rows behind the last one get their zeros from either half
+  if (half < 0) head_grad<C>(p, mt * C::BM, nt, smem);
+  else head_grad<Half>(p, mt * C::BM + half * Half::BM, nt, smem);
 }
 
 // u (slab of this workgroup's share of K) += G W over a piece.
@@ -1610,6 +1667,10 @@ int head_tile_logits(int T, int H, int V, bool bwd, int cus, int* splits) {
   for (int i = 0; i < kHeadShapeCount; ++i)
     for (int s = 1; s <= 16 && (s == 1 || (s <= (H + 63) / 64 && (int64_t)T * V * s <= (16 << 20))); ++s) {
       float c = head_cost(kHeadShapes[i], T, V, H, s, cus, 1.0f);
+      if (i == 0 && s == 1) {  // halves in the last round (head_tile_tail): those of shape 2
+        const int tiles = cdiv(T, 256) * cdiv(V, 256), last = tiles % cus;
+        if (last > 0 && last * 2 <= cus) c -= (float)((H + 63) / 64) * 0.52f + 2.0f;
+      }
       if (s > 1) {
         const float bytes = (float)T * (float)V * (float)s * 8.0f;
         c += bytes / 8e6f + (bwd ? 6.0f : 1.0f + (float)V * (float)s * 2.5e-4f);
@@ -1645,8 +1706,9 @@ int head_tile_dz(int T, int H, int K, int cus) {
   }
   return best;
 }
-// Workgroups for nm x nn tiles (a multiple of the 8 XCDs).
-int head_grid(int64_t nm, int64_t nn) { return cdiv(nm * nn, 8) * 8; }
+// Workgroups for nm x nn tiles (a multiple of the 8 XCDs); with `halves` of a
+// last round besides.
+int head_grid(int64_t nm, int64_t nn, int halves = 0) { return cdiv(nm * nn, 8) * 8 + cdiv(halves, 8) * 8; }
 int head_cus() {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) dev = 0;
@@ -1777,6 +1839,7 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
   g.Hp = p.Hp;
   g.V = p.V;
   g.top = p.top;
+  g.slots = head_cus();
   g.rows = q.rows;
   g.count = q.count;
   g.r = q.r;
@@ -1851,7 +1914,8 @@ void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
   }
   head_dispatch(p.tile_l, [&](auto c) {
     using C = decltype(c);
-    hipLaunchKernelGGL((k_head_stats<C, false>), dim3(head_grid(cdiv(p.T, C::BM), f.nvb)), dim3(C::NT), 0, s, g);
+    hipLaunchKernelGGL((k_head_stats<C, false>), dim3(head_grid(cdiv(p.T, C::BM), f.nvb, C::FIVE ? g.slots : 0)),
+                       dim3(C::NT), 0, s, g);
   });
   hipLaunchKernelGGL(k_head_finish<false>, dim3(cdiv(p.T, 4)), dim3(256), 0, s, f);
 }
@@ -1874,7 +1938,8 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
     } else {
       head_dispatch(p.tile_l, [&](auto c) {
         using C = decltype(c);
-        hipLaunchKernelGGL(k_head_grad<C>, dim3(head_grid(cdiv(p.T, C::BM), p.piece / C::BN)), dim3(C::NT), 0, s, g);
+        hipLaunchKernelGGL(k_head_grad<C>, dim3(head_grid(cdiv(p.T, C::BM), p.piece / C::BN, C::FIVE ? g.slots : 0)),
+                           dim3(C::NT), 0, s, g);
       });
     }
     if (p.distill)

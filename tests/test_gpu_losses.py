@@ -116,6 +116,33 @@ def test_distillation(torch_gpu, T, H, V, K, nans):
     _close(gw, d_w, b_w, "d_w")
 
 
+@pytest.mark.parametrize("kind", ["ce", "distill"])
+@pytest.mark.parametrize("T,H,V,ignored", [(2100, 520, 9000, 0.0), (2100, 520, 9000, 0.9), (2100, 520, 9000, 0.96),
+                                           (2900, 256, 7001, 0.1)])
+def test_head_last_round(torch_gpu, T, H, V, ignored, kind):
+    """Large tiles whose last round is done in halves, some of them without rows."""
+    h, w, y, dl, g = _inputs(T, H, V, ignored=ignored)
+    if kind == "ce":
+        ref = lr.ce_ref(h, w, y)
+        lse, loss, b_lse, b_loss = ref.loss()
+        got, got_lse = moe.lm_head_loss(h, w, y)
+        gh, gw = moe.lm_head_loss_backward(h, w, y, got, got_lse, dl, weight_grad=True)
+    else:
+        ids, tl = _teacher(T, 5, V, g)
+        tl = torch.where(tl.isnan() & (ids >= 0) & (ids < V), 0.5, tl)
+        ids = torch.where((y < 0)[:, None], -1, ids).int()
+        ref, have, q = lr.distill_ref(h, w, ids, tl)
+        lse, loss, logp, b_lse, b_loss, b_logp = lr.distill_loss(ref, ids, have, q)
+        got, got_lse, got_logp = moe.lm_head_distill(h, w, ids, tl)
+        _close(got_logp, logp, b_logp, "logp")
+        gh, gw = moe.lm_head_distill_backward(h, w, ids, tl, got_lse, got_logp, dl, weight_grad=True)
+    _close(got_lse, lse, b_lse, "lse")
+    _close(got, loss, b_loss, "loss")
+    d_h, b_h, d_w, b_w = ref.grads(dl, True)
+    _close(gh, d_h, b_h, "d_h")
+    _close(gw, d_w, b_w, "d_w")
+
+
 @pytest.mark.parametrize("T,H,V", [(5, 64, 300), (70, 136, 301), (300, 64, 500), (1100, 64, 129), (9, 4096, 300)])
 def test_distillation_lowest_logits(torch_gpu, T, H, V):
     """Teacher logits of the type's lowest value are slots that are there: probability 0 beside others, equal where
