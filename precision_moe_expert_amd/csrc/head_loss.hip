@@ -645,7 +645,8 @@ MOE_DEV bool head_tile(int bid, int nm, int nn, int& m, int& n) {
   return true;
 }
 // The same where the last round of tiles would leave half of the CUs idle: its
-// tiles are done as two halves of BM/2 rows each.  Halves: `half` is 0 or 1;
+// tiles are done as two halves of BM/2 rows each (2867 rows of 2048 x 50257:
+// 523 -> 487 us; 3686 of 7168 x 32000: 1365 -> 1320).  Halves: `half` is 0 or 1;
 // -1: a whole tile.
 MOE_DEV bool head_tile_tail(int bid, int nm, int nn, int slots, int& m, int& n, int& half) {
   const int nt = nm * nn;
