@@ -1627,7 +1627,7 @@ struct HeadShape {
 };
 constexpr HeadShape kHeadShapes[] = {
     {256, 256, 1, 1.36f, 7.0f}, {256, 128, 1, 0.78f, 5.0f}, {128, 256, 1, 0.84f, 5.0f},
-    {128, 128, 1, 0.54f, 4.0f}, {64, 128, 2, 0.60f, 3.5f},
+    {128, 128, 1, 0.54f, 4.0f}, {64, 128, 2, 0.60f, 3.5f}, {192, 128, 1, 0.72f, 4.5f},
 };
 constexpr int kHeadShapeCount = sizeof(kHeadShapes) / sizeof(kHeadShapes[0]);
 template <typename F>
@@ -1637,6 +1637,7 @@ void head_dispatch(int shape, F f) {
     case 1: f(HeadTile<256, 128, 4, 2, 3, 2>()); break;
     case 2: f(HeadTile<128, 256, 2, 4, 3, 2>()); break;
     case 3: f(HeadTile<128, 128, 2, 4, 4, 2>()); break;
+    case 5: f(HeadTile<192, 128, 4, 2, 3, 2>()); break;
     default: f(HeadTile<64, 128, 2, 2, 3, 2>()); break;
   }
 }
@@ -1656,7 +1657,9 @@ float head_cost(const HeadShape& t, int M, int N, int K, int splits, int cus, fl
 // The cheapest tile for h W^T.  Within 0.3% of the best tile of each of those
 // shapes on average, 10% at most (always 256 x 256: 1.6 times the best at 16
 // rows of 512 x 8000 and 1.7 at 64 rows of 7168 x 32000; always 64 x 128: 2
-// times at 1500 rows).
+// times at 1500 rows).  The 192-row tile is for 129 to 192 rows and for such
+// remainders: 190 rows of 7168 x 32000 129 -> 115 us (256 x 128), gradient of
+// 180 rows of 2048 x 32000 83 -> 70.
 // With K split (splits > 1) the slabs are written and read at about 8 MB per
 // microsecond, the forward reads a row of them with one block and the backward
 // has a launch more.  Against unsplit: forward of 2 x 6488 x 1118 45 -> 19 us,
@@ -1731,11 +1734,12 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
     o = (o + bytes + 255) / 256 * 256;
     return at;
   };
-  const size_t t = (size_t)T, rows = (t + 255) / 256 * 256;  // whole tiles
   p.Hp = (H + 63) / 64 * 64;
   const int cus = head_cus();
   p.tile_l = head_tile_logits(T, H, V, bwd, cus, &p.psplits);
   p.bm = kHeadShapes[p.tile_l].bm;
+  const size_t t = (size_t)T, r256 = (t + 255) / 256 * 256, r192 = (t + 191) / 192 * 192;
+  const size_t rows = r256 > r192 ? r256 : r192;  // whole tiles of any shape
   if (bwd) {
     // columns of G per piece: 512 MB of G, at least 256 columns (256 MB, which
     // the last-level cache would hold: 2% slower at 8192 x 7168 x 32000 and 14%

@@ -116,6 +116,16 @@ def test_distillation(torch_gpu, T, H, V, K, nans):
     _close(gw, d_w, b_w, "d_w")
 
 
+@pytest.mark.parametrize("T,H,V", [(130, 256, 24001), (192, 520, 24001), (193, 512, 24001), (370, 520, 16001), (560, 256, 9001)])
+def test_cross_entropy_between_tiles(torch_gpu, T, H, V):
+    test_cross_entropy(torch_gpu, T, H, V, 1e-6, 0.9)
+
+
+@pytest.mark.parametrize("T,H,V", [(150, 256, 24001), (192, 520, 24001), (370, 256, 16001)])
+def test_distillation_between_tiles(torch_gpu, T, H, V):
+    test_distillation(torch_gpu, T, H, V, 7, False)
+
+
 @pytest.mark.parametrize("kind", ["ce", "distill"])
 @pytest.mark.parametrize("T,H,V,ignored", [(2100, 520, 9000, 0.0), (2100, 520, 9000, 0.9), (2100, 520, 9000, 0.96),
                                            (2900, 256, 7001, 0.1)])
