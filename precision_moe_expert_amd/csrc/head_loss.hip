@@ -1669,7 +1669,7 @@ int head_tile_logits(int T, int H, int V, bool bwd, int cus, int* splits) {
   int best = 0;
   float least = -1.0f;
   for (int i = 0; i < kHeadShapeCount; ++i)
-    for (int s = 1; s <= 16 && (s == 1 || (s <= (H + 63) / 64 && (int64_t)T * V * s <= (16 << 20))); ++s) {
+    for (int s = 1; s <= 16 && (s == 1 || (s <= (H + 63) / 64 && (int64_t)T * ((V + 3) & ~3) * s <= (16 << 20))); ++s) {
       float c = head_cost(kHeadShapes[i], T, V, H, s, cus, 1.0f);
       if (i == 0 && s == 1) {  // halves in the last round (head_tile_tail): those of shape 2
         const int tiles = cdiv(T, 256) * cdiv(V, 256), last = tiles % cus;
