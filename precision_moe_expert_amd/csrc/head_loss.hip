@@ -491,12 +491,12 @@ struct HeadTile {
   using Half = std::conditional_t<FIVE, HeadTile<BM_ / 2, BN_, WM_, WN_, 3, WPS_>, HeadTile>;
 };
 
-// SQ (64 rows of A, 256 threads): also sums into *ss the squares of the 16
+// SQ (four threads per row of A): also sums into *ss the squares of the 16
 // values that thread t sees per stage of row t / 4 of A.
 template <class C, bool KMA, bool KMB, bool SQ = false>
 MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[C::MI][C::NJ], uint8_t* smem,
                      float* ss = nullptr) {
-  static_assert(!SQ || (!KMA && C::BM == 64 && C::NT == 256 && !C::FIVE), "rows per thread");
+  static_assert(!SQ || (!KMA && C::NT == 4 * C::BM && !C::FIVE), "rows per thread");
   using OA = HeadOperand<C::BM, KMA, C::NW>;
   using OB = HeadOperand<C::BN, KMB, C::NW>;
   constexpr int S = C::S, MI = C::MI, NJ = C::NJ, NPER = OA::ND + OB::ND;
@@ -701,8 +701,8 @@ struct HeadGemm {
 
 // Forward: per row and block of BN columns the maximum of y = l log2 e and the
 // sum of 2^(y - maximum), and the logits at the target's ids (the tile goes
-// through LDS for those).  DIRECT: for up to 64 rows of a width that is a
-// multiple of 64 the rows are read where they are and their 1/rms is formed
+// through LDS for those).  DIRECT: for one tile row (up to 128) of a width that is
+// a multiple of 64 the rows are read where they are and their 1/rms is formed
 // from the staged pieces, so nothing has to be launched before this.
 template <class C>
 struct HeadStats {
@@ -1870,9 +1870,8 @@ static void launch_head_part(const HeadPlan& p, const HeadGemm& g, hipStream_t s
 }
 
 void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
-  using Direct = HeadTile<64, 128, 2, 2, 3, 2>;
   const bool part = p.psplits > 1;
-  const bool direct = p.H % 64 == 0 && (part ? p.T <= HEAD_SAME : p.T <= Direct::BM && p.bm == Direct::BM);
+  const bool direct = p.H % 64 == 0 && (part ? p.T <= HEAD_SAME : p.T <= p.bm && p.tile_l >= 2 && p.tile_l <= 4);
   HeadGemm g = direct ? HeadGemm{} : head_common(p, a, s);
   g.h = a.h;
   g.h_stride = a.h_stride;
@@ -1913,7 +1912,11 @@ void launch_head_loss(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
     return;
   }
   if (direct) {
-    hipLaunchKernelGGL((k_head_stats<Direct, true>), dim3(head_grid(1, f.nvb)), dim3(Direct::NT), 0, s, g);
+    head_dispatch(p.tile_l, [&](auto c) {
+      using C = decltype(c);
+      if constexpr (C::NT == 4 * C::BM)
+        hipLaunchKernelGGL((k_head_stats<C, true>), dim3(head_grid(1, f.nvb)), dim3(C::NT), 0, s, g);
+    });
     hipLaunchKernelGGL(k_head_finish<true>, dim3(cdiv(p.T, 4)), dim3(256), 0, s, f);
     return;
   }

@@ -116,6 +116,27 @@ def test_distillation(torch_gpu, T, H, V, K, nans):
     _close(gw, d_w, b_w, "d_w")
 
 
+@pytest.mark.parametrize("T,H,V", [(66, 1024, 50001), (100, 1024, 32000), (128, 1536, 30001), (65, 512, 24001)])
+def test_forward_of_one_tile_row(torch_gpu, T, H, V):
+    """65 to 128 rows, read where they are, strided ones too."""
+    h, w, y, _, g = _inputs(T, H, V)
+    wide = torch.full((T, H + 16), math.nan, device="cuda").bfloat16()
+    wide[:, :H] = torch.where((y >= 0)[:, None], h, math.nan)
+    ref = lr.ce_ref(h, w, y, 1e-6, 0.8)
+    lse, loss, b_lse, b_loss = ref.loss()
+    got, got_lse = moe.lm_head_loss(wide[:, :H], w, y, logit_scale=0.8)
+    _close(got_lse, lse, b_lse, "lse")
+    _close(got, loss, b_loss, "loss")
+    ids, tl = _teacher(T, 33, V, g)
+    tl = torch.where(tl.isnan() & (ids >= 0) & (ids < V), 0.5, tl)
+    ref, have, q = lr.distill_ref(h, w, ids, tl, 0.7)
+    lse, loss, logp, b_lse, b_loss, b_logp = lr.distill_loss(ref, ids, have, q)
+    got, got_lse, got_logp = moe.lm_head_distill(h, w, ids, tl, teacher_scale=0.7)
+    _close(got_lse, lse, b_lse, "lse")
+    _close(got_logp, logp, b_logp, "logp")
+    _close(got, loss, b_loss, "loss")
+
+
 @pytest.mark.parametrize("T,H,V", [(130, 256, 24001), (192, 520, 24001), (193, 512, 24001), (370, 520, 16001), (560, 256, 9001)])
 def test_cross_entropy_between_tiles(torch_gpu, T, H, V):
     test_cross_entropy(torch_gpu, T, H, V, 1e-6, 0.9)
