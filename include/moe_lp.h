@@ -416,8 +416,10 @@ moe_status moe_lm_head_loss(const moe_lm_head* head, const void* h_bf16, const v
  * With p = softmax(logits), r = 1/sqrt(mean(h^2) + norm_eps) (1 without a norm):
  *   G[t][v] = logit_scale * r_t * d_loss[t] * (p[t][v] - [v = y_t])
  *   u = G W,  d_h = u - r^2 h mean(h u) (without a norm: u),  d_W = G^T h.
- * G is rounded to bf16 once, as the operand of the two products; sums, u and
- * the norm's terms are fp32.  d_h and d_w must not overlap the inputs.
+ * G is rounded to bf16 as the operand of the two products, and what that takes
+ * off its entries at the targets is added to u and to d_W (up to 65536 targets);
+ * sums, u and the norm's terms are fp32, d_h and d_W are rounded once.  d_h and
+ * d_w must not overlap the inputs.
  * T = 0 writes zeros to d_w. */
 moe_status moe_lm_head_loss_backward(const moe_lm_head* head, const void* h_bf16, const void* w_lm_bf16,
                                      const int32_t* targets, const float* loss, const float* lse,

@@ -10,10 +10,11 @@
 //             bf16, its entries at the target's ids replaced by
 //             s r g (p - q); then u += G W (dL/dz r) and d_W = G^T h.  One such
 //             entry is as large as the rest of its row together, so its bf16
-//             rounding (up to 2^-8) would be the gradient's where few rows
-//             count.  Where these entries are not many they are therefore kept
-//             in fp32 beside a G that is 0 there; entry x row of W is added to
-//             u, and entry x row of h to d_W
+//             rounding (up to 2^-8) would show in the gradients as much as the
+//             gradients' own.  What that rounding takes off is therefore added
+//             to u (times the id's row of W) and to d_W (times the row of h),
+//             both before they are rounded: the entries and the rest of G
+//             cancel in a trained head's d_W, so nothing may be rounded between
 // with r = 1 / sqrt(mean h^2 + eps), s the logit scale and g = dL/dloss.
 // r s multiplies the fp32 accumulators: the products' operands are the bf16
 // inputs themselves, and G is the one value that is rounded on the way.
@@ -227,7 +228,6 @@ struct HeadRowsArgs {
   HeadRow* info;
   int32_t* eid;          // backward, cross entropy: the row's target (-1: none) and G there
   float* ev;
-  int32_t* uses;         // entries of each id, null: not counted
   float* lq;
 };
 
@@ -362,7 +362,6 @@ __global__ __launch_bounds__(256) void k_head_gather(HeadRowsArgs p) {
       if (p.loss != nullptr) {
         p.eid[c] = w.tgt;
         p.ev[c] = w.f * expm1f(-p.loss[t]);  // p - 1 = exp(-loss) - 1
-        if (p.uses != nullptr) atomicAdd(&p.uses[w.tgt], 1);
       }
     }
     p.info[c] = w;
@@ -409,6 +408,8 @@ struct HeadSrc {
   uint32_t ld;
   int mn;
   int k;
+  const int32_t* list = nullptr;  // rows taken through a list (HeadOperand's ROWS)
+  int zero = 0;                   // a row of zeros
 };
 
 // global_load_lds with a uniform base and a 32-bit lane offset.
@@ -416,14 +417,20 @@ MOE_DEV void hl_dma(const char* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
 
-// One operand of a tile: R rows (or columns) by 64 K per stage.
-template <int R, bool KM, int NW>
+// The same with an address of each lane's own.
+MOE_DEV void hl_dma_at(const char* addr, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(addr) : "memory");
+}
+
+// One operand of a tile: R rows (or columns) by 64 K per stage.  ROWS (m
+// contiguous): K row k is row list[k] of the matrix at p, a row of zeros past k.
+template <int R, bool KM, int NW, bool ROWS = false>
 struct HeadOperand {
   static constexpr int BYTES = R * 128;
   static constexpr int ND = R / 8 / NW;  // DMAs per wave and stage
   static constexpr int RB = KM ? R * 2 : 128;
   static constexpr int LPR = RB / 16;     // lanes per row of a DMA
-  static_assert(R % (8 * NW) == 0 && (!KM || R >= 128), "tile");
+  static_assert(R % (8 * NW) == 0 && (!KM || R >= 128) && (!ROWS || (KM && LPR == 32)), "tile");
   HeadSrc s;
   uint32_t off[ND];
   MOE_DEV static int row_of(int wave, int lane, int j) { return (wave * ND + j) * (64 / LPR) + lane / LPR; }
@@ -435,7 +442,7 @@ struct HeadOperand {
       if (KM) {
         const int f = (row & 3) | ((row >> 1) & 4);
         const int col = min((((q >> 1) ^ f) << 4) + (q & 1) * 8, s.mn - 8);
-        off[j] = (uint32_t)row * s.ld + col * 2;
+        off[j] = (ROWS ? 0 : (uint32_t)row * s.ld) + col * 2;
       } else {
         off[j] = (uint32_t)min(row, s.mn - 1) * s.ld + ((q ^ ((row >> 1) & 7)) << 4);
       }
@@ -445,6 +452,17 @@ struct HeadOperand {
   // reach past the end of K.
   template <bool LAST>
   MOE_DEV void issue(int j, int kt, uint32_t lds, int wave, int lane) const {
+    if constexpr (ROWS) {
+      // the two K rows of this DMA, by scalar loads (the list has 64 more
+      // entries behind it, whatever they hold)
+      typedef const __attribute__((address_space(4))) int32_t* const_i32;
+      const int k0 = __builtin_amdgcn_readfirstlane(kt * 64 + (wave * ND + j) * 2);
+      const const_i32 l = (const_i32)(uintptr_t)(s.list + k0);
+      const int a = k0 < s.k ? l[0] : s.zero, b = k0 + 1 < s.k ? l[1] : s.zero;
+      hl_dma_at(s.p + (int64_t)(lane < 32 ? a : b) * s.ld + off[j],
+                __builtin_amdgcn_readfirstlane(lds + (wave * ND + j) * 1024));
+      return;
+    }
     uint32_t o = off[j];
     const int over = kt * 64 + 64 - s.k;  // K past the end (uniform)
     if (LAST && over > 0) {
@@ -501,13 +519,14 @@ struct HeadTile {
 };
 
 // SQ (four threads per row of A): also sums into *ss the squares of the 16
-// values that thread t sees per stage of row t / 4 of A.
-template <class C, bool KMA, bool KMB, bool SQ = false>
+// values that thread t sees per stage of row t / 4 of A.  ADD: adds to acc, and
+// B's rows come through a list.
+template <class C, bool KMA, bool KMB, bool SQ = false, bool ADD = false>
 MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[C::MI][C::NJ], uint8_t* smem,
                      float* ss = nullptr) {
   static_assert(!SQ || (!KMA && C::NT == 4 * C::BM && !C::FIVE), "rows per thread");
   using OA = HeadOperand<C::BM, KMA, C::NW>;
-  using OB = HeadOperand<C::BN, KMB, C::NW>;
+  using OB = HeadOperand<C::BN, KMB, C::NW, ADD>;
   constexpr int S = C::S, MI = C::MI, NJ = C::NJ, NPER = OA::ND + OB::ND;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   OA oa;
@@ -529,10 +548,11 @@ MOE_DEV void head_mm(const HeadSrc& sa, const HeadSrc& sb, int KT, f32x4 (&acc)[
   };
   const int ba = OA::lane_base((wave / C::WN) * MI * 16, lane);
   const int bb = OB::lane_base((wave % C::WN) * NJ * 16, lane);
+  if (!ADD)
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+      for (int j = 0; j < NJ; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int s = 0; s < S; ++s)
     if (s < KT)
@@ -689,9 +709,12 @@ struct HeadGemm {
   const int32_t* count;   // rows, splits of G W
   const float* r;         // [count]
   int32_t* eid;           // [count][top] G's entries at the target's ids: id (-1: none),
-  float* ev;              //   value (distillation: exact only)
-  bool exact;             // they are kept apart from G
-  int32_t* uses;          // [V] entries of each id, null: not counted
+  float* ev;              //   value (null: none are kept)
+  bool exact;             // what rounding them takes off is added to u and d_w
+  const int2* rtile;      // d_w: first row and rows of each 256 ids in rlist and rem
+  const int32_t* rlist;   // rows of hc with an entry among those ids
+  const uint16_t* rem;    // [..][256] what rounding took off those entries
+  int zero_row;           // of hc
   const HeadRow* info;    // [..]
   float scale;
   const int32_t* ids;
@@ -918,14 +941,13 @@ MOE_DEV void head_grad(const HeadGemm& p, int m0, int nt, uint8_t* smem) {
   if (full) write(std::true_type());
   else write(std::false_type());
   if (!p.distill) {
-    // the lane that wrote a row's target puts s r g (p - 1) over it, or 0 where
-    // such entries are kept apart
+    // the lane that wrote a row's target puts s r g (p - 1) over it
 #pragma unroll
     for (int i = 0; i < C::MI; ++i) {
       const int tc = info[i].tgt - n0 - wn;
       if (tc >= 0 && tc < C::NJ * 16 && ((tc >> 2) & 3) == lg)
         *reinterpret_cast<uint16_t*>(HeadOut<C>::at(smem, wm + i * 16 + ln, wn + tc)) =
-            p.exact ? 0 : (uint16_t)f32_to_bf16_bits(p.ev[m0 + wm + i * 16 + ln]);
+            (uint16_t)f32_to_bf16_bits(p.ev[m0 + wm + i * 16 + ln]);
     }
   }
   lds_barrier();
@@ -990,7 +1012,8 @@ MOE_DEV void head_dz(const HeadGemm& p, int bid, uint8_t* smem) {
   }
 }
 
-// d_w rows [v0, v0 + piece) = G^T h.
+// d_w rows [v0, v0 + piece) = G^T h, with rem^T h of the rows that have entries
+// there in the same accumulators: d_w is rounded once.
 template <class C>
 MOE_DEV void head_dw(const HeadGemm& p, int bid, uint8_t* smem) {
   const int n = *p.count, M = min(p.piece, p.V - p.v0);
@@ -1007,6 +1030,17 @@ MOE_DEV void head_dw(const HeadGemm& p, int bid, uint8_t* smem) {
     for (int i = 0; i < C::MI; ++i)
 #pragma unroll
       for (int j = 0; j < C::NJ; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  if (p.rtile != nullptr) {
+    static_assert(C::BM == 256, "rem's width");
+    const int2 r = p.rtile[(p.v0 + m0) / 256];
+    const int first = __builtin_amdgcn_readfirstlane(r.x), k = __builtin_amdgcn_readfirstlane(r.y);
+    if (k > 0) {
+      const HeadSrc ra = {reinterpret_cast<const char*>(p.rem + (int64_t)first * 256), 512, 256, k};
+      const HeadSrc rb = {reinterpret_cast<const char*>(p.hc + n0), (uint32_t)p.Hp * 2, p.Hp - n0, k, p.rlist + first,
+                          p.zero_row};
+      head_mm<C, true, true, false, true>(ra, rb, (k + 63) / 64, acc, smem);
+    }
   }
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
   const int wm = wave / C::WN * C::MI * 16, wn = wave % C::WN * C::NJ * 16;
@@ -1105,7 +1139,7 @@ __global__ __launch_bounds__(256) void k_head_part_grad(HeadGemm p, int bm) {
     for (int e = 0; e < 4; ++e) {
       const int at = v + k * 4 + e;
       x[k * 4 + e] = c < n && at < p.V ? w.f * hl_exp2(fmaf(z[e], w.f2, -w.l2)) : 0.0f;
-      if (!p.distill && at == w.tgt && at < p.V) x[k * 4 + e] = p.exact ? 0.0f : p.ev[c];
+      if (!p.distill && at == w.tgt && at < p.V) x[k * 4 + e] = p.ev[c];
     }
   }
   *reinterpret_cast<u32x4*>(p.g + (int64_t)c * p.piece + v) =
@@ -1305,17 +1339,15 @@ __global__ __launch_bounds__(256) void k_head_part_finish(HeadGemm g, HeadFinish
 }
 
 // Distillation's backward: the entries s r g (p - q) at the slots' ids, from
-// the forward's log-probs, one wave per row.  Slots that repeat an id add their
-// q, and the first of them is the entry.  ev null: into G's columns [v0, v0 +
-// piece); else 0 goes there, and with the first piece the entries to ev and
-// their ids to eid.  8 us for 1500 rows of 33 slots: reads that wait for each
+// the forward's log-probs, one wave per row, into G's columns [v0, v0 + piece).
+// Slots that repeat an id add their q, and the first of them is the entry.  ev
+// not null: with the first piece the entries go to ev too, their ids to eid.  8 us for 1500 rows of 33 slots: reads that wait for each
 // other.
 __global__ __launch_bounds__(256) void k_head_targets(const int32_t* __restrict__ rows, const int32_t* __restrict__ count,
                                                       const int32_t* __restrict__ ids, const float* __restrict__ lq,
                                                       const float* __restrict__ logp, const HeadRow* __restrict__ info,
                                                       int top, int v0, int piece, uint16_t* __restrict__ g,
-                                                      int32_t* __restrict__ eid, float* __restrict__ ev,
-                                                      int32_t* __restrict__ uses) {
+                                                      int32_t* __restrict__ eid, float* __restrict__ ev) {
   __shared__ int sid[4][256];
   __shared__ float sq[4][256];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -1346,14 +1378,125 @@ __global__ __launch_bounds__(256) void k_head_targets(const int32_t* __restrict_
     if (ev != nullptr && v0 == 0) {
       eid[(int64_t)c * top + j] = first ? id : -1;
       ev[(int64_t)c * top + j] = x;
-      if (first && uses != nullptr) atomicAdd(&uses[id], 1);
     }
-    if (here && first) g[(int64_t)c * piece + v] = ev != nullptr ? 0 : (uint16_t)f32_to_bf16_bits(x);
+    if (here && first) g[(int64_t)c * piece + v] = (uint16_t)f32_to_bf16_bits(x);
   }
 }
 
-// Adds row c's fp32 entries [first, top) in steps of `step` times their rows of
-// W, 8 columns from col, to a and b; four rows' loads in flight.
+// What the rounding of an entry to bf16 took off (0 where that has no value).
+MOE_DEV float head_rem(float x) {
+  const float r = x - bf16_bits_to_f32(f32_to_bf16_bits(x));
+  return fabsf(r) < INFINITY ? r : 0.0f;
+}
+
+// For d_w: the tokens that have entries among each 256 ids, in order, and what
+// rounding took off those entries as rows of 256 bf16 (again rounded: 2^-16 of
+// the entry is left), which head_dw multiplies by the tokens' rows of h.  The
+// tokens of 256 ids lie behind the entries of all lower ids, so that one row per
+// entry is room enough; places that stay free get tile -1.
+struct HeadRem {
+  const int32_t* eid;
+  const float* ev;
+  const int32_t* count;
+  int top;
+  int2* tile;         // first place, tokens
+  int32_t* list;      // [places] token
+  int32_t* own;       // [places] tile
+  uint16_t* rem;      // [places][256]
+  uint16_t* zero_row; // of hc
+  int Hp;
+};
+// Row `at` by 32 lanes: token c's entries among ids lo .. lo + 255.
+MOE_DEV void head_rem_row(const HeadRem& p, int at, int c, int lo, int l, uint16_t* buf) {
+  const int32_t* id = p.eid + (int64_t)c * p.top;
+  const float* ev = p.ev + (int64_t)c * p.top;
+  *reinterpret_cast<u32x4*>(buf + l * 8) = (u32x4){0, 0, 0, 0};
+  for (int j = l; j < p.top; j += 32) {
+    const int v = id[j] - lo;
+    const float x = ev[j];
+    if (v >= 0 && v < 256) buf[v] = (uint16_t)f32_to_bf16_bits(head_rem(x));  // an id has one entry at most
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the lanes are of one wave
+  __builtin_amdgcn_wave_barrier();
+  *reinterpret_cast<u32x4*>(p.rem + (int64_t)at * 256 + l * 8) = *reinterpret_cast<const u32x4*>(buf + l * 8);
+}
+// One block per 256 ids finds its tokens; with `rows` it forms their rows too:
+// one block forms up to HEAD_FEW rows in less time than another launch takes,
+// but 8192 tokens of one id in 500 us.
+__global__ __launch_bounds__(1024) void k_head_rem_list(HeadRem p, bool rows) {
+  __shared__ __align__(16) uint16_t buf[32][256];
+  __shared__ int wsum[2][16], wown[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lo = blockIdx.x * 256, n = *p.count, total = n * p.top;
+  if (blockIdx.x == 0)
+    for (int i = tid; i < p.Hp / 8; i += 1024) *reinterpret_cast<u32x4*>(p.zero_row + i * 8) = (u32x4){0, 0, 0, 0};
+  int below = 0, mine = 0;
+#pragma unroll 8
+  for (int e = tid; e < total; e += 1024) {
+    const int id = p.eid[e];
+    below += id >= 0 && id < lo;
+    mine += (uint32_t)(id - lo) < 256u;
+  }
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) {
+    below += shfl_xor(below, x);
+    mine += shfl_xor(mine, x);
+  }
+  if (lane == 0) {
+    wsum[0][wave] = below;
+    wown[wave] = mine;
+  }
+  __syncthreads();
+  int first = 0, places = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) {
+    first += wsum[0][w];
+    places += wown[w];
+  }
+  int k = 0;
+  if (places > 0)
+    for (int c0 = 0, b = 1; c0 < n; c0 += 1024, b ^= 1) {
+      const int c = c0 + tid;
+      bool on = false;
+      if (c < n)
+#pragma unroll 8
+        for (int j = 0; j < p.top; ++j) on |= (uint32_t)(p.eid[(int64_t)c * p.top + j] - lo) < 256u;
+      const uint64_t m = __ballot(on);
+      if (lane == 0) wsum[b][wave] = __popcll(m);
+      __syncthreads();  // the sums before are in the other half, so one barrier is enough
+      int at = first + k + __popcll(m & ((1ull << lane) - 1));
+#pragma unroll
+      for (int w = 0; w < 16; ++w) {
+        const int v = wsum[b][w];
+        if (w < wave) at += v;
+        k += v;
+      }
+      if (on) {
+        p.list[at] = c;
+        p.own[at] = blockIdx.x;
+      }
+    }
+  if (tid == 0) p.tile[blockIdx.x] = make_int2(first, k);
+  // the last block's end with the last place
+  const int end = blockIdx.x + 1 < gridDim.x ? first + places : total;
+  if (!rows) {
+    for (int i = first + k + tid; i < end; i += 1024) p.own[i] = -1;
+    return;
+  }
+  __syncthreads();
+  for (int i = tid >> 5; i < k; i += 32) head_rem_row(p, first + i, p.list[first + i], lo, tid & 31, buf[tid >> 5]);
+}
+// The rows of all places, 32 lanes each.
+__global__ __launch_bounds__(256) void k_head_rem_rows(HeadRem p) {
+  __shared__ __align__(16) uint16_t buf[8][256];
+  const int g = threadIdx.x >> 5, at = blockIdx.x * 8 + g;
+  const int tile = at < *p.count * p.top ? p.own[at] : -1;
+  if (tile >= 0) head_rem_row(p, at, p.list[at], tile * 256, threadIdx.x & 31, buf[g]);
+}
+
+// Adds what rounding took off row c's entries [first, top), in steps of `step`,
+// times their rows of W, 8 columns from col, to a and b; four rows' loads in
+// flight.
 MOE_DEV void head_add_entries(const HeadGemm& p, int c, int first, int step, int col, f32x4& a, f32x4& b) {
   const int32_t* id = p.eid + (int64_t)c * p.top;
   const float* ev = p.ev + (int64_t)c * p.top;
@@ -1363,7 +1506,7 @@ MOE_DEV void head_add_entries(const HeadGemm& p, int c, int first, int step, int
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int at = k + j * step, v = at < p.top ? id[at] : -1;
-      x[j] = v >= 0 ? ev[at] : 0.0f;
+      x[j] = v >= 0 ? head_rem(ev[at]) : 0.0f;
       w[j] = (u32x4){0, 0, 0, 0};
       if (v >= 0) w[j] = *reinterpret_cast<const u32x4*>(p.w + (int64_t)v * p.w_stride + col);
     }
@@ -1377,87 +1520,6 @@ MOE_DEV void head_add_entries(const HeadGemm& p, int c, int first, int step, int
         b[2 * e + 1] = fmaf(x[j], bf16_bits_to_f32(w[j][e + 2] >> 16), b[2 * e + 1]);
       }
   }
-}
-
-// d_w rows at the ids of fp32 entries: += entry x row of h.  Block (e, j): entry
-// e and its columns 2048 j ..; the first entry of an id adds all of that id, in
-// their order, so results do not depend on the execution; the others' blocks
-// end.  Where there are many entries, uses[id] (how many have it) spares most of
-// them the search for others.  Reads a row of h and rewrites one of d_w per entry:
-// 81 us for 8192 entries of 7168 (352 MB, 4.3 TB/s).
-__global__ __launch_bounds__(256) void k_head_dw_entries(HeadGemm p) {
-  __shared__ int at[2048];
-  __shared__ int wsum[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int total = p.count[0] * p.top, e0 = blockIdx.x;
-  const int id = e0 < total ? p.eid[e0] : -1;
-  if (id < 0) return;
-  const bool alone = p.uses != nullptr && p.uses[id] == 1;
-  // bits of the thread's 8 entries from e (a multiple of 8) on that have the id
-  auto same = [&](int e) {
-    uint32_t bits = 0;
-    if (e < total) {  // the list is padded to a multiple of 8
-      const i32x4 x = *reinterpret_cast<const i32x4*>(p.eid + e), y = *reinterpret_cast<const i32x4*>(p.eid + e + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bits |= (uint32_t)(x[i] == id && e + i < total) << i;
-        bits |= (uint32_t)(y[i] == id && e + 4 + i < total) << (4 + i);
-      }
-    }
-    return bits;
-  };
-  if (!alone) {
-    int seen = 0;
-    for (int b = 0; b < e0; b += 2048) {
-      const int e = b + tid * 8;
-      uint32_t bits = same(e);
-      if (e + 8 > e0) bits &= e < e0 ? (1u << (e0 - e)) - 1 : 0;
-      seen |= bits != 0;
-    }
-    if (__syncthreads_or(seen)) return;
-  }
-  const int col = blockIdx.y * 2048 + tid * 8;
-  const bool in = col < p.H;
-  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int b = e0 / 2048 * 2048; b < (alone ? e0 + 1 : total); b += 2048) {
-    // the entries of this id among these 2048, in order: 8 per thread (none
-    // before e0)
-    const uint32_t mine = !alone ? same(b + tid * 8) : e0 - b - tid * 8 >= 0 && e0 - b - tid * 8 < 8 ? 1u << (e0 - b - tid * 8) : 0;
-    int before = __popc(mine);
-    const int k = before;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(before, d, 64);
-      if (lane >= d) before += v;
-    }
-    __syncthreads();  // the previous list has been read
-    if (lane == 63) wsum[wave] = before;
-    __syncthreads();
-    before -= k;
-    for (int w = 0; w < wave; ++w) before += wsum[w];
-    const int n = wsum[0] + wsum[1] + wsum[2] + wsum[3];
-    for (int i = 0; i < 8; ++i)
-      if ((mine >> i) & 1) at[before++] = tid * 8 + i;
-    __syncthreads();
-    if (in)
-      for (int j = 0; j < n; ++j) {
-        const int e = b + at[j];
-        const float x = p.ev[e];
-        const u32x4 q = *reinterpret_cast<const u32x4*>(p.hc + (int64_t)(e / p.top) * p.Hp + col);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[2 * i] = fmaf(x, bf16_bits_to_f32(q[i] & 0xFFFFu), acc[2 * i]);
-          acc[2 * i + 1] = fmaf(x, bf16_bits_to_f32(q[i] >> 16), acc[2 * i + 1]);
-        }
-      }
-  }
-  if (!in) return;
-  uint16_t* o = p.dw + (int64_t)id * p.H + col;
-  u32x4 q = *reinterpret_cast<const u32x4*>(o);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    q[i] = bf16x2_bits(bf16_bits_to_f32(q[i] & 0xFFFFu) + acc[2 * i], bf16_bits_to_f32(q[i] >> 16) + acc[2 * i + 1]);
-  *reinterpret_cast<u32x4*>(o) = q;
 }
 
 // d_h = u - r^2 h mean(h u), or u without a norm, u the sum of its slabs;
@@ -1768,19 +1830,23 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
   }
   p.r = take(rows * 4);
   p.info = take(rows * sizeof(HeadRow));
-  // G's entries at the target's ids are kept apart in fp32 up to 65536 of them
-  // (beyond, their roundings average out, and finding equal ids grows with the
-  // square), for distillation while their rows of W are at most a quarter of it
+  // what rounding takes off G's entries at the target's ids is added up to 65536
+  // of them, for distillation while their rows of W are at most a quarter of it
   const int64_t entries = (int64_t)T * top;
   p.exact = bwd && entries <= 65536 && (!distill || entries <= V / 4);
-  p.eid = take(p.exact || (bwd && !distill) ? t * top * 4 + 32 : 0);
-  p.uses = take(p.exact && entries > 2048 ? (size_t)V * 4 : 0);
-  p.ev = take(p.exact || (bwd && !distill) ? t * top * 4 : 0);
+  const bool keep = p.exact || (bwd && !distill);
+  p.eid = take(keep ? t * top * 4 : 0);
+  p.ev = take(keep ? t * top * 4 : 0);
+  p.rtile = take(p.exact ? (size_t)cdiv(V, 256) * 8 : 0);
+  p.rlist = take(p.exact ? (t * top + 64) * 4 : 0);
+  p.rown = take(p.exact ? t * top * 4 : 0);
+  p.rem = take(p.exact ? t * top * 512 : 0);
   p.flag = take(distill ? t : 0);
   p.rows = take(t * 4);
   p.cidx = take(t * 4);
   p.count = take(8);
-  p.hc = take(rows * p.Hp * 2);
+  p.hc = take((rows + p.exact) * p.Hp * 2);  // a row of zeros last
+  p.zero_row = (int)rows;
   p.lq = take(distill ? t * top * 4 : 0);
   p.lp = take(p.psplits > 1 ? t * ((V + 3) / 4 * 4) * p.psplits * 4 : 0);
   if (!bwd) {
@@ -1832,10 +1898,6 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
   q.info = reinterpret_cast<HeadRow*>(ws + p.info);
   q.eid = reinterpret_cast<int32_t*>(ws + p.eid);
   q.ev = reinterpret_cast<float*>(ws + p.ev);
-  if (a.dw != nullptr && p.exact && (int64_t)p.T * p.top > 2048) {  // one search of 2048 entries costs less
-    q.uses = reinterpret_cast<int32_t*>(ws + p.uses);
-    launch_zero_f32(reinterpret_cast<float*>(q.uses), p.V, s);
-  }
   q.lq = reinterpret_cast<float*>(ws + p.lq);
   if (flag != nullptr)
     hipLaunchKernelGGL(k_head_teacher, dim3(cdiv(p.T, 4)), dim3(256), 0, s, a.ids, a.tlogits, p.T, p.V, p.top,
@@ -1865,7 +1927,6 @@ static HeadGemm head_common(const HeadPlan& p, const HeadArgs& a, hipStream_t s)
   g.eid = q.eid;
   g.ev = p.distill && !p.exact ? nullptr : q.ev;
   g.exact = p.exact;
-  g.uses = q.uses;
   g.info = q.info;
   g.distill = p.distill;
   g.scale = a.scale;
@@ -1967,7 +2028,22 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
     if (p.distill)
       hipLaunchKernelGGL(k_head_targets, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.rows, g.count, a.ids,
                          reinterpret_cast<const float*>(a.ws + p.lq), a.logp, g.info, p.top, g.v0, p.piece, g.g, g.eid,
-                         p.exact ? g.ev : nullptr, g.uses);
+                         g.ev);
+    if (a.dw != nullptr && p.exact && i == 0) {
+      HeadRem r{g.eid, g.ev, g.count, p.top};
+      r.tile = reinterpret_cast<int2*>(a.ws + p.rtile);
+      r.list = reinterpret_cast<int32_t*>(a.ws + p.rlist);
+      r.own = reinterpret_cast<int32_t*>(a.ws + p.rown);
+      r.rem = reinterpret_cast<uint16_t*>(a.ws + p.rem);
+      r.zero_row = const_cast<uint16_t*>(g.hc) + (int64_t)p.zero_row * p.Hp;
+      r.Hp = p.Hp;
+      g.rtile = r.tile;
+      g.rlist = r.list;
+      g.rem = r.rem;
+      g.zero_row = p.zero_row;
+      hipLaunchKernelGGL(k_head_rem_list, dim3(cdiv(p.V, 256)), dim3(1024), 0, s, r, p.T <= HEAD_FEW);
+      if (p.T > HEAD_FEW) hipLaunchKernelGGL(k_head_rem_rows, dim3(cdiv((int64_t)p.T * p.top, 8)), dim3(256), 0, s, r);
+    }
     if (a.dw != nullptr && p.tile_z == 0) {
       hipLaunchKernelGGL(k_head_dz_dw<HeadBig>, dim3(ndz + ndw), dim3(HeadBig::NT), 0, s, g, ndz);
       continue;
@@ -1978,8 +2054,6 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
     });
     if (a.dw != nullptr) hipLaunchKernelGGL(k_head_dw<HeadBig>, dim3(ndw), dim3(HeadBig::NT), 0, s, g);
   }
-  if (a.dw != nullptr && p.exact)
-    hipLaunchKernelGGL(k_head_dw_entries, dim3(p.T * p.top, cdiv(p.H, 2048)), dim3(256), 0, s, g);
   const int32_t* cidx = reinterpret_cast<const int32_t*>(a.ws + p.cidx);
   int P = 8;
   while (P < p.H / 8) P *= 2;
