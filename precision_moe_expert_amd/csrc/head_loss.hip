@@ -710,7 +710,7 @@ struct HeadGemm {
   const float* r;         // [count]
   int32_t* eid;           // [count][top] G's entries at the target's ids: id (-1: none),
   float* ev;              //   value (null: none are kept)
-  bool exact;             // what rounding them takes off is added to u and d_w
+  bool exact;             // what rounding them takes off is added to u
   const int2* rtile;      // d_w: first row and rows of each 256 ids in rlist and rem
   const int32_t* rlist;   // rows of hc with an entry among those ids
   const uint16_t* rem;    // [..][256] what rounding took off those entries
@@ -1830,22 +1830,29 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
   }
   p.r = take(rows * 4);
   p.info = take(rows * sizeof(HeadRow));
-  // what rounding takes off G's entries at the target's ids is added up to 65536
-  // of them, for distillation while their rows of W are at most a quarter of it
+  // What rounding takes off G's entries at the target's ids is always added for
+  // cross entropy (with d_w one place of 512 bytes per token).  A teacher's ids
+  // cost a row of W each for u, and their tokens K steps of d_w: taken while they
+  // are few for the vocabulary.  Taken against not, us: 1500 x 2048 x 50257 with
+  // 33 ids 548 / 516 frozen, 901 / 793 with d_w; 4096 x 7168 x 32000 with 33
+  // 2953 / 2697 and 4641 / 3964; 200 x 7168 x 32000 with 64 301 / 244 and 556 /
+  // 436.  Past the rule 4096 x 7168 x 32000 with 64 would be 3200 / 2714 and 5187
+  // / 3967, with 128 3719 / 2738 and 6186 / 4000: there the entries stay rounded,
+  // which leaves 1.4 times the results' own rounding instead of 1.0.
   const int64_t entries = (int64_t)T * top;
-  p.exact = bwd && entries <= 65536 && (!distill || entries <= V / 4);
-  const bool keep = p.exact || (bwd && !distill);
-  p.eid = take(keep ? t * top * 4 : 0);
-  p.ev = take(keep ? t * top * 4 : 0);
-  p.rtile = take(p.exact ? (size_t)cdiv(V, 256) * 8 : 0);
-  p.rlist = take(p.exact ? (t * top + 64) * 4 : 0);
-  p.rown = take(p.exact ? t * top * 4 : 0);
-  p.rem = take(p.exact ? t * top * 512 : 0);
+  p.exact = bwd && (!distill || (int64_t)top * 900 <= V || entries <= V / 2);
+  p.exact_w = p.exact && entries <= (1 << 20);
+  p.eid = take(p.exact ? t * top * 4 : 0);
+  p.ev = take(p.exact ? t * top * 4 : 0);
+  p.rtile = take(p.exact_w ? (size_t)cdiv(V, 256) * 8 : 0);
+  p.rlist = take(p.exact_w ? (t * top + 64) * 4 : 0);
+  p.rown = take(p.exact_w ? t * top * 4 : 0);
+  p.rem = take(p.exact_w ? t * top * 512 : 0);
   p.flag = take(distill ? t : 0);
   p.rows = take(t * 4);
   p.cidx = take(t * 4);
   p.count = take(8);
-  p.hc = take((rows + p.exact) * p.Hp * 2);  // a row of zeros last
+  p.hc = take((rows + p.exact_w) * p.Hp * 2);  // a row of zeros last
   p.zero_row = (int)rows;
   p.lq = take(distill ? t * top * 4 : 0);
   p.lp = take(p.psplits > 1 ? t * ((V + 3) / 4 * 4) * p.psplits * 4 : 0);
@@ -2029,7 +2036,7 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
       hipLaunchKernelGGL(k_head_targets, dim3(cdiv(p.T, 4)), dim3(256), 0, s, g.rows, g.count, a.ids,
                          reinterpret_cast<const float*>(a.ws + p.lq), a.logp, g.info, p.top, g.v0, p.piece, g.g, g.eid,
                          g.ev);
-    if (a.dw != nullptr && p.exact && i == 0) {
+    if (a.dw != nullptr && p.exact_w && i == 0) {
       HeadRem r{g.eid, g.ev, g.count, p.top};
       r.tile = reinterpret_cast<int2*>(a.ws + p.rtile);
       r.list = reinterpret_cast<int32_t*>(a.ws + p.rlist);

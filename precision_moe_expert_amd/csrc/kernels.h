@@ -203,8 +203,8 @@ struct HeadPlan {
   int bm;                 // rows of the former
   int psplits;            // ways its K is split (1: not)
   int dz_max;             // most workgroups of the G W product
-  bool exact;             // what bf16 takes off G's entries at the target's ids is added
-  int zero_row;           // row of zeros behind the gathered rows (exact)
+  bool exact, exact_w;    // what bf16 takes off G's entries at the target's ids is added to u, to d_w
+  int zero_row;           // row of zeros behind the gathered rows (exact_w)
   size_t r, info, eid, ev, rtile, rlist, rown, rem, flag, rows, cidx, count, hc, lq, lp, zt, stats, u, g, total;
 };
 struct HeadArgs {

@@ -59,3 +59,32 @@ def test_fitted_head(torch_gpu, T, H, V):
     assert norm(gw.double() - d_w) <= 1.25 * _rounding(d_w) + STEP * size_w.sum().sqrt()
     f = V // 3
     assert norm(gw[f].double() - d_w[f]) <= 1.25 * _rounding(d_w[f]) + 3 * STEP * size_w[f].sqrt()
+
+
+# (T, H, V, K) where the entries at the slots' ids are few for the vocabulary, and where they are many and stay rounded
+SLOTS = [(1500, 512, 32000, 33), (200, 1024, 32000, 64), (2500, 256, 4500, 5), (30, 264, 1000, 16), (70, 512, 20001, 128),
+         (1500, 512, 8000, 33), (600, 256, 1000, 64)]
+
+
+@pytest.mark.parametrize("T,H,V,K", SLOTS)
+def test_fitted_student(torch_gpu, T, H, V, K):
+    """A teacher close to the student: its ids are the student's best ones, so that their entries of G are most of it,
+    and p and q cancel in part."""
+    h, w, _, dl, g = _fitted(T, H, V, T + K)
+    z = h.double() / torch.sqrt((h.double() ** 2).mean(1, keepdim=True) + 1e-6)
+    top = (2.0 * (z @ w.double().t())).float()
+    top = (top + torch.randn(top.shape, generator=g, device="cuda")).topk(K, 1)
+    ids, tl = top.indices.int(), top.values
+    ids[::9] = -1
+    ref, have, q = lr.distill_ref(h, w, ids, tl, 0.5)
+    loss, lse, logp = moe.lm_head_distill(h, w, ids, tl, teacher_scale=0.5)
+    gh, gw = moe.lm_head_distill_backward(h, w, ids, tl, lse, logp, dl, weight_grad=True, teacher_scale=0.5)
+    d_h, _, d_w, _ = ref.grads(dl, True)
+    G = (ref.r * dl[ref.rows].double())[:, None] * (ref.p - ref.q)
+    if K * 900 <= V or T * K <= V // 2:
+        G = torch.where(ref.q > 0, 0.0, G)
+    size_h = (G ** 2).sum(0) @ (ref.w ** 2).sum(1)
+    size_w = (G ** 2).sum(1) @ (ref.x ** 2).sum(1)
+    norm = torch.linalg.norm
+    assert norm(gh.double() - d_h) <= 1.25 * _rounding(d_h) + STEP * size_h.sqrt()
+    assert norm(gw.double() - d_w) <= 1.25 * _rounding(d_w) + STEP * size_w.sqrt()
