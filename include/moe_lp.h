@@ -443,10 +443,10 @@ moe_status moe_lm_head_distill(const moe_lm_head* head, int32_t top, float teach
 /* Its gradient: as moe_lm_head_loss_backward with
  *   G[t][v] = logit_scale * r_t * d_loss[t] * (p[t][v] - sum_j q_j [id_j = v]);
  * lse and logp from moe_lm_head_distill.  None for the teacher.  What rounding
- * takes off the entries at the slots' ids is added where those are few for the
- * vocabulary (top at most V / 900, or T top at most V / 2; to d_W up to T top =
- * 2^20): past that it would cost more (18% of a frozen gradient at 64 of 32000
- * ids) than it gives. */
+ * takes off the entries at the slots' ids is added where those are few (top at
+ * most V / 900, or T top at most V / 2 or 1024; to d_W up to T top = 2^20); past
+ * that they stay rounded, as the rest of G (18% of a frozen gradient's time at 64
+ * of 32000 ids). */
 moe_status moe_lm_head_distill_backward(const moe_lm_head* head, int32_t top, float teacher_scale,
                                         const void* h_bf16, const void* w_lm_bf16, const int32_t* teacher_ids,
                                         const float* teacher_logits, const float* lse, const float* logp,

@@ -1494,24 +1494,37 @@ __global__ __launch_bounds__(256) void k_head_rem_rows(HeadRem p) {
   if (tile >= 0) head_rem_row(p, at, p.list[at], tile * 256, threadIdx.x & 31, buf[g]);
 }
 
-// Adds what rounding took off row c's entries [first, top), in steps of `step`,
-// times their rows of W, 8 columns from col, to a and b; four rows' loads in
-// flight.
-MOE_DEV void head_add_entries(const HeadGemm& p, int c, int first, int step, int col, f32x4& a, f32x4& b) {
-  const int32_t* id = p.eid + (int64_t)c * p.top;
-  const float* ev = p.ev + (int64_t)c * p.top;
-  for (int k = first; k < p.top; k += 4 * step) {
-    u32x4 w[4];
-    float x[4];
+// A row's entries as the u of its token takes them: ids (-1: none) and what
+// rounding took off.
+struct HeadEntries {
+  int id[256];
+  float rem[256];
+};
+// Row c's entries into LDS (a barrier has to follow).
+MOE_DEV void head_load_entries(const HeadGemm& p, int c, HeadEntries& s) {
+  const int j = threadIdx.x;
+  if (j < p.top) {
+    s.id[j] = p.eid[(int64_t)c * p.top + j];
+    s.rem[j] = head_rem(p.ev[(int64_t)c * p.top + j]);
+  }
+}
+// Adds entries [first, top) in steps of `step`, times their rows of W, 8 columns
+// from col, to a and b; eight rows' loads in flight (four, and each iteration's
+// ids read before them: 8 x 7168 x 2000 with 64 slots 75 us, 38 without entries).
+MOE_DEV void head_add_entries(const HeadGemm& p, const HeadEntries& s, int first, int step, int col, f32x4& a,
+                              f32x4& b) {
+  for (int k = first; k < p.top; k += 8 * step) {
+    u32x4 w[8];
+    float x[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int at = k + j * step, v = at < p.top ? id[at] : -1;
-      x[j] = v >= 0 ? head_rem(ev[at]) : 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      const int at = k + j * step, v = at < p.top ? s.id[at] : -1;
+      x[j] = v >= 0 ? s.rem[at] : 0.0f;
       w[j] = (u32x4){0, 0, 0, 0};
       if (v >= 0) w[j] = *reinterpret_cast<const u32x4*>(p.w + (int64_t)v * p.w_stride + col);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         a[2 * e] = fmaf(x[j], bf16_bits_to_f32(w[j][e] & 0xFFFFu), a[2 * e]);
@@ -1536,12 +1549,17 @@ __global__ __launch_bounds__(NT) void k_head_dh_narrow(HeadGemm p, const uint16_
                                                         uint16_t* __restrict__ dh) {
   __shared__ __align__(16) f32x4 sum[2][NT];
   __shared__ float part[NT / 64];
+  __shared__ HeadEntries ent;
   const int t = blockIdx.x, c = cidx[t], H = p.H, np = H / 8, tid = threadIdx.x;
   const int i = tid & (P - 1), g = tid / P, groups = NT / P;
   uint16_t* o = dh + (int64_t)t * H + i * 8;
   if (c < 0) {
     if (g == 0 && i < np) *reinterpret_cast<u32x4*>(o) = (u32x4){0, 0, 0, 0};
     return;
+  }
+  if (p.exact) {
+    head_load_entries(p, c, ent);
+    __syncthreads();
   }
   const int splits = p.count[1];
   const int64_t slab = (int64_t)p.count[0] * H;
@@ -1568,7 +1586,7 @@ __global__ __launch_bounds__(NT) void k_head_dh_narrow(HeadGemm p, const uint16_
       a += *reinterpret_cast<const f32x4*>(us + s * slab);
       b += *reinterpret_cast<const f32x4*>(us + s * slab + 4);
     }
-    if (p.exact) head_add_entries(p, c, g, groups, i * 8, a, b);
+    if (p.exact) head_add_entries(p, ent, g, groups, i * 8, a, b);
   }
   if (groups > 1) {
     sum[0][tid] = a;
@@ -1614,11 +1632,16 @@ __global__ __launch_bounds__(256) void k_head_dh(HeadGemm p, const uint16_t* __r
                                                  const int32_t* __restrict__ cidx, bool norm,
                                                  uint16_t* __restrict__ dh) {
   __shared__ float part[4];
+  __shared__ HeadEntries ent;
   const int t = blockIdx.x, c = cidx[t], H = p.H, np = H / 8;
   uint16_t* o = dh + (int64_t)t * H;
   if (c < 0) {
     for (int i = threadIdx.x; i < np; i += 256) *reinterpret_cast<u32x4*>(o + i * 8) = (u32x4){0, 0, 0, 0};
     return;
+  }
+  if (p.exact) {
+    head_load_entries(p, c, ent);
+    __syncthreads();
   }
   const int splits = p.count[1];
   const int64_t slab = (int64_t)p.count[0] * H;
@@ -1660,7 +1683,7 @@ __global__ __launch_bounds__(256) void k_head_dh(HeadGemm p, const uint16_t* __r
       a[k] += *reinterpret_cast<const f32x4*>(us + s * slab);
       b[k] += *reinterpret_cast<const f32x4*>(us + s * slab + 4);
     }
-    if (p.exact) head_add_entries(p, c, 0, 1, i * 8, a[k], b[k]);
+    if (p.exact) head_add_entries(p, ent, 0, 1, i * 8, a[k], b[k]);
   }
   float f = 0.0f;
   if (norm) {
@@ -1833,14 +1856,14 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
   // What rounding takes off G's entries at the target's ids is always added for
   // cross entropy (with d_w one place of 512 bytes per token).  A teacher's ids
   // cost a row of W each for u, and their tokens K steps of d_w: taken while they
-  // are few for the vocabulary.  Taken against not, us: 1500 x 2048 x 50257 with
-  // 33 ids 548 / 516 frozen, 901 / 793 with d_w; 4096 x 7168 x 32000 with 33
-  // 2953 / 2697 and 4641 / 3964; 200 x 7168 x 32000 with 64 301 / 244 and 556 /
-  // 436.  Past the rule 4096 x 7168 x 32000 with 64 would be 3200 / 2714 and 5187
-  // / 3967, with 128 3719 / 2738 and 6186 / 4000: there the entries stay rounded,
+  // are few, altogether or for the vocabulary.  Taken against not, us: 64 x 1024 x
+  // 1000 with 16 ids 28 / 27 frozen, 43 / 33 with d_w; 1500 x 2048 x 50257 with 33
+  // 549 / 524 and 907 / 798; 200 x 7168 x 32000 with 64 270 / 246 and 534 / 437.
+  // Past the rule 4096 x 7168 x 32000 with 64 would be 3215 / 2727 and 5200 /
+  // 3979, with 128 3737 / 2752 and 6151 / 4022: there the entries stay rounded,
   // which leaves 1.4 times the results' own rounding instead of 1.0.
   const int64_t entries = (int64_t)T * top;
-  p.exact = bwd && (!distill || (int64_t)top * 900 <= V || entries <= V / 2);
+  p.exact = bwd && (!distill || (int64_t)top * 900 <= V || entries <= (V > 2048 ? V / 2 : 1024));
   p.exact_w = p.exact && entries <= (1 << 20);
   p.eid = take(p.exact ? t * top * 4 : 0);
   p.ev = take(p.exact ? t * top * 4 : 0);
