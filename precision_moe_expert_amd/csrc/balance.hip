@@ -65,8 +65,8 @@ MOE_DEV void bl_load(const float* __restrict__ row, int E, int ln, float (&v)[NV
 
 // v <- softmax of the row; a row of -infinities gives zeros.  2^(x log2 e - c)
 // in one fused operation: c's own rounding is the same for the whole row and
-// drops out.  Where c would pass the fp32 range (a row of the lowest values) m is
-// taken off first.
+// drops out.  It is up to 2^-24 |c|, which for a row of a mask's values (-1e10) is
+// past the exponents of fp32: far from 0 m is taken off first.
 template <int N>
 MOE_DEV void bl_softmax(float (&v)[N]) {
   constexpr float kLog2e = 1.44269504088896340736f;
@@ -74,7 +74,7 @@ MOE_DEV void bl_softmax(float (&v)[N]) {
 #pragma unroll
   for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
   m = bl_max16(m);
-  const float far = fabsf(m) > 2.0e38f && m != -INFINITY ? m : 0.0f;
+  const float far = fabsf(m) > 65536.0f && m != -INFINITY ? m : 0.0f;
   const float c = m == -INFINITY ? 0.0f : (m - far) * kLog2e;
   float s = 0.0f;
 #pragma unroll
