@@ -42,6 +42,10 @@ MOE_DEV float hl_max64(float v) {
   return v;
 }
 MOE_DEV float hl_exp2(float v) { return __builtin_amdgcn_exp2f(v); }  // one instruction, 1 ulp
+// Beyond this the rounding of y = l log2 e, up to 2^-24 |y|, is no longer small
+// as an exponent (at 2^31 it is past fp32's): exponents are formed another way.
+constexpr float kFarLogit = 1.0e6f;
+MOE_DEV float hl_not_above_0(float v) { return v > 0.0f ? 0.0f : v; }  // NaN stays
 // Joins two (maximum, sum of 2^(y - maximum)) pairs; an empty one has sum 0.
 MOE_DEV void hl_merge(float& m, float& s, float m2, float s2) {
   if (s2 == 0.0f) return;
@@ -51,7 +55,13 @@ MOE_DEV void hl_merge(float& m, float& s, float m2, float s2) {
     return;
   }
   const float M = fmaxf(m, m2);
-  s = s * hl_exp2(m - M) + s2 * hl_exp2(m2 - M);
+  float d, d2;
+  {
+#pragma clang fp contract(off)  // with a product behind m or m2 its rounding would stay in the difference
+    d = m - M;
+    d2 = m2 - M;
+  }
+  s = s * hl_exp2(d) + s2 * hl_exp2(d2);
   m = M;
 }
 
@@ -790,12 +800,21 @@ MOE_DEV void head_stats(const HeadGemm& p, int n, int m0, int nt, uint8_t* smem)
         for (int e = 0; e < 4; ++e)
           if (ALL || n0 + wn + j * 16 + lg * 4 + e < p.V) mx = fmaxf(mx, acc[i][j][e]);
       mx = fmaxf(mx, shfl_xor(mx, 16));
-      mx = fmaxf(mx, shfl_xor(mx, 32)) * info[i].f2;
+      const float top = fmaxf(mx, shfl_xor(mx, 32));
+      mx = top * info[i].f2;
+      if (!__any(fabsf(mx) > kFarLogit)) {
 #pragma unroll
-      for (int j = 0; j < C::NJ; ++j)
+        for (int j = 0; j < C::NJ; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (ALL || n0 + wn + j * 16 + lg * 4 + e < p.V) s += hl_exp2(fmaf(acc[i][j][e], info[i].f2, -mx));
+          for (int e = 0; e < 4; ++e)
+            if (ALL || n0 + wn + j * 16 + lg * 4 + e < p.V) s += hl_exp2(fmaf(acc[i][j][e], info[i].f2, -mx));
+      } else {
+#pragma unroll
+        for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (ALL || n0 + wn + j * 16 + lg * 4 + e < p.V) s += hl_exp2((acc[i][j][e] - top) * info[i].f2);
+      }
       s += shfl_xor(s, 16);
       s += shfl_xor(s, 32);
       if (lg == 0) {
@@ -926,6 +945,15 @@ MOE_DEV void head_grad(const HeadGemm& p, int m0, int nt, uint8_t* smem) {
 #pragma unroll
     for (int i = 0; i < C::MI; ++i) {
       uint8_t* o = HeadOut<C>::at(smem, wm + i * 16 + ln, wn + lg * 4);
+      if (__any(fabsf(info[i].l2) > kFarLogit)) {  // p <= 1 whatever roundings of l and lse leave
+#pragma unroll
+        for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i][j][e] = hl_not_above_0(fmaf(acc[i][j][e], info[i].f2, -info[i].l2));
+        info[i].f2 = 1.0f;
+        info[i].l2 = 0.0f;
+      }
 #pragma unroll
       for (int j = 0; j < C::NJ; ++j) {
         float x[4];
@@ -1138,7 +1166,7 @@ __global__ __launch_bounds__(256) void k_head_part_grad(HeadGemm p, int bm) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int at = v + k * 4 + e;
-      x[k * 4 + e] = c < n && at < p.V ? w.f * hl_exp2(fmaf(z[e], w.f2, -w.l2)) : 0.0f;
+      x[k * 4 + e] = c < n && at < p.V ? w.f * hl_exp2(hl_not_above_0(fmaf(z[e], w.f2, -w.l2))) : 0.0f;
       if (!p.distill && at == w.tgt && at < p.V) x[k * 4 + e] = p.ev[c];
     }
   }
@@ -1213,14 +1241,14 @@ __global__ __launch_bounds__(256) void k_head_finish(HeadFinish p) {
       const int j = i * 64 + lane;
       if (j < p.top) {
         const bool have = !(lq[i] == -INFINITY);
-        const float lp = have ? p.zt[(int64_t)c * p.top + j] - l : 0.0f;
+        const float lp = have ? hl_not_above_0(p.zt[(int64_t)c * p.top + j] - l) : 0.0f;
         p.logp[(int64_t)t * p.top + j] = lp;
         if (have) kl = fmaf(expf(lq[i]), lq[i] - lp, kl);
       }
     }
     kl = hl_sum64(kl);
   } else {
-    kl = l - p.zt[c];
+    kl = -hl_not_above_0(p.zt[c] - l);
   }
   if (lane == 0) {
     p.loss[t] = kl;
@@ -1291,13 +1319,13 @@ __global__ __launch_bounds__(256) void k_head_part_finish(HeadGemm g, HeadFinish
     float y[4], mx = -INFINITY;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      y[e] = v + e < p.V ? z[e] * f2 : -INFINITY;
+      y[e] = v + e < p.V ? z[e] : -INFINITY;
       mx = fmaxf(mx, y[e]);
     }
     float sum = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum += hl_exp2(y[e] - mx);
-    hl_merge(m, s, mx, sum);
+    for (int e = 0; e < 4; ++e) sum += hl_exp2((y[e] - mx) * f2);
+    hl_merge(m, s, mx * f2, sum);
   }
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) {
@@ -1323,14 +1351,14 @@ __global__ __launch_bounds__(256) void k_head_part_finish(HeadGemm g, HeadFinish
       const int j = i * 64 + lane;
       if (j < p.top) {
         const bool have = !(lq[i] == -INFINITY);
-        const float lp = have ? head_part1(g, c, p.ids[(int64_t)t * p.top + j]) * f - l : 0.0f;
+        const float lp = have ? hl_not_above_0(head_part1(g, c, p.ids[(int64_t)t * p.top + j]) * f - l) : 0.0f;
         p.logp[(int64_t)t * p.top + j] = lp;
         if (have) kl = fmaf(expf(lq[i]), lq[i] - lp, kl);
       }
     }
     kl = hl_sum64(kl);
   } else {
-    kl = l - head_part1(g, c, p.ids[t]) * f;
+    kl = -hl_not_above_0(head_part1(g, c, p.ids[t]) * f - l);
   }
   if (lane == 0) {
     p.loss[t] = kl;

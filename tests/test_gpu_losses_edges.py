@@ -37,3 +37,49 @@ def test_balance_far_logits(torch_gpu, T, E, k):
     d = moe.balance_loss_backward(layer, logits.cuda(), counts, tokens, g.cuda())
     a = 0.7 * E / (k * T * T) * ref["counts"][0].double()
     assert ((d.cpu().double() - ref["d_logits"]).abs() <= a.max() * ((E + 64) * F32 + 2 * step)).all()
+
+
+@pytest.mark.parametrize("scale,eps", [(1e9, 1e-6), (3e12, 1e-6), (1e25, 1e-6), (2.0 ** 31, 0.0)])
+@pytest.mark.parametrize("T,H,V", [(3, 64, 5000), (70, 136, 301), (300, 64, 500), (1100, 64, 9001), (9, 4096, 300)])
+def test_head_far_logits(torch_gpu, T, H, V, scale, eps):
+    """A temperature near 0: logits of 1e9 and beyond.  The losses are within the rounding of such logits; what the
+    gradients weigh, p - [target], stays within -1 and 1 and the gradients finite."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + V)
+    h = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    w = (torch.randn(V, H, generator=g, device="cuda") / math.sqrt(H)).bfloat16()
+    y = torch.randint(0, V, (T,), generator=g, device="cuda").int()
+    y[::3] = (lr.ce_ref(h, w, y, eps, 1.0).logits[::3]).argmax(1).int()  # p = 1 there
+    ids = torch.stack([y, (y + 7) % V], 1).int().contiguous()
+    tl = torch.randn(T, 2, generator=g, device="cuda")
+    ref = lr.ce_ref(h, w, y, eps, scale)
+    lse, want, b_lse, b_loss = ref.loss()
+    loss, got_lse = moe.lm_head_loss(h, w, y, norm_eps=eps, logit_scale=scale)
+    assert ((got_lse.double() - lse).abs() <= b_lse).all() and ((loss.double() - want).abs() <= b_loss).all()
+    assert (loss >= 0).all()
+    kl, klse, logp = moe.lm_head_distill(h, w, ids, tl, norm_eps=eps, logit_scale=scale)
+    assert ((klse.double() - lse).abs() <= b_lse).all() and kl.isfinite().all() and (logp <= 0).all()
+    dl = torch.randn(T, generator=g, device="cuda")
+    grads = moe.lm_head_loss_backward(h, w, y, loss, lse.float(), dl, weight_grad=True, norm_eps=eps,
+                                      logit_scale=scale)
+    grads += moe.lm_head_distill_backward(h, w, ids, tl, klse, logp, dl, weight_grad=True, norm_eps=eps,
+                                          logit_scale=scale)
+    size = (scale * ref.r * dl.double().abs()).max()
+    for d, rows in zip(grads, (ref.w, ref.x, ref.w, ref.x)):
+        # at most every |entry| 1 of G's row or column, u and its part along h
+        assert d.isfinite().all() and d.double().abs().max() <= 4 * size * rows.abs().sum(0).max() + 4 * size * rows.abs().sum()
+
+
+@pytest.mark.parametrize("T,H,V", [(4, 64, 40), (300, 64, 500), (9, 4096, 300)])
+def test_confident_losses_are_not_negative(torch_gpu, T, H, V):
+    """Rows that are their target's row of W many times over: lse and the target's logit are equal but for rounding."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    w = torch.randn(V, H, generator=g, device="cuda").bfloat16()
+    y = torch.randint(0, V, (T,), generator=g, device="cuda").int()
+    h = w[y.long()].contiguous()
+    loss, lse = moe.lm_head_loss(h, w, y, norm_eps=0.0, logit_scale=7.3)
+    assert (loss >= 0).all() and (loss <= lse.abs() * 8 * F32).all()
+    logp = moe.lm_head_distill(h, w, y[:, None].contiguous(), torch.zeros(T, 1, device="cuda"), norm_eps=0.0,
+                               logit_scale=7.3)[2]
+    assert (logp <= 0).all()
