@@ -375,7 +375,8 @@ moe_status moe_lm_head_logprob(int32_t T, int32_t H, int32_t V, const void* h_bf
 
 /* An LM head (host memory).  logits[t][v] = logit_scale * <z_t, W_v> with
  * z_t = h_t / sqrt(mean(h_t^2) + norm_eps), the parameter-free RMSNorm of
- * moe_lm_head_logprob, or z_t = h_t for norm_eps = 0. */
+ * moe_lm_head_logprob, or z_t = h_t for norm_eps = 0.  The forward entries are
+ * MOE_ERR_UNSUPPORTED where T V comes to 2^39 (more tiles than a launch holds). */
 typedef struct {
   int32_t num_tokens; /* T: 0..2^20                                              */
   int32_t hidden;     /* H: multiple of 8, at most 32768                         */

@@ -1919,6 +1919,13 @@ HeadPlan head_plan(int T, int H, int V, int top, bool distill, bool bwd) {
     p.g = take(rows * p.piece * 2);
   }
   p.total = o;
+  // a launch has fewer than 2^32 threads in a dimension
+  if (!bwd && p.psplits == 1)
+    head_dispatch(p.tile_l, [&](auto c) {
+      using C = decltype(c);
+      const int64_t blocks = (int64_t)((T + C::BM - 1) / C::BM) * ((V + C::BN - 1) / C::BN) + 2 * cus + 16;
+      if (blocks * C::NT >= (1ll << 32)) p.total = 0;
+    });
   return p;
 }
 

@@ -205,6 +205,7 @@ struct HeadPlan {
   int dz_max;             // most workgroups of the G W product
   bool exact, exact_w;    // what bf16 takes off G's entries at the target's ids is added to u, to d_w
   int zero_row;           // row of zeros behind the gathered rows (exact_w)
+  // total 0: more tiles than a launch has room for
   size_t r, info, eid, ev, rtile, rlist, rown, rem, flag, rows, cidx, count, hc, lq, lp, zt, stats, u, g, total;
 };
 struct HeadArgs {

@@ -1159,6 +1159,7 @@ moe_status moe_lm_head_loss(const moe_lm_head* head, const void* h_bf16, const v
   const void* ptrs[] = {h_bf16, w_lm_bf16, targets, loss, lse, ws};
   if (!all_aligned16(ptrs)) return MOE_ERR_INVALID_ARGUMENT;
   const HeadPlan p = plan_of(head, 0, false);
+  if (p.total == 0) return MOE_ERR_UNSUPPORTED;
   if (ws_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   HeadArgs a = head_args(head, h_bf16, w_lm_bf16, targets, ws);
   a.loss = loss;
@@ -1177,6 +1178,7 @@ moe_status moe_lm_head_loss_backward(const moe_lm_head* head, const void* h_bf16
   const void* ptrs[] = {h_bf16, w_lm_bf16, targets, loss, lse, d_loss, d_h_bf16, ws};
   if (!all_aligned16(ptrs) || !aligned16(d_w_bf16)) return MOE_ERR_INVALID_ARGUMENT;
   const HeadPlan p = plan_of(head, 0, true);
+  if (p.total == 0) return MOE_ERR_UNSUPPORTED;
   if (ws_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   HeadArgs a = head_args(head, h_bf16, w_lm_bf16, targets, ws);
   a.loss = const_cast<float*>(loss);
@@ -1197,6 +1199,7 @@ moe_status moe_lm_head_distill(const moe_lm_head* head, int32_t top, float teach
   const void* ptrs[] = {h_bf16, w_lm_bf16, teacher_ids, teacher_logits, loss, lse, logp, ws};
   if (!all_aligned16(ptrs)) return MOE_ERR_INVALID_ARGUMENT;
   const HeadPlan p = plan_of(head, top, false);
+  if (p.total == 0) return MOE_ERR_UNSUPPORTED;
   if (ws_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   HeadArgs a = head_args(head, h_bf16, w_lm_bf16, teacher_ids, ws);
   a.tlogits = teacher_logits;
@@ -1219,6 +1222,7 @@ moe_status moe_lm_head_distill_backward(const moe_lm_head* head, int32_t top, fl
   const void* ptrs[] = {h_bf16, w_lm_bf16, teacher_ids, teacher_logits, lse, logp, d_loss, d_h_bf16, ws};
   if (!all_aligned16(ptrs) || !aligned16(d_w_bf16)) return MOE_ERR_INVALID_ARGUMENT;
   const HeadPlan p = plan_of(head, top, true);
+  if (p.total == 0) return MOE_ERR_UNSUPPORTED;
   if (ws_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   HeadArgs a = head_args(head, h_bf16, w_lm_bf16, teacher_ids, ws);
   a.tlogits = teacher_logits;
