@@ -404,8 +404,10 @@ size_t moe_lm_head_loss_workspace_bytes(const moe_lm_head* head, int32_t top, in
  * loss[t] = lse[t] - logits[t][y_t] (the negative log-prob).
  * h: [T][H] bf16 (h_stride); w_lm: [V][H] bf16 (w_stride); targets: [T] int32;
  * loss, lse: [T] fp32.  A negative target marks a token that does not count:
- * loss = lse = 0, its row of h is not read and no product is spent on it.  A
- * target >= V gives loss = NaN, lse = 0, and is otherwise the same. */
+ * loss = lse = 0, and its row of h has no part in anything, whatever it holds
+ * (it may be read).  Above 256 tokens such rows are gathered out before the
+ * products; up to 256 they take their place in the tiles.  A target >= V gives
+ * loss = NaN, lse = 0, and is otherwise the same. */
 moe_status moe_lm_head_loss(const moe_lm_head* head, const void* h_bf16, const void* w_lm_bf16,
                             const int32_t* targets, float* loss, float* lse, void* ws, size_t ws_bytes, void* stream);
 
