@@ -434,12 +434,21 @@ def lm_head_logprob(h: torch.Tensor, w_lm: torch.Tensor, targets: torch.Tensor, 
 
 # ---- training losses ----
 
+def _aligned(t, name: str) -> int:
+    """The tensor's address, which the library wants on 16 bytes (a slice may start between them)."""
+    p = t.data_ptr()
+    if p % 16:
+        raise ValueError(f"{name}: address not 16-byte aligned (a view that starts inside another tensor); "
+                         "pass a clone()")
+    return p
+
+
 def _typed(t, name: str, dtype, shape, device):
-    """A contiguous tensor of this type and shape on the call's device."""
+    """The address of a contiguous tensor of this type and shape on the call's device."""
     if t is None or t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous {dtype} tensor of shape {tuple(shape)} on {device} expected, got "
                          + ("None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}"))
-    return t.data_ptr()
+    return _aligned(t, name)
 
 
 def _rows(t, name: str, device):
@@ -447,10 +456,10 @@ def _rows(t, name: str, device):
     if t.dtype != torch.bfloat16 or t.dim() != 2 or t.device != device or not t.is_cuda:
         raise ValueError(f"{name}: bf16 device matrix expected, got {t.dtype} {tuple(t.shape)} on {t.device}")
     if t.is_contiguous():
-        return t.data_ptr(), 0
+        return _aligned(t, name), 0
     if t.stride(1) != 1 or t.stride(0) < t.shape[1]:
         raise ValueError(f"{name}: rows must be contiguous and must not overlap, got strides {t.stride()}")
-    return t.data_ptr(), t.stride(0)
+    return _aligned(t, name), t.stride(0)
 
 
 def _raw_stream(device) -> int:

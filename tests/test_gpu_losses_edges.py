@@ -83,3 +83,28 @@ def test_confident_losses_are_not_negative(torch_gpu, T, H, V):
     logp = moe.lm_head_distill(h, w, y[:, None].contiguous(), torch.zeros(T, 1, device="cuda"), norm_eps=0.0,
                                logit_scale=7.3)[2]
     assert (logp <= 0).all()
+
+
+def test_unaligned_views_are_named(torch_gpu):
+    """The labels of a shifted sequence start between 16-byte addresses: the refusal says which argument, and a clone
+    is taken."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    h = torch.randn(9, 64, generator=g, device="cuda").bfloat16()
+    w = torch.randn(100, 64, generator=g, device="cuda").bfloat16()
+    ids = torch.randint(0, 100, (9,), generator=g, device="cuda").int()
+    with pytest.raises(ValueError, match="targets.*aligned"):
+        moe.lm_head_loss(h[:-1], w, ids[1:])
+    loss, lse = moe.lm_head_loss(h[:-1], w, ids[1:].clone())
+    ref = lr.ce_ref(h[:-1], w, ids[1:])
+    assert ((loss.double() - ref.loss()[1]).abs() <= ref.loss()[3]).all()
+    dl = torch.ones(9, device="cuda")
+    with pytest.raises(ValueError, match="d_loss.*aligned"):
+        moe.lm_head_loss_backward(h[:-1], w, ids[1:].clone(), loss, lse, dl[1:])
+    with pytest.raises(ValueError, match="^h: .*aligned"):
+        moe.lm_head_loss(torch.empty(9 * 64 + 4, device="cuda").bfloat16()[4:].view(9, 64), w, ids)
+    layer = moe.make_layer(8, 256, 128, 16, 2, moe.FMT_INT4)
+    lg, top = torch.randn(8, 16, device="cuda"), torch.zeros(8, 2, dtype=torch.int32, device="cuda")
+    mask = torch.ones(9, dtype=torch.bool, device="cuda")
+    with pytest.raises(ValueError, match="token_mask.*aligned"):
+        moe.balance_loss(layer, lg, top, token_mask=mask[1:])
