@@ -108,3 +108,28 @@ def test_unaligned_views_are_named(torch_gpu):
     mask = torch.ones(9, dtype=torch.bool, device="cuda")
     with pytest.raises(ValueError, match="token_mask.*aligned"):
         moe.balance_loss(layer, lg, top, token_mask=mask[1:])
+
+
+@pytest.mark.parametrize("T,H,V", [(3, 64, 5000), (70, 136, 301), (300, 64, 500), (1100, 64, 901), (9, 4096, 300)])
+def test_lowest_ids(torch_gpu, T, H, V):
+    """The type's lowest and highest ids mark tokens and slots that are not there."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    h = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    w = (torch.randn(V, H, generator=g, device="cuda") / math.sqrt(H)).bfloat16()
+    y = torch.randint(0, V, (T,), generator=g, device="cuda").int()
+    y[1::2] = -2 ** 31
+    ids = torch.stack([y, torch.full_like(y, -2 ** 31), torch.full_like(y, 2 ** 31 - 1), y], 1).contiguous()
+    tl = torch.randn(T, 4, generator=g, device="cuda")
+    dl = torch.randn(T, generator=g, device="cuda")
+    loss, lse = moe.lm_head_loss(h, w, y)
+    kl, klse, logp = moe.lm_head_distill(h, w, ids, tl)
+    ref = lr.ce_ref(h, w, y)
+    assert ((lse.double() - ref.loss()[0]).abs() <= ref.loss()[2]).all()
+    assert ((loss.double() - ref.loss()[1]).abs() <= ref.loss()[3]).all()
+    assert ((klse.double() - ref.loss()[0]).abs() <= ref.loss()[2]).all() and (logp[:, 1:3] == 0).all()
+    d_h, b_h, d_w, b_w = ref.grads(dl, True)  # a teacher whose slots are all the one id is that id
+    for gh, gw in (moe.lm_head_loss_backward(h, w, y, loss, lse, dl, weight_grad=True),
+                   moe.lm_head_distill_backward(h, w, ids, tl, klse, logp, dl, weight_grad=True)):
+        assert ((gh.double() - d_h).abs() <= b_h * 1.01 + 1e-30).all()
+        assert ((gw.double() - d_w).abs() <= b_w * 1.01 + 1e-30).all()
