@@ -11,9 +11,9 @@
 // works on four tokens at once and every lane keeps the running sums of its
 // own experts in registers over all its tokens.
 //
-// 32768 x 384 in 40 segments, a fifth of the tokens masked: gradient 24 us for 91
-// MB (3.8 TB/s).  16384 x 256 in 13 segments: sums 7.5 us and finish 6.2, the
-// second waiting for the first.  64 x 384 in one launch: 5.8 us.
+// 32768 x 384 in 40 segments, a fifth of the tokens masked: gradient 24-26 us for
+// 91 MB (3.5-3.8 TB/s).  16384 x 256 in 13 segments: sums 7.4-8.8 us and finish
+// 5.8-6.9, the second waiting for the first.  64 x 384 in one launch: 5.7-6.4 us.
 #include "common.h"
 #include "kernels.h"
 

@@ -18,8 +18,8 @@
 // with r = 1 / sqrt(mean h^2 + eps), s the logit scale and g = dL/dloss.
 // r s multiplies the fp32 accumulators: the products' operands are the bf16
 // inputs themselves, and G is the one value that is rounded on the way.
-// Tokens that do not count are left out of the products: rows[] lists the
-// others, and operand rows are fetched through it.
+// Above 256 tokens those that do not count are left out of the products: rows[]
+// lists the others, which are gathered.
 #include "common.h"
 #include "kernels.h"
 
@@ -399,12 +399,13 @@ __global__ __launch_bounds__(256) void k_head_gather(HeadRowsArgs p) {
 // holds 4 consecutive columns of one row.
 //
 // Large products are bound by the MFMAs at the clock that the power limit leaves:
-// 8192 x 7168 x 32000 takes 2.54 ms for h W^T with G's epilogue and 5.23 for
-// both others, 1.4-1.5 PFLOP/s with the matrix cores busy 0.82 of the cycles.
+// 8192 x 7168 x 32000 takes 2.52-2.62 ms for h W^T with G's epilogue and 5.34-5.66
+// for both others, 1.3-1.5 PFLOP/s with the matrix cores busy 0.81 of the cycles.
 // 256 x 256 tiles read each operand least, and eight waves of 128 x 64 of them
 // hold two K halves of fragments beside 128 accumulators (four waves of 128 x 128:
 // 8.9 against 8.5 ms for the whole gradient).  Few rows are bound by the stream
-// of W: 64 rows of 7168 x 32000 78 us, 5.8 TB/s.
+// of W: 64 rows of 7168 x 32000 79-85 us, 5.4-5.8 TB/s; one row of 2048 x 32000
+// 33 us, 4.0 TB/s from memory (22 where the last-level cache holds W).
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -1369,8 +1370,8 @@ __global__ __launch_bounds__(256) void k_head_part_finish(HeadGemm g, HeadFinish
 // Distillation's backward: the entries s r g (p - q) at the slots' ids, from
 // the forward's log-probs, one wave per row, into G's columns [v0, v0 + piece).
 // Slots that repeat an id add their q, and the first of them is the entry.  ev
-// not null: with the first piece the entries go to ev too, their ids to eid.  8 us for 1500 rows of 33 slots: reads that wait for each
-// other.
+// not null: with the first piece the entries go to ev too, their ids to eid.
+// 8 us for 1500 rows of 33 slots: reads that wait for each other.
 __global__ __launch_bounds__(256) void k_head_targets(const int32_t* __restrict__ rows, const int32_t* __restrict__ count,
                                                       const int32_t* __restrict__ ids, const float* __restrict__ lq,
                                                       const float* __restrict__ logp, const HeadRow* __restrict__ info,
@@ -1448,9 +1449,12 @@ MOE_DEV void head_rem_row(const HeadRem& p, int at, int c, int lo, int l, uint16
   __builtin_amdgcn_wave_barrier();
   *reinterpret_cast<u32x4*>(p.rem + (int64_t)at * 256 + l * 8) = *reinterpret_cast<const u32x4*>(buf + l * 8);
 }
-// One block per 256 ids finds its tokens; with `rows` it forms their rows too:
-// one block forms up to HEAD_FEW rows in less time than another launch takes,
-// but 8192 tokens of one id in 500 us.
+// One block per 256 ids finds its tokens; with `rows` it forms their rows too.
+// That spares a launch, but one block forms the rows of a frequent id alone.
+// Gradients of 512 x 8000 with d_w, rows here against a launch of their own:
+// 128 tokens of uniform ids 38.6 / 40.2 us, of Zipf ids 40.9 / 41.9; 256 42.9 /
+// 44.8 and 47.5 / 47.3; 1000 73.6 / 74.7 and 95.9 / 87.0.
+constexpr int HEAD_REM_ROWS = 256;
 __global__ __launch_bounds__(1024) void k_head_rem_list(HeadRem p, bool rows) {
   __shared__ __align__(16) uint16_t buf[32][256];
   __shared__ int wsum[2][16], wown[16];
@@ -1569,8 +1573,9 @@ MOE_DEV void head_add_entries(const HeadGemm& p, const HeadEntries& s, int first
 // its NT threads in groups of P = the power of two at or above H / 8, each of
 // which adds every (NT / P)-th slab; the groups' sums are added in order.  NT is
 // 1024 where tokens are few and adding the groups is not the longer part.
-// Bound by the slabs' reads: 11 us for 200 x 7168 in nine slabs, 1024 threads
-// against 256: 3 x 1560 with 44 targets 21 -> 10.5 us, 107 x 4136 13.3 -> 9.1.
+// Bound by the slabs' reads: 12 us for 200 x 7168 in nine slabs, 1024 threads
+// against 256: 3 x 1560 with 44 targets 21 -> 10.5 us, 107 x 4136 13.3 -> 9.1; with
+// many targets by their rows of W: 1500 x 2048 with 33 39-50 us, 4-5 TB/s.
 template <int NT>
 __global__ __launch_bounds__(NT) void k_head_dh_narrow(HeadGemm p, const uint16_t* __restrict__ h, int64_t h_stride,
                                                         const int32_t* __restrict__ cidx, bool norm, int P,
@@ -2106,8 +2111,9 @@ void launch_head_loss_bwd(const HeadPlan& p, const HeadArgs& a, hipStream_t s) {
       g.rlist = r.list;
       g.rem = r.rem;
       g.zero_row = p.zero_row;
-      hipLaunchKernelGGL(k_head_rem_list, dim3(cdiv(p.V, 256)), dim3(1024), 0, s, r, p.T <= HEAD_FEW);
-      if (p.T > HEAD_FEW) hipLaunchKernelGGL(k_head_rem_rows, dim3(cdiv((int64_t)p.T * p.top, 8)), dim3(256), 0, s, r);
+      hipLaunchKernelGGL(k_head_rem_list, dim3(cdiv(p.V, 256)), dim3(1024), 0, s, r, p.T <= HEAD_REM_ROWS);
+      if (p.T > HEAD_REM_ROWS)
+        hipLaunchKernelGGL(k_head_rem_rows, dim3(cdiv((int64_t)p.T * p.top, 8)), dim3(256), 0, s, r);
     }
     if (a.dw != nullptr && p.tile_z == 0) {
       hipLaunchKernelGGL(k_head_dz_dw<HeadBig>, dim3(ndz + ndw), dim3(HeadBig::NT), 0, s, g, ndz);
