@@ -1422,7 +1422,10 @@ MOE_DEV float head_rem(float x) {
 // rounding took off those entries as rows of 256 bf16 (again rounded: 2^-16 of
 // the entry is left), which head_dw multiplies by the tokens' rows of h.  The
 // tokens of 256 ids lie behind the entries of all lower ids, so that one row per
-// entry is room enough; places that stay free get tile -1.
+// entry is room enough; places that stay free get tile -1.  Lists and rows are
+// 9-10 and 5 us for 8192 targets of 32000 ids, 16-19 and 8-9 for 1500 x 33 of
+// 50257, dependent reads; in head_dw they are 1-2 more K steps a tile (128 of
+// tokens) and 4 (24).
 struct HeadRem {
   const int32_t* eid;
   const float* ev;
