@@ -397,7 +397,8 @@ typedef struct {
  * otherwise the forward keeps two floats per token and block of vocabulary
  * rows.  The backward keeps the scaled softmax gradient (bf16) of one piece of
  * the vocabulary at a time (at most about 512 MB, or 256 columns where more
- * tokens need more), and partial sums of dL/dz (fp32, up to 64 [T][H]). */
+ * tokens need more), partial sums of dL/dz (fp32, up to 64 [T][H]), and about
+ * half a KB per target (at most 2^20 of them) for d_W. */
 size_t moe_lm_head_loss_workspace_bytes(const moe_lm_head* head, int32_t top, int32_t backward);
 
 /* Cross entropy of target ids: lse[t] = log sum_v exp(logits[t][v]),
