@@ -46,6 +46,7 @@ MOE_DEV float hl_exp2(float v) { return __builtin_amdgcn_exp2f(v); }  // one ins
 // as an exponent (at 2^31 it is past fp32's): exponents are formed another way.
 constexpr float kFarLogit = 1.0e6f;
 MOE_DEV float hl_not_above_0(float v) { return v > 0.0f ? 0.0f : v; }  // NaN stays
+MOE_DEV float hl_not_below_0(float v) { return v < 0.0f ? 0.0f : v; }
 // Joins two (maximum, sum of 2^(y - maximum)) pairs; an empty one has sum 0.
 MOE_DEV void hl_merge(float& m, float& s, float m2, float s2) {
   if (s2 == 0.0f) return;
@@ -1253,7 +1254,7 @@ __global__ __launch_bounds__(256) void k_head_finish(HeadFinish p) {
     }
     kl = hl_sum64(kl);
   } else {
-    kl = -hl_not_above_0(p.zt[c] - l);
+    kl = hl_not_below_0(l - p.zt[c]);
   }
   if (lane == 0) {
     p.loss[t] = kl;
@@ -1363,7 +1364,7 @@ __global__ __launch_bounds__(256) void k_head_part_finish(HeadGemm g, HeadFinish
     }
     kl = hl_sum64(kl);
   } else {
-    kl = -hl_not_above_0(head_part1(g, c, p.ids[t]) * f - l);
+    kl = hl_not_below_0(l - head_part1(g, c, p.ids[t]) * f);
   }
   if (lane == 0) {
     p.loss[t] = kl;

@@ -133,3 +133,16 @@ def test_lowest_ids(torch_gpu, T, H, V):
                    moe.lm_head_distill_backward(h, w, ids, tl, klse, logp, dl, weight_grad=True)):
         assert ((gh.double() - d_h).abs() <= b_h * 1.01 + 1e-30).all()
         assert ((gw.double() - d_w).abs() <= b_w * 1.01 + 1e-30).all()
+
+
+@pytest.mark.parametrize("T,H", [(1, 64), (300, 72), (5, 4096)])
+def test_one_id_costs_nothing(torch_gpu, T, H):
+    """A vocabulary of one id: loss +0 (not -0) and no gradient."""
+    h = torch.randn(T, H, device="cuda").bfloat16()
+    w = torch.randn(1, H, device="cuda").bfloat16()
+    y = torch.zeros(T, dtype=torch.int32, device="cuda")
+    loss, lse = moe.lm_head_loss(h, w, y)
+    # lse is l itself but for the rounding of l log2 e and back
+    assert not torch.signbit(loss).any() and (loss <= 8 * F32 * lse.abs()).all()
+    d_h, d_w = moe.lm_head_loss_backward(h, w, y, torch.zeros_like(loss), lse, torch.ones_like(loss), weight_grad=True)
+    assert (d_h == 0).all() and (d_w == 0).all()
