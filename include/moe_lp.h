@@ -491,6 +491,155 @@ moe_status moe_balance_loss_backward(const moe_layer* layer, const float* logits
                                      const int32_t* tokens, const float* d_loss, int32_t accumulate,
                                      float* d_logits, void* stream);
 
+/* ---- The gate ----------------------------------------------------------------
+ * Routing of models whose gate scores every expert, chooses by score plus a
+ * balance bias within the best groups of experts, and weighs by the scores:
+ * what moe_route_permute (softmax over the chosen logits) does not do. */
+
+enum { MOE_GATE_SOFTMAX = 0, MOE_GATE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+
+/* The largest number of groups. */
+#define MOE_GATE_MAX_GROUPS 64
+
+/* A gate (host memory).  For the logits l of a token and the bias b (0 without
+ * one), an expert is out where l or b is -infinity or NaN; then
+ *   s_e = 1 / (1 + exp(-l_e)), or the softmax of l over the experts that are
+ *         in; 0 for experts that are out
+ *   c_e = s_e + b_e, formed in 64 bits
+ * Experts lie in num_groups groups of E / num_groups consecutive ids.  A group
+ * counts its largest c, or the sum of its two largest (of the experts that are
+ * in; a single one counts alone).  The top_k experts with the largest c are
+ * chosen within the top_groups best groups; equal values go to the lowest group
+ * and the lowest id (c compared to 42 bits of its mantissa).  Experts that are
+ * out come behind all others of the chosen groups.  The weights are
+ *   w_j = scale s_j, or with renormalize scale s_j / sum_i s_i (0 where that sum
+ *   is 0). */
+typedef struct {
+  int32_t score;       /* MOE_GATE_SOFTMAX or MOE_GATE_SIGMOID                        */
+  int32_t num_groups;  /* divides num_experts; 1 (no groups) .. MOE_GATE_MAX_GROUPS   */
+  int32_t top_groups;  /* 1..num_groups, with room for top_k experts                  */
+  int32_t group_score; /* MOE_GROUP_MAX or MOE_GROUP_TOP2                             */
+  int32_t renormalize; /* 0 or 1                                                      */
+  float scale;         /* finite, > 0                                                 */
+} moe_gate;
+
+/* moe_route_permute through a gate.  bias: NULL or [E] fp32.  out->topk_ids in
+ * descending order of c.  The arrays of the permutation (expert_offsets to
+ * num_active) may be NULL, all of them together: then only topk_ids and topk_w
+ * are written, and ws may be NULL.  ws: >= moe_route_workspace_bytes(). */
+moe_status moe_route_gated(const moe_layer* layer, const moe_gate* gate, const float* logits, const float* bias,
+                           const moe_route_out* out, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradient for given d_topk_w = dL/dtopk_w [T][k] fp32, the choice being
+ * constant: with ds_j = scale d_w_j, or with renormalize
+ * ds_j = (scale d_w_j - sum_i d_w_i w_i) / sum_i s_i,
+ *   sigmoid: d_logits[t][ids_j] = ds_j s_j (1 - s_j), 0 elsewhere
+ *   softmax: d_logits[t][e] = s_e (ds_e - sum_j ds_j s_j)
+ * (ds_e = 0 for experts not chosen).  Ids outside [0, E) have no part; an id that
+ * a token has twice takes both gradients.  The bias has no gradient.  d_logits:
+ * [T][E] fp32, written, or with accumulate != 0 added to what it holds. */
+moe_status moe_route_gated_backward(const moe_layer* layer, const moe_gate* gate, const float* logits,
+                                    const float* bias, const int32_t* topk_ids, const float* d_topk_w,
+                                    int32_t accumulate, float* d_logits, void* stream);
+
+/* moe_expert_forward with its routing through a gate: the same arguments,
+ * result and workspace. */
+moe_status moe_expert_forward_gated(const moe_layer* layer, const moe_gate* gate, const void* x_bf16,
+                                    const float* logits, const float* bias, const moe_qweights* qweights,
+                                    const moe_scales* scales, const void* adapter_bf16, int32_t chunk_experts,
+                                    void* out_bf16, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_expert_backward of moe_expert_forward_gated: d_logits through the gate
+ * (moe_route_gated_backward of g_tj = <d_out_t, y_tj>), the rest and the
+ * workspace as there; not timed. */
+moe_status moe_expert_backward_gated(const moe_layer* layer, const moe_gate* gate, const void* x_bf16,
+                                     const float* logits, const float* bias, const moe_qweights* qweights,
+                                     const moe_scales* scales, const void* bwd_weights, const void* adapter_bf16,
+                                     const void* d_out_bf16, int32_t chunk_experts, void* d_x_bf16, float* d_logits,
+                                     float* d_adapter, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- The dense FP8 projection -------------------------------------------------
+ * The linear layers beside the experts (a shared expert's among them) in the
+ * experts' FP8 format: E4M3 codes W [N][K] with an fp32 scale per block of
+ * 128 x 128, [ceil(N/128)][ceil(K/128)] (the last blocks may be smaller), and
+ * activations quantized per 128 columns of a row as moe_quantize_activations
+ * does (MOE_W_FP8_E4M3_B128, or MOE_W_FP8_E4M3_B128_POW2 with powers of two on
+ * both sides).  A workspace serves one call at a time. */
+typedef struct {
+  int32_t num_tokens;   /* M: 0..2^20                                              */
+  int32_t in_features;  /* K: multiple of 16, at most 2^17                         */
+  int32_t out_features; /* N: the same                                             */
+  int32_t wformat;      /* MOE_W_FP8_E4M3_B128 or MOE_W_FP8_E4M3_B128_POW2         */
+  int64_t x_stride;     /* elements between rows of x: 0 (= K), or a multiple of 8, K..2^22 */
+  int64_t dy_stride;    /* the same for d_y and N                                  */
+} moe_linear;
+
+/* What a call forms, for the workspace's size. */
+enum { MOE_LINEAR_FORWARD = 0, MOE_LINEAR_D_X = 1, MOE_LINEAR_D_W = 2 };
+
+/* Workspace bytes of moe_fp8_linear (grads = MOE_LINEAR_FORWARD) or of
+ * moe_fp8_linear_backward (MOE_LINEAR_D_X, MOE_LINEAR_D_W, or both or-ed): the
+ * codes and scales of the quantized operands, and parts of the sums (fp32) where
+ * there are few tiles.  0 for an invalid or unsupported descriptor. */
+size_t moe_fp8_linear_workspace_bytes(const moe_linear* lin, int32_t grads);
+
+/* y = Q(x) W^T: x [M][K] bf16 (x_stride), y [M][N] bf16 (contiguous).  The
+ * matrix cores add products of codes 8 at a time, aligned to the largest with 13
+ * bits kept below it (1.4e-5 of a sum of normal values), everything else is added
+ * in fp32; y is rounded once. */
+moe_status moe_fp8_linear(const moe_linear* lin, const void* x_bf16, const void* w, const float* w_scale,
+                          void* y_bf16, void* ws, size_t ws_bytes, void* stream);
+
+/* W's transposed copy for the backward: w_t [K][N] codes and w_t_scale
+ * [ceil(K/128)][ceil(N/128)]; num_tokens is not used. */
+moe_status moe_fp8_linear_transpose(const moe_linear* lin, const void* w, const float* w_scale, void* w_t,
+                                    float* w_t_scale, void* stream);
+
+/* Gradients for given d_y = dL/dy [M][N] bf16 (dy_stride):
+ *   d_x [M][K] bf16 = Q(d_y) W over the transposed copy; NULL: not formed (w_t
+ *                     and w_t_scale are not read)
+ *   d_w [N][K] bf16 = Qt(d_y)^T Qt(x), where Qt quantizes per column and block of
+ *                     128 tokens; NULL: not formed (frozen; x is not read)
+ * The quantizers pass gradients straight through.  Sums as in moe_fp8_linear,
+ * each result rounded once.  num_tokens = 0 writes zeros to d_w. */
+moe_status moe_fp8_linear_backward(const moe_linear* lin, const void* d_y_bf16, const void* w_t,
+                                   const float* w_t_scale, const void* x_bf16, void* d_x_bf16, void* d_w_bf16,
+                                   void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Clipping by the global norm ----------------------------------------------
+ * Of the gradients that a step has formed (adapters, router, projections, head). */
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dtype;
+
+/* One tensor of a list (host memory; the list is not needed after the call).
+ * Addresses are aligned to the element (whole 16 bytes are faster). */
+typedef struct {
+  const void* data; /* device                                                         */
+  void* out;        /* device: where the clipped values go; data itself: in place     */
+  int64_t num;      /* elements, >= 0                                                 */
+  int32_t dtype;    /* a moe_dtype value, of data and out                             */
+} moe_tensor;
+
+/* Workspace bytes of moe_grad_norm and moe_grad_clip for n tensors. */
+size_t moe_grad_norm_workspace_bytes(int32_t n);
+
+/* norm[0] = sqrt(sum of the squares of every element) in fp32 (device; 0 for an
+ * empty list).  Squares and sums are formed in 64 bits, in an order that the sizes
+ * fix.  `out` is not used. */
+moe_status moe_grad_norm(const moe_tensor* tensors, int32_t n, float* norm, void* ws, size_t ws_bytes, void* stream);
+
+/* The norm, and out = data c with c = max_norm / norm in fp32 where norm >
+ * max_norm, else out = data (nothing is written in place).  A norm that is not
+ * finite in fp32 clips nothing: the caller sees it and leaves the step out.
+ * max_norm >= 0.
+ * The tensors must not overlap. */
+moe_status moe_grad_clip(const moe_tensor* tensors, int32_t n, float max_norm, float* norm, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* The second half alone, for a norm [1] that the caller holds on the device (one
+ * joined over ranks). */
+moe_status moe_grad_scale(const moe_tensor* tensors, int32_t n, const float* norm, float max_norm, void* stream);
+
 /* ---- Allocation-free forward -------------------------------------------
  * For callers that cannot allocate device memory or pass a workspace: code
  * under HIP graph capture, tight serving loops, harnesses that forbid

@@ -25,8 +25,15 @@ EXPORTED = ("moe_abi_version", "moe_status_str", "moe_workspace_bytes", "moe_rou
             "moe_backward_workspace_bytes", "moe_expert_backward", "moe_pack_weights_kblocked",
             "moe_quantize_activations", "moe_expert_forward_noalloc", "moe_lm_head_loss_workspace_bytes",
             "moe_lm_head_loss", "moe_lm_head_loss_backward", "moe_lm_head_distill", "moe_lm_head_distill_backward",
-            "moe_balance_loss_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward")
+            "moe_balance_loss_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward", "moe_route_gated",
+            "moe_route_gated_backward", "moe_expert_forward_gated", "moe_expert_backward_gated",
+            "moe_fp8_linear_workspace_bytes", "moe_fp8_linear", "moe_fp8_linear_transpose", "moe_fp8_linear_backward",
+            "moe_grad_norm_workspace_bytes", "moe_grad_norm", "moe_grad_clip", "moe_grad_scale")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # MOE_NOALLOC_SCRATCH_BYTES
+GATE_SOFTMAX, GATE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
+LINEAR_FORWARD, LINEAR_D_X, LINEAR_D_W = 0, 1, 2
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # moe_dtype
 STAGES = ("route", "permute", "act", "gemm1", "gemm2", "combine", "dequant")
 
 
@@ -55,6 +62,21 @@ class MoeLmHead(ctypes.Structure):
     _fields_ = [("num_tokens", ctypes.c_int32), ("hidden", ctypes.c_int32), ("vocab", ctypes.c_int32),
                 ("norm_eps", ctypes.c_float), ("logit_scale", ctypes.c_float), ("h_stride", ctypes.c_int64),
                 ("w_stride", ctypes.c_int64)]
+
+
+class MoeGate(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class MoeLinear(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("wformat", ctypes.c_int32), ("x_stride", ctypes.c_int64), ("dy_stride", ctypes.c_int64)]
+
+
+class MoeTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("num", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -150,6 +172,22 @@ def lib() -> ctypes.CDLL:
         L.moe_balance_loss_backward.restype = ctypes.c_int
         L.moe_balance_loss_backward.argtypes = [ctypes.POINTER(MoeLayer)] + [vp] * 3 + [i32] + [vp] * 3 + [i32, vp,
                                                                                                           vp]
+        layer, gate, lin = ctypes.POINTER(MoeLayer), ctypes.POINTER(MoeGate), ctypes.POINTER(MoeLinear)
+        tensors, qw, sc = ctypes.POINTER(MoeTensor), ctypes.POINTER(MoeQWeights), ctypes.POINTER(MoeScales)
+        for name, args in (
+                ("moe_route_gated", [layer, gate, vp, vp, ctypes.POINTER(MoeRouteOut), vp, sz, vp]),
+                ("moe_route_gated_backward", [layer, gate] + [vp] * 4 + [i32, vp, vp]),
+                ("moe_expert_forward_gated", [layer, gate, vp, vp, vp, qw, sc, vp, i32, vp, vp, sz, vp]),
+                ("moe_expert_backward_gated", [layer, gate, vp, vp, vp, qw, sc, vp, vp, vp, i32] + [vp] * 4 + [sz, vp]),
+                ("moe_fp8_linear", [lin] + [vp] * 5 + [sz, vp]),
+                ("moe_fp8_linear_transpose", [lin] + [vp] * 5),
+                ("moe_fp8_linear_backward", [lin] + [vp] * 7 + [sz, vp]),
+                ("moe_grad_norm", [tensors, i32, vp, vp, sz, vp]),
+                ("moe_grad_clip", [tensors, i32, f32, vp, vp, sz, vp]),
+                ("moe_grad_scale", [tensors, i32, vp, f32, vp])):
+            getattr(L, name).restype, getattr(L, name).argtypes = ctypes.c_int, args
+        L.moe_fp8_linear_workspace_bytes.restype, L.moe_fp8_linear_workspace_bytes.argtypes = sz, [lin, i32]
+        L.moe_grad_norm_workspace_bytes.restype, L.moe_grad_norm_workspace_bytes.argtypes = sz, [i32]
         _lib = L
     return _lib
 
@@ -645,3 +683,265 @@ def balance_loss_backward(layer: MoeLayer, logits, counts, tokens, d_loss, token
         _check(lib().moe_balance_loss_backward(ctypes.byref(layer), lp, mp, op, S, cp, np_, dl, add, dp, _raw_stream(dev)),
                "moe_balance_loss_backward")
     return d_logits
+
+
+# ---- the gate ----
+
+def make_gate(score: int = GATE_SIGMOID, groups: int = 1, top_groups: int = 1, group_score: int = GROUP_TOP2,
+              renormalize: bool = True, scale: float = 1.0) -> MoeGate:
+    """A gate's descriptor (moe_gate): score GATE_SOFTMAX or GATE_SIGMOID, the
+    top_groups best of `groups` groups by GROUP_MAX or GROUP_TOP2."""
+    return MoeGate(score, groups, top_groups, group_score, int(renormalize), scale)
+
+
+def _workspace(nbytes: int, ws, device):
+    """(workspace, its bytes): the caller's, or a new one."""
+    if ws is None:
+        ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError("ws: contiguous tensor on the call's device expected")
+    return ws, ws.numel() * ws.element_size()
+
+
+def _gate_inputs(layer, logits, bias):
+    """(device, pointer of logits, pointer of bias or None) of a gate's call."""
+    dev, E = logits.device, layer.num_experts
+    return (dev, _typed(logits, "logits", torch.float32, (layer.num_tokens, E), dev),
+            None if bias is None else _typed(bias, "bias", torch.float32, (E,), dev))
+
+
+def route_gated(layer: MoeLayer, gate: MoeGate, logits, bias=None, permute: bool = True, ws=None) -> dict:
+    """moe_route_gated on router logits [T][E] fp32 with a balance bias [E] fp32:
+    a dict as route_permute's; without `permute` only topk_ids and topk_w."""
+    T, E, k = layer.num_tokens, layer.num_experts, layer.top_k
+    with _On(logits.device):
+        dev, lp, bp = _gate_inputs(layer, logits, bias)
+        out = dict(topk_ids=torch.empty((T, k), dtype=torch.int32, device=dev),
+                   topk_w=torch.empty((T, k), dtype=torch.float32, device=dev))
+        wp, nb = None, 0
+        if permute:
+            for name, n in (("expert_offsets", E + 1), ("sorted_rows", T * k), ("row_of", T * k),
+                            ("active_experts", E), ("num_active", 4)):
+                out[name] = (torch.empty if T else torch.zeros)(n, dtype=torch.int32, device=dev)
+            ws, nb = _workspace(lib().moe_route_workspace_bytes(ctypes.byref(layer)), ws, dev)
+            wp = ws.data_ptr()
+        ro = MoeRouteOut(*[t.data_ptr() for t in out.values()])
+        _check(lib().moe_route_gated(ctypes.byref(layer), ctypes.byref(gate), lp, bp, ctypes.byref(ro), wp, nb,
+                                     _raw_stream(dev)), "moe_route_gated")
+    return out
+
+
+def route_gated_backward(layer: MoeLayer, gate: MoeGate, logits, topk_ids, d_topk_w, bias=None,
+                         d_logits: torch.Tensor | None = None):
+    """moe_route_gated_backward: dL/dlogits [T][E] fp32 for d_topk_w [T][k] fp32, with
+    topk_ids from route_gated.  Where d_logits is given (balance_loss_backward's),
+    the gradient is added to it."""
+    T, E, k = layer.num_tokens, layer.num_experts, layer.top_k
+    with _On(logits.device):
+        dev, lp, bp = _gate_inputs(layer, logits, bias)
+        ip = _typed(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+        wp = _typed(d_topk_w, "d_topk_w", torch.float32, (T, k), dev)
+        add = d_logits is not None
+        if not add:
+            d_logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        dp = _typed(d_logits, "d_logits", torch.float32, (T, E), dev)
+        _check(lib().moe_route_gated_backward(ctypes.byref(layer), ctypes.byref(gate), lp, bp, ip, wp, add, dp,
+                                              _raw_stream(dev)), "moe_route_gated_backward")
+    return d_logits
+
+
+def expert_forward_gated(layer: MoeLayer, gate: MoeGate, x, logits, w13, w2, s13, s2, bias=None, adapter=None,
+                         chunk_experts: int = 1, out: torch.Tensor | None = None, ws=None, g13=None, g2=None):
+    """moe_expert_forward_gated: expert_forward with its routing through a gate."""
+    with _On(logits.device):
+        dev, lp, bp = _gate_inputs(layer, logits, bias)
+        if out is None:
+            out = torch.empty((layer.num_tokens, layer.hidden), dtype=torch.bfloat16, device=dev)
+        ws, nb = _workspace(workspace_bytes(layer, chunk_experts), ws, dev)
+        _check_forward_args(layer, x, logits, w13, w2, s13, s2, adapter, out, g13, g2)
+        qw = MoeQWeights(_ptr(w13), _ptr(w2))
+        sc = MoeScales(_ptr(s13), _ptr(s2), _ptr(g13), _ptr(g2))
+        _check(lib().moe_expert_forward_gated(ctypes.byref(layer), ctypes.byref(gate), _ptr(x), lp, bp,
+                                              ctypes.byref(qw), ctypes.byref(sc), _ptr(adapter), int(chunk_experts),
+                                              _ptr(out), ws.data_ptr(), nb, _raw_stream(dev)),
+               "moe_expert_forward_gated")
+    return out
+
+
+def expert_backward_gated(layer: MoeLayer, gate: MoeGate, x, logits, w13, w2, s13, s2, bwd_weights, d_out, bias=None,
+                          adapter=None, chunk_experts: int = 1, ws=None, g13=None, g2=None):
+    """moe_expert_backward_gated -> (d_x [T][H] bf16, d_logits [T][E] fp32, d_adapter fp32 or None)."""
+    T, H, E = layer.num_tokens, layer.hidden, layer.num_experts
+    with _On(logits.device):
+        dev, lp, bp = _gate_inputs(layer, logits, bias)
+        d_x = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        d_logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        d_adapter = None if adapter is None else torch.empty(adapter.shape, dtype=torch.float32, device=dev)
+        ws, nb = _workspace(backward_workspace_bytes(layer, chunk_experts), ws, dev)
+        _check_forward_args(layer, x, logits, w13, w2, s13, s2, adapter, d_x, g13, g2)
+        _need(d_out, "d_out", T * H * 2, 2)
+        _need(bwd_weights, "bwd_weights", backward_weights_bytes(layer))
+        qw = MoeQWeights(_ptr(w13), _ptr(w2))
+        sc = MoeScales(_ptr(s13), _ptr(s2), _ptr(g13), _ptr(g2))
+        _check(lib().moe_expert_backward_gated(ctypes.byref(layer), ctypes.byref(gate), _ptr(x), lp, bp,
+                                               ctypes.byref(qw), ctypes.byref(sc), _ptr(bwd_weights), _ptr(adapter),
+                                               _ptr(d_out), int(chunk_experts), d_x.data_ptr(), d_logits.data_ptr(),
+                                               _ptr(d_adapter), ws.data_ptr(), nb, _raw_stream(dev)),
+               "moe_expert_backward_gated")
+    return d_x, d_logits, d_adapter
+
+
+# ---- the dense FP8 projection ----
+
+def _codes(w, name: str, device):
+    """The address of a matrix of E4M3 codes (uint8 or float8_e4m3fn)."""
+    if w.dtype == torch.float8_e4m3fn:
+        w = w.view(torch.uint8)
+    return _typed(w, name, torch.uint8, w.shape if w.dim() == 2 else (0, 0), device)
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def fp8_linear_workspace_bytes(M: int, K: int, N: int, grads: int = LINEAR_FORWARD) -> int:
+    """Workspace of fp8_linear, or of fp8_linear_backward for LINEAR_D_X, LINEAR_D_W or both or-ed."""
+    return lib().moe_fp8_linear_workspace_bytes(ctypes.byref(MoeLinear(M, K, N, FMT_FP8, 0, 0)), grads)
+
+
+def fp8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, fmt: int = FMT_FP8,
+               out: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """moe_fp8_linear: x [M][K] bf16 (rows may be strided) through W [N][K] in E4M3
+    codes with scales [ceil(N/128)][ceil(K/128)] fp32 -> [M][N] bf16."""
+    dev = x.device
+    with _On(dev):
+        xp, xs = _rows(x, "x", dev)
+        wp = _codes(w, "w", dev)
+        (M, K), N = x.shape, w.shape[0]
+        if w.shape[1] != K:
+            raise ValueError(f"x has {K} columns, w {w.shape[1]}")
+        sp = _typed(w_scale, "w_scale", torch.float32, (_blocks(N), _blocks(K)), dev)
+        lin = MoeLinear(M, K, N, fmt, xs, 0)
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        op = _typed(out, "out", torch.bfloat16, (M, N), dev)
+        ws, nb = _workspace(lib().moe_fp8_linear_workspace_bytes(ctypes.byref(lin), LINEAR_FORWARD), ws, dev)
+        _check(lib().moe_fp8_linear(ctypes.byref(lin), xp, wp, sp, op, ws.data_ptr(), nb, _raw_stream(dev)),
+               "moe_fp8_linear")
+    return out
+
+
+def fp8_linear_transpose(w: torch.Tensor, w_scale: torch.Tensor):
+    """moe_fp8_linear_transpose -> (w_t [K][N] uint8, w_t_scale): what fp8_linear_backward reads."""
+    dev = w.device
+    with _On(dev):
+        wp = _codes(w, "w", dev)
+        N, K = w.shape
+        sp = _typed(w_scale, "w_scale", torch.float32, (_blocks(N), _blocks(K)), dev)
+        wt = torch.empty((K, N), dtype=torch.uint8, device=dev)
+        st = torch.empty((_blocks(K), _blocks(N)), dtype=torch.float32, device=dev)
+        _check(lib().moe_fp8_linear_transpose(ctypes.byref(MoeLinear(0, K, N, FMT_FP8, 0, 0)), wp, sp, wt.data_ptr(),
+                                              st.data_ptr(), _raw_stream(dev)), "moe_fp8_linear_transpose")
+    return wt, st
+
+
+def fp8_linear_backward(d_y: torch.Tensor, w_t: torch.Tensor, w_t_scale: torch.Tensor, fmt: int = FMT_FP8,
+                        x: torch.Tensor | None = None, input_grad: bool = True, weight_grad: bool = False,
+                        ws: torch.Tensor | None = None):
+    """moe_fp8_linear_backward -> (d_x [M][K] bf16 or None, d_w [N][K] bf16 or None) for
+    d_y [M][N] bf16, with fp8_linear_transpose's copy of W and, for d_w, the
+    forward's x [M][K] bf16 (rows of d_y and x may be strided)."""
+    dev = d_y.device
+    with _On(dev):
+        yp, ys = _rows(d_y, "d_y", dev)
+        wp = _codes(w_t, "w_t", dev)
+        (M, N), K = d_y.shape, w_t.shape[0]
+        if w_t.shape[1] != N:
+            raise ValueError(f"d_y has {N} columns, w_t {w_t.shape[1]}")
+        sp = _typed(w_t_scale, "w_t_scale", torch.float32, (_blocks(K), _blocks(N)), dev)
+        xp, xs = None, 0
+        if weight_grad:
+            if x is None:
+                raise ValueError("x: needed for the weight's gradient")
+            xp, xs = _rows(x, "x", dev)
+            if tuple(x.shape) != (M, K):
+                raise ValueError(f"x: shape {(M, K)} expected, got {tuple(x.shape)}")
+        lin = MoeLinear(M, K, N, fmt, xs, ys)
+        d_x = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if input_grad else None
+        d_w = torch.empty((N, K), dtype=torch.bfloat16, device=dev) if weight_grad else None
+        grads = (LINEAR_D_X if input_grad else 0) | (LINEAR_D_W if weight_grad else 0)
+        ws, nb = _workspace(lib().moe_fp8_linear_workspace_bytes(ctypes.byref(lin), grads), ws, dev)
+        _check(lib().moe_fp8_linear_backward(ctypes.byref(lin), yp, wp, sp, xp, _ptr(d_x), _ptr(d_w), ws.data_ptr(),
+                                             nb, _raw_stream(dev)), "moe_fp8_linear_backward")
+    return d_x, d_w
+
+
+# ---- clipping by the global norm ----
+
+def _tensors(grads, out, write: bool = True):
+    """(device, moe_tensor array, count) of a list of gradients; out: None (in place), or where the results go."""
+    grads = list(grads)
+    dest = grads if out is None else list(out)
+    if len(dest) != len(grads):
+        raise ValueError(f"out: {len(dest)} tensors for {len(grads)}")
+    dev, spans = grads[0].device if grads else None, []
+    arr = (MoeTensor * max(1, len(grads)))()
+    for i, (g, o) in enumerate(zip(grads, dest)):
+        for t, name in ((g, "grads"),) if o is g else ((g, "grads"), (o, "out")):
+            if t.dtype not in _DTYPES or not t.is_contiguous() or t.device != dev or not t.is_cuda:
+                raise ValueError(f"{name}[{i}]: contiguous fp32, bf16 or fp16 tensor on {dev} expected, got {t.dtype} "
+                                 f"{tuple(t.shape)} on {t.device}")
+        if o is not g and (o.dtype != g.dtype or o.shape != g.shape):
+            raise ValueError(f"out[{i}]: {g.dtype} {tuple(g.shape)} expected, got {o.dtype} {tuple(o.shape)}")
+        gp, op, n = g.data_ptr(), o.data_ptr(), g.numel()
+        if write and n:
+            nb = n * g.element_size()
+            spans.append((op, op + nb, True))
+            if op != gp:
+                spans.append((gp, gp + nb, False))
+        arr[i] = MoeTensor(gp, op, n, _DTYPES[g.dtype])
+    written = read = 0  # ends of what lies before, in the order of addresses
+    for first, end, writes in sorted(spans):
+        if first < written or (writes and first < read):
+            raise ValueError("grads, out: tensors overlap")
+        written, read = (max(written, end), read) if writes else (written, max(read, end))
+    return dev, arr, len(grads)
+
+
+def _device_or_current(dev):
+    return torch.device("cuda", torch.cuda.current_device()) if dev is None else dev
+
+
+def grad_norm(grads, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """moe_grad_norm: the 2-norm over every element of every tensor (fp32, bf16 or
+    fp16), as a device tensor [1] fp32."""
+    dev, arr, n = _tensors(grads, None, write=False)
+    dev = _device_or_current(dev)
+    with _On(dev):
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+        ws, nb = _workspace(lib().moe_grad_norm_workspace_bytes(n), ws, dev)
+        _check(lib().moe_grad_norm(arr, n, norm.data_ptr(), ws.data_ptr(), nb, _raw_stream(dev)), "moe_grad_norm")
+    return norm
+
+
+def clip_grads(grads, max_norm: float, out=None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """moe_grad_clip: scales the tensors by max_norm / norm where their common norm
+    is larger, in place or into the tensors `out`; returns the norm [1] fp32."""
+    dev, arr, n = _tensors(grads, out)
+    dev = _device_or_current(dev)
+    with _On(dev):
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+        ws, nb = _workspace(lib().moe_grad_norm_workspace_bytes(n), ws, dev)
+        _check(lib().moe_grad_clip(arr, n, max_norm, norm.data_ptr(), ws.data_ptr(), nb, _raw_stream(dev)),
+               "moe_grad_clip")
+    return norm
+
+
+def scale_grads(grads, norm: torch.Tensor, max_norm: float, out=None) -> None:
+    """moe_grad_scale: the scaling of clip_grads for a norm [1] fp32 on the device (one joined over ranks)."""
+    dev, arr, n = _tensors(grads, out)
+    dev = _device_or_current(dev)
+    with _On(dev):
+        if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != dev:
+            raise ValueError(f"norm: one fp32 value on {dev} expected")
+        _check(lib().moe_grad_scale(arr, n, norm.data_ptr(), max_norm, _raw_stream(dev)), "moe_grad_scale")

@@ -238,4 +238,79 @@ void launch_balance_bwd(const float* logits, const uint8_t* mask, const int32_t*
                         const int32_t* counts, const int32_t* tokens, const float* dloss, int accumulate,
                         float* dlogits, hipStream_t s);
 
+// The gate (scores, choice of experts, weights) and its gradient.
+constexpr int GATE_MAX_GROUPS = 64;
+struct GateArgs {
+  const float* logits;    // [T][E]
+  const float* bias;      // [E] or null
+  int T, E, k;
+  int sigmoid;            // else softmax
+  int groups, top_groups;
+  int top2;               // a group's value: the sum of its two largest, else the largest
+  int renorm;
+  float scale;
+  int32_t* ids;           // [T][k]
+  float* w;               // [T][k]
+  const float* dw;        // backward: dL/dw [T][k]
+  float* dlogits;         // backward: [T][E]
+  int accumulate;
+};
+void launch_gate(const GateArgs& a, hipStream_t s);
+void launch_gate_bwd(const GateArgs& a, hipStream_t s);
+// g[q] = sum of row row_of[q]'s nparts parts of gpart, for R pairs q
+void launch_pair_grad(const int32_t* row_of, const float* gpart, int nparts, int R, float* g, hipStream_t s);
+
+// Global norm and clipping of a list of tensors.
+struct ClipTensor {
+  const void* p;
+  void* out;
+  int64_t n;
+  int32_t dtype;      // a moe_dtype value
+  int32_t chunk0;     // chunks of the tensors before it in this launch
+};
+constexpr int CLIP_TENSORS = 80;   // per launch: the list travels as a kernel argument
+constexpr int CLIP_BLOCKS = 1024;  // partial sums per launch
+struct ClipList {
+  ClipTensor t[CLIP_TENSORS];
+  int n, chunks;
+};
+int64_t clip_chunks(int64_t elems, int dtype);
+void launch_norm_parts(const ClipList& l, double* parts, hipStream_t s);
+void launch_norm_finish(const double* parts, int nparts, float* norm, hipStream_t s);
+// nparts > 0: the norm is formed from the parts (and written by the launch with
+// write != 0), else read
+void launch_clip(const ClipList& l, const double* parts, int nparts, float* norm, int write, float max_norm,
+                 hipStream_t s);
+
+// The dense FP8 projection.  One product: C[m][n] over K blocks of 128.
+struct LinGemm {
+  const uint8_t* a;       // codes [m][lda], zeros behind K
+  int64_t lda;
+  int m;
+  const uint8_t* b;       // codes [n][ldb], kbytes of a row valid
+  int64_t ldb;
+  int n, kbytes;
+  int kt;                 // K blocks
+  const float* sa;        // [kt][sa_ld]
+  int sa_ld;
+  const float* sb;        // [n/128][sb_ld], or per row: [kt][sb_ld]
+  int sb_ld;
+  uint16_t* out;          // bf16 [m][ldo]
+  int64_t ldo;
+  int splits;             // ways K is split (1: not)
+  float* part;            // [splits][m][n]
+};
+struct LinPlan {
+  size_t q, s, part, qa, qb, sqa, sqb, wpart, total;  // byte offsets into the workspace
+  int splits, wsplits;
+};
+LinPlan lin_plan(int M, int K, int N, bool backward, bool input_grad, bool weight_grad);
+// y [M][out_n] = Q(x) W^T over x [M][C], W [out_n][C]
+void launch_linear(const LinPlan& pl, const uint16_t* x, int64_t stride, int M, int C, int out_n, const uint8_t* w,
+                   const float* sw, bool pow2, uint16_t* y, char* ws, hipStream_t s);
+void launch_linear_dw(const LinPlan& pl, const uint16_t* dy, int64_t dy_stride, const uint16_t* x, int64_t x_stride,
+                      int M, int K, int N, bool pow2, uint16_t* dw, char* ws, hipStream_t s);
+void launch_linear_transpose(const uint8_t* w, const float* sc, int N, int K, uint8_t* wt, float* st, hipStream_t s);
+void launch_linear_zero(void* p, int64_t bytes, hipStream_t s);
+
 }  // namespace moe

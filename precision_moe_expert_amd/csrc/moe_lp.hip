@@ -204,9 +204,68 @@ struct Scope {
   ~Scope() { if (t) t->end(); }
 };
 
+// A gate with its bias, checked; null: softmax over the chosen logits.
+struct Gate {
+  const moe_gate* g;
+  const float* bias;
+};
+
 moe_status forward_impl(const moe_layer* layer, const void* x_bf16, const float* logits, const moe_qweights* qw,
                         const moe_scales* sc, const void* adapter_bf16, int32_t chunk_experts, void* out_bf16,
-                        void* ws, size_t ws_bytes, void* stream, StageTimer* tm);
+                        void* ws, size_t ws_bytes, void* stream, StageTimer* tm, const Gate* gate = nullptr);
+
+// Validates a gate for a layer.
+moe_status check_gate(const moe_gate* g, const float* bias, const Dims& d) {
+  if (g == nullptr || !aligned16(bias)) return MOE_ERR_INVALID_ARGUMENT;
+  if (g->score != MOE_GATE_SOFTMAX && g->score != MOE_GATE_SIGMOID) return MOE_ERR_INVALID_ARGUMENT;
+  if (g->group_score != MOE_GROUP_MAX && g->group_score != MOE_GROUP_TOP2) return MOE_ERR_INVALID_ARGUMENT;
+  if (g->renormalize != 0 && g->renormalize != 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (g->num_groups < 1 || d.E % g->num_groups != 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (g->top_groups < 1 || g->top_groups > g->num_groups || g->top_groups * (d.E / g->num_groups) < d.k)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!(g->scale > 0.0f && g->scale <= 3.0e38f)) return MOE_ERR_INVALID_ARGUMENT;
+  return g->num_groups > MOE_GATE_MAX_GROUPS ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+GateArgs gate_args(const Dims& d, const moe_gate* g, const float* logits, const float* bias) {
+  GateArgs a{};
+  a.logits = logits;
+  a.bias = bias;
+  a.T = d.T;
+  a.E = d.E;
+  a.k = d.k;
+  a.sigmoid = g->score == MOE_GATE_SIGMOID;
+  a.groups = g->num_groups;
+  a.top_groups = g->top_groups;
+  a.top2 = g->group_score == MOE_GROUP_TOP2;
+  a.renorm = g->renormalize;
+  a.scale = g->scale;
+  return a;
+}
+
+// The permutation of out.topk_ids by expert (ws: moe_route_workspace_bytes).
+void permute_into(const Dims& d, const moe_route_out& out, void* ws, hipStream_t s) {
+  char* base = static_cast<char*>(ws);
+  int32_t* tile_a = reinterpret_cast<int32_t*>(base);
+  int32_t* tile_16 = reinterpret_cast<int32_t*>(base + align_up((size_t)(d.E + 1) * 4));
+  int32_t* tiles = reinterpret_cast<int32_t*>(base + 2 * align_up((size_t)(d.E + 1) * 4));
+  int32_t* hist = reinterpret_cast<int32_t*>(base + 2 * align_up((size_t)(d.E + 1) * 4) +
+                                             align_up((size_t)max_row_tiles(d.R, d.E) * 16));
+  launch_permute(out.topk_ids, (int)d.R, d.E, choose_bm(d), hist, out.expert_offsets, out.sorted_rows, out.row_of,
+                 out.active_experts, out.num_active, tile_a, tile_16, tiles, nullptr, 0, s);
+}
+
+// The choice of a layer's experts and their weights.
+void route(const Dims& d, const Gate* gate, const float* logits, int32_t* ids, float* w, hipStream_t s) {
+  if (gate == nullptr) {
+    launch_route(logits, d.T, d.E, d.k, ids, w, s);
+    return;
+  }
+  GateArgs a = gate_args(d, gate->g, logits, gate->bias);
+  a.ids = ids;
+  a.w = w;
+  launch_gate(a, s);
+}
 
 }  // namespace
 
@@ -294,15 +353,8 @@ moe_status moe_route_permute(const moe_layer* layer, const float* logits, const 
     if (p == nullptr || !aligned16(p)) return MOE_ERR_INVALID_ARGUMENT;
   if (ws_bytes < moe_route_workspace_bytes(layer)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  char* base = static_cast<char*>(ws);
-  int32_t* tile_a = reinterpret_cast<int32_t*>(base);
-  int32_t* tile_16 = reinterpret_cast<int32_t*>(base + align_up((size_t)(d.E + 1) * 4));
-  int32_t* tiles = reinterpret_cast<int32_t*>(base + 2 * align_up((size_t)(d.E + 1) * 4));
-  int32_t* hist = reinterpret_cast<int32_t*>(base + 2 * align_up((size_t)(d.E + 1) * 4) +
-                                             align_up((size_t)max_row_tiles(d.R, d.E) * 16));
   launch_route(logits, d.T, d.E, d.k, out->topk_ids, out->topk_w, s);
-  launch_permute(out->topk_ids, (int)d.R, d.E, choose_bm(d), hist, out->expert_offsets, out->sorted_rows,
-                 out->row_of, out->active_experts, out->num_active, tile_a, tile_16, tiles, nullptr, 0, s);
+  permute_into(d, *out, ws, s);
   return launch_status();
 }
 
@@ -334,9 +386,10 @@ moe_status moe_expert_forward_timed(const moe_layer* layer, const void* x_bf16, 
 namespace {
 moe_status forward_impl(const moe_layer* layer, const void* x_bf16, const float* logits, const moe_qweights* qw,
                         const moe_scales* sc, const void* adapter_bf16, int32_t chunk_experts, void* out_bf16,
-                        void* ws, size_t ws_bytes, void* stream, StageTimer* tm) {
+                        void* ws, size_t ws_bytes, void* stream, StageTimer* tm, const Gate* gate) {
   Dims d;
   moe_status st = check_layer(layer, &d);
+  if (st == MOE_OK && gate != nullptr) st = check_gate(gate->g, gate->bias, d);
   if (st != MOE_OK) return st;
   if (chunk_experts < 1 || qw == nullptr || sc == nullptr) return MOE_ERR_INVALID_ARGUMENT;
   if ((adapter_bf16 != nullptr) != d.oft) return MOE_ERR_INVALID_ARGUMENT;
@@ -375,7 +428,7 @@ moe_status forward_impl(const moe_layer* layer, const void* x_bf16, const float*
   const int bm = choose_bm(d);
 
   // 1-2. route and permute
-  { Scope sc_(tm, MOE_STAGE_ROUTE); launch_route(logits, d.T, d.E, d.k, ids, wts, s); }
+  { Scope sc_(tm, MOE_STAGE_ROUTE); route(d, gate, logits, ids, wts, s); }
   { Scope sc_(tm, MOE_STAGE_PERMUTE);
     launch_permute(ids, (int)d.R, d.E, bm, hist, offsets, sorted_rows, row_of, active, num_active, tile_a, tile_16,
                    tiles, queue, queue_ints(d), s); }
@@ -776,9 +829,11 @@ namespace {
 moe_status backward_impl(const moe_layer* layer, const void* x_bf16, const float* logits, const moe_qweights* qw,
                          const moe_scales* sc, const void* bwd_weights, const void* adapter_bf16,
                          const void* d_out_bf16, int32_t chunk_experts, void* d_x_bf16, float* d_logits,
-                         float* d_adapter, void* ws, size_t ws_bytes, void* stream, StageTimer* tm) {
+                         float* d_adapter, void* ws, size_t ws_bytes, void* stream, StageTimer* tm,
+                         const Gate* gate = nullptr) {
   Dims d;
   moe_status st = check_backward(layer, &d);
+  if (st == MOE_OK && gate != nullptr) st = check_gate(gate->g, gate->bias, d);
   if (st != MOE_OK) return st;
   if (chunk_experts < 1 || qw == nullptr || sc == nullptr) return MOE_ERR_INVALID_ARGUMENT;
   if ((adapter_bf16 != nullptr) != d.oft || (d_adapter != nullptr) != d.oft) return MOE_ERR_INVALID_ARGUMENT;
@@ -826,7 +881,7 @@ moe_status backward_impl(const moe_layer* layer, const void* x_bf16, const float
   int32_t* tile_a_r = bm_r == bm ? tile_a : I32(wl.tile_a_r);
   int32_t* tiles_r = bm_r == bm ? tiles : I32(wl.tiles_r);
 
-  { Scope sc_(tm, MOE_STAGE_ROUTE); launch_route(logits, d.T, d.E, d.k, ids, wts, s); }
+  { Scope sc_(tm, MOE_STAGE_ROUTE); route(d, gate, logits, ids, wts, s); }
   { Scope sc_(tm, MOE_STAGE_PERMUTE);
     // second pass (same permutation) for the recompute's tile list when its height differs
     if (bm_r != bm)
@@ -960,7 +1015,18 @@ moe_status backward_impl(const moe_layer* layer, const void* x_bf16, const float
     dx_rows = dxr;
   }
   launch_unpermute_sum(dx_rows, row_of, d.T, d.k, d.H, static_cast<uint16_t*>(d_x_bf16), s);
-  launch_router_grad(ids, wts, row_of, gpart, d.I / 256, d.T, d.k, d.E, d_logits, s);
+  if (gate == nullptr) {
+    launch_router_grad(ids, wts, row_of, gpart, d.I / 256, d.T, d.k, d.E, d_logits, s);
+  } else {
+    // dL/dw of every pair, where the SwiGLU gradients were (the last product has read them)
+    float* dwts = reinterpret_cast<float*>(dab);
+    launch_pair_grad(row_of, gpart, d.I / 256, (int)d.R, dwts, s);
+    GateArgs a = gate_args(d, gate->g, logits, gate->bias);
+    a.ids = ids;
+    a.dw = dwts;
+    a.dlogits = d_logits;
+    launch_gate_bwd(a, s);
+  }
   }
   return launch_status();
 }
@@ -1278,6 +1344,267 @@ moe_status moe_balance_loss_backward(const moe_layer* layer, const float* logits
   if (!all_aligned16(ptrs) || !aligned16(token_mask) || !aligned16(seg_offsets)) return MOE_ERR_INVALID_ARGUMENT;
   launch_balance_bwd(logits, token_mask, seg_offsets, num_segs, d.T, d.E, d.k, counts, tokens, d_loss, accumulate,
                      d_logits, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- the gate
+
+extern "C" {
+
+moe_status moe_route_gated(const moe_layer* layer, const moe_gate* gate, const float* logits, const float* bias,
+                           const moe_route_out* out, void* ws, size_t ws_bytes, void* stream) {
+  Dims d;
+  moe_status st = check_layer(layer, &d);
+  if (st == MOE_OK) st = check_gate(gate, bias, d);
+  if (st != MOE_OK) return st;
+  if (out == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (d.T == 0) return MOE_OK;
+  const void* ptrs[] = {logits, out->topk_ids, out->topk_w};
+  const void* perm[] = {out->expert_offsets, out->sorted_rows, out->row_of, out->active_experts, out->num_active};
+  int have = 0;
+  for (const void* p : perm) have += p != nullptr;
+  for (const void* p : ptrs)
+    if (p == nullptr || !aligned16(p)) return MOE_ERR_INVALID_ARGUMENT;
+  if (have != 0) {
+    for (const void* p : perm)
+      if (p == nullptr || !aligned16(p)) return MOE_ERR_INVALID_ARGUMENT;
+    if (ws == nullptr || !aligned16(ws)) return MOE_ERR_INVALID_ARGUMENT;
+    if (ws_bytes < moe_route_workspace_bytes(layer)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const Gate gt{gate, bias};
+  route(d, &gt, logits, out->topk_ids, out->topk_w, s);
+  if (have != 0) permute_into(d, *out, ws, s);
+  return launch_status();
+}
+
+moe_status moe_route_gated_backward(const moe_layer* layer, const moe_gate* gate, const float* logits,
+                                    const float* bias, const int32_t* topk_ids, const float* d_topk_w,
+                                    int32_t accumulate, float* d_logits, void* stream) {
+  Dims d;
+  moe_status st = check_layer(layer, &d);
+  if (st == MOE_OK) st = check_gate(gate, bias, d);
+  if (st != MOE_OK) return st;
+  if (d.T == 0) return MOE_OK;
+  const void* ptrs[] = {logits, topk_ids, d_topk_w, d_logits};
+  for (const void* p : ptrs)
+    if (p == nullptr || !aligned16(p)) return MOE_ERR_INVALID_ARGUMENT;
+  GateArgs a = gate_args(d, gate, logits, bias);
+  a.ids = const_cast<int32_t*>(topk_ids);
+  a.dw = d_topk_w;
+  a.dlogits = d_logits;
+  a.accumulate = accumulate != 0;
+  launch_gate_bwd(a, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+moe_status moe_expert_forward_gated(const moe_layer* layer, const moe_gate* gate, const void* x_bf16,
+                                    const float* logits, const float* bias, const moe_qweights* qw,
+                                    const moe_scales* sc, const void* adapter_bf16, int32_t chunk_experts,
+                                    void* out_bf16, void* ws, size_t ws_bytes, void* stream) {
+  const Gate gt{gate, bias};
+  return forward_impl(layer, x_bf16, logits, qw, sc, adapter_bf16, chunk_experts, out_bf16, ws, ws_bytes, stream,
+                      nullptr, &gt);
+}
+
+moe_status moe_expert_backward_gated(const moe_layer* layer, const moe_gate* gate, const void* x_bf16,
+                                     const float* logits, const float* bias, const moe_qweights* qw,
+                                     const moe_scales* sc, const void* bwd_weights, const void* adapter_bf16,
+                                     const void* d_out_bf16, int32_t chunk_experts, void* d_x_bf16, float* d_logits,
+                                     float* d_adapter, void* ws, size_t ws_bytes, void* stream) {
+  const Gate gt{gate, bias};
+  return backward_impl(layer, x_bf16, logits, qw, sc, bwd_weights, adapter_bf16, d_out_bf16, chunk_experts, d_x_bf16,
+                       d_logits, d_adapter, ws, ws_bytes, stream, nullptr, &gt);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- the dense FP8 projection
+
+namespace {
+
+moe_status check_linear(const moe_linear* l) {
+  if (l == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (l->num_tokens < 0 || l->in_features <= 0 || l->out_features <= 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (l->wformat != MOE_W_FP8_E4M3_B128 && l->wformat != MOE_W_FP8_E4M3_B128_POW2)
+    return l->wformat == MOE_W_INT4_G32_BF16 || l->wformat == MOE_W_MXFP4 || l->wformat == MOE_W_NVFP4
+               ? MOE_ERR_UNSUPPORTED
+               : MOE_ERR_INVALID_ARGUMENT;
+  const int64_t st[] = {l->x_stride, l->dy_stride}, width[] = {l->in_features, l->out_features};
+  for (int i = 0; i < 2; ++i) {
+    if (st[i] < 0 || (st[i] != 0 && st[i] < width[i])) return MOE_ERR_INVALID_ARGUMENT;
+    if (st[i] % 8 != 0 || st[i] > (1 << 22) || width[i] % 16 != 0 || width[i] > (1 << 17)) return MOE_ERR_UNSUPPORTED;
+  }
+  return l->num_tokens > (1 << 20) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+LinPlan linear_plan(const moe_linear* l, int32_t grads) {
+  return lin_plan(l->num_tokens, l->in_features, l->out_features, grads != MOE_LINEAR_FORWARD,
+                  (grads & MOE_LINEAR_D_X) != 0, (grads & MOE_LINEAR_D_W) != 0);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_fp8_linear_workspace_bytes(const moe_linear* lin, int32_t grads) {
+  if (check_linear(lin) != MOE_OK || grads < 0 || grads > (MOE_LINEAR_D_X | MOE_LINEAR_D_W)) return 0;
+  return linear_plan(lin, grads).total;
+}
+
+moe_status moe_fp8_linear(const moe_linear* lin, const void* x_bf16, const void* w, const float* w_scale,
+                          void* y_bf16, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status st = check_linear(lin);
+  if (st != MOE_OK) return st;
+  if (lin->num_tokens == 0) return MOE_OK;
+  const void* ptrs[] = {x_bf16, w, w_scale, y_bf16, ws};
+  if (!all_aligned16(ptrs)) return MOE_ERR_INVALID_ARGUMENT;
+  const LinPlan p = linear_plan(lin, MOE_LINEAR_FORWARD);
+  if (ws_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  launch_linear(p, static_cast<const uint16_t*>(x_bf16), lin->x_stride ? lin->x_stride : lin->in_features,
+                lin->num_tokens, lin->in_features, lin->out_features, static_cast<const uint8_t*>(w), w_scale,
+                lin->wformat == MOE_W_FP8_E4M3_B128_POW2, static_cast<uint16_t*>(y_bf16), static_cast<char*>(ws),
+                static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+moe_status moe_fp8_linear_transpose(const moe_linear* lin, const void* w, const float* w_scale, void* w_t,
+                                    float* w_t_scale, void* stream) {
+  const moe_status st = check_linear(lin);
+  if (st != MOE_OK) return st;
+  const void* ptrs[] = {w, w_scale, w_t, w_t_scale};
+  if (!all_aligned16(ptrs)) return MOE_ERR_INVALID_ARGUMENT;
+  launch_linear_transpose(static_cast<const uint8_t*>(w), w_scale, lin->out_features, lin->in_features,
+                          static_cast<uint8_t*>(w_t), w_t_scale, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+moe_status moe_fp8_linear_backward(const moe_linear* lin, const void* d_y_bf16, const void* w_t,
+                                   const float* w_t_scale, const void* x_bf16, void* d_x_bf16, void* d_w_bf16,
+                                   void* ws, size_t ws_bytes, void* stream) {
+  const moe_status st = check_linear(lin);
+  if (st != MOE_OK) return st;
+  if (d_x_bf16 == nullptr && d_w_bf16 == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned16(d_x_bf16) || !aligned16(d_w_bf16)) return MOE_ERR_INVALID_ARGUMENT;
+  const int M = lin->num_tokens, K = lin->in_features, N = lin->out_features;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (M == 0) {
+    if (d_w_bf16 == nullptr) return MOE_OK;
+    launch_linear_zero(d_w_bf16, (int64_t)N * K * 2, s);
+    return launch_status();
+  }
+  const void* ptrs[] = {d_y_bf16, ws};
+  const void* of_dx[] = {w_t, w_t_scale};
+  const void* of_dw[] = {x_bf16};
+  if (!all_aligned16(ptrs) || (d_x_bf16 != nullptr && !all_aligned16(of_dx)) ||
+      (d_w_bf16 != nullptr && !all_aligned16(of_dw)))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const LinPlan p = linear_plan(lin, (d_x_bf16 ? MOE_LINEAR_D_X : 0) | (d_w_bf16 ? MOE_LINEAR_D_W : 0));
+  if (ws_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const bool pow2 = lin->wformat == MOE_W_FP8_E4M3_B128_POW2;
+  const uint16_t* dy = static_cast<const uint16_t*>(d_y_bf16);
+  const int64_t dys = lin->dy_stride ? lin->dy_stride : N, xs = lin->x_stride ? lin->x_stride : K;
+  if (d_x_bf16 != nullptr)
+    launch_linear(p, dy, dys, M, N, K, static_cast<const uint8_t*>(w_t), w_t_scale, pow2,
+                  static_cast<uint16_t*>(d_x_bf16), static_cast<char*>(ws), s);
+  if (d_w_bf16 != nullptr)
+    launch_linear_dw(p, dy, dys, static_cast<const uint16_t*>(x_bf16), xs, M, K, N, pow2,
+                     static_cast<uint16_t*>(d_w_bf16), static_cast<char*>(ws), s);
+  return launch_status();
+}
+
+}  // extern "C"
+
+// -------------------------------------------- clipping by the global norm
+
+namespace {
+
+moe_status check_tensors(const moe_tensor* t, int32_t n, bool out) {
+  if (n < 0 || (n > 0 && t == nullptr)) return MOE_ERR_INVALID_ARGUMENT;
+  for (int32_t i = 0; i < n; ++i) {
+    if (t[i].num < 0 || t[i].dtype < MOE_DTYPE_F32 || t[i].dtype > MOE_DTYPE_F16) return MOE_ERR_INVALID_ARGUMENT;
+    if (t[i].num > (1ll << 40)) return MOE_ERR_UNSUPPORTED;
+    if (t[i].num == 0) continue;
+    const uintptr_t low = t[i].dtype == MOE_DTYPE_F32 ? 3 : 1;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(t[i].data), b = reinterpret_cast<uintptr_t>(t[i].out);
+    if (a == 0 || (a & low) != 0 || (out && (b == 0 || (b & low) != 0))) return MOE_ERR_INVALID_ARGUMENT;
+  }
+  return MOE_OK;
+}
+
+// Calls f(list) for the tensors with elements, CLIP_TENSORS at a time; the
+// number of calls.
+template <typename F>
+int for_lists(const moe_tensor* t, int32_t n, F f) {
+  int calls = 0;
+  for (int32_t i = 0; i < n;) {
+    ClipList l;
+    l.n = 0;
+    int64_t chunks = 0;
+    for (; i < n && l.n < CLIP_TENSORS; ++i) {
+      if (t[i].num == 0) continue;
+      const int64_t c = clip_chunks(t[i].num, t[i].dtype);
+      if (chunks + c > INT32_MAX / 2) break;  // one tensor has at most 2^28 chunks
+      l.t[l.n++] = ClipTensor{t[i].data, t[i].out, t[i].num, t[i].dtype, (int32_t)chunks};
+      chunks += c;
+    }
+    if (l.n == 0) continue;
+    l.chunks = (int)chunks;
+    f(l, calls++);
+  }
+  return calls;
+}
+
+int list_count(const moe_tensor* t, int32_t n) {
+  return for_lists(t, n, [](const ClipList&, int) {});
+}
+
+moe_status norm_impl(const moe_tensor* t, int32_t n, float* norm, void* ws, size_t ws_bytes, bool clip, float max_norm,
+                     void* stream) {
+  const moe_status st = check_tensors(t, n, clip);
+  if (st != MOE_OK) return st;
+  if (norm == nullptr || !aligned4(norm) || ws == nullptr || !aligned16(ws)) return MOE_ERR_INVALID_ARGUMENT;
+  if (clip && !(max_norm >= 0.0f)) return MOE_ERR_INVALID_ARGUMENT;
+  const int lists = list_count(t, n), nparts = lists * CLIP_BLOCKS;
+  if (ws_bytes < moe_grad_norm_workspace_bytes(n) || ws_bytes < (size_t)nparts * 8) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  double* parts = static_cast<double*>(ws);
+  for_lists(t, n, [&](const ClipList& l, int i) { launch_norm_parts(l, parts + (size_t)i * CLIP_BLOCKS, s); });
+  if (clip && lists > 0)
+    for_lists(t, n, [&](const ClipList& l, int i) { launch_clip(l, parts, nparts, norm, i == 0, max_norm, s); });
+  else
+    launch_norm_finish(parts, nparts, norm, s);
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_grad_norm_workspace_bytes(int32_t n) {
+  if (n < 0) return 0;
+  return (size_t)(n / CLIP_TENSORS + 1) * CLIP_BLOCKS * 8;
+}
+
+moe_status moe_grad_norm(const moe_tensor* tensors, int32_t n, float* norm, void* ws, size_t ws_bytes, void* stream) {
+  return norm_impl(tensors, n, norm, ws, ws_bytes, false, 0.0f, stream);
+}
+
+moe_status moe_grad_clip(const moe_tensor* tensors, int32_t n, float max_norm, float* norm, void* ws,
+                         size_t ws_bytes, void* stream) {
+  return norm_impl(tensors, n, norm, ws, ws_bytes, true, max_norm, stream);
+}
+
+moe_status moe_grad_scale(const moe_tensor* tensors, int32_t n, const float* norm, float max_norm, void* stream) {
+  const moe_status st = check_tensors(tensors, n, true);
+  if (st != MOE_OK) return st;
+  if (norm == nullptr || !aligned4(norm) || !(max_norm >= 0.0f)) return MOE_ERR_INVALID_ARGUMENT;
+  if (list_count(tensors, n) == 0) return MOE_OK;
+  for_lists(tensors, n, [&](const ClipList& l, int) {
+    launch_clip(l, nullptr, 0, const_cast<float*>(norm), 0, max_norm, static_cast<hipStream_t>(stream));
+  });
   return launch_status();
 }
 
