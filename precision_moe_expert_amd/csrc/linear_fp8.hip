@@ -10,6 +10,8 @@
 // products at a time, aligned to the largest with 13 bits kept below it: sums of
 // normal values come out 1.4e-5 of their size off, 1/100 of what rounding to
 // bf16 then costs, and never more than 7 2^-13 of the groups' largest products.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -17,8 +19,13 @@ namespace moe {
 
 namespace {
 
+// LDS loads of 16 (4) bytes per lane: uniform base, a lane's 32-bit offset.
 MOE_DEV void lin_dma(const char* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+
+MOE_DEV void lin_dma4(const char* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
 
 // The scale of a block with largest magnitude amax.
@@ -158,14 +165,18 @@ struct LinTile {
   static constexpr int MI = BM / WM / 16, NJ = BN / WN / 16;
   static constexpr int NDA = BM / 8 / NW, NDB = BN / 8 / NW;  // DMAs per wave and stage, 8 rows each
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && NJ * 16 <= 128, "tile");
-  static constexpr int SC = (BM > BN ? BM : BN) > 256 ? 2048 : 1024;  // bytes of a stage's scales, one side
-  static constexpr int STAGE = (BM + BN) * 128 + 2 * SC;
+  // a stage's scales: 64 rows (256 bytes) by one wave's DMA
+  static constexpr int UA = (BM + 63) / 64, UB = (BN + 63) / 64;
+  static_assert(UA + UB <= NW, "a wave for each");
+  static constexpr int NPER = NDA + NDB + 1;
+  static constexpr int STAGE = (BM + BN) * 128 + (UA + UB) * 256;
   static constexpr int LS = BN * 2 + 16;                      // epilogue's row stride
   static constexpr int SMEM = S * STAGE > BM * LS ? S * STAGE : BM * LS;
   static_assert(SMEM <= 160 * 1024, "LDS");
 };
 
 constexpr int LIN_GM = 4;  // tile rows of a band
+constexpr int LIN_MAX_KT = 1024;
 
 // Workgroup -> tile: each XCD takes a contiguous range of tiles, ordered in
 // bands of LIN_GM tile rows, so that the tiles it works on at one time share few
@@ -187,8 +198,10 @@ MOE_DEV bool lin_tile(int bid, int nm, int nn, int& m, int& n) {
 // one row, so one scale serves a whole fragment.
 template <class C, bool VEC, bool P2>
 __global__ __launch_bounds__(C::NT, C::WPS) void k_lin(LinGemm p) {
-  constexpr int MI = C::MI, NJ = C::NJ, S = C::S, NPER = C::NDA + C::NDB;
+  constexpr int MI = C::MI, NJ = C::NJ, S = C::S, NPER = C::NPER;
   __shared__ __align__(16) uint8_t smem[C::SMEM];
+  constexpr int NB = (C::BN + 127) / 128;
+  __shared__ float sws[VEC ? 1 : NB * LIN_MAX_KT];
   const int nm = (p.m + C::BM - 1) / C::BM, nn = (p.n + C::BN - 1) / C::BN;
   const int ntile = nm * nn, grid1 = (ntile + 7) / 8 * 8;
   const int split = blockIdx.x / grid1;
@@ -218,84 +231,155 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_lin(LinGemm p) {
   }
   const char* pa = reinterpret_cast<const char*>(p.a) + (int64_t)m0 * p.lda;
   const char* pb = reinterpret_cast<const char*>(p.b) + (int64_t)n0 * p.ldb;
-  constexpr int OB = C::BM * 128, OSA = OB + C::BN * 128, OSB = OSA + C::SC;
-  auto issue = [&](int kt, int slot) {
+  constexpr int OB = C::BM * 128, OSA = OB + C::BN * 128, OSB = OSA + C::UA * 256;
+  // this wave's 64 scales of a stage (waves without any repeat the first ones)
+  const bool of_b = VEC && wave >= C::UA && wave < C::UA + C::UB;
+  const int unit = of_b ? wave - C::UA : wave < C::UA ? wave : 0;
+  const char* psc = reinterpret_cast<const char*>(of_b ? p.sb + (int64_t)k0 * p.sb_ld + n0 : p.sa + (int64_t)k0 * p.sa_ld + m0) + unit * 256;
+  const int64_t sc_ld = (int64_t)(of_b ? p.sb_ld : p.sa_ld) * 4;
+  const uint32_t sc_lds = (of_b ? OSB : OSA) + unit * 256;
+  const int part0 = (ds ^ (dr >> 1)) << 4;  // of an even DMA's rows; odd: ^ 64
+  // DMA d of stage kt: A's rows, B's, scales.  LAST: B's rows may end within it
+  // (what is read instead meets A's zeros).
+  auto issue1 = [&](auto last_, int d, int kt, int slot) {
     const uint32_t st = smem0 + slot * C::STAGE;
     const int64_t at = (int64_t)(k0 + kt) * 128;
-#pragma unroll
-    for (int j = 0; j < C::NDA; ++j)
-      lin_dma(pa + at, oa[j], __builtin_amdgcn_readfirstlane(st + (wave * C::NDA + j) * 1024));
-    const int left = p.kbytes - (k0 + kt) * 128;  // of B's rows; A holds zeros behind
-#pragma unroll
-    for (int j = 0; j < C::NDB; ++j) {
+    if (d < C::NDA) {
+      lin_dma(pa + at, oa[d < C::NDA ? d : 0], __builtin_amdgcn_readfirstlane(st + (wave * C::NDA + d) * 1024));
+    } else if (d < C::NDA + C::NDB) {
+      const int j = d - C::NDA;
       uint32_t o = ob[j];
-      if (left < 128) {
-        const int r = (wave * C::NDB + j) * 8 + dr, part = (ds ^ ((r >> 1) & 7)) << 4;
-        if (part >= left) o -= part;
+      if constexpr (decltype(last_)::value) {
+        const int part = part0 ^ (((wave * C::NDB + j) & 1) << 6);
+        o -= part >= p.kbytes - (int)at ? part : 0;
       }
       lin_dma(pb + at, o, __builtin_amdgcn_readfirstlane(st + OB + (wave * C::NDB + j) * 1024));
+    } else {
+      lin_dma4(psc + kt * sc_ld, lane * 4, __builtin_amdgcn_readfirstlane(st + sc_lds));
     }
-    // the tile's scales of this K block; the first waves carry one more DMA
-    if (wave == 0)
-      lin_dma(reinterpret_cast<const char*>(p.sa + (int64_t)(k0 + kt) * p.sa_ld + m0), lane * 16,
-              __builtin_amdgcn_readfirstlane(st + OSA));
-    if (VEC && wave == 1)
-      lin_dma(reinterpret_cast<const char*>(p.sb + (int64_t)(k0 + kt) * p.sb_ld + n0), lane * 16,
-              __builtin_amdgcn_readfirstlane(st + OSB));
   };
   f32x4 acc[MI][NJ];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (!VEC) {
+    // W's scales of the tile's column blocks
+    for (int i = threadIdx.x; i < NB * KT; i += C::NT)
+      sws[i / KT * LIN_MAX_KT + i % KT] = p.sb[(int64_t)min(n0 / 128 + i / KT, (p.n - 1) / 128) * p.sb_ld + k0 + i % KT];
+  }
 #pragma unroll
-  for (int s = 0; s + 1 < S; ++s)
-    if (s < KT) issue(s, s);
-  // block scales of this wave's columns (one block: 64 or fewer of 128)
-  const int nb = min(n0 + wn * NJ * 16, p.n - 1) / 128;
-  const float* sbp = VEC ? nullptr : p.sb + (int64_t)nb * p.sb_ld + k0;
-  float swn = VEC ? 1.0f : ld_uniform_f32(sbp);
-  const bool more = wave == 0 || (VEC && wave == 1);
+  for (int s = 0; s < S; ++s)
+    if (s < KT)
+#pragma unroll
+      for (int d = 0; d < NPER; ++d) issue1(std::true_type(), d, s, s);
+
   const int swz = (ln >> 1) & 7;
-  int slot = 0;
-  for (int kt = 0; kt < KT; ++kt) {
-    const int ahead = min(S - 2, KT - 1 - kt);
-    if (more) wait_stages<NPER + 1>(ahead);
-    else wait_stages<NPER>(ahead);
-    lds_barrier();
-    if (kt + S - 1 < KT) issue(kt + S - 1, slot == 0 ? S - 1 : slot - 1);
-    const float sw = swn;
-    if (!VEC && kt + 1 < KT) swn = ld_uniform_f32(sbp + kt + 1);
-    const uint8_t* st = smem + slot * C::STAGE;
-    const float* sas = reinterpret_cast<const float*>(st + OSA) + wm * MI * 16 + ln;
-    const float* sbs = reinterpret_cast<const float*>(st + OSB) + wn * NJ * 16 + lg * 4;
-    auto frag = [&](int off, int r0) {
-      const uint8_t* row = st + off + (r0 + ln) * 128;
-      const u32x4 lo = *reinterpret_cast<const u32x4*>(row + ((lg ^ swz) << 4));
-      const u32x4 hi = *reinterpret_cast<const u32x4*>(row + (((lg + 4) ^ swz) << 4));
-      return (i32x8){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-    };
-    i32x8 bf[NJ];
-    f32x4 sb4[NJ];
+  const int f0 = ln * 128 + ((lg ^ swz) << 4), f1 = ln * 128 + (((lg + 4) ^ swz) << 4);
+  auto frag = [&](const uint8_t* base) {
+    const u32x4 lo = *reinterpret_cast<const u32x4*>(base + f0);
+    const u32x4 hi = *reinterpret_cast<const u32x4*>(base + f1);
+    return (i32x8){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+  };
+  // operands of the current step: B's fragments, A's of two row blocks, scales
+  i32x8 bf[NJ], af[2];
+  float sa[2];
+  f32x4 sbv[NJ];   // VEC: of this lane's 4 columns
+  int ebv[NJ];     // VEC, P2: exponent for the row this lane gives
+  auto read_a = [&](const uint8_t* st, int i, int x) {
+    af[x] = frag(st + (wm * MI + i) * 2048);
+    sa[x] = reinterpret_cast<const float*>(st + OSA)[(wm * MI + i) * 16 + ln];
+  };
+  auto read_b = [&](const uint8_t* st, int j) {
+    bf[j] = frag(st + OB + (wn * NJ + j) * 2048);
+    if constexpr (VEC && P2)
+      ebv[j] = e8m0_of_pow2(reinterpret_cast<const float*>(st + OSB)[(wn * NJ + j) * 16 + ln]);
+  };
+  auto read_sb = [&](const uint8_t* st) {
+    if constexpr (VEC && !P2)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      bf[j] = frag(OB, (wn * NJ + j) * 16);
-      if (VEC) sb4[j] = *reinterpret_cast<const f32x4*>(sbs + j * 16);
-    }
+      for (int j = 0; j < NJ; ++j)
+        sbv[j] = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(st + OSB) + (wn * NJ + j) * 16 + lg * 4);
+  };
+  wait_stages<NPER>(min(S, KT) - 1);
+  lds_barrier();
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) read_b(smem, j);
+  read_sb(smem);
+  read_a(smem, 0, 0);
+  int slot = 0;
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 part[NJ];
+  auto fold = [&](int i, int j, float s) {  // adds row block i's products, scaled
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(part[j][q], VEC ? s * sbv[j][q] : s, acc[i][j][q]);
+  };
+  // A row block's MFMAs run while the one before is scaled and added and the next
+  // one's fragments are read.  The barrier that ends a stage stands before its
+  // last row block, whose MFMAs then cover the first reads of the next stage.
+  const float* swp = sws + (VEC ? 0 : (wn * NJ * 16) / 128 * LIN_MAX_KT);
+  // LOAD: 0 no stage left to request, 1 stage kt + S, 2 the same and it is the last
+  auto step = [&](auto next_, auto load_, int kt) {
+    constexpr bool next = decltype(next_)::value;
+    constexpr int load = decltype(load_)::value;
+    using Last = std::integral_constant<bool, load == 2>;
+    const uint8_t* st = smem + slot * C::STAGE;
+    const int nslot = slot + 1 == S ? 0 : slot + 1;
+    const uint8_t* nst = smem + nslot * C::STAGE;
+    const float sw = VEC ? 1.0f : swp[kt];
+    const int esw = e8m0_of_pow2(sw);
+    float fs = 0.0f;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const i32x8 af = frag(0, (wm * MI + i) * 16);
-      const float sa = sas[i * 16];
+      const bool last = i + 1 == MI;
+      __builtin_amdgcn_sched_barrier(0);
+      if (!last) {
+        read_a(st, i + 1, (i + 1) & 1);
+      } else if (next) {
+        // the last fragments of this stage are in registers, the next stage has
+        // landed; past the barrier this one's place is free
+        wait_vmcnt_clamped<load ? (S - 2) * NPER : 0>();
+        lds_barrier();
+      }
+      const float s = P2 ? 0.0f : VEC ? sa[i & 1] : sa[i & 1] * sw;
+      const int ea = P2 ? e8m0_of_pow2(sa[i & 1]) : 0;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-        const f32x4 part = mfma_fp8_16x16x128(bf[j], af, zero);
+        if constexpr (P2) {
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i & 1], acc[i][j], 0, 0, 0,
+                                                                        VEC ? ebv[j] : esw, 0, ea);
+        } else {
+          const f32x4 np = mfma_fp8_16x16x128(bf[j], af[i & 1], zero);
+          if (i > 0) fold(i - 1, j, fs);
+          part[j] = np;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (last && next) {
+          read_b(nst, j);
+          if (j + 1 == NJ) read_a(nst, 0, 0);
+        }
+        if (last && load) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(part[q], VEC ? sa * sb4[j][q] : sa * sw, acc[i][j][q]);
+          for (int d = j * NPER / NJ; d < (j + 1) * NPER / NJ; ++d) issue1(Last(), d, kt + S, slot);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
+      fs = s;
     }
-    slot = slot + 1 == S ? 0 : slot + 1;
-  }
+    if constexpr (!P2) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) fold(MI - 1, j, fs);
+    }
+    if (next) read_sb(nst);
+    slot = nslot;
+  };
+  int kt = 0;
+#pragma unroll 1
+  for (; kt < KT - S - 1; ++kt) step(std::true_type(), std::integral_constant<int, 1>(), kt);
+  if (kt < KT - S) step(std::true_type(), std::integral_constant<int, 2>(), kt++);
+#pragma unroll 1
+  for (; kt < KT - 1; ++kt) step(std::true_type(), std::integral_constant<int, 0>(), kt);
+  step(std::false_type(), std::integral_constant<int, 0>(), kt);
   if (p.splits > 1) {
     float* o = p.part + (int64_t)split * p.m * p.n;
 #pragma unroll
@@ -361,8 +445,9 @@ template <class C>
 void lin_launch(const LinGemm& g, bool vec, bool pow2, hipStream_t s) {
   const int64_t nt = (int64_t)((g.m + C::BM - 1) / C::BM) * ((g.n + C::BN - 1) / C::BN);
   const dim3 grid((unsigned)((nt + 7) / 8 * 8 * g.splits)), b(C::NT);
-  (void)pow2;
-  if (vec) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, true, false>), grid, b, 0, s, g);
+  if (vec && pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, true, true>), grid, b, 0, s, g);
+  else if (vec) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, true, false>), grid, b, 0, s, g);
+  else if (pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, false, true>), grid, b, 0, s, g);
   else hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, false, false>), grid, b, 0, s, g);
 }
 
