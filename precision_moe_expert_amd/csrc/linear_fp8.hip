@@ -164,7 +164,7 @@ struct LinTile {
   static constexpr int NW = WM * WN, NT = NW * 64;
   static constexpr int MI = BM / WM / 16, NJ = BN / WN / 16;
   static constexpr int NDA = BM / 8 / NW, NDB = BN / 8 / NW;  // DMAs per wave and stage, 8 rows each
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && NJ * 16 <= 128, "tile");
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && NJ * 16 <= 128 && (MI == 2 || MI % 4 == 0), "tile");
   // a stage's scales: 64 rows (256 bytes) by one wave's DMA
   static constexpr int UA = (BM + 63) / 64, UB = (BN + 63) / 64;
   static_assert(UA + UB <= NW, "a wave for each");
@@ -268,11 +268,15 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_lin(LinGemm p) {
     for (int i = threadIdx.x; i < NB * KT; i += C::NT)
       sws[i / KT * LIN_MAX_KT + i % KT] = p.sb[(int64_t)min(n0 / 128 + i / KT, (p.n - 1) / 128) * p.sb_ld + k0 + i % KT];
   }
+  // of the stage that is S - 1 ahead, the first DMAs are requested as soon as its
+  // place is free, the others with the row blocks that follow
+  constexpr int FIRST = MI == 2 ? NPER : 4, FPER = (FIRST + 1) / 2;              // in the last two row blocks
+  constexpr int ROWS = MI - 2 > 3 ? 3 : MI == 2 ? 1 : MI - 2, PER = (NPER - FIRST + ROWS - 1) / ROWS;
 #pragma unroll
   for (int s = 0; s < S; ++s)
     if (s < KT)
 #pragma unroll
-      for (int d = 0; d < NPER; ++d) issue1(std::true_type(), d, s, s);
+      for (int d = 0; d < (s + 1 < S ? NPER : FIRST); ++d) issue1(std::true_type(), d, s, s);
 
   const int swz = (ln >> 1) & 7;
   const int f0 = ln * 128 + ((lg ^ swz) << 4), f1 = ln * 128 + (((lg + 4) ^ swz) << 4);
@@ -281,9 +285,9 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_lin(LinGemm p) {
     const u32x4 hi = *reinterpret_cast<const u32x4*>(base + f1);
     return (i32x8){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
   };
-  // operands of the current step: B's fragments, A's of two row blocks, scales
-  i32x8 bf[NJ], af[2];
-  float sa[2];
+  // operands: B's fragments, A's of this row block and the next two, scales
+  i32x8 bf[NJ], af[4];
+  float sa[4];
   f32x4 sbv[NJ];   // VEC: of this lane's 4 columns
   int ebv[NJ];     // VEC, P2: exponent for the row this lane gives
   auto read_a = [&](const uint8_t* st, int i, int x) {
@@ -301,12 +305,14 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_lin(LinGemm p) {
       for (int j = 0; j < NJ; ++j)
         sbv[j] = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(st + OSB) + (wn * NJ + j) * 16 + lg * 4);
   };
-  wait_stages<NPER>(min(S, KT) - 1);
+  if (KT < S) wait_vmcnt<0>();
+  else wait_vmcnt_clamped<(S - 2) * NPER + FIRST>();
   lds_barrier();
 #pragma unroll
   for (int j = 0; j < NJ; ++j) read_b(smem, j);
   read_sb(smem);
   read_a(smem, 0, 0);
+  read_a(smem, 1, 1);
   int slot = 0;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   f32x4 part[NJ];
@@ -314,15 +320,18 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_lin(LinGemm p) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(part[j][q], VEC ? s * sbv[j][q] : s, acc[i][j][q]);
   };
-  // A row block's MFMAs run while the one before is scaled and added and the next
-  // one's fragments are read.  The barrier that ends a stage stands before its
-  // last row block, whose MFMAs then cover the first reads of the next stage.
+  // A row block's MFMAs run while the one before is scaled and added and the one
+  // after the next is read.  The barrier that ends a stage stands before its last
+  // two row blocks, whose MFMAs then cover the first reads of the next stage.
   const float* swp = sws + (VEC ? 0 : (wn * NJ * 16) / 128 * LIN_MAX_KT);
-  // LOAD: 0 no stage left to request, 1 stage kt + S, 2 the same and it is the last
-  auto step = [&](auto next_, auto load_, int kt) {
+  // REST: of stage kt + S - 1 to request: 0 it is not there, 1 its other DMAs, 2 the
+  // same and it is the last; LOAD: the same of the first DMAs of stage kt + S
+  auto step = [&](auto next_, auto rest_, auto load_, int kt) {
     constexpr bool next = decltype(next_)::value;
-    constexpr int load = decltype(load_)::value;
-    using Last = std::integral_constant<bool, load == 2>;
+    constexpr int rest = decltype(rest_)::value, load = decltype(load_)::value;
+    using RestLast = std::integral_constant<bool, rest == 2>;
+    using LoadLast = std::integral_constant<bool, load == 2>;
+    const int pslot = slot == 0 ? S - 1 : slot - 1;
     const uint8_t* st = smem + slot * C::STAGE;
     const int nslot = slot + 1 == S ? 0 : slot + 1;
     const uint8_t* nst = smem + nslot * C::STAGE;
@@ -331,37 +340,41 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_lin(LinGemm p) {
     float fs = 0.0f;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const bool last = i + 1 == MI;
+      const bool last = i + 1 == MI, free = i + 2 >= MI;  // free: this stage's fragments are all in registers
       __builtin_amdgcn_sched_barrier(0);
-      if (!last) {
-        read_a(st, i + 1, (i + 1) & 1);
+      if (!free) {
+        read_a(st, i + 2, (i + 2) & 3);
       } else if (next) {
-        // the last fragments of this stage are in registers, the next stage has
-        // landed; past the barrier this one's place is free
-        wait_vmcnt_clamped<load ? (S - 2) * NPER : 0>();
-        lds_barrier();
+        if (!last) {
+          // the next stage has landed; past the barrier this one's place is free
+          wait_vmcnt_clamped<rest ? (S - 2) * NPER : 0>();
+          lds_barrier();
+        }
+        if (MI > 2) read_a(nst, i + 2 - MI, i + 2 - MI);
       }
-      const float s = P2 ? 0.0f : VEC ? sa[i & 1] : sa[i & 1] * sw;
-      const int ea = P2 ? e8m0_of_pow2(sa[i & 1]) : 0;
+      const float s = P2 ? 0.0f : VEC ? sa[i & 3] : sa[i & 3] * sw;
+      const int ea = P2 ? e8m0_of_pow2(sa[i & 3]) : 0;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         if constexpr (P2) {
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i & 1], acc[i][j], 0, 0, 0,
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i & 3], acc[i][j], 0, 0, 0,
                                                                         VEC ? ebv[j] : esw, 0, ea);
         } else {
-          const f32x4 np = mfma_fp8_16x16x128(bf[j], af[i & 1], zero);
+          const f32x4 np = mfma_fp8_16x16x128(bf[j], af[i & 3], zero);
           if (i > 0) fold(i - 1, j, fs);
           part[j] = np;
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (last && next) {
-          read_b(nst, j);
-          if (j + 1 == NJ) read_a(nst, 0, 0);
-        }
-        if (last && load) {
+        if (last && next) read_b(nst, j);
+        if (MI == 2 && next && j + 1 == NJ) read_a(nst, i, i);
+        if (rest && i < ROWS)
 #pragma unroll
-          for (int d = j * NPER / NJ; d < (j + 1) * NPER / NJ; ++d) issue1(Last(), d, kt + S, slot);
-        }
+          for (int d = j * PER / NJ; d < (j + 1) * PER / NJ; ++d)
+            if (FIRST + i * PER + d < NPER) issue1(RestLast(), FIRST + i * PER + d, kt + S - 1, pslot);
+        if (free && load)
+#pragma unroll
+          for (int d = j * FPER / NJ; d < (j + 1) * FPER / NJ; ++d)
+            if ((last ? FPER : 0) + d < FIRST) issue1(LoadLast(), (last ? FPER : 0) + d, kt + S, slot);
         __builtin_amdgcn_sched_barrier(0);
       }
       fs = s;
@@ -373,13 +386,17 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_lin(LinGemm p) {
     if (next) read_sb(nst);
     slot = nslot;
   };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
   int kt = 0;
 #pragma unroll 1
-  for (; kt < KT - S - 1; ++kt) step(std::true_type(), std::integral_constant<int, 1>(), kt);
-  if (kt < KT - S) step(std::true_type(), std::integral_constant<int, 2>(), kt++);
+  for (; kt < KT - S - 1; ++kt) step(std::true_type(), I1(), I1(), kt);
+  if (kt < KT - S) step(std::true_type(), I1(), I2(), kt++);
+  if (kt < KT - S + 1) step(std::true_type(), I2(), I0(), kt++);
 #pragma unroll 1
-  for (; kt < KT - 1; ++kt) step(std::true_type(), std::integral_constant<int, 0>(), kt);
-  step(std::false_type(), std::integral_constant<int, 0>(), kt);
+  for (; kt < KT - 1; ++kt) step(std::true_type(), I0(), I0(), kt);
+  step(std::false_type(), I0(), I0(), kt);
   if (p.splits > 1) {
     float* o = p.part + (int64_t)split * p.m * p.n;
 #pragma unroll
