@@ -299,17 +299,19 @@ struct LinGemm {
   int64_t ldo;
   int splits;             // ways K is split (1: not)
   float* part;            // [splits][m][n]
+  int halved;             // last tiles that are done as two halves
 };
 struct LinPlan {
   size_t q, s, part, qa, qb, sqa, sqb, wpart, total;  // byte offsets into the workspace
-  int splits, wsplits;
 };
 LinPlan lin_plan(int M, int K, int N, bool backward, bool input_grad, bool weight_grad);
-// y [M][out_n] = Q(x) W^T over x [M][C], W [out_n][C]
-void launch_linear(const LinPlan& pl, const uint16_t* x, int64_t stride, int M, int C, int out_n, const uint8_t* w,
+// y [M][N] = Q(x) W^T
+void launch_linear(const LinPlan& pl, const uint16_t* x, int64_t stride, int M, int K, int N, const uint8_t* w,
                    const float* sw, bool pow2, uint16_t* y, char* ws, hipStream_t s);
-void launch_linear_dw(const LinPlan& pl, const uint16_t* dy, int64_t dy_stride, const uint16_t* x, int64_t x_stride,
-                      int M, int K, int N, bool pow2, uint16_t* dw, char* ws, hipStream_t s);
+// dx [M][K] and dw [N][K], either null: not formed
+void launch_linear_bwd(const LinPlan& pl, const uint16_t* dy, int64_t dy_stride, const uint8_t* wt, const float* swt,
+                       const uint16_t* x, int64_t x_stride, int M, int K, int N, bool pow2, uint16_t* dx, uint16_t* dw,
+                       char* ws, hipStream_t s);
 void launch_linear_transpose(const uint8_t* w, const float* sc, int N, int K, uint8_t* wt, float* st, hipStream_t s);
 void launch_linear_zero(void* p, int64_t bytes, hipStream_t s);
 

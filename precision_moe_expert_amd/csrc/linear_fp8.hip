@@ -38,6 +38,40 @@ MOE_DEV float lin_scale(float amax) {
 
 MOE_DEV float lin_bf16(uint32_t w, int odd) { return odd ? __uint_as_float(w & 0xFFFF0000u) : __uint_as_float(w << 16); }
 
+// A block's scale and what divides by it.
+//
+// The quotient x / s, rounded once to fp32, by one multiplication and one
+// correction, q = x r, q + r (x - q s), with r = 1 / s: the same bits as the
+// division for all 16384 pairs of bf16 mantissas of x and the block's largest
+// (checked one by one; without the correction 1 code in 2750 differs).  Exact
+// remainders need s above 2^-90; below, it is divided.  |x| <= amax, so no quotient
+// is past e4m3's largest.
+template <bool P2>
+struct LinBlock {
+  float s, r;
+  MOE_DEV explicit LinBlock(float amax) {
+    s = lin_scale<P2>(amax);
+    r = P2 ? pow2_reciprocal(s) : 1.0f / s;
+  }
+  MOE_DEV float div(float x) const {
+    if (P2) return x * r;
+    const float q = x * r;
+    return fmaf(fmaf(-q, s, x), r, q);
+  }
+  // four codes
+  MOE_DEV uint32_t codes(float a, float b, float c, float d) const {
+    float q[4] = {div(a), div(b), div(c), div(d)};
+    if (!P2 && s < 0x1p-90f) {
+      q[0] = a / s;
+      q[1] = b / s;
+      q[2] = c / s;
+      q[3] = d / s;
+    }
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
+  }
+};
+
 // ---- quantizers -------------------------------------------------------------
 
 // Q: rows of x [M][C] bf16 -> codes [M][Cp] (Cp: C up to whole blocks of 128,
@@ -65,56 +99,72 @@ __global__ __launch_bounds__(256) void k_lin_rows(const uint16_t* __restrict__ x
       f[j] = lin_bf16(v[i][j >> 1], j & 1);
       amax = fmaxf(amax, fabsf(f[j]));
     }
-    const float s = lin_scale<P2>(row16_max_nonneg(amax));
-    u32x2 o;
-    o.x = cvt_e4m3x4(f[0] / s, f[1] / s, f[2] / s, f[3] / s);
-    o.y = cvt_e4m3x4(f[4] / s, f[5] / s, f[6] / s, f[7] / s);
+    const LinBlock<P2> k(row16_max_nonneg(amax));
+    const u32x2 o = {k.codes(f[0], f[1], f[2], f[3]), k.codes(f[4], f[5], f[6], f[7])};
     *reinterpret_cast<u32x2*>(q + (int64_t)m * Cp + (b0 + i) * 128 + l * 8) = o;
-    if (l == 0) sc[(int64_t)(b0 + i) * ld + m] = s;
+    if (l == 0) sc[(int64_t)(b0 + i) * ld + m] = k.s;
   }
 }
 
 // Qt: x [M][C] -> codes [C][Mp] (zeros behind M) and scales [Mp/128][ld].  A
-// workgroup takes 128 tokens by 64 columns; a thread holds 4 tokens of 8.
-template <bool P2>
+// workgroup takes 128 tokens by 128 columns, a thread 8 tokens of 8.  ROWS: Q of
+// the same tile as well (rq [M][Cp], rs [Cp/128][rld]), for one read of both.
+template <bool P2, bool ROWS>
 __global__ __launch_bounds__(256) void k_lin_cols(const uint16_t* __restrict__ x, int64_t stride, int M, int C, int Mp,
-                                                  uint8_t* __restrict__ q, float* __restrict__ sc, int ld) {
+                                                  uint8_t* __restrict__ q, float* __restrict__ sc, int ld,
+                                                  uint8_t* __restrict__ rq, float* __restrict__ rs, int rld) {
   constexpr int LS = 132;  // bytes between a column's codes
-  __shared__ __align__(16) uint8_t codes[64 * LS];
-  __shared__ float red[4][64];
-  const int t0 = blockIdx.y * 128, c0 = blockIdx.x * 64;
-  const int cg = threadIdx.x & 7, rr = threadIdx.x >> 3, wave = threadIdx.x >> 6;
+  __shared__ __align__(16) uint8_t codes[128 * LS];
+  __shared__ float red[4][128];
+  const int t0 = blockIdx.y * 128, c0 = blockIdx.x * 128;
+  const int cg = threadIdx.x & 15, rr = threadIdx.x >> 4, wave = threadIdx.x >> 6;
   const bool in = c0 + cg * 8 < C;
-  u32x4 v[4];
+  u32x4 v[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + rr * 4 + i;
+  for (int i = 0; i < 8; ++i) {
+    const int t = t0 + rr * 8 + i;
     v[i] = (u32x4){0, 0, 0, 0};
     if (in && t < M) v[i] = *reinterpret_cast<const u32x4*>(x + t * stride + c0 + cg * 8);
   }
-  float amax[8];
+  auto at = [&](int i, int j) { return lin_bf16(v[i][j >> 1], j & 1); };
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    amax[j] = 0.0f;
+    float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) amax[j] = fmaxf(amax[j], fabsf(lin_bf16(v[i][j >> 1], j & 1)));
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(at(i, j)));
+    a = fmaxf(a, shfl_xor(a, 16));
+    a = fmaxf(a, shfl_xor(a, 32));
+    if ((threadIdx.x & 48) == 0) red[wave][cg * 8 + j] = a;
+  }
+  if constexpr (ROWS) {
+    const int64_t Cp = (C + 127) / 128 * 128;
 #pragma unroll
-    for (int o = 8; o < 64; o <<= 1) amax[j] = fmaxf(amax[j], shfl_xor(amax[j], o));
-    if ((threadIdx.x & 56) == 0) red[wave][cg * 8 + j] = amax[j];
+    for (int i = 0; i < 8; ++i) {
+      const int t = t0 + rr * 8 + i;
+      float a = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(at(i, j)));
+      const LinBlock<P2> k(row16_max_nonneg(a));
+      if (t < M) {
+        *reinterpret_cast<u32x2*>(rq + t * Cp + c0 + cg * 8) =
+            (u32x2){k.codes(at(i, 0), at(i, 1), at(i, 2), at(i, 3)), k.codes(at(i, 4), at(i, 5), at(i, 6), at(i, 7))};
+        if (cg == 0) rs[(int64_t)blockIdx.x * rld + t] = k.s;
+      }
+    }
   }
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int c = cg * 8 + j;
-    const float s = lin_scale<P2>(fmaxf(fmaxf(red[0][c], red[1][c]), fmaxf(red[2][c], red[3][c])));
-    *reinterpret_cast<uint32_t*>(codes + c * LS + rr * 4) =
-        cvt_e4m3x4(lin_bf16(v[0][j >> 1], j & 1) / s, lin_bf16(v[1][j >> 1], j & 1) / s,
-                   lin_bf16(v[2][j >> 1], j & 1) / s, lin_bf16(v[3][j >> 1], j & 1) / s);
-    if (rr == 0 && in) sc[(int64_t)blockIdx.y * ld + c0 + c] = s;
+    const LinBlock<P2> k(fmaxf(fmaxf(red[0][c], red[1][c]), fmaxf(red[2][c], red[3][c])));
+    uint32_t* o = reinterpret_cast<uint32_t*>(codes + c * LS + rr * 8);
+    o[0] = k.codes(at(0, j), at(1, j), at(2, j), at(3, j));
+    o[1] = k.codes(at(4, j), at(5, j), at(6, j), at(7, j));
+    if (rr == 0 && in) sc[(int64_t)blockIdx.y * ld + c0 + c] = k.s;
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {  // 4-byte pieces: 32 per column
+  for (int i = 0; i < 16; ++i) {  // 4-byte pieces: 32 per column
     const int p = threadIdx.x + i * 256, c = p >> 5, w = p & 31;
     if (c0 + c < C)
       *reinterpret_cast<uint32_t*>(q + (int64_t)(c0 + c) * Mp + t0 + w * 4) =
@@ -173,6 +223,8 @@ struct LinTile {
   static constexpr int LS = BN * 2 + 16;                      // epilogue's row stride
   static constexpr int SMEM = S * STAGE > BM * LS ? S * STAGE : BM * LS;
   static_assert(SMEM <= 160 * 1024, "LDS");
+  // what the tiles of a last round may be done with
+  using Half = std::conditional_t<BM == 256, LinTile<BM_ / 2, BN_, WM_, WN_, 3, WPS_>, LinTile>;
 };
 
 constexpr int LIN_GM = 4;  // tile rows of a band
@@ -180,34 +232,46 @@ constexpr int LIN_MAX_KT = 1024;
 
 // Workgroup -> tile: each XCD takes a contiguous range of tiles, ordered in
 // bands of LIN_GM tile rows, so that the tiles it works on at one time share few
-// row and column panels in its L2.
-MOE_DEV bool lin_tile(int bid, int nm, int nn, int& m, int& n) {
-  const int total = nm * nn, per = (total + 7) >> 3, at = bid >> 3, idx = (bid & 7) * per + at;
-  if (at >= per || idx >= total) return false;
+// row and column panels in its L2.  The last `halved` tiles are done as two
+// halves each (half = 0, 1; -1: a whole tile).
+MOE_DEV int lin_place(int bid, int total) {
+  const int per = (total + 7) >> 3, at = bid >> 3, idx = (bid & 7) * per + at;
+  return at >= per || idx >= total ? -1 : idx;
+}
+MOE_DEV bool lin_tile(int bid, int nm, int nn, int halved, int& m, int& n, int& half) {
+  const int whole = nm * nn - halved, grid = (whole + 7) & ~7;
+  int idx;
+  half = -1;
+  if (bid < grid) {
+    idx = lin_place(bid, whole);
+  } else {
+    idx = lin_place(bid - grid, halved * 2);
+    half = idx & 1;
+    if (idx >= 0) idx = whole + (idx >> 1);
+  }
+  if (idx < 0) return false;
   const int band = idx / (LIN_GM * nn), rem = idx - band * LIN_GM * nn;
   const int gm = min(LIN_GM, nm - band * LIN_GM);
   n = rem / gm;
   m = band * LIN_GM + rem - n * gm;
   return true;
 }
+__host__ MOE_DEV int lin_grid(int tiles, int halved) {
+  return ((tiles - halved + 7) & ~7) + ((halved * 2 + 7) & ~7);
+}
 
-}  // namespace
+template <class C>
+constexpr int lin_sws() { return (C::BN + 127) / 128 * LIN_MAX_KT; }
 
+// A tile: rows from m0, columns from n0, over the K blocks of a split.
+//
 // VEC: B's scales are per row (d_w), else per 128 rows.  The accumulators are
 // formed transposed (B's fragment first): a lane holds 4 consecutive columns of
 // one row, so one scale serves a whole fragment.
 template <class C, bool VEC, bool P2>
-__global__ __launch_bounds__(C::NT, C::WPS) void k_lin(LinGemm p) {
+MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, float* sws) {
   constexpr int MI = C::MI, NJ = C::NJ, S = C::S, NPER = C::NPER;
-  __shared__ __align__(16) uint8_t smem[C::SMEM];
   constexpr int NB = (C::BN + 127) / 128;
-  __shared__ float sws[VEC ? 1 : NB * LIN_MAX_KT];
-  const int nm = (p.m + C::BM - 1) / C::BM, nn = (p.n + C::BN - 1) / C::BN;
-  const int ntile = nm * nn, grid1 = (ntile + 7) / 8 * 8;
-  const int split = blockIdx.x / grid1;
-  int tm, tn;
-  if (!lin_tile(blockIdx.x - split * grid1, nm, nn, tm, tn)) return;
-  const int m0 = tm * C::BM, n0 = tn * C::BN;
   const int k0 = (int)((int64_t)p.kt * split / p.splits), k1 = (int)((int64_t)p.kt * (split + 1) / p.splits);
   const int KT = k1 - k0;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -341,6 +405,12 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_lin(LinGemm p) {
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       const bool last = i + 1 == MI, free = i + 2 >= MI;  // free: this stage's fragments are all in registers
+      // of a SIMD's two waves the one that is behind goes first: else the older
+      // one runs ahead, and the other does its half alone
+      if (MI > 2 && i == 0) __builtin_amdgcn_s_setprio(3);
+      if (MI > 2 && i == MI / 4) __builtin_amdgcn_s_setprio(2);
+      if (MI > 2 && i == MI / 2) __builtin_amdgcn_s_setprio(1);
+      if (MI > 2 && i == MI / 4 * 3) __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
       if (!free) {
         read_a(st, i + 2, (i + 2) & 3);
@@ -429,6 +499,126 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_lin(LinGemm p) {
   }
 }
 
+template <class C, bool VEC, bool P2>
+MOE_DEV void lin_work(const LinGemm& p, int bid, uint8_t* smem, float* sws) {
+  const int nm = (p.m + C::BM - 1) / C::BM, nn = (p.n + C::BN - 1) / C::BN;
+  const int grid = lin_grid(nm * nn, p.halved), split = bid / grid;
+  int tm, tn, half;
+  if (!lin_tile(bid - split * grid, nm, nn, p.halved, tm, tn, half)) return;
+  if (half < 0) {
+    lin_mm<C, VEC, P2>(p, tm * C::BM, tn * C::BN, split, smem, sws);
+  } else {
+    const int m0 = tm * C::BM + half * C::Half::BM;
+    if (m0 < p.m) lin_mm<typename C::Half, VEC, P2>(p, m0, tn * C::BN, split, smem, sws);
+  }
+}
+
+template <class C>
+struct LinLds {
+  static constexpr int BYTES = C::SMEM > C::Half::SMEM ? C::SMEM : C::Half::SMEM;
+};
+
+}  // namespace
+
+template <class C, bool VEC, bool P2>
+__global__ __launch_bounds__(C::NT, C::WPS) void k_lin(LinGemm p) {
+  __shared__ __align__(16) uint8_t smem[LinLds<C>::BYTES];
+  __shared__ float sws[VEC ? 1 : lin_sws<C>()];
+  lin_work<C, VEC, P2>(p, blockIdx.x, smem, sws);
+}
+
+// Both gradients in one launch (`first` workgroups for the product a): alone
+// each would leave a part of its last round's CUs idle.
+template <class C, bool VECA, bool P2>
+__global__ __launch_bounds__(C::NT, C::WPS) void k_lin_both(LinGemm a, LinGemm b, int first) {
+  __shared__ __align__(16) uint8_t smem[LinLds<C>::BYTES];
+  __shared__ float sws[lin_sws<C>()];
+  if ((int)blockIdx.x < first) lin_work<C, VECA, P2>(a, blockIdx.x, smem, sws);
+  else lin_work<C, !VECA, P2>(b, blockIdx.x - first, smem, sws);
+}
+
+// ---- few rows ---------------------------------------------------------------
+
+// Up to LIN_FEW rows: a workgroup takes 16 columns, its NW waves the K blocks in
+// turn; W's fragments come from memory in the layout that the MFMA wants (16 rows
+// of 64 + 64 bytes), U blocks requested before the first is used, while the rows
+// are quantized by each workgroup into LDS: one launch in place of three.  Bound
+// by the stream of W.
+constexpr int LIN_FEW = 4, LIN_FEW_U = 4, LIN_FEW_BYTES = 48 * 1024;
+template <int NW, bool P2>
+__global__ __launch_bounds__(NW * 64) void k_lin_few(LinGemm p, const uint16_t* __restrict__ x, int64_t x_stride) {
+  constexpr int U = LIN_FEW_U;
+  extern __shared__ __align__(16) uint8_t few_codes[];      // [m][lda], then the scales [m][kt]
+  __shared__ f32x4 sums[NW][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int ln = lane & 15, lg = lane >> 4;
+  const int n0 = blockIdx.x * 16, KT = p.kt;
+  const uint8_t* wrow = p.b + (int64_t)(n0 + ln) * p.ldb;   // n is a multiple of 16
+  const float* ws = p.sb + (int64_t)(n0 / 128) * p.sb_ld;
+  u32x4 w[U][2];
+  float sw[U];
+  auto load_w = [&](int u, int kb) {
+    if (kb >= KT) return;                                   // the whole wave
+    const int at = kb * 128, left = p.kbytes - at;          // past the end: the block's first bytes (A has zeros)
+    w[u][0] = *reinterpret_cast<const u32x4*>(wrow + at + (lg * 16 < left ? lg * 16 : 0));
+    w[u][1] = *reinterpret_cast<const u32x4*>(wrow + at + (64 + lg * 16 < left ? 64 + lg * 16 : 0));
+    sw[u] = ws[kb];
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) load_w(u, wave + u * NW);
+  float* fs = reinterpret_cast<float*>(few_codes + p.m * p.lda);
+  {
+    const int l = threadIdx.x & 15;
+    for (int g = threadIdx.x >> 4; g < p.m * KT; g += NW * 4) {
+      const int m = g / KT, kb = g - m * KT, c = kb * 128 + l * 8;
+      u32x4 v = {0, 0, 0, 0};
+      if (c < p.kbytes) v = *reinterpret_cast<const u32x4*>(x + m * x_stride + c);
+      float f[8], amax = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[j] = lin_bf16(v[j >> 1], j & 1);
+        amax = fmaxf(amax, fabsf(f[j]));
+      }
+      const LinBlock<P2> k(row16_max_nonneg(amax));
+      const u32x2 o = {k.codes(f[0], f[1], f[2], f[3]), k.codes(f[4], f[5], f[6], f[7])};
+      *reinterpret_cast<u32x2*>(few_codes + m * p.lda + c) = o;
+      if (l == 0) fs[m * KT + kb] = k.s;
+    }
+    lds_barrier();
+  }
+  const int m = min(ln, p.m - 1);                           // rows past the last are not stored
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k0 = wave; k0 < KT; k0 += NW * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = k0 + u * NW;
+      if (kb < KT) {
+        const u32x4 lo = w[u][0], hi = w[u][1];
+        const float s = sw[u] * fs[m * KT + kb];
+        load_w(u, kb + NW * U);
+        const i32x8 bf = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+        const uint8_t* row = few_codes + m * p.lda + kb * 128 + lg * 16;
+        const u32x4 alo = *reinterpret_cast<const u32x4*>(row), ahi = *reinterpret_cast<const u32x4*>(row + 64);
+        const i32x8 af = {(int)alo.x, (int)alo.y, (int)alo.z, (int)alo.w,
+                          (int)ahi.x, (int)ahi.y, (int)ahi.z, (int)ahi.w};
+        const f32x4 part = mfma_fp8_16x16x128(bf, af, (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[q] = fmaf(part[q], s, acc[q]);
+      }
+    }
+  }
+  sums[wave][lane] = acc;
+  __syncthreads();
+  // the waves' sums in their order: lane (row, 4 columns)
+  if (wave == 0 && ln < p.m) {
+    f32x4 s = sums[0][lane];
+#pragma unroll
+    for (int v = 1; v < NW; ++v) s += sums[v][lane];
+    const u32x2 o = {bf16x2_bits(s[0], s[1]), bf16x2_bits(s[2], s[3])};
+    *reinterpret_cast<u32x2*>(p.out + (int64_t)ln * p.ldo + n0 + lg * 4) = o;
+  }
+}
+
 // Sum of the splits' parts, in their order, rounded to bf16.
 __global__ __launch_bounds__(256) void k_lin_join(const float* __restrict__ part, int splits, int64_t mn, int n,
                                                   int64_t ldo, uint16_t* __restrict__ out) {
@@ -452,48 +642,115 @@ __global__ __launch_bounds__(256) void k_lin_zero(uint32_t* __restrict__ p, int6
 
 namespace {
 
-using LinLarge = LinTile<256, 256, 2, 4, 2, 2>;
-using LinMid = LinTile<128, 128, 2, 2, 2, 2>;
-using LinThin = LinTile<32, 128, 1, 4, 4, 2>;
+// Tiles of a product, and what they cost (cycles of a CU, measured at 8192 x
+// 7168 x 4096 and smaller calls): a K block of one tile, the rest of a tile; `per`
+// workgroups share a CU.
+using LinT0 = LinTile<256, 256, 2, 4, 2, 2>;
+using LinT1 = LinTile<128, 256, 2, 4, 3, 2>;
+using LinT2 = LinTile<128, 128, 2, 2, 2, 2>;
+using LinT3 = LinTile<64, 128, 1, 4, 3, 2>;
+using LinT4 = LinTile<32, 128, 1, 4, 3, 2>;
+struct LinShape {
+  int bm, bn, per;
+  float step, rest;
+};
+constexpr LinShape kLinShapes[] = {
+    {256, 256, 1, 2500, 9000}, {128, 256, 1, 1400, 6000}, {128, 128, 2, 1700, 5000}, {64, 128, 2, 1000, 4000},
+    {32, 128, 2, 900, 4000}};
+constexpr int kLinShapeCount = 5;
+constexpr int kLinCus = 256;
 
 inline size_t lin_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+inline int lin_tiles(int64_t m, int64_t n, const LinShape& s) {
+  return (int)((m + s.bm - 1) / s.bm * ((n + s.bn - 1) / s.bn));
+}
+
+struct LinChoice {
+  int shape, splits, halved;
+};
+
+// The tile and the ways K is split for a product: the least of what the rounds
+// of workgroups cost, and of writing and joining the parts (fp32) where K is
+// split.  A last round of 256 x 256 tiles that would leave half of the CUs idle is
+// done in halves.
+LinChoice lin_choose(int64_t m, int64_t n, int kt) {
+  LinChoice best{0, 1, 0};
+  float least = 0.0f;
+  for (int i = 0; i < kLinShapeCount; ++i) {
+    const LinShape& s = kLinShapes[i];
+    const int tiles = lin_tiles(m, n, s), slots = kLinCus * s.per;
+    for (int sp = 1; sp <= 16 && (sp == 1 || kt / sp >= 2); ++sp) {
+      if (sp > 1 && (int64_t)sp * m * n * 4 > (64 << 20)) break;
+      const int64_t wgs = (int64_t)tiles * sp, full = wgs / slots;
+      const int rem = (int)(wgs - full * slots);
+      const float one = (float)((kt + sp - 1) / sp) * s.step + s.rest;
+      const bool half = i == 0 && sp == 1 && rem > 0 && rem * 2 <= slots;
+      // a round that leaves CUs to one workgroup instead of two costs less
+      const float last = rem == 0 ? 0.0f : half ? 0.6f * one : s.per == 2 && rem * 2 <= slots ? 0.7f * one : one;
+      float cost = (float)full * one + last;
+      if (sp > 1) cost += 6000.0f + (float)((double)sp * m * n * 8 / 2000.0);  // about 4 TB/s at 2 GHz
+      if (i == 0 && sp == 1 ? true : cost < least) {
+        least = cost;
+        best = LinChoice{i, sp, half ? rem : 0};
+      }
+    }
+  }
+  return best;
+}
 
 template <class C>
 void lin_launch(const LinGemm& g, bool vec, bool pow2, hipStream_t s) {
-  const int64_t nt = (int64_t)((g.m + C::BM - 1) / C::BM) * ((g.n + C::BN - 1) / C::BN);
-  const dim3 grid((unsigned)((nt + 7) / 8 * 8 * g.splits)), b(C::NT);
+  const int nt = ((g.m + C::BM - 1) / C::BM) * ((g.n + C::BN - 1) / C::BN);
+  const dim3 grid(lin_grid(nt, g.halved) * g.splits), b(C::NT);
   if (vec && pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, true, true>), grid, b, 0, s, g);
   else if (vec) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, true, false>), grid, b, 0, s, g);
   else if (pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, false, true>), grid, b, 0, s, g);
   else hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, false, false>), grid, b, 0, s, g);
 }
 
-// Tile of a product: 0 large, 1 mid, 2 thin.
-int lin_tile_of(int64_t m, int64_t n) {
-  if (m <= 64) return 2;
-  return (m + 255) / 256 * ((n + 255) / 256) >= 200 ? 0 : 1;
-}
-
-int lin_splits_of(int64_t m, int64_t n, int kt) {
-  static const int bm[] = {256, 128, 32}, bn[] = {256, 128, 128};
-  const int t = lin_tile_of(m, n);
-  if (t == 0) return 1;
-  const int64_t tiles = (m + bm[t] - 1) / bm[t] * ((n + bn[t] - 1) / bn[t]);
-  int64_t sp = 512 / tiles;
-  if (sp > kt / 4) sp = kt / 4;
-  return sp < 1 ? 1 : sp > 16 ? 16 : (int)sp;
-}
-
-void lin_product(LinGemm g, bool vec, bool pow2, hipStream_t s) {
-  const int t = lin_tile_of(g.m, g.n);
-  if (t == 0) lin_launch<LinLarge>(g, vec, pow2, s);
-  else if (t == 1) lin_launch<LinMid>(g, vec, pow2, s);
-  else lin_launch<LinThin>(g, vec, pow2, s);
+void lin_product(LinGemm g, const LinChoice& c, bool vec, bool pow2, hipStream_t s) {
+  g.splits = c.splits;
+  g.halved = c.halved;
+  switch (c.shape) {
+    case 0: lin_launch<LinT0>(g, vec, pow2, s); break;
+    case 1: lin_launch<LinT1>(g, vec, pow2, s); break;
+    case 2: lin_launch<LinT2>(g, vec, pow2, s); break;
+    case 3: lin_launch<LinT3>(g, vec, pow2, s); break;
+    default: lin_launch<LinT4>(g, vec, pow2, s); break;
+  }
   if (g.splits > 1) {
     const int64_t mn = (int64_t)g.m * g.n;
     hipLaunchKernelGGL(k_lin_join, dim3((unsigned)((mn / 4 + 255) / 256)), dim3(256), 0, s, g.part, g.splits, mn, g.n,
                        g.ldo, g.out);
   }
+}
+
+inline bool lin_is_few(int64_t m, int kt) { return m <= LIN_FEW && m * kt * 132 <= LIN_FEW_BYTES; }
+
+template <int NW>
+void lin_few(const LinGemm& g, const uint16_t* x, int64_t x_stride, bool pow2, hipStream_t s) {
+  const dim3 grid(g.n / 16), b(NW * 64);
+  const size_t lds = (size_t)g.m * g.kt * 132;
+  if (pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin_few<NW, true>), grid, b, lds, s, g, x, x_stride);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin_few<NW, false>), grid, b, lds, s, g, x, x_stride);
+}
+
+// Both products in one launch, the one with more K blocks first.
+void lin_products(LinGemm dx, LinGemm dw, bool pow2, hipStream_t s) {
+  using C = LinT0;
+  const bool dw_first = dw.kt > dx.kt;
+  const LinGemm &a = dw_first ? dw : dx, &b0 = dw_first ? dx : dw;
+  LinGemm b = b0;
+  const int na = lin_tiles(a.m, a.n, kLinShapes[0]), nb = lin_tiles(b.m, b.n, kLinShapes[0]);
+  // the last round of the shorter tiles, in halves if it would leave half of the CUs idle
+  const int rem = (int)(((int64_t)na * a.kt / b.kt + nb) % kLinCus);
+  b.halved = rem * 2 <= kLinCus && rem <= nb ? rem : 0;
+  const int first = lin_grid(na, 0);
+  const dim3 grid(first + lin_grid(nb, b.halved)), t(C::NT);
+  if (dw_first && pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin_both<C, true, true>), grid, t, 0, s, a, b, first);
+  else if (dw_first) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin_both<C, true, false>), grid, t, 0, s, a, b, first);
+  else if (pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin_both<C, false, true>), grid, t, 0, s, a, b, first);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin_both<C, false, false>), grid, t, 0, s, a, b, first);
 }
 
 void lin_rows(const uint16_t* x, int64_t stride, int M, int C, bool pow2, uint8_t* q, float* sc, int ld, hipStream_t s) {
@@ -503,11 +760,17 @@ void lin_rows(const uint16_t* x, int64_t stride, int M, int C, bool pow2, uint8_
   else hipLaunchKernelGGL(k_lin_rows<false>, g, dim3(256), 0, s, x, stride, M, C, Cp, q, sc, ld);
 }
 
-void lin_cols(const uint16_t* x, int64_t stride, int M, int C, bool pow2, uint8_t* q, float* sc, int ld, hipStream_t s) {
+// rq null: Qt alone
+void lin_cols(const uint16_t* x, int64_t stride, int M, int C, bool pow2, uint8_t* q, float* sc, int ld, uint8_t* rq,
+              float* rs, int rld, hipStream_t s) {
   const int Mp = (int)lin_up(M, 128);
-  const dim3 g((C + 63) / 64, Mp / 128);
-  if (pow2) hipLaunchKernelGGL(k_lin_cols<true>, g, dim3(256), 0, s, x, stride, M, C, Mp, q, sc, ld);
-  else hipLaunchKernelGGL(k_lin_cols<false>, g, dim3(256), 0, s, x, stride, M, C, Mp, q, sc, ld);
+  const dim3 g((C + 127) / 128, Mp / 128), b(256);
+#define COLS(P, R) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin_cols<P, R>), g, b, 0, s, x, stride, M, C, Mp, q, sc, ld, rq, rs, rld)
+  if (pow2 && rq) COLS(true, true);
+  else if (pow2) COLS(true, false);
+  else if (rq) COLS(false, true);
+  else COLS(false, false);
+#undef COLS
 }
 
 // Scales of r rows, with room for the last tile's whole DMA behind them.
@@ -515,8 +778,8 @@ inline int lin_scale_ld(int r) { return (int)lin_up((size_t)r, 256) + 256; }
 
 }  // namespace
 
-// Workspace of a product over rows r: codes [r][c up to 128] and their scales,
-// parts of the sums where K is split.
+// Workspace: codes and scales of the quantized operands, parts of the sums where
+// K is split.
 LinPlan lin_plan(int M, int K, int N, bool backward, bool input_grad, bool weight_grad) {
   LinPlan p{};
   if (M == 0) return p;  // nothing to multiply
@@ -531,8 +794,8 @@ LinPlan lin_plan(int M, int K, int N, bool backward, bool input_grad, bool weigh
     const int kt = (C + 127) / 128;
     p.q = take((size_t)M * kt * 128);
     p.s = take((size_t)kt * lin_scale_ld(M) * 4);
-    p.splits = lin_splits_of(M, out, kt);
-    p.part = take(p.splits > 1 ? (size_t)p.splits * M * out * 4 : 0);
+    const int sp = lin_is_few(M, kt) ? 1 : lin_choose(M, out, kt).splits;
+    p.part = take(sp > 1 ? (size_t)sp * M * out * 4 : 0);
   }
   if (weight_grad) {
     const int kt = (M + 127) / 128;
@@ -540,63 +803,100 @@ LinPlan lin_plan(int M, int K, int N, bool backward, bool input_grad, bool weigh
     p.qb = take((size_t)K * kt * 128);
     p.sqa = take((size_t)kt * lin_scale_ld(N) * 4);
     p.sqb = take((size_t)kt * lin_scale_ld(K) * 4);
-    p.wsplits = lin_splits_of(N, K, kt);
-    p.wpart = take(p.wsplits > 1 ? (size_t)p.wsplits * N * K * 4 : 0);
+    const int sp = lin_choose(N, K, kt).splits;
+    p.wpart = take(sp > 1 ? (size_t)sp * N * K * 4 : 0);
   }
   p.total = o;
   return p;
 }
 
-void launch_linear(const LinPlan& pl, const uint16_t* x, int64_t stride, int M, int C, int out_n, const uint8_t* w,
-                   const float* sw, bool pow2, uint16_t* y, char* ws, hipStream_t s) {
-  uint8_t* q = reinterpret_cast<uint8_t*>(ws + pl.q);
-  float* sc = reinterpret_cast<float*>(ws + pl.s);
-  lin_rows(x, stride, M, C, pow2, q, sc, lin_scale_ld(M), s);
+namespace {
+
+// y [M][n] = Q(x) W^T for x [M][C] quantized into the workspace
+LinGemm lin_rows_product(const LinPlan& pl, int M, int C, int n, const uint8_t* w, const float* sw, uint16_t* y,
+                         char* ws) {
   LinGemm g{};
-  g.a = q;
+  g.a = reinterpret_cast<uint8_t*>(ws + pl.q);
   g.lda = (int64_t)lin_up(C, 128);
   g.m = M;
   g.b = w;
   g.ldb = C;
-  g.n = out_n;
+  g.n = n;
   g.kbytes = C;
   g.kt = (C + 127) / 128;
-  g.sa = sc;
+  g.sa = reinterpret_cast<float*>(ws + pl.s);
   g.sa_ld = lin_scale_ld(M);
   g.sb = sw;
   g.sb_ld = g.kt;
   g.out = y;
-  g.ldo = out_n;
-  g.splits = pl.splits;
+  g.ldo = n;
+  g.splits = 1;
   g.part = reinterpret_cast<float*>(ws + pl.part);
-  lin_product(g, false, pow2, s);
+  return g;
 }
 
-void launch_linear_dw(const LinPlan& pl, const uint16_t* dy, int64_t dy_stride, const uint16_t* x, int64_t x_stride,
-                      int M, int K, int N, bool pow2, uint16_t* dw, char* ws, hipStream_t s) {
-  uint8_t* qa = reinterpret_cast<uint8_t*>(ws + pl.qa);
-  uint8_t* qb = reinterpret_cast<uint8_t*>(ws + pl.qb);
-  float* sqa = reinterpret_cast<float*>(ws + pl.sqa);
-  float* sqb = reinterpret_cast<float*>(ws + pl.sqb);
-  lin_cols(dy, dy_stride, M, N, pow2, qa, sqa, lin_scale_ld(N), s);
-  lin_cols(x, x_stride, M, K, pow2, qb, sqb, lin_scale_ld(K), s);
+LinGemm lin_cols_product(const LinPlan& pl, int M, int K, int N, uint16_t* dw, char* ws) {
   LinGemm g{};
   g.lda = g.ldb = (int64_t)lin_up(M, 128);
-  g.a = qa;
+  g.a = reinterpret_cast<uint8_t*>(ws + pl.qa);
   g.m = N;
-  g.b = qb;
+  g.b = reinterpret_cast<uint8_t*>(ws + pl.qb);
   g.n = K;
   g.kbytes = (int)g.lda;
   g.kt = (int)(g.lda / 128);
-  g.sa = sqa;
+  g.sa = reinterpret_cast<float*>(ws + pl.sqa);
   g.sa_ld = lin_scale_ld(N);
-  g.sb = sqb;
+  g.sb = reinterpret_cast<float*>(ws + pl.sqb);
   g.sb_ld = lin_scale_ld(K);
   g.out = dw;
   g.ldo = K;
-  g.splits = pl.wsplits;
+  g.splits = 1;
   g.part = reinterpret_cast<float*>(ws + pl.wpart);
-  lin_product(g, true, pow2, s);
+  return g;
+}
+
+// Quantizes the rows of x [m][kbytes] into the product's A and forms it.
+void lin_forward(const LinGemm& g, const uint16_t* x, int64_t stride, bool pow2, hipStream_t s) {
+  if (lin_is_few(g.m, g.kt)) {
+    if (g.kt > 32) lin_few<16>(g, x, stride, pow2, s);
+    else lin_few<8>(g, x, stride, pow2, s);
+    return;
+  }
+  lin_rows(x, stride, g.m, g.kbytes, pow2, const_cast<uint8_t*>(g.a), const_cast<float*>(g.sa), g.sa_ld, s);
+  lin_product(g, lin_choose(g.m, g.n, g.kt), false, pow2, s);
+}
+
+}  // namespace
+
+void launch_linear(const LinPlan& pl, const uint16_t* x, int64_t stride, int M, int K, int N, const uint8_t* w,
+                   const float* sw, bool pow2, uint16_t* y, char* ws, hipStream_t s) {
+  lin_forward(lin_rows_product(pl, M, K, N, w, sw, y, ws), x, stride, pow2, s);
+}
+
+void launch_linear_bwd(const LinPlan& pl, const uint16_t* dy, int64_t dy_stride, const uint8_t* wt, const float* swt,
+                       const uint16_t* x, int64_t x_stride, int M, int K, int N, bool pow2, uint16_t* dx, uint16_t* dw,
+                       char* ws, hipStream_t s) {
+  const LinGemm gx = lin_rows_product(pl, M, N, K, wt, swt, dx, ws), gw = lin_cols_product(pl, M, K, N, dw, ws);
+  const bool both = dx && dw && !lin_is_few(M, gx.kt);  // one read of dy for both of its forms
+  if (dw) {
+    lin_cols(dy, dy_stride, M, N, pow2, const_cast<uint8_t*>(gw.a), const_cast<float*>(gw.sa), gw.sa_ld,
+             both ? const_cast<uint8_t*>(gx.a) : nullptr, const_cast<float*>(gx.sa), gx.sa_ld, s);
+    lin_cols(x, x_stride, M, K, pow2, const_cast<uint8_t*>(gw.b), const_cast<float*>(gw.sb), gw.sb_ld, nullptr, nullptr,
+             0, s);
+  }
+  const LinChoice cw = lin_choose(N, K, gw.kt);
+  if (both) {
+    const LinChoice cx = lin_choose(M, K, gx.kt);
+    if (cx.shape == 0 && cx.splits == 1 && cw.shape == 0 && cw.splits == 1) {
+      lin_products(gx, gw, pow2, s);
+    } else {
+      lin_product(gx, cx, false, pow2, s);
+      lin_product(gw, cw, true, pow2, s);
+    }
+    return;
+  }
+  if (dx) lin_forward(gx, dy, dy_stride, pow2, s);
+  if (dw) lin_product(gw, cw, true, pow2, s);
 }
 
 void launch_linear_transpose(const uint8_t* w, const float* sc, int N, int K, uint8_t* wt, float* st, hipStream_t s) {

@@ -1506,12 +1506,9 @@ moe_status moe_fp8_linear_backward(const moe_linear* lin, const void* d_y_bf16, 
   const bool pow2 = lin->wformat == MOE_W_FP8_E4M3_B128_POW2;
   const uint16_t* dy = static_cast<const uint16_t*>(d_y_bf16);
   const int64_t dys = lin->dy_stride ? lin->dy_stride : N, xs = lin->x_stride ? lin->x_stride : K;
-  if (d_x_bf16 != nullptr)
-    launch_linear(p, dy, dys, M, N, K, static_cast<const uint8_t*>(w_t), w_t_scale, pow2,
-                  static_cast<uint16_t*>(d_x_bf16), static_cast<char*>(ws), s);
-  if (d_w_bf16 != nullptr)
-    launch_linear_dw(p, dy, dys, static_cast<const uint16_t*>(x_bf16), xs, M, K, N, pow2,
-                     static_cast<uint16_t*>(d_w_bf16), static_cast<char*>(ws), s);
+  launch_linear_bwd(p, dy, dys, static_cast<const uint8_t*>(w_t), w_t_scale, static_cast<const uint16_t*>(x_bf16), xs,
+                    M, K, N, pow2, static_cast<uint16_t*>(d_x_bf16), static_cast<uint16_t*>(d_w_bf16),
+                    static_cast<char*>(ws), s);
   return launch_status();
 }
 
