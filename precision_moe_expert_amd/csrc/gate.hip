@@ -59,26 +59,19 @@ MOE_DEV uint64_t gate_key(double c, bool out, int e) {
 
 }  // namespace
 
-// LPT lanes per token (16: four tokens per wave; 64: one), lane r of them with
-// the experts r, r + LPT, ...: SLOTS, E <= LPT SLOTS.  Scores are formed in 64
-// bits, since two neighbours' order decides which expert runs.  LDS per token:
-// the scores, the group values.
-template <int LPT, int SLOTS>
-__global__ __launch_bounds__(64) void k_gate(GateArgs p) {
-  extern __shared__ __align__(16) double gate_lds[];
-  constexpr int TPW = 64 / LPT;
-  const int lane = threadIdx.x, r = lane % LPT, E = p.E;
-  const int t = blockIdx.x * TPW + lane / LPT;
-  const bool live = t < p.T;
-  const float* row = p.logits + (int64_t)(live ? t : 0) * E;
-  double* sc = gate_lds + (lane / LPT) * (E + GATE_MAX_GROUPS);
+// One token by the whole wave, lane r with the experts r, r + 64, ...: SLOTS, E <=
+// 64 SLOTS.  Scores are formed in 64 bits, since two neighbours' order decides
+// which expert runs.  lds: E + GATE_MAX_GROUPS numbers.
+template <int SLOTS>
+MOE_DEV void gate_token(const GateArgs& p, int t, double* sc) {
+  const int r = threadIdx.x & 63, E = p.E;
+  const float* row = p.logits + (int64_t)t * E;
   double* gv = sc + E;
-
   float l[SLOTS], b[SLOTS];
   bool out[SLOTS];
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i) {
-    const int e = r + LPT * i;
+    const int e = r + 64 * i;
     l[i] = e < E ? row[e] : -INFINITY;
     b[i] = e < E && p.bias ? p.bias[e] : 0.0f;
     out[i] = gate_out(l[i]) || gate_out(b[i]);
@@ -91,21 +84,21 @@ __global__ __launch_bounds__(64) void k_gate(GateArgs p) {
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) m = out[i] ? m : fmaxf(m, l[i]);
-    m = gate_max<LPT>(m);
+    m = gate_max<64>(m);
     double z = 0.0;
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
       s[i] = out[i] ? 0.0 : l[i] == m ? 1.0 : exp((double)l[i] - (double)m);
       z += s[i];
     }
-    z = gate_sum<LPT>(z);
+    z = gate_sum<64>(z);
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) s[i] = z > 0.0 ? s[i] / z : 0.0;
   }
   uint64_t key[SLOTS];
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i) {
-    const int e = r + LPT * i;
+    const int e = r + 64 * i;
     const double c = s[i] + (double)b[i];
     key[i] = e < E ? gate_key(c, out[i], e) : 0ull;
     if (p.groups > 1 && e < E) sc[e] = out[i] ? -INFINITY : c;
@@ -113,52 +106,297 @@ __global__ __launch_bounds__(64) void k_gate(GateArgs p) {
   if (p.groups > 1) {
     gate_sync();
     const int per = E / p.groups;
-    for (int g = r; g < p.groups; g += LPT) {
+    double v = -INFINITY;
+    if (r < p.groups) {
       double a = -INFINITY, a2 = -INFINITY;
+#pragma unroll 4
       for (int i = 0; i < per; ++i) {
-        const double v = sc[g * per + i];
-        a2 = fmax(a2, fmin(a, v));
-        a = fmax(a, v);
+        const double x = sc[r * per + i];
+        a2 = fmax(a2, fmin(a, x));
+        a = fmax(a, x);
       }
-      gv[g] = p.top2 && a2 > -INFINITY ? a + a2 : a;
+      v = p.top2 && a2 > -INFINITY ? a + a2 : a;
+      gv[r] = v;
     }
     gate_sync();
-    uint64_t chosen = 0;  // of this lane's groups r, r + LPT, ... (bit i)
-    for (int g = r, i = 0; g < p.groups; g += LPT, ++i) {
-      const double v = gv[g];
-      int rank = 0;
-      for (int j = 0; j < p.groups; ++j) rank += (gv[j] > v || (gv[j] == v && j < g)) ? 1 : 0;
-      if (rank < p.top_groups) chosen |= 1ull << i;
-    }
-    gate_sync();
-    for (int g = r, i = 0; g < p.groups; g += LPT, ++i) gv[g] = (chosen >> i) & 1 ? 1.0 : 0.0;
-    gate_sync();
+    int rank = 0;
+    for (int j = 0; j < p.groups; ++j) rank += (gv[j] > v || (gv[j] == v && j < r)) ? 1 : 0;
+    const uint64_t chosen = __ballot(r < p.groups && rank < p.top_groups);  // bit: group
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
-      const int e = r + LPT * i;
-      if (e < E && gv[e / per] == 0.0) key[i] = 0;
+      const int e = r + 64 * i;
+      if (e < E && !((chosen >> (e / per)) & 1)) key[i] = 0;
     }
     gate_sync();
   }
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i)
-    if (r + LPT * i < E) sc[r + LPT * i] = s[i];
+    if (r + 64 * i < E) sc[r + 64 * i] = s[i];
   int mine = 0;
   for (int j = 0; j < p.k; ++j) {
     uint64_t best = 0;
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) best = key[i] > best ? key[i] : best;
-    best = gate_max_u64<LPT>(best);
+    best = gate_max_u64<64>(best);
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) key[i] = key[i] == best ? 0ull : key[i];
     if (r == j) mine = 1023 - (int)(best & 1023u);
   }
   gate_sync();
   const double sj = r < p.k ? sc[mine] : 0.0;
-  const double tot = p.renorm ? gate_sum<LPT>(sj) : 1.0;
-  if (!live || r >= p.k) return;
-  p.ids[(int64_t)t * p.k + r] = mine;
-  p.w[(int64_t)t * p.k + r] = tot > 0.0 ? (float)((double)p.scale * sj / tot) : 0.0f;
+  const double tot = p.renorm ? gate_sum<16>(sj) : 1.0;
+  if (r < p.k) {
+    p.ids[(int64_t)t * p.k + r] = mine;
+    p.w[(int64_t)t * p.k + r] = tot > 0.0 ? (float)((double)p.scale * sj / tot) : 0.0f;
+  }
+  gate_sync();  // the next token's
+}
+
+template <int SLOTS>
+__global__ __launch_bounds__(64) void k_gate_wave(GateArgs p) {
+  extern __shared__ __align__(16) double gate_lds[];
+  gate_token<SLOTS>(p, blockIdx.x, gate_lds);
+}
+
+MOE_DEV uint32_t gate_max16(uint32_t v) {
+  v = max(v, (uint32_t)dpp_i32<0xB1>((int)v));   // quad_perm [1,0,3,2]
+  v = max(v, (uint32_t)dpp_i32<0x4E>((int)v));   // quad_perm [2,3,0,1]
+  v = max(v, (uint32_t)dpp_i32<0x124>((int)v));  // row_ror:4
+  return max(v, (uint32_t)dpp_i32<0x128>((int)v));
+}
+template <int CTRL>
+MOE_DEV float gate_dpp(float v) { return __int_as_float(dpp_i32<CTRL>(__float_as_int(v))); }
+MOE_DEV float gate_max16(float v) {
+  v = fmaxf(v, gate_dpp<0xB1>(v));
+  v = fmaxf(v, gate_dpp<0x4E>(v));
+  v = fmaxf(v, gate_dpp<0x124>(v));
+  return fmaxf(v, gate_dpp<0x128>(v));
+}
+MOE_DEV float gate_sum16(float v) {
+  v += gate_dpp<0xB1>(v);
+  v += gate_dpp<0x4E>(v);
+  v += gate_dpp<0x124>(v);
+  return v + gate_dpp<0x128>(v);
+}
+// exp(x), x <= 0, to about an ulp: the product with log2 e in two parts.
+MOE_DEV float gate_exp(float x) {
+  x = fmaxf(x, -200.0f);  // 0 from -104 on
+  const float t = x * 1.44269504f, lo = fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;
+  return fmaf(__builtin_amdgcn_exp2f(t) * lo, 0.693147181f, __builtin_amdgcn_exp2f(t));
+}
+// The two largest of two pairs.
+template <int CTRL>
+MOE_DEV void gate_top2(float& a, float& a2) {
+  const float b = gate_dpp<CTRL>(a), b2 = gate_dpp<CTRL>(a2);
+  a2 = fmaxf(fminf(a, b), fmaxf(a2, b2));
+  a = fmaxf(a, b);
+}
+
+// The four largest of a lane's keys in falling order, of those below `last`.
+template <int SL>
+MOE_DEV void gate_largest4(const uint32_t (&key)[SL], uint32_t last, uint32_t (&t)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) t[q] = 0;
+#pragma unroll
+  for (int i = 0; i < SL; ++i) {
+    uint32_t x = key[i] < last ? key[i] : 0u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t m = max(t[q], x);
+      x = min(t[q], x);
+      t[q] = m;
+    }
+  }
+}
+
+// Four tokens per wave, 16 lanes each, lane r with the experts from r ceil(E / 16)
+// on (SL at most); 1, 2, 4, 8 or 16 groups, with groups E a multiple of 16.
+//
+// The choice is made on fp32 scores as 22-bit steps below the largest c, down to
+// what two experts of every lane reach; a lane keeps its four largest keys sorted,
+// and a round takes the largest of 16 heads.  Where two values that the choice
+// depends on lie within what fp32 may be off (about 1 token in 1000 of a trained
+// router's), or it reaches an expert below the steps or out, the token is done
+// again in 64 bits.  16384 x 256 in 8 groups: 31 us with 64-bit scores for all, 22
+// with rounds over all keys.
+template <int SL, int SLOTS, bool ALIGNED>
+__global__ __launch_bounds__(64) void k_gate(GateArgs p) {
+  extern __shared__ __align__(16) double gate_lds[];
+  const int lane = threadIdx.x, r = lane & 15, E = p.E;
+  const int t = blockIdx.x * 4 + (lane >> 4);
+  const bool live = t < p.T;
+  const float* row = p.logits + (int64_t)(live ? t : p.T - 1) * E;
+  const int sl = ALIGNED ? SL : (E + 15) / 16, e0 = r * sl, n = min(sl, E - e0);  // n may be < 1
+  auto load = [&](const float* v, float (&o)[SL]) {
+    if constexpr (ALIGNED) {
+#pragma unroll
+      for (int i = 0; i < SL / 4; ++i) {
+        const f32x4 q = *reinterpret_cast<const f32x4*>(v + e0 + 4 * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[4 * i + j] = q[j];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < SL; ++i) o[i] = i < n ? v[e0 + i] : -INFINITY;
+    }
+  };
+  float c[SL], b[SL];
+  load(row, c);
+#pragma unroll
+  for (int i = 0; i < SL; ++i) b[i] = 0.0f;
+  if (p.bias) load(p.bias, b);
+  // an expert that is out gets -infinity for c (a quarter of each: no overflow)
+  bool out[SL];
+#pragma unroll
+  for (int i = 0; i < SL; ++i) out[i] = !(fmaf(c[i], 0.25f, 0.25f * b[i]) > -INFINITY);
+  // scores; tol: what two values of c may be off against each other.  Sigmoid: an
+  // argument rounded by 2^-24 moves s by at most 0.23 of that, and three
+  // operations follow; softmax: its terms, their sum of E and the quotient.
+  float m = 0.0f, tol = 8e-7f, z = 1.0f;
+  if (p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < SL; ++i)
+      c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(c[i] * -1.44269504f));
+  } else {
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < SL; ++i) m = out[i] ? m : fmaxf(m, c[i]);
+    m = gate_max16(m);
+    z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      c[i] = out[i] ? 0.0f : c[i] == m ? 1.0f : gate_exp(c[i] - m);
+      z += c[i];
+    }
+    z = gate_sum16(z);
+    const float iz = 1.0f / z;  // z >= 1 where an expert is in
+    tol = 4e-6f * iz;
+#pragma unroll
+    for (int i = 0; i < SL; ++i) c[i] *= iz;
+  }
+  float a = -INFINITY, a2 = -INFINITY;  // this lane's largest, and the next
+#pragma unroll
+  for (int i = 0; i < SL; ++i) {
+    c[i] = out[i] ? -INFINITY : c[i] + b[i];
+    a2 = fmaxf(a2, fminf(a, c[i]));
+    a = fmaxf(a, c[i]);
+  }
+  bool sure = true;
+  bool mine_in = true;   // this lane's group is chosen
+  if (p.groups > 1) {
+    float ga = a, ga2 = a2;
+    const int lanes = 16 / p.groups, g = r / lanes;
+    if (lanes > 1) gate_top2<0xB1>(ga, ga2);
+    if (lanes > 2) gate_top2<0x4E>(ga, ga2);
+    if (lanes > 4) gate_top2<0x141>(ga, ga2);  // row_half_mirror
+    if (lanes > 8) gate_top2<0x140>(ga, ga2);  // row_mirror
+    const bool two = p.top2 && ga2 > -INFINITY;
+    const float v = two ? ga + ga2 : ga;
+    int rank = 0;
+    for (int j = 1; j < p.groups; ++j) {
+      const int og = (g + j) & (p.groups - 1);
+      const float o = __shfl(v, (lane & 48) + og * lanes, 64);
+      rank += (o > v || (o == v && og < g)) ? 1 : 0;
+    }
+    mine_in = rank < p.top_groups;
+    // the least chosen group against the best of the others
+    const float least = -gate_max16(mine_in ? -v : -INFINITY), other = gate_max16(mine_in ? -INFINITY : v);
+    const float size = gate_max16(ga > -INFINITY ? fmaxf(fabsf(ga), two ? fabsf(ga2) : 0.0f) : 0.0f);
+    sure = p.top_groups == p.groups || other == -INFINITY || least - other > 4.0f * tol + 1e-6f * size;
+  }
+  // steps from hi down to the least of the lanes' second largest (of the only one)
+  const float hi = gate_max16(mine_in ? a : -INFINITY);
+  const float low = mine_in ? (a2 > -INFINITY ? a2 : a > -INFINITY ? a : INFINITY) : INFINITY;
+  const float range = hi + gate_max16(-low);
+  // infinite or NaN (no range, infinite values): every key has step 1, nothing is sure
+  const float unit = 4190000.0f / range;
+  const uint32_t code = 1023u - e0;
+  uint32_t key[SL], top[4];
+#pragma unroll
+  for (int i = 0; i < SL; ++i)
+    key[i] = ((uint32_t)fmaxf(fmaf(c[i] - hi, unit, 4194302.0f), 1.0f) << 10) + code - i;
+  gate_largest4<SL>(key, mine_in ? 0xFFFFFFFFu : 0u, top);
+  tol += 2.4e-7f * fmaxf(fabsf(hi), fabsf(hi - range));
+  const float gap = 2.0f * tol * unit + 3.0f;
+  const uint32_t need = gap < 4.0e6f ? (uint32_t)gap : 4194303u;  // NaN: the latter
+  bool more = SL > 4 && top[3] != 0u;  // there may be keys behind the four
+  int mine = 0;
+  uint32_t popped = 0;
+  // takes the largest key away, for lane j's choice
+  auto take = [&](int j, uint32_t best) {
+    if (r == j) mine = 1023 - (int)(best & 1023u);
+    if (top[0] == best) {
+      popped = best;
+#pragma unroll
+      for (int q = 0; q < 3; ++q) top[q] = top[q + 1];
+      top[3] = 0u;
+    }
+    if (SL > 4 && __any(more && top[0] == 0u)) {
+      if (more && top[0] == 0u) {
+        gate_largest4<SL>(key, popped, top);
+        more = top[3] != 0u;
+      }
+    }
+  };
+  bool order = true;  // of the chosen among each other
+  uint32_t before = 0;
+  for (int j = 0; j < p.k; ++j) {
+    const uint32_t best = gate_max16(top[0]);
+    sure = sure && best >= 2048u;
+    order = order && (j == 0 || (before >> 10) - (best >> 10) >= need);
+    take(j, best);
+    before = best;
+  }
+  int among = p.k;  // experts that the chosen are among
+  uint32_t next = gate_max16(top[0]);
+  if (__any(next != 0u && (before >> 10) - (next >> 10) < need)) {
+    // the first that is not chosen is as near: it is looked at too, if the one behind it is not
+    const bool near = next != 0u && (before >> 10) - (next >> 10) < need;
+    take(p.k, next);
+    const uint32_t then = gate_max16(top[0]);
+    if (near) {
+      among = p.k + 1;
+      order = false;
+      sure = sure && p.k < 16 && next >= 2048u && (then == 0u || (next >> 10) - (then >> 10) >= need);
+    }
+  }
+  // their order in 64 bits (softmax without a bias: that of its terms)
+  sure = sure && (order || p.sigmoid || !p.bias);
+  if (__any(live && sure && !order)) {
+    uint64_t k64 = 0;
+    if (r < among && sure) {
+      const float l = row[mine];
+      const double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)m);
+      k64 = gate_key(p.bias ? s + (double)p.bias[mine] : s, false, mine);
+    }
+    int rank = 0, chosen = 0;
+    for (int j = 0; j <= p.k; ++j)
+      rank += __shfl((unsigned long long)k64, (lane & 48) + min(j, 15), 64) > k64 && j < among ? 1 : 0;
+    for (int j = 0; j <= p.k; ++j) {
+      const int from = (lane & 48) + min(j, 15), id = __shfl(mine, from, 64);
+      if (__shfl(rank, from, 64) == r && j < among) chosen = id;
+    }
+    if (sure && !order) mine = chosen;
+  }
+  uint64_t again = __ballot(live && !sure);
+  if (live && sure) {
+    // the weights of the chosen in 64 bits, but for softmax's sum
+    double s = 0.0;
+    if (r < p.k) {
+      const float l = row[mine];
+      s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)m);
+    }
+    const double tot = p.renorm ? gate_sum<16>(s) : (double)z;
+    if (r < p.k) {
+      p.ids[(int64_t)t * p.k + r] = mine;
+      p.w[(int64_t)t * p.k + r] = tot > 0.0 ? (float)((double)p.scale * s / tot) : 0.0f;
+    }
+  }
+  while (again) {
+    const int w = __ffsll((unsigned long long)again) - 1;
+    again &= ~(0xFFFFull << (w & 48));
+    gate_token<SLOTS>(p, blockIdx.x * 4 + (w >> 4), gate_lds);
+  }
 }
 
 // d_logits of one token by 16 lanes: with ds_j = scale dw_j, or with weights
@@ -260,32 +498,31 @@ __global__ __launch_bounds__(256) void k_pair_grad(const int32_t* __restrict__ r
   g[q] = s;
 }
 
-template <int LPT>
-static void launch_gate_lpt(const GateArgs& a, hipStream_t s) {
-  const dim3 g((a.T + 64 / LPT - 1) / (64 / LPT)), b(64);
-  const size_t lds = (size_t)(64 / LPT) * (a.E + GATE_MAX_GROUPS) * 8;
-  const int n = (a.E + LPT - 1) / LPT;
-#define GATE(S) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gate<LPT, S>), g, b, lds, s, a)
-  if constexpr (LPT == 64) {
-    if (n <= 2) GATE(2);
-    else if (n <= 4) GATE(4);
-    else if (n <= 6) GATE(6);
-    else if (n <= 8) GATE(8);
-    else GATE(16);
-  } else {
-    if (n <= 4) GATE(4);
-    else if (n <= 8) GATE(8);
-    else if (n <= 16) GATE(16);
-    else if (n <= 24) GATE(24);
-    else GATE(32);
-  }
-#undef GATE
-}
-
 void launch_gate(const GateArgs& a, hipStream_t s) {
   if (a.T == 0) return;
-  if (a.T <= 1024 || a.E > 512) launch_gate_lpt<64>(a, s);
-  else launch_gate_lpt<16>(a, s);
+  const size_t lds = (size_t)(a.E + GATE_MAX_GROUPS) * 8;
+  const bool g16 = a.groups == 1 || (a.groups <= 16 && (a.groups & (a.groups - 1)) == 0 && a.E % 16 == 0);
+  if (a.E <= 512 && g16) {
+    const dim3 g((a.T + 3) / 4), b(64);
+#define GATE(SL, S)                                                                                        \
+  do {                                                                                                     \
+    if (a.E == 16 * SL) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gate<SL, S, true>), g, b, lds, s, a);         \
+    else hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gate<SL, S, false>), g, b, lds, s, a);                       \
+  } while (0)
+    if (a.E <= 64) GATE(4, 1);
+    else if (a.E <= 128) GATE(8, 2);
+    else if (a.E <= 256) GATE(16, 4);
+    else if (a.E <= 384) GATE(24, 6);
+    else GATE(32, 8);
+#undef GATE
+    return;
+  }
+  const dim3 g(a.T), b(64);
+#define GATE(S) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gate_wave<S>), g, b, lds, s, a)
+  if (a.E <= 128) GATE(2);
+  else if (a.E <= 512) GATE(8);
+  else GATE(16);
+#undef GATE
 }
 
 void launch_gate_bwd(const GateArgs& a, hipStream_t s) {

@@ -36,8 +36,10 @@ def _check_forward(logits, bias, k, sigmoid=True, groups=1, top=1, top2=True, re
                         None if bias is None else bias.cuda(), permute=permute)
     assert torch.equal(r["topk_ids"].cpu(), want)
     got = r["topk_w"].cpu().double()
-    # formed in 64 bits, rounded once
-    assert bool(((got - w).abs() <= w.abs() * ref.F32 * (1 + 1e-6) + 1e-44).all())
+    # formed in 64 bits, rounded once; softmax's sum over all experts may be one of fp32 terms: the difference and the
+    # exponential of each (5 half steps), at most E / 16 + 4 additions in a row
+    steps = 1 if sigmoid or renorm else E // 16 + 12
+    assert bool(((got - w).abs() <= w.abs() * ref.F32 * (steps + 1e-6) + 1e-44).all())
     return r
 
 
@@ -99,6 +101,29 @@ def test_far_logits(T):
     big[12] = INF
     big[13] = -1e30
     _check_forward(logits, big, 5, True, groups=4, top=2)
+
+
+@pytest.mark.parametrize("T", [3, 260])
+@pytest.mark.parametrize("groups,top", [(1, 1), (4, 2), (3, 2)])
+def test_values_closer_than_fp32(T, groups, top):
+    """Biases that put neighbours within a few 1e-9 of each other, inside a group and between groups."""
+    g = torch.Generator().manual_seed(T)
+    logits = torch.randn(T, 48, generator=g)
+    bias = (0.5 - torch.sigmoid(logits[1].double())).float()            # row 1: every c is 0.5 to a rounding
+    _check_forward(logits, bias, 6, True, groups, top)
+    _check_forward(logits, bias, 6, True, groups, top, top2=False)
+    p = torch.softmax(logits.double(), 1)
+    _check_forward(logits, (0.01 - p[2]).float(), 6, False, groups, top, renorm=False)
+
+
+def test_a_chosen_score_of_zero():
+    logits = torch.zeros(5, 32)
+    logits[:, 9] = -1e4
+    bias = torch.zeros(32)
+    bias[9] = 5.0
+    _check_forward(logits, bias, 1)
+    _check_forward(logits, bias, 3)
+    _check_forward(logits, bias, 2, sigmoid=False)
 
 
 def test_close_values_are_told_apart():
