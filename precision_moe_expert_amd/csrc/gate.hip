@@ -399,90 +399,182 @@ __global__ __launch_bounds__(64) void k_gate(GateArgs p) {
   }
 }
 
-// d_logits of one token by 16 lanes: with ds_j = scale dw_j, or with weights
-// that sum to scale, ds_j = (scale dw_j - sum_i dw_i w_i) / sum_i s_i,
+// What the gradients of one token's weights (16 lanes, r < k with a slot) come to:
+// with ds_j = scale dw_j, or with weights that sum to scale,
+// ds_j = (scale dw_j - sum_i dw_i w_i) / sum_i s_i,
 //   sigmoid: dl_j = ds_j s_j (1 - s_j)
 //   softmax: dl_e = s_e (ds_e - sum_j ds_j s_j); where the weights were
 //            renormalised the last sum is 0.
 // Ids outside [0, E) are left out, an id that is there twice gets both.
+struct GateSlot {
+  int id;
+  bool there, in;
+  float l, dw;
+};
+MOE_DEV GateSlot gate_slot(const GateArgs& p, int64_t t, int r, const float* row) {
+  GateSlot s;
+  s.id = r < p.k ? p.ids[t * p.k + r] : -1;
+  s.there = s.id >= 0 && s.id < p.E;
+  s.l = s.there ? row[s.id] : -INFINITY;
+  s.in = s.there && !gate_out(s.l) && !(p.bias && gate_out(p.bias[s.id]));
+  s.dw = r < p.k ? p.dw[t * p.k + r] : 0.0f;
+  return s;
+}
+// m, iz: softmax's maximum and the reciprocal of its sum (renormalised: of the
+// chosen, and any).  `add`: of the slot's own logit, without softmax's common sum
+// `dot`; sparse gradients are whole.  True: this lane writes for its id.
+MOE_DEV bool gate_slot_grad(const GateArgs& p, const GateSlot& s, int r, float m, float iz, float& add, float& dot) {
+  float sj = 0.0f, sp = 0.0f;
+  if (s.in) {
+    if (p.sigmoid) {
+      const float e = expf(-fabsf(s.l)), q = 1.0f / (1.0f + e);
+      sj = s.l >= 0.0f ? q : e * q;
+      sp = e * q * q;
+    } else {
+      sj = (s.l == m ? 1.0f : expf(s.l - m)) * iz;
+      sp = sj;
+    }
+  }
+  float g = p.scale * s.dw;
+  if (p.renorm) {
+    const float tot = gate_sum16(sj), it = tot > 0.0f ? 1.0f / tot : 0.0f;
+    g = (g - gate_sum16(g * sj) * it) * it;
+  }
+  dot = gate_sum16(s.in ? g * sj : 0.0f);
+  add = s.in ? g * sp : 0.0f;
+  // one lane per id: the first with it takes what the others add
+  bool first = s.there;
+  const int base = threadIdx.x & 48;
+  for (int j = 0; j < p.k; ++j) {
+    const int o = __shfl(s.id, base + j, 64);
+    const float v = __shfl(add, base + j, 64);
+    if (o == s.id && j < r) first = false;
+    if (o == s.id && j > r) add += v;
+  }
+  return first;
+}
+
+// Four tokens per wave, lane r with the experts 4 (r + 16 i) .. + 3 (E a multiple
+// of 4): a row is read once, if at all (softmax whose weights are not
+// renormalised is the one gradient that every logit has a part in), and written
+// once.  What the chosen get goes through LDS.
+template <int SL>
+__global__ __launch_bounds__(64) void k_gate_bwd_rows(GateArgs p) {
+  __shared__ __align__(16) float lds[4][64 * SL / 4];
+  constexpr int N = SL / 4;
+  const int lane = threadIdx.x, r = lane & 15, E = p.E;
+  const int t = blockIdx.x * 4 + (lane >> 4);
+  const bool live = t < p.T, dense = !p.sigmoid && !p.renorm;
+  const int64_t tt = live ? t : p.T - 1;
+  const float* row = p.logits + tt * E;
+  float* out = p.dlogits + tt * E;
+  float* ds = lds[lane >> 4];
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  const GateSlot s = gate_slot(p, tt, r, row);
+#pragma unroll
+  for (int i = 0; i < N; ++i) *reinterpret_cast<f32x4*>(ds + 4 * (r + 16 * i)) = zero;
+  f32x4 e[N];
+  float m = -INFINITY, iz = 1.0f;
+  if (dense) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = 4 * (r + 16 * i);
+      e[i] = at < E ? *reinterpret_cast<const f32x4*>(row + at) : (f32x4){-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (p.bias && at < E) {
+        const f32x4 b = *reinterpret_cast<const f32x4*>(p.bias + at);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) e[i][q] = gate_out(b[q]) ? -INFINITY : e[i][q];
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        e[i][q] = e[i][q] != e[i][q] ? -INFINITY : e[i][q];
+        m = fmaxf(m, e[i][q]);
+      }
+    }
+    m = gate_max16(m);
+    float z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float x = e[i][q];
+        e[i][q] = x == -INFINITY ? 0.0f : x == m ? 1.0f : gate_exp(x - m);
+        z += e[i][q];
+      }
+    z = gate_sum16(z);
+    iz = z > 0.0f ? 1.0f / z : 0.0f;
+  } else if (!p.sigmoid) {
+    m = gate_max16(s.in ? s.l : -INFINITY);
+  }
+  float add, dot;
+  const bool first = gate_slot_grad(p, s, r, m, iz, add, dot);
+  if (p.accumulate && !dense) {
+    if (live && first) out[s.id] += add;
+    return;
+  }
+  gate_sync();
+  if (first) ds[s.id] = add;
+  gate_sync();
+  if (!live) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int at = 4 * (r + 16 * i);
+    if (at < E) {
+      f32x4 v = *reinterpret_cast<const f32x4*>(ds + at);
+      if (dense) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = fmaf(-dot, e[i][q] * iz, v[q]);
+      }
+      if (p.accumulate) v += *reinterpret_cast<const f32x4*>(out + at);
+      *reinterpret_cast<f32x4*>(out + at) = v;
+    }
+  }
+}
+
+// The same for any E, element by element.
 __global__ __launch_bounds__(64) void k_gate_bwd(GateArgs p) {
   extern __shared__ __align__(16) float gate_bwd_lds[];
   const int lane = threadIdx.x, r = lane & 15, E = p.E;
   const int t = blockIdx.x * 4 + (lane >> 4);
-  const bool live = t < p.T;
-  const int64_t tt = live ? t : 0;
+  const bool live = t < p.T, dense = !p.sigmoid && !p.renorm;
+  const int64_t tt = live ? t : p.T - 1;
   const float* row = p.logits + tt * E;
+  float* out = p.dlogits + tt * E;
   float* ds = gate_bwd_lds + (lane >> 4) * E;
-  const int id = r < p.k ? p.ids[tt * p.k + r] : -1;
-  const bool there = id >= 0 && id < E;
-  const float lj = there ? row[id] : -INFINITY;
-  const bool in = there && !gate_out(lj) && !(p.bias && gate_out(p.bias[id]));
-  const float dw = r < p.k ? p.dw[tt * p.k + r] : 0.0f;
-  const bool dense = !p.sigmoid && !p.renorm;
-  float m = 0.0f, iz = 1.0f;
-  if (!p.sigmoid) {
-    m = in ? lj : -INFINITY;
-    if (dense)
-      for (int e = r; e < E; e += 16) {
-        const float v = row[e];
-        if (!gate_out(v) && !(p.bias && gate_out(p.bias[e]))) m = fmaxf(m, v);
-      }
-    m = gate_max<16>(m);
+  const GateSlot s = gate_slot(p, tt, r, row);
+  auto at = [&](int e) { return gate_out(row[e]) || (p.bias && gate_out(p.bias[e])) ? -INFINITY : row[e]; };
+  float m = s.in ? s.l : -INFINITY, iz = 1.0f;
+  if (dense)
+    for (int e = r; e < E; e += 16) m = fmaxf(m, at(e));
+  m = gate_max16(m);
+  if (dense) {
     float z = 0.0f;
-    if (dense) {
-      for (int e = r; e < E; e += 16) {
-        const float v = row[e];
-        if (!gate_out(v) && !(p.bias && gate_out(p.bias[e]))) z += v == m ? 1.0f : expf(v - m);
-      }
-      z = gate_sum<16>(z);
-    } else {
-      z = 1.0f;  // any: only ratios of chosen scores are used
+    for (int e = r; e < E; e += 16) {
+      const float v = at(e);
+      z += v == -INFINITY ? 0.0f : v == m ? 1.0f : gate_exp(v - m);
     }
+    z = gate_sum16(z);
     iz = z > 0.0f ? 1.0f / z : 0.0f;
   }
-  float sj = 0.0f, sp = 0.0f;  // the score, and its derivative (softmax: by its own logit, but for the sum)
-  if (in) {
-    if (p.sigmoid) {
-      const float e = expf(-fabsf(lj)), q = 1.0f / (1.0f + e);
-      sj = lj >= 0.0f ? q : e * q;
-      sp = e * q * q;
-    } else {
-      sj = (lj == m ? 1.0f : expf(lj - m)) * iz;
-      sp = sj;
-    }
-  }
-  float g = p.scale * dw;
-  if (p.renorm) {
-    const float tot = gate_sum<16>(sj), it = tot > 0.0f ? 1.0f / tot : 0.0f;
-    g = (g - gate_sum<16>(g * sj) * it) * it;
-  }
-  const float dot = dense ? gate_sum<16>(in ? g * sj : 0.0f) : 0.0f;
-  float add = in ? g * sp : 0.0f;
-  // one lane per id: the first with it takes what the others add
-  bool first = there;
-  for (int j = 0; j < p.k; ++j) {
-    const int o = __shfl(id, (lane & 48) + j, 64);
-    const float v = __shfl(add, (lane & 48) + j, 64);
-    if (o == id && j < r) first = false;
-    if (o == id && j > r) add += v;
-  }
+  float add, dot;
+  const bool first = gate_slot_grad(p, s, r, m, iz, add, dot);
   if (p.accumulate && !dense) {
-    if (live && first) p.dlogits[tt * E + id] += add;
+    if (live && first) out[s.id] += add;
     return;
   }
   for (int e = r; e < E; e += 16) ds[e] = 0.0f;
   gate_sync();
-  if (first) ds[id] = add;
+  if (first) ds[s.id] = add;
   gate_sync();
   if (!live) return;
   for (int e = r; e < E; e += 16) {
     float v = ds[e];
     if (dense) {
-      const float x = row[e];
-      if (!gate_out(x) && !(p.bias && gate_out(p.bias[e]))) v -= dot * ((x == m ? 1.0f : expf(x - m)) * iz);
+      const float x = at(e);
+      v = fmaf(-dot, (x == -INFINITY ? 0.0f : x == m ? 1.0f : gate_exp(x - m)) * iz, v);
     }
-    if (p.accumulate) v += p.dlogits[tt * E + e];
-    p.dlogits[tt * E + e] = v;
+    if (p.accumulate) v += out[e];
+    out[e] = v;
   }
 }
 
@@ -527,7 +619,15 @@ void launch_gate(const GateArgs& a, hipStream_t s) {
 
 void launch_gate_bwd(const GateArgs& a, hipStream_t s) {
   if (a.T == 0) return;
-  hipLaunchKernelGGL(k_gate_bwd, dim3((a.T + 3) / 4), dim3(64), (size_t)a.E * 16, s, a);
+  const dim3 g((a.T + 3) / 4), b(64);
+#define GATE(SL) hipLaunchKernelGGL(k_gate_bwd_rows<SL>, g, b, 0, s, a)
+  if (a.E % 4 != 0 || a.E > 512) hipLaunchKernelGGL(k_gate_bwd, g, b, (size_t)a.E * 16, s, a);
+  else if (a.E <= 64) GATE(4);
+  else if (a.E <= 128) GATE(8);
+  else if (a.E <= 256) GATE(16);
+  else if (a.E <= 384) GATE(24);
+  else GATE(32);
+#undef GATE
 }
 
 void launch_pair_grad(const int32_t* row_of, const float* gpart, int nparts, int R, float* g, hipStream_t s) {
