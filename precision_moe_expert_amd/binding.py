@@ -173,7 +173,7 @@ def lib() -> ctypes.CDLL:
         L.moe_balance_loss_backward.argtypes = [ctypes.POINTER(MoeLayer)] + [vp] * 3 + [i32] + [vp] * 3 + [i32, vp,
                                                                                                           vp]
         layer, gate, lin = ctypes.POINTER(MoeLayer), ctypes.POINTER(MoeGate), ctypes.POINTER(MoeLinear)
-        tensors, qw, sc = ctypes.POINTER(MoeTensor), ctypes.POINTER(MoeQWeights), ctypes.POINTER(MoeScales)
+        qw, sc = ctypes.POINTER(MoeQWeights), ctypes.POINTER(MoeScales)
         for name, args in (
                 ("moe_route_gated", [layer, gate, vp, vp, ctypes.POINTER(MoeRouteOut), vp, sz, vp]),
                 ("moe_route_gated_backward", [layer, gate] + [vp] * 4 + [i32, vp, vp]),
@@ -182,9 +182,9 @@ def lib() -> ctypes.CDLL:
                 ("moe_fp8_linear", [lin] + [vp] * 5 + [sz, vp]),
                 ("moe_fp8_linear_transpose", [lin] + [vp] * 5),
                 ("moe_fp8_linear_backward", [lin] + [vp] * 7 + [sz, vp]),
-                ("moe_grad_norm", [tensors, i32, vp, vp, sz, vp]),
-                ("moe_grad_clip", [tensors, i32, f32, vp, vp, sz, vp]),
-                ("moe_grad_scale", [tensors, i32, vp, f32, vp])):
+                ("moe_grad_norm", [vp, i32, vp, vp, sz, vp]),        # first: an array of MoeTensor, or its words
+                ("moe_grad_clip", [vp, i32, f32, vp, vp, sz, vp]),
+                ("moe_grad_scale", [vp, i32, vp, f32, vp])):
             getattr(L, name).restype, getattr(L, name).argtypes = ctypes.c_int, args
         L.moe_fp8_linear_workspace_bytes.restype, L.moe_fp8_linear_workspace_bytes.argtypes = sz, [lin, i32]
         L.moe_grad_norm_workspace_bytes.restype, L.moe_grad_norm_workspace_bytes.argtypes = sz, [i32]
@@ -483,7 +483,7 @@ def _aligned(t, name: str) -> int:
 
 def _typed(t, name: str, dtype, shape, device):
     """The address of a contiguous tensor of this type and shape on the call's device."""
-    if t is None or t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t is None or t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous {dtype} tensor of shape {tuple(shape)} on {device} expected, got "
                          + ("None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}"))
     return _aligned(t, name)
@@ -694,13 +694,23 @@ def make_gate(score: int = GATE_SIGMOID, groups: int = 1, top_groups: int = 1, g
     return MoeGate(score, groups, top_groups, group_score, int(renormalize), scale)
 
 
-def _workspace(nbytes: int, ws, device):
-    """(workspace, its bytes): the caller's, or a new one."""
+def _elsewhere(device) -> bool:
+    """Whether a call's device is not the current one (the caller then makes it current and calls itself again)."""
+    if device.type != "cuda":
+        raise ValueError("device tensors expected")
+    return device.index != torch._C._cuda_getDevice()
+
+
+def _workspace(nbytes: int, ws, like):
+    """(workspace, its address, its bytes): the caller's, a new one, or none where none is needed."""
     if ws is None:
-        ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
-    elif ws.device != device or not ws.is_contiguous():
+        if nbytes == 0:
+            return None, None, 0
+        ws = like.new_empty(nbytes, dtype=torch.uint8)
+        return ws, ws.data_ptr(), nbytes
+    if ws.device != like.device or not ws.is_contiguous():
         raise ValueError("ws: contiguous tensor on the call's device expected")
-    return ws, ws.numel() * ws.element_size()
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _gate_inputs(layer, logits, bias):
@@ -713,21 +723,22 @@ def _gate_inputs(layer, logits, bias):
 def route_gated(layer: MoeLayer, gate: MoeGate, logits, bias=None, permute: bool = True, ws=None) -> dict:
     """moe_route_gated on router logits [T][E] fp32 with a balance bias [E] fp32:
     a dict as route_permute's; without `permute` only topk_ids and topk_w."""
+    if _elsewhere(logits.device):
+        with torch.cuda.device(logits.device):
+            return route_gated(layer, gate, logits, bias, permute, ws)
     T, E, k = layer.num_tokens, layer.num_experts, layer.top_k
-    with _On(logits.device):
-        dev, lp, bp = _gate_inputs(layer, logits, bias)
-        out = dict(topk_ids=torch.empty((T, k), dtype=torch.int32, device=dev),
-                   topk_w=torch.empty((T, k), dtype=torch.float32, device=dev))
-        wp, nb = None, 0
-        if permute:
-            for name, n in (("expert_offsets", E + 1), ("sorted_rows", T * k), ("row_of", T * k),
-                            ("active_experts", E), ("num_active", 4)):
-                out[name] = (torch.empty if T else torch.zeros)(n, dtype=torch.int32, device=dev)
-            ws, nb = _workspace(lib().moe_route_workspace_bytes(ctypes.byref(layer)), ws, dev)
-            wp = ws.data_ptr()
-        ro = MoeRouteOut(*[t.data_ptr() for t in out.values()])
-        _check(lib().moe_route_gated(ctypes.byref(layer), ctypes.byref(gate), lp, bp, ctypes.byref(ro), wp, nb,
-                                     _raw_stream(dev)), "moe_route_gated")
+    dev, lp, bp = _gate_inputs(layer, logits, bias)
+    ids, w = logits.new_empty((T, k), dtype=torch.int32), logits.new_empty((T, k))
+    out = dict(topk_ids=ids, topk_w=w)
+    ro, wp, nb = MoeRouteOut(ids.data_ptr(), w.data_ptr()), None, 0
+    if permute:
+        for name, n in (("expert_offsets", E + 1), ("sorted_rows", T * k), ("row_of", T * k), ("active_experts", E),
+                        ("num_active", 4)):
+            out[name] = (torch.empty if T else torch.zeros)(n, dtype=torch.int32, device=dev)
+            setattr(ro, name, out[name].data_ptr())
+        ws, wp, nb = _workspace(lib().moe_route_workspace_bytes(ctypes.byref(layer)), ws, logits)
+    _check(lib().moe_route_gated(ctypes.byref(layer), ctypes.byref(gate), lp, bp, ctypes.byref(ro), wp, nb,
+                                 _raw_stream(dev)), "moe_route_gated")
     return out
 
 
@@ -736,17 +747,19 @@ def route_gated_backward(layer: MoeLayer, gate: MoeGate, logits, topk_ids, d_top
     """moe_route_gated_backward: dL/dlogits [T][E] fp32 for d_topk_w [T][k] fp32, with
     topk_ids from route_gated.  Where d_logits is given (balance_loss_backward's),
     the gradient is added to it."""
+    if _elsewhere(logits.device):
+        with torch.cuda.device(logits.device):
+            return route_gated_backward(layer, gate, logits, topk_ids, d_topk_w, bias, d_logits)
     T, E, k = layer.num_tokens, layer.num_experts, layer.top_k
-    with _On(logits.device):
-        dev, lp, bp = _gate_inputs(layer, logits, bias)
-        ip = _typed(topk_ids, "topk_ids", torch.int32, (T, k), dev)
-        wp = _typed(d_topk_w, "d_topk_w", torch.float32, (T, k), dev)
-        add = d_logits is not None
-        if not add:
-            d_logits = torch.empty((T, E), dtype=torch.float32, device=dev)
-        dp = _typed(d_logits, "d_logits", torch.float32, (T, E), dev)
-        _check(lib().moe_route_gated_backward(ctypes.byref(layer), ctypes.byref(gate), lp, bp, ip, wp, add, dp,
-                                              _raw_stream(dev)), "moe_route_gated_backward")
+    dev, lp, bp = _gate_inputs(layer, logits, bias)
+    ip = _typed(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+    wp = _typed(d_topk_w, "d_topk_w", torch.float32, (T, k), dev)
+    add = d_logits is not None
+    if not add:
+        d_logits = torch.empty_like(logits)
+    dp = _typed(d_logits, "d_logits", torch.float32, (T, E), dev)
+    _check(lib().moe_route_gated_backward(ctypes.byref(layer), ctypes.byref(gate), lp, bp, ip, wp, add, dp,
+                                          _raw_stream(dev)), "moe_route_gated_backward")
     return d_logits
 
 
@@ -757,13 +770,13 @@ def expert_forward_gated(layer: MoeLayer, gate: MoeGate, x, logits, w13, w2, s13
         dev, lp, bp = _gate_inputs(layer, logits, bias)
         if out is None:
             out = torch.empty((layer.num_tokens, layer.hidden), dtype=torch.bfloat16, device=dev)
-        ws, nb = _workspace(workspace_bytes(layer, chunk_experts), ws, dev)
+        ws, wp, nb = _workspace(workspace_bytes(layer, chunk_experts), ws, logits)
         _check_forward_args(layer, x, logits, w13, w2, s13, s2, adapter, out, g13, g2)
         qw = MoeQWeights(_ptr(w13), _ptr(w2))
         sc = MoeScales(_ptr(s13), _ptr(s2), _ptr(g13), _ptr(g2))
         _check(lib().moe_expert_forward_gated(ctypes.byref(layer), ctypes.byref(gate), _ptr(x), lp, bp,
                                               ctypes.byref(qw), ctypes.byref(sc), _ptr(adapter), int(chunk_experts),
-                                              _ptr(out), ws.data_ptr(), nb, _raw_stream(dev)),
+                                              _ptr(out), wp, nb, _raw_stream(dev)),
                "moe_expert_forward_gated")
     return out
 
@@ -777,7 +790,7 @@ def expert_backward_gated(layer: MoeLayer, gate: MoeGate, x, logits, w13, w2, s1
         d_x = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
         d_logits = torch.empty((T, E), dtype=torch.float32, device=dev)
         d_adapter = None if adapter is None else torch.empty(adapter.shape, dtype=torch.float32, device=dev)
-        ws, nb = _workspace(backward_workspace_bytes(layer, chunk_experts), ws, dev)
+        ws, wp, nb = _workspace(backward_workspace_bytes(layer, chunk_experts), ws, logits)
         _check_forward_args(layer, x, logits, w13, w2, s13, s2, adapter, d_x, g13, g2)
         _need(d_out, "d_out", T * H * 2, 2)
         _need(bwd_weights, "bwd_weights", backward_weights_bytes(layer))
@@ -786,7 +799,7 @@ def expert_backward_gated(layer: MoeLayer, gate: MoeGate, x, logits, w13, w2, s1
         _check(lib().moe_expert_backward_gated(ctypes.byref(layer), ctypes.byref(gate), _ptr(x), lp, bp,
                                                ctypes.byref(qw), ctypes.byref(sc), _ptr(bwd_weights), _ptr(adapter),
                                                _ptr(d_out), int(chunk_experts), d_x.data_ptr(), d_logits.data_ptr(),
-                                               _ptr(d_adapter), ws.data_ptr(), nb, _raw_stream(dev)),
+                                               _ptr(d_adapter), wp, nb, _raw_stream(dev)),
                "moe_expert_backward_gated")
     return d_x, d_logits, d_adapter
 
@@ -814,20 +827,22 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, fmt: int
     """moe_fp8_linear: x [M][K] bf16 (rows may be strided) through W [N][K] in E4M3
     codes with scales [ceil(N/128)][ceil(K/128)] fp32 -> [M][N] bf16."""
     dev = x.device
-    with _On(dev):
-        xp, xs = _rows(x, "x", dev)
-        wp = _codes(w, "w", dev)
-        (M, K), N = x.shape, w.shape[0]
-        if w.shape[1] != K:
-            raise ValueError(f"x has {K} columns, w {w.shape[1]}")
-        sp = _typed(w_scale, "w_scale", torch.float32, (_blocks(N), _blocks(K)), dev)
-        lin = MoeLinear(M, K, N, fmt, xs, 0)
-        if out is None:
-            out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        op = _typed(out, "out", torch.bfloat16, (M, N), dev)
-        ws, nb = _workspace(lib().moe_fp8_linear_workspace_bytes(ctypes.byref(lin), LINEAR_FORWARD), ws, dev)
-        _check(lib().moe_fp8_linear(ctypes.byref(lin), xp, wp, sp, op, ws.data_ptr(), nb, _raw_stream(dev)),
-               "moe_fp8_linear")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return fp8_linear(x, w, w_scale, fmt, out, ws)
+    xp, xs = _rows(x, "x", dev)
+    wp = _codes(w, "w", dev)
+    (M, K), N = x.shape, w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"x has {K} columns, w {w.shape[1]}")
+    sp = _typed(w_scale, "w_scale", torch.float32, (_blocks(N), _blocks(K)), dev)
+    lin = MoeLinear(M, K, N, fmt, xs, 0)
+    if out is None:
+        out = x.new_empty((M, N))
+    op = _typed(out, "out", torch.bfloat16, (M, N), dev)
+    need = lib().moe_fp8_linear_workspace_bytes(ctypes.byref(lin), LINEAR_FORWARD) if ws is None else 0
+    ws, wsp, nb = _workspace(need, ws, x)
+    _check(lib().moe_fp8_linear(ctypes.byref(lin), xp, wp, sp, op, wsp, nb, _raw_stream(dev)), "moe_fp8_linear")
     return out
 
 
@@ -852,27 +867,30 @@ def fp8_linear_backward(d_y: torch.Tensor, w_t: torch.Tensor, w_t_scale: torch.T
     d_y [M][N] bf16, with fp8_linear_transpose's copy of W and, for d_w, the
     forward's x [M][K] bf16 (rows of d_y and x may be strided)."""
     dev = d_y.device
-    with _On(dev):
-        yp, ys = _rows(d_y, "d_y", dev)
-        wp = _codes(w_t, "w_t", dev)
-        (M, N), K = d_y.shape, w_t.shape[0]
-        if w_t.shape[1] != N:
-            raise ValueError(f"d_y has {N} columns, w_t {w_t.shape[1]}")
-        sp = _typed(w_t_scale, "w_t_scale", torch.float32, (_blocks(K), _blocks(N)), dev)
-        xp, xs = None, 0
-        if weight_grad:
-            if x is None:
-                raise ValueError("x: needed for the weight's gradient")
-            xp, xs = _rows(x, "x", dev)
-            if tuple(x.shape) != (M, K):
-                raise ValueError(f"x: shape {(M, K)} expected, got {tuple(x.shape)}")
-        lin = MoeLinear(M, K, N, fmt, xs, ys)
-        d_x = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if input_grad else None
-        d_w = torch.empty((N, K), dtype=torch.bfloat16, device=dev) if weight_grad else None
-        grads = (LINEAR_D_X if input_grad else 0) | (LINEAR_D_W if weight_grad else 0)
-        ws, nb = _workspace(lib().moe_fp8_linear_workspace_bytes(ctypes.byref(lin), grads), ws, dev)
-        _check(lib().moe_fp8_linear_backward(ctypes.byref(lin), yp, wp, sp, xp, _ptr(d_x), _ptr(d_w), ws.data_ptr(),
-                                             nb, _raw_stream(dev)), "moe_fp8_linear_backward")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return fp8_linear_backward(d_y, w_t, w_t_scale, fmt, x, input_grad, weight_grad, ws)
+    yp, ys = _rows(d_y, "d_y", dev)
+    wp = _codes(w_t, "w_t", dev)
+    (M, N), K = d_y.shape, w_t.shape[0]
+    if w_t.shape[1] != N:
+        raise ValueError(f"d_y has {N} columns, w_t {w_t.shape[1]}")
+    sp = _typed(w_t_scale, "w_t_scale", torch.float32, (_blocks(K), _blocks(N)), dev)
+    xp, xs = None, 0
+    if weight_grad:
+        if x is None:
+            raise ValueError("x: needed for the weight's gradient")
+        xp, xs = _rows(x, "x", dev)
+        if tuple(x.shape) != (M, K):
+            raise ValueError(f"x: shape {(M, K)} expected, got {tuple(x.shape)}")
+    lin = MoeLinear(M, K, N, fmt, xs, ys)
+    d_x = d_y.new_empty((M, K)) if input_grad else None
+    d_w = d_y.new_empty((N, K)) if weight_grad else None
+    grads = (LINEAR_D_X if input_grad else 0) | (LINEAR_D_W if weight_grad else 0)
+    need = lib().moe_fp8_linear_workspace_bytes(ctypes.byref(lin), grads) if ws is None else 0
+    ws, wsp, nb = _workspace(need, ws, d_y)
+    _check(lib().moe_fp8_linear_backward(ctypes.byref(lin), yp, wp, sp, xp, _ptr(d_x), _ptr(d_w), wsp, nb,
+                                         _raw_stream(dev)), "moe_fp8_linear_backward")
     return d_x, d_w
 
 
@@ -882,66 +900,78 @@ def _tensors(grads, out, write: bool = True):
     """(device, moe_tensor array, count) of a list of gradients; out: None (in place), or where the results go."""
     grads = list(grads)
     dest = grads if out is None else list(out)
-    if len(dest) != len(grads):
-        raise ValueError(f"out: {len(dest)} tensors for {len(grads)}")
-    dev, spans = grads[0].device if grads else None, []
-    arr = (MoeTensor * max(1, len(grads)))()
+    n = len(grads)
+    if len(dest) != n:
+        raise ValueError(f"out: {len(dest)} tensors for {n}")
+    if n == 0:
+        return torch.device("cuda", torch.cuda.current_device()), None, 0
+    dev, spans, flat = grads[0].device, [], []
+    if dev.type != "cuda":
+        raise ValueError("device tensors expected")
+    index = dev.index
     for i, (g, o) in enumerate(zip(grads, dest)):
-        for t, name in ((g, "grads"),) if o is g else ((g, "grads"), (o, "out")):
-            if t.dtype not in _DTYPES or not t.is_contiguous() or t.device != dev or not t.is_cuda:
-                raise ValueError(f"{name}[{i}]: contiguous fp32, bf16 or fp16 tensor on {dev} expected, got {t.dtype} "
-                                 f"{tuple(t.shape)} on {t.device}")
-        if o is not g and (o.dtype != g.dtype or o.shape != g.shape):
-            raise ValueError(f"out[{i}]: {g.dtype} {tuple(g.shape)} expected, got {o.dtype} {tuple(o.shape)}")
-        gp, op, n = g.data_ptr(), o.data_ptr(), g.numel()
-        if write and n:
-            nb = n * g.element_size()
-            spans.append((op, op + nb, True))
-            if op != gp:
-                spans.append((gp, gp + nb, False))
-        arr[i] = MoeTensor(gp, op, n, _DTYPES[g.dtype])
+        kind = _DTYPES.get(g.dtype)
+        if kind is None or g.get_device() != index or not g.is_contiguous():
+            raise ValueError(f"grads[{i}]: contiguous fp32, bf16 or fp16 tensor on {dev} expected, got {g.dtype} "
+                             f"{tuple(g.shape)} on {g.device}")
+        first, size = g.data_ptr(), g.numel()
+        to = first
+        if o is not g:
+            if o.dtype != g.dtype or o.shape != g.shape or o.get_device() != index or not o.is_contiguous():
+                raise ValueError(f"out[{i}]: contiguous {g.dtype} {tuple(g.shape)} on {dev} expected, got {o.dtype} "
+                                 f"{tuple(o.shape)} on {o.device}")
+            to = o.data_ptr()
+        if write and size:
+            nb = size * 4 if kind == 0 else size * 2
+            spans.append((to, to + nb, True))
+            if to != first:
+                spans.append((first, first + nb, False))
+        flat += (first, to, size, kind)
+    spans.sort()
     written = read = 0  # ends of what lies before, in the order of addresses
-    for first, end, writes in sorted(spans):
+    for first, end, writes in spans:
         if first < written or (writes and first < read):
             raise ValueError("grads, out: tensors overlap")
-        written, read = (max(written, end), read) if writes else (written, max(read, end))
-    return dev, arr, len(grads)
+        if writes:
+            written = end
+        elif end > read:
+            read = end
+    # moe_tensor is four 8-byte words (the type in the lower half of the last)
+    return dev, (ctypes.c_int64 * (4 * n))(*flat), n
 
 
-def _device_or_current(dev):
-    return torch.device("cuda", torch.cuda.current_device()) if dev is None else dev
+def _norm_call(grads, out, ws, max_norm):
+    dev, arr, n = _tensors(grads, out, write=max_norm is not None)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return _norm_call(grads, out, ws, max_norm)
+    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    ws, wp, nb = _workspace(lib().moe_grad_norm_workspace_bytes(n) if ws is None else 0, ws, norm)
+    if max_norm is None:
+        _check(lib().moe_grad_norm(arr, n, norm.data_ptr(), wp, nb, _raw_stream(dev)), "moe_grad_norm")
+    else:
+        _check(lib().moe_grad_clip(arr, n, max_norm, norm.data_ptr(), wp, nb, _raw_stream(dev)), "moe_grad_clip")
+    return norm
 
 
 def grad_norm(grads, ws: torch.Tensor | None = None) -> torch.Tensor:
     """moe_grad_norm: the 2-norm over every element of every tensor (fp32, bf16 or
     fp16), as a device tensor [1] fp32."""
-    dev, arr, n = _tensors(grads, None, write=False)
-    dev = _device_or_current(dev)
-    with _On(dev):
-        norm = torch.empty(1, dtype=torch.float32, device=dev)
-        ws, nb = _workspace(lib().moe_grad_norm_workspace_bytes(n), ws, dev)
-        _check(lib().moe_grad_norm(arr, n, norm.data_ptr(), ws.data_ptr(), nb, _raw_stream(dev)), "moe_grad_norm")
-    return norm
+    return _norm_call(grads, None, ws, None)
 
 
 def clip_grads(grads, max_norm: float, out=None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """moe_grad_clip: scales the tensors by max_norm / norm where their common norm
     is larger, in place or into the tensors `out`; returns the norm [1] fp32."""
-    dev, arr, n = _tensors(grads, out)
-    dev = _device_or_current(dev)
-    with _On(dev):
-        norm = torch.empty(1, dtype=torch.float32, device=dev)
-        ws, nb = _workspace(lib().moe_grad_norm_workspace_bytes(n), ws, dev)
-        _check(lib().moe_grad_clip(arr, n, max_norm, norm.data_ptr(), ws.data_ptr(), nb, _raw_stream(dev)),
-               "moe_grad_clip")
-    return norm
+    return _norm_call(grads, out, ws, float(max_norm))
 
 
 def scale_grads(grads, norm: torch.Tensor, max_norm: float, out=None) -> None:
     """moe_grad_scale: the scaling of clip_grads for a norm [1] fp32 on the device (one joined over ranks)."""
     dev, arr, n = _tensors(grads, out)
-    dev = _device_or_current(dev)
-    with _On(dev):
-        if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != dev:
-            raise ValueError(f"norm: one fp32 value on {dev} expected")
-        _check(lib().moe_grad_scale(arr, n, norm.data_ptr(), max_norm, _raw_stream(dev)), "moe_grad_scale")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return scale_grads(grads, norm, max_norm, out)
+    if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != dev:
+        raise ValueError(f"norm: one fp32 value on {dev} expected")
+    _check(lib().moe_grad_scale(arr, n, norm.data_ptr(), max_norm, _raw_stream(dev)), "moe_grad_scale")

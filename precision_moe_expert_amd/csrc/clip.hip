@@ -137,7 +137,7 @@ int64_t clip_chunks(int64_t elems, int dtype) {
 __global__ __launch_bounds__(256) void k_norm_parts(ClipList l, double* __restrict__ parts) {
   __shared__ double sh[4];
   double s = 0.0;
-  for (int at = blockIdx.x; at < l.chunks; at += CLIP_BLOCKS) {
+  for (int at = blockIdx.x; at < l.chunks; at += gridDim.x) {
     const ClipChunk c = clip_chunk(l, at);
     const ClipTensor& t = l.t[c.t];
     if (t.dtype == MOE_DTYPE_F32) s += clip_squares<MOE_DTYPE_F32>(t.p, c.first, c.n);
@@ -170,7 +170,7 @@ __global__ __launch_bounds__(256) void k_clip(ClipList l, const double* __restri
   // not finite: also a norm past fp32's range, which the caller sees as infinite
   const bool clip = n > (double)max_norm && (float)n < INFINITY;
   const float c = clip ? (float)((double)max_norm / n) : 1.0f;
-  for (int at = l.chunks - 1 - blockIdx.x; at >= 0; at -= CLIP_BLOCKS) {
+  for (int at = l.chunks - 1 - (int)blockIdx.x; at >= 0; at -= (int)gridDim.x) {
     const ClipChunk k = clip_chunk(l, at);
     const ClipTensor& t = l.t[k.t];
     if (!clip && t.p == t.out) continue;
@@ -180,8 +180,11 @@ __global__ __launch_bounds__(256) void k_clip(ClipList l, const double* __restri
   }
 }
 
-void launch_norm_parts(const ClipList& l, double* parts, hipStream_t s) {
-  hipLaunchKernelGGL(k_norm_parts, dim3(CLIP_BLOCKS), dim3(256), 0, s, l, parts);
+static int clip_grid(const ClipList& l) { return l.chunks < CLIP_BLOCKS ? l.chunks : CLIP_BLOCKS; }
+
+int launch_norm_parts(const ClipList& l, double* parts, hipStream_t s) {
+  hipLaunchKernelGGL(k_norm_parts, dim3(clip_grid(l)), dim3(256), 0, s, l, parts);
+  return clip_grid(l);
 }
 
 void launch_norm_finish(const double* parts, int nparts, float* norm, hipStream_t s) {
@@ -190,8 +193,7 @@ void launch_norm_finish(const double* parts, int nparts, float* norm, hipStream_
 
 void launch_clip(const ClipList& l, const double* parts, int nparts, float* norm, int write, float max_norm,
                  hipStream_t s) {
-  const int grid = l.chunks < CLIP_BLOCKS ? (l.chunks > 0 ? l.chunks : 1) : CLIP_BLOCKS;
-  hipLaunchKernelGGL(k_clip, dim3(grid), dim3(256), 0, s, l, parts, nparts, norm, write, max_norm);
+  hipLaunchKernelGGL(k_clip, dim3(clip_grid(l)), dim3(256), 0, s, l, parts, nparts, norm, write, max_norm);
 }
 
 }  // namespace moe

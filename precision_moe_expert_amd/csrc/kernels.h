@@ -269,13 +269,13 @@ struct ClipTensor {
   int32_t chunk0;     // chunks of the tensors before it in this launch
 };
 constexpr int CLIP_TENSORS = 80;   // per launch: the list travels as a kernel argument
-constexpr int CLIP_BLOCKS = 1024;  // partial sums per launch
+constexpr int CLIP_BLOCKS = 1024;  // partial sums per launch at most
 struct ClipList {
   ClipTensor t[CLIP_TENSORS];
   int n, chunks;
 };
 int64_t clip_chunks(int64_t elems, int dtype);
-void launch_norm_parts(const ClipList& l, double* parts, hipStream_t s);
+int launch_norm_parts(const ClipList& l, double* parts, hipStream_t s);  // the parts it writes
 void launch_norm_finish(const double* parts, int nparts, float* norm, hipStream_t s);
 // nparts > 0: the norm is formed from the parts (and written by the launch with
 // write != 0), else read

@@ -790,11 +790,11 @@ LinPlan lin_plan(int M, int K, int N, bool backward, bool input_grad, bool weigh
     return at;
   };
   const int C = backward ? N : K, out = backward ? K : N;  // contracted and formed
-  if (!backward || input_grad) {
+  if ((!backward || input_grad) && !lin_is_few(M, (C + 127) / 128)) {
     const int kt = (C + 127) / 128;
     p.q = take((size_t)M * kt * 128);
     p.s = take((size_t)kt * lin_scale_ld(M) * 4);
-    const int sp = lin_is_few(M, kt) ? 1 : lin_choose(M, out, kt).splits;
+    const int sp = lin_choose(M, out, kt).splits;
     p.part = take(sp > 1 ? (size_t)sp * M * out * 4 : 0);
   }
   if (weight_grad) {

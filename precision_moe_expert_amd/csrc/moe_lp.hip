@@ -1459,9 +1459,9 @@ moe_status moe_fp8_linear(const moe_linear* lin, const void* x_bf16, const void*
   const moe_status st = check_linear(lin);
   if (st != MOE_OK) return st;
   if (lin->num_tokens == 0) return MOE_OK;
-  const void* ptrs[] = {x_bf16, w, w_scale, y_bf16, ws};
-  if (!all_aligned16(ptrs)) return MOE_ERR_INVALID_ARGUMENT;
+  const void* ptrs[] = {x_bf16, w, w_scale, y_bf16};
   const LinPlan p = linear_plan(lin, MOE_LINEAR_FORWARD);
+  if (!all_aligned16(ptrs) || !aligned16(ws) || (ws == nullptr && p.total > 0)) return MOE_ERR_INVALID_ARGUMENT;
   if (ws_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   launch_linear(p, static_cast<const uint16_t*>(x_bf16), lin->x_stride ? lin->x_stride : lin->in_features,
                 lin->num_tokens, lin->in_features, lin->out_features, static_cast<const uint8_t*>(w), w_scale,
@@ -1495,13 +1495,13 @@ moe_status moe_fp8_linear_backward(const moe_linear* lin, const void* d_y_bf16, 
     launch_linear_zero(d_w_bf16, (int64_t)N * K * 2, s);
     return launch_status();
   }
-  const void* ptrs[] = {d_y_bf16, ws};
+  const LinPlan p = linear_plan(lin, (d_x_bf16 ? MOE_LINEAR_D_X : 0) | (d_w_bf16 ? MOE_LINEAR_D_W : 0));
+  const void* ptrs[] = {d_y_bf16};
   const void* of_dx[] = {w_t, w_t_scale};
   const void* of_dw[] = {x_bf16};
-  if (!all_aligned16(ptrs) || (d_x_bf16 != nullptr && !all_aligned16(of_dx)) ||
+  if (!all_aligned16(ptrs) || !aligned16(ws) || (ws == nullptr && p.total > 0) || (d_x_bf16 != nullptr && !all_aligned16(of_dx)) ||
       (d_w_bf16 != nullptr && !all_aligned16(of_dw)))
     return MOE_ERR_INVALID_ARGUMENT;
-  const LinPlan p = linear_plan(lin, (d_x_bf16 ? MOE_LINEAR_D_X : 0) | (d_w_bf16 ? MOE_LINEAR_D_W : 0));
   if (ws_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const bool pow2 = lin->wformat == MOE_W_FP8_E4M3_B128_POW2;
   const uint16_t* dy = static_cast<const uint16_t*>(d_y_bf16);
@@ -1564,11 +1564,13 @@ moe_status norm_impl(const moe_tensor* t, int32_t n, float* norm, void* ws, size
   if (st != MOE_OK) return st;
   if (norm == nullptr || !aligned4(norm) || ws == nullptr || !aligned16(ws)) return MOE_ERR_INVALID_ARGUMENT;
   if (clip && !(max_norm >= 0.0f)) return MOE_ERR_INVALID_ARGUMENT;
-  const int lists = list_count(t, n), nparts = lists * CLIP_BLOCKS;
-  if (ws_bytes < moe_grad_norm_workspace_bytes(n) || ws_bytes < (size_t)nparts * 8) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const int lists = list_count(t, n);
+  if (ws_bytes < moe_grad_norm_workspace_bytes(n) || ws_bytes < (size_t)lists * CLIP_BLOCKS * 8)
+    return MOE_ERR_WORKSPACE_TOO_SMALL;
   hipStream_t s = static_cast<hipStream_t>(stream);
   double* parts = static_cast<double*>(ws);
-  for_lists(t, n, [&](const ClipList& l, int i) { launch_norm_parts(l, parts + (size_t)i * CLIP_BLOCKS, s); });
+  int nparts = 0;
+  for_lists(t, n, [&](const ClipList& l, int) { nparts += launch_norm_parts(l, parts + nparts, s); });
   if (clip && lists > 0)
     for_lists(t, n, [&](const ClipList& l, int i) { launch_clip(l, parts, nparts, norm, i == 0, max_norm, s); });
   else

@@ -154,7 +154,9 @@ def test_empty_and_refused():
             bad()
     with pytest.raises(binding.MoeError):
         moe.fp8_linear(x, codes, s, moe.FMT_MXFP4)
+    tiny = torch.empty(64, dtype=torch.uint8, device="cuda")
+    assert torch.equal(moe.fp8_linear(x, codes, s, ws=tiny), moe.fp8_linear(x, codes, s))   # 4 rows need none
     with pytest.raises(binding.MoeError):
-        moe.fp8_linear(x, codes, s, ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        moe.fp8_linear(x.repeat(2, 1), codes, s, ws=tiny)
     with pytest.raises(binding.MoeError):
         moe.fp8_linear_backward(d_y, wt, st, input_grad=False)

@@ -118,6 +118,10 @@ def test_linear_pointers_and_workspace():
         need = L.moe_fp8_linear_workspace_bytes(R(lin), grads)
         assert need > 0 and _bwd(lin, ptrs, need - 1) == SMALL
     assert L.moe_fp8_linear_workspace_bytes(R(lin), 4) == 0 and L.moe_fp8_linear_workspace_bytes(R(lin), -1) == 0
+    few = _linear(M=4)  # quantized on the way: no workspace
+    assert L.moe_fp8_linear_workspace_bytes(R(few), 0) == 0 and L.moe_fp8_linear_workspace_bytes(R(few), 1) == 0
+    assert _fwd(few, {4: FAKE + 8}) == INV and L.moe_fp8_linear_workspace_bytes(R(few), 2) > 0
+    assert _bwd(few, {4: None}, 0) == SMALL and _bwd(few, {4: None, 6: None}, 0) == INV
     none = _linear(M=0)
     assert [L.moe_fp8_linear_workspace_bytes(R(none), g) for g in range(4)] == [0] * 4
     assert _fwd(none, {i: None for i in range(5)}) == OK
