@@ -217,8 +217,8 @@ struct LinTile {
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && NJ * 16 <= 128 && (MI == 2 || MI % 4 == 0), "tile");
   // a stage's scales: 64 rows (256 bytes) by one wave's DMA
   static constexpr int UA = (BM + 63) / 64, UB = (BN + 63) / 64;
-  static_assert(UA + UB <= NW, "a wave for each");
-  static constexpr int NPER = NDA + NDB + 1;
+  static constexpr int NDS = (UA + UB + NW - 1) / NW;
+  static constexpr int NPER = NDA + NDB + NDS;
   static constexpr int STAGE = (BM + BN) * 128 + (UA + UB) * 256;
   static constexpr int LS = BN * 2 + 16;                      // epilogue's row stride
   static constexpr int SMEM = S * STAGE > BM * LS ? S * STAGE : BM * LS;
@@ -296,12 +296,19 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
   const char* pa = reinterpret_cast<const char*>(p.a) + (int64_t)m0 * p.lda;
   const char* pb = reinterpret_cast<const char*>(p.b) + (int64_t)n0 * p.ldb;
   constexpr int OB = C::BM * 128, OSA = OB + C::BN * 128, OSB = OSA + C::UA * 256;
-  // this wave's 64 scales of a stage (waves without any repeat the first ones)
-  const bool of_b = VEC && wave >= C::UA && wave < C::UA + C::UB;
-  const int unit = of_b ? wave - C::UA : wave < C::UA ? wave : 0;
-  const char* psc = reinterpret_cast<const char*>(of_b ? p.sb + (int64_t)k0 * p.sb_ld + n0 : p.sa + (int64_t)k0 * p.sa_ld + m0) + unit * 256;
-  const int64_t sc_ld = (int64_t)(of_b ? p.sb_ld : p.sa_ld) * 4;
-  const uint32_t sc_lds = (of_b ? OSB : OSA) + unit * 256;
+  // this wave's units of 64 scales of a stage (one past the last: the first again)
+  const char* psc[C::NDS];
+  int64_t sc_ld[C::NDS];
+  uint32_t sc_lds[C::NDS];
+#pragma unroll
+  for (int d = 0; d < C::NDS; ++d) {
+    const int u = wave + C::NW * d;
+    const bool of_b = VEC && u >= C::UA && u < C::UA + C::UB;
+    const int unit = of_b ? u - C::UA : u < C::UA ? u : 0;
+    psc[d] = reinterpret_cast<const char*>(of_b ? p.sb + (int64_t)k0 * p.sb_ld + n0 : p.sa + (int64_t)k0 * p.sa_ld + m0) + unit * 256;
+    sc_ld[d] = (int64_t)(of_b ? p.sb_ld : p.sa_ld) * 4;
+    sc_lds[d] = (of_b ? OSB : OSA) + unit * 256;
+  }
   const int part0 = (ds ^ (dr >> 1)) << 4;  // of an even DMA's rows; odd: ^ 64
   // DMA d of stage kt: A's rows, B's, scales.  LAST: B's rows may end within it
   // (what is read instead meets A's zeros).
@@ -319,7 +326,8 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
       }
       lin_dma(pb + at, o, __builtin_amdgcn_readfirstlane(st + OB + (wave * C::NDB + j) * 1024));
     } else {
-      lin_dma4(psc + kt * sc_ld, lane * 4, __builtin_amdgcn_readfirstlane(st + sc_lds));
+      const int u = d - C::NDA - C::NDB;
+      lin_dma4(psc[u] + kt * sc_ld[u], lane * 4, __builtin_amdgcn_readfirstlane(st + sc_lds[u]));
     }
   };
   f32x4 acc[MI][NJ];
