@@ -581,8 +581,8 @@ enum { MOE_LINEAR_FORWARD = 0, MOE_LINEAR_D_X = 1, MOE_LINEAR_D_W = 2 };
 /* Workspace bytes of moe_fp8_linear (grads = MOE_LINEAR_FORWARD) or of
  * moe_fp8_linear_backward (MOE_LINEAR_D_X, MOE_LINEAR_D_W, or both or-ed): the
  * codes and scales of the quantized operands, and parts of the sums (fp32) where
- * there are few tiles.  0 where none is needed (up to 4 rows of x or d_y; ws may
- * then be NULL), and for an invalid or unsupported descriptor. */
+ * there are few tiles.  0 where none is needed (a few rows of x or d_y; ws may then
+ * be NULL), and for an invalid or unsupported descriptor. */
 size_t moe_fp8_linear_workspace_bytes(const moe_linear* lin, int32_t grads);
 
 /* y = Q(x) W^T: x [M][K] bf16 (x_stride), y [M][N] bf16 (contiguous).  The

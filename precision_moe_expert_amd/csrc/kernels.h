@@ -301,7 +301,11 @@ struct LinGemm {
   float* part;            // [splits][m][n]
   int halved;             // last tiles that are done as two halves
 };
+struct LinChoice {
+  int shape, splits, halved;
+};
 struct LinPlan {
+  LinChoice choice, wchoice;  // of y's or d_x's product, of d_w's
   size_t q, s, part, qa, qb, sqa, sqb, wpart, total;  // byte offsets into the workspace
 };
 LinPlan lin_plan(int M, int K, int N, bool backward, bool input_grad, bool weight_grad);

@@ -547,12 +547,13 @@ __global__ __launch_bounds__(C::NT, C::WPS) void k_lin_both(LinGemm a, LinGemm b
 
 // ---- few rows ---------------------------------------------------------------
 
-// Up to LIN_FEW rows: a workgroup takes 16 columns, its NW waves the K blocks in
-// turn; W's fragments come from memory in the layout that the MFMA wants (16 rows
-// of 64 + 64 bytes), U blocks requested before the first is used, while the rows
-// are quantized by each workgroup into LDS: one launch in place of three.  Bound
-// by the stream of W.
-constexpr int LIN_FEW = 4, LIN_FEW_U = 4, LIN_FEW_BYTES = 48 * 1024;
+// Up to 16 rows: a workgroup takes 16 columns, its NW waves the K blocks in turn;
+// W's fragments come from memory in the layout that the MFMA wants (16 rows of 64 +
+// 64 bytes), U blocks requested before the first is used, while the rows are
+// quantized by each workgroup into LDS: one launch in place of two or three.  One
+// row is bound by the stream of W (7168 x 4096 9.0 us, 3.3 TB/s; tiles 16.3), more
+// rows by their quantizing in every workgroup.
+constexpr int LIN_FEW_U = 4;
 template <int NW, bool P2>
 __global__ __launch_bounds__(NW * 64) void k_lin_few(LinGemm p, const uint16_t* __restrict__ x, int64_t x_stride) {
   constexpr int U = LIN_FEW_U;
@@ -673,10 +674,6 @@ inline int lin_tiles(int64_t m, int64_t n, const LinShape& s) {
   return (int)((m + s.bm - 1) / s.bm * ((n + s.bn - 1) / s.bn));
 }
 
-struct LinChoice {
-  int shape, splits, halved;
-};
-
 // The tile and the ways K is split for a product: the least of what the rounds
 // of workgroups cost, and of writing and joining the parts (fp32) where K is
 // split.  A last round of 256 x 256 tiles that would leave half of the CUs idle is
@@ -688,7 +685,7 @@ LinChoice lin_choose(int64_t m, int64_t n, int kt) {
     const LinShape& s = kLinShapes[i];
     const int tiles = lin_tiles(m, n, s), slots = kLinCus * s.per;
     for (int sp = 1; sp <= 16 && (sp == 1 || kt / sp >= 2); ++sp) {
-      if (sp > 1 && (int64_t)sp * m * n * 4 > (64 << 20)) break;
+      if (sp > 1 && ((int64_t)sp * m * n * 4 > (64 << 20) || (int64_t)tiles * (sp - 1) >= 2 * slots)) break;
       const int64_t wgs = (int64_t)tiles * sp, full = wgs / slots;
       const int rem = (int)(wgs - full * slots);
       const float one = (float)((kt + sp - 1) / sp) * s.step + s.rest;
@@ -733,7 +730,14 @@ void lin_product(LinGemm g, const LinChoice& c, bool vec, bool pow2, hipStream_t
   }
 }
 
-inline bool lin_is_few(int64_t m, int kt) { return m <= LIN_FEW && m * kt * 132 <= LIN_FEW_BYTES; }
+// Whether a product is k_lin_few's: what it keeps of the rows has to fit 64 KB of LDS,
+// and at 13 to 16 rows it pays only for short ones (12 x 4096 x 2048 12.5 us, in tiles
+// 14.6; 16 rows 15.0 and 13.3; 16 x 1024 x 1024 4.8 and 7.6; 6 x 7168 x 4096 13.3 and
+// 16.4).
+inline int lin_few_waves(int kt) { return kt > 32 ? 16 : 8; }
+inline bool lin_is_few(int64_t m, int kt) {
+  return m * kt * 132 + lin_few_waves(kt) * 1024 <= 65536 && (m <= 12 || (m <= 16 && m * kt <= 128));
+}
 
 template <int NW>
 void lin_few(const LinGemm& g, const uint16_t* x, int64_t x_stride, bool pow2, hipStream_t s) {
@@ -802,8 +806,8 @@ LinPlan lin_plan(int M, int K, int N, bool backward, bool input_grad, bool weigh
     const int kt = (C + 127) / 128;
     p.q = take((size_t)M * kt * 128);
     p.s = take((size_t)kt * lin_scale_ld(M) * 4);
-    const int sp = lin_choose(M, out, kt).splits;
-    p.part = take(sp > 1 ? (size_t)sp * M * out * 4 : 0);
+    p.choice = lin_choose(M, out, kt);
+    p.part = take(p.choice.splits > 1 ? (size_t)p.choice.splits * M * out * 4 : 0);
   }
   if (weight_grad) {
     const int kt = (M + 127) / 128;
@@ -811,8 +815,8 @@ LinPlan lin_plan(int M, int K, int N, bool backward, bool input_grad, bool weigh
     p.qb = take((size_t)K * kt * 128);
     p.sqa = take((size_t)kt * lin_scale_ld(N) * 4);
     p.sqb = take((size_t)kt * lin_scale_ld(K) * 4);
-    const int sp = lin_choose(N, K, kt).splits;
-    p.wpart = take(sp > 1 ? (size_t)sp * N * K * 4 : 0);
+    p.wchoice = lin_choose(N, K, kt);
+    p.wpart = take(p.wchoice.splits > 1 ? (size_t)p.wchoice.splits * N * K * 4 : 0);
   }
   p.total = o;
   return p;
@@ -864,21 +868,21 @@ LinGemm lin_cols_product(const LinPlan& pl, int M, int K, int N, uint16_t* dw, c
 }
 
 // Quantizes the rows of x [m][kbytes] into the product's A and forms it.
-void lin_forward(const LinGemm& g, const uint16_t* x, int64_t stride, bool pow2, hipStream_t s) {
+void lin_forward(const LinPlan& pl, const LinGemm& g, const uint16_t* x, int64_t stride, bool pow2, hipStream_t s) {
   if (lin_is_few(g.m, g.kt)) {
-    if (g.kt > 32) lin_few<16>(g, x, stride, pow2, s);
+    if (lin_few_waves(g.kt) == 16) lin_few<16>(g, x, stride, pow2, s);
     else lin_few<8>(g, x, stride, pow2, s);
     return;
   }
   lin_rows(x, stride, g.m, g.kbytes, pow2, const_cast<uint8_t*>(g.a), const_cast<float*>(g.sa), g.sa_ld, s);
-  lin_product(g, lin_choose(g.m, g.n, g.kt), false, pow2, s);
+  lin_product(g, pl.choice, false, pow2, s);
 }
 
 }  // namespace
 
 void launch_linear(const LinPlan& pl, const uint16_t* x, int64_t stride, int M, int K, int N, const uint8_t* w,
                    const float* sw, bool pow2, uint16_t* y, char* ws, hipStream_t s) {
-  lin_forward(lin_rows_product(pl, M, K, N, w, sw, y, ws), x, stride, pow2, s);
+  lin_forward(pl, lin_rows_product(pl, M, K, N, w, sw, y, ws), x, stride, pow2, s);
 }
 
 void launch_linear_bwd(const LinPlan& pl, const uint16_t* dy, int64_t dy_stride, const uint8_t* wt, const float* swt,
@@ -892,9 +896,8 @@ void launch_linear_bwd(const LinPlan& pl, const uint16_t* dy, int64_t dy_stride,
     lin_cols(x, x_stride, M, K, pow2, const_cast<uint8_t*>(gw.b), const_cast<float*>(gw.sb), gw.sb_ld, nullptr, nullptr,
              0, s);
   }
-  const LinChoice cw = lin_choose(N, K, gw.kt);
+  const LinChoice &cx = pl.choice, &cw = pl.wchoice;
   if (both) {
-    const LinChoice cx = lin_choose(M, K, gx.kt);
     if (cx.shape == 0 && cx.splits == 1 && cw.shape == 0 && cw.splits == 1) {
       lin_products(gx, gw, pow2, s);
     } else {
@@ -903,7 +906,7 @@ void launch_linear_bwd(const LinPlan& pl, const uint16_t* dy, int64_t dy_stride,
     }
     return;
   }
-  if (dx) lin_forward(gx, dy, dy_stride, pow2, s);
+  if (dx) lin_forward(pl, gx, dy, dy_stride, pow2, s);
   if (dw) lin_product(gw, cw, true, pow2, s);
 }
 

@@ -69,6 +69,14 @@ def test_large(M, K, N, pow2):
     _check(M, K, N, pow2, 1)
 
 
+@pytest.mark.parametrize("M,K,N", [(12, 4096, 48), (13, 4096, 48), (16, 1024, 32), (16, 1040, 32), (6, 7168, 16),
+                                   (7, 7168, 16), (3, 14336, 16), (1, 47104, 16), (1, 131072, 16), (2, 16, 131072)])
+def test_few_rows_of_any_length(M, K, N):
+    """Both sides of what is quantized on the way, up to the longest rows and most columns."""
+    for pow2 in (False, True):
+        _check(M, K, N, pow2, K, dw=K * N < 1 << 20)
+
+
 def test_one_gradient_alone():
     _check(70, 256, 144, False, 3, dx=True, dw=False)
     _check(70, 256, 144, False, 3, dx=False, dw=True)
@@ -157,6 +165,6 @@ def test_empty_and_refused():
     tiny = torch.empty(64, dtype=torch.uint8, device="cuda")
     assert torch.equal(moe.fp8_linear(x, codes, s, ws=tiny), moe.fp8_linear(x, codes, s))   # 4 rows need none
     with pytest.raises(binding.MoeError):
-        moe.fp8_linear(x.repeat(2, 1), codes, s, ws=tiny)
+        moe.fp8_linear(x.repeat(8, 1), codes, s, ws=tiny)
     with pytest.raises(binding.MoeError):
         moe.fp8_linear_backward(d_y, wt, st, input_grad=False)
