@@ -417,7 +417,7 @@ MOE_DEV GateSlot gate_slot(const GateArgs& p, int64_t t, int r, const float* row
   s.there = s.id >= 0 && s.id < p.E;
   s.l = s.there ? row[s.id] : -INFINITY;
   s.in = s.there && !gate_out(s.l) && !(p.bias && gate_out(p.bias[s.id]));
-  s.dw = r < p.k ? p.dw[t * p.k + r] : 0.0f;
+  s.dw = s.in ? p.dw[t * p.k + r] : 0.0f;  // of an absent slot whatever is there has no part
   return s;
 }
 // m, iz: softmax's maximum and the reciprocal of its sum (renormalised: of the
@@ -594,7 +594,7 @@ void launch_gate(const GateArgs& a, hipStream_t s) {
   if (a.T == 0) return;
   const size_t lds = (size_t)(a.E + GATE_MAX_GROUPS) * 8;
   const bool g16 = a.groups == 1 || (a.groups <= 16 && (a.groups & (a.groups - 1)) == 0 && a.E % 16 == 0);
-  if (a.E <= 512 && g16) {
+  if (g16) {
     const dim3 g((a.T + 3) / 4), b(64);
 #define GATE(SL, S)                                                                                        \
   do {                                                                                                     \
@@ -605,7 +605,8 @@ void launch_gate(const GateArgs& a, hipStream_t s) {
     else if (a.E <= 128) GATE(8, 2);
     else if (a.E <= 256) GATE(16, 4);
     else if (a.E <= 384) GATE(24, 6);
-    else GATE(32, 8);
+    else if (a.E <= 512) GATE(32, 8);
+    else GATE(64, 16);
 #undef GATE
     return;
   }
@@ -621,12 +622,13 @@ void launch_gate_bwd(const GateArgs& a, hipStream_t s) {
   if (a.T == 0) return;
   const dim3 g((a.T + 3) / 4), b(64);
 #define GATE(SL) hipLaunchKernelGGL(k_gate_bwd_rows<SL>, g, b, 0, s, a)
-  if (a.E % 4 != 0 || a.E > 512) hipLaunchKernelGGL(k_gate_bwd, g, b, (size_t)a.E * 16, s, a);
+  if (a.E % 4 != 0) hipLaunchKernelGGL(k_gate_bwd, g, b, (size_t)a.E * 16, s, a);
   else if (a.E <= 64) GATE(4);
   else if (a.E <= 128) GATE(8);
   else if (a.E <= 256) GATE(16);
   else if (a.E <= 384) GATE(24);
-  else GATE(32);
+  else if (a.E <= 512) GATE(32);
+  else GATE(64);
 #undef GATE
 }
 

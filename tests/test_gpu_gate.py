@@ -46,7 +46,8 @@ def _check_forward(logits, bias, k, sigmoid=True, groups=1, top=1, top2=True, re
 @pytest.mark.parametrize("T", [1, 5, 1024, 1031])
 @pytest.mark.parametrize("E,k,groups,top", [(256, 8, 8, 4), (256, 8, 1, 1), (384, 6, 1, 1), (72, 4, 8, 3), (8, 8, 2, 2),
                                             (60, 5, 4, 2), (1, 1, 1, 1), (1024, 16, 64, 20), (700, 3, 7, 2),
-                                            (9, 2, 9, 2), (512, 1, 2, 1)])
+                                            (9, 2, 9, 2), (512, 1, 2, 1), (1024, 8, 16, 4), (1000, 16, 1, 1),
+                                            (528, 6, 2, 2), (33, 16, 1, 1), (17, 9, 1, 1)])
 def test_choice_and_weights(T, E, k, groups, top):
     if T > 1000 and E > 400:
         T = 40 if T == 1024 else 1030
@@ -174,7 +175,7 @@ def _check_backward(logits, bias, ids, dw, sigmoid, renorm, scale=2.5, start=Non
 
 
 @pytest.mark.parametrize("T", [1, 6, 64, 1027])
-@pytest.mark.parametrize("E,k", [(256, 8), (384, 8), (60, 5), (1, 1), (1024, 16), (67, 3)])
+@pytest.mark.parametrize("E,k", [(256, 8), (384, 8), (60, 5), (1, 1), (1024, 16), (67, 3), (516, 2), (640, 8)])
 def test_gradient(T, E, k):
     logits, bias, g = _case(T, E, T + E, out=0.1)
     for sigmoid in (True, False):
@@ -201,6 +202,29 @@ def test_gradient_of_odd_rows(sigmoid, renorm):
     got = _check_backward(logits, bias, ids, dw, sigmoid, renorm)
     assert bool((got[1] == 0).all())
     _check_backward(logits, bias, ids, dw, sigmoid, renorm, start=torch.ones(8, 24))
+
+
+@pytest.mark.parametrize("E", [24, 26])
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_nan_in_absent_places(sigmoid, renorm, E):
+    """Gradients and logits that belong to no slot or to an expert that is out."""
+    logits, bias, g = _case(6, E, 11)
+    ids, _ = ref.gate(logits, bias, 4, sigmoid)
+    dw = torch.randn(6, 4, generator=g)
+    ids[0, 1], dw[0, 1] = -1, math.nan
+    ids[1, 3], dw[1, 3] = 1 << 30, INF
+    bias[int(ids[2, 0])] = -INF
+    clean = dw.clone()
+    clean[(ids < 0) | (ids >= E)] = 0.0
+    out = torch.where((ids >= 0) & (ids < E), bias[ids.long().clamp(0, E - 1)] == -INF, False)
+    dw[out] = math.nan
+    clean[out] = 0.0
+    logits[:, bias == -INF] = math.nan
+    layer, gate = _layer(6, E, 4), _gate(sigmoid, 1, 1, True, renorm, 1.0)
+    got = moe.route_gated_backward(layer, gate, logits.cuda(), ids.cuda(), dw.cuda(), bias.cuda()).cpu().double()
+    want, bound = ref.gate_grad(logits, bias, ids, clean, sigmoid, renorm, 1.0)
+    assert bool(((got - want).abs() <= bound).all())
 
 
 def test_gradient_against_differences():
