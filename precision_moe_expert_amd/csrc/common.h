@@ -80,6 +80,8 @@ MOE_DEV float pow2_at_least(float x) {
 MOE_DEV float pow2_reciprocal(float p) { return __uint_as_float((254u - (__float_as_uint(p) >> 23)) << 23); }
 // E8M0 byte (biased exponent) of a power-of-two float.
 MOE_DEV int e8m0_of_pow2(float p) { return (int)((__float_as_uint(p) >> 23) & 0xFFu); }
+// ... and back (0 stands for 2^-127).
+MOE_DEV float pow2_of_e8m0(int e) { return __uint_as_float(e == 0 ? 0x00400000u : (uint32_t)e << 23); }
 
 // silu(g) = g * sigmoid(g); the reciprocal is the hardware one (1 ulp).
 MOE_DEV float silu_f32(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }

@@ -317,6 +317,5 @@ void launch_linear_bwd(const LinPlan& pl, const uint16_t* dy, int64_t dy_stride,
                        const uint16_t* x, int64_t x_stride, int M, int K, int N, bool pow2, uint16_t* dx, uint16_t* dw,
                        char* ws, hipStream_t s);
 void launch_linear_transpose(const uint8_t* w, const float* sc, int N, int K, uint8_t* wt, float* st, hipStream_t s);
-void launch_linear_zero(void* p, int64_t bytes, hipStream_t s);
 
 }  // namespace moe

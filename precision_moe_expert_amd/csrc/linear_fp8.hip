@@ -113,8 +113,9 @@ template <bool P2, bool ROWS>
 __global__ __launch_bounds__(256) void k_lin_cols(const uint16_t* __restrict__ x, int64_t stride, int M, int C, int Mp,
                                                   uint8_t* __restrict__ q, float* __restrict__ sc, int ld,
                                                   uint8_t* __restrict__ rq, float* __restrict__ rs, int rld) {
-  constexpr int LS = 132;  // bytes between a column's codes
-  __shared__ __align__(16) uint8_t codes[128 * LS];
+  // a column's 128 codes, 16-byte piece w at w ^ (column / 8 & 7): a thread's 8-byte
+  // writes and the 16-byte reads both spread over the banks
+  __shared__ __align__(16) uint8_t codes[128 * 128];
   __shared__ float red[4][128];
   const int t0 = blockIdx.y * 128, c0 = blockIdx.x * 128;
   const int cg = threadIdx.x & 15, rr = threadIdx.x >> 4, wave = threadIdx.x >> 6;
@@ -157,18 +158,17 @@ __global__ __launch_bounds__(256) void k_lin_cols(const uint16_t* __restrict__ x
   for (int j = 0; j < 8; ++j) {
     const int c = cg * 8 + j;
     const LinBlock<P2> k(fmaxf(fmaxf(red[0][c], red[1][c]), fmaxf(red[2][c], red[3][c])));
-    uint32_t* o = reinterpret_cast<uint32_t*>(codes + c * LS + rr * 8);
-    o[0] = k.codes(at(0, j), at(1, j), at(2, j), at(3, j));
-    o[1] = k.codes(at(4, j), at(5, j), at(6, j), at(7, j));
+    *reinterpret_cast<u32x2*>(codes + c * 128 + (((rr >> 1) ^ (cg & 7)) << 4) + (rr & 1) * 8) =
+        (u32x2){k.codes(at(0, j), at(1, j), at(2, j), at(3, j)), k.codes(at(4, j), at(5, j), at(6, j), at(7, j))};
     if (rr == 0 && in) sc[(int64_t)blockIdx.y * ld + c0 + c] = k.s;
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {  // 4-byte pieces: 32 per column
-    const int p = threadIdx.x + i * 256, c = p >> 5, w = p & 31;
+  for (int i = 0; i < 4; ++i) {
+    const int p = threadIdx.x + i * 256, c = p >> 3, w = p & 7;
     if (c0 + c < C)
-      *reinterpret_cast<uint32_t*>(q + (int64_t)(c0 + c) * Mp + t0 + w * 4) =
-          *reinterpret_cast<const uint32_t*>(codes + c * LS + w * 4);
+      *reinterpret_cast<u32x4*>(q + (int64_t)(c0 + c) * Mp + t0 + w * 16) =
+          *reinterpret_cast<const u32x4*>(codes + c * 128 + ((w ^ ((c >> 3) & 7)) << 4));
   }
 }
 
@@ -222,7 +222,7 @@ struct LinTile {
   static constexpr int STAGE = (BM + BN) * 128 + (UA + UB) * 256;
   static constexpr int LS = BN * 2 + 16;                      // epilogue's row stride
   static constexpr int SMEM = S * STAGE > BM * LS ? S * STAGE : BM * LS;
-  static_assert(SMEM <= 160 * 1024, "LDS");
+  static_assert(SMEM <= 160 * 1024 && BN <= 256, "LDS; two blocks of scales at most");
   // what the tiles of a last round may be done with
   using Half = std::conditional_t<BM == 256, LinTile<BM_ / 2, BN_, WM_, WN_, 3, WPS_>, LinTile>;
 };
@@ -335,10 +335,16 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  // W's scales of the tile's column blocks, on their way before the stages are
+  // requested and put into LDS after
+  constexpr int NSW = NB * LIN_MAX_KT / C::NT > 4 ? 4 : NB * LIN_MAX_KT / C::NT;
+  float swr[NSW];
+  const float* swp0 = VEC ? nullptr : p.sb + (int64_t)(n0 / 128) * p.sb_ld + k0;
+  const int64_t sw_next = min(1, (p.n - 1) / 128 - n0 / 128) * (int64_t)p.sb_ld;  // to the second block's, if there is one
+  auto sw_at = [&](int i) { return i < KT ? swp0[i] : swp0[sw_next + i - KT]; };
   if constexpr (!VEC) {
-    // W's scales of the tile's column blocks
-    for (int i = threadIdx.x; i < NB * KT; i += C::NT)
-      sws[i / KT * LIN_MAX_KT + i % KT] = p.sb[(int64_t)min(n0 / 128 + i / KT, (p.n - 1) / 128) * p.sb_ld + k0 + i % KT];
+#pragma unroll
+    for (int q = 0; q < NSW; ++q) swr[q] = sw_at(min((int)threadIdx.x + q * C::NT, NB * KT - 1));
   }
   // of the stage that is S - 1 ahead, the first DMAs are requested as soon as its
   // place is free, the others with the row blocks that follow
@@ -350,6 +356,14 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
 #pragma unroll
       for (int d = 0; d < (s + 1 < S ? NPER : FIRST); ++d) issue1(std::true_type(), d, s, s);
 
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int q = 0; q < NSW; ++q) {
+      const int i = threadIdx.x + q * C::NT;
+      if (i < NB * KT) sws[i < KT ? i : LIN_MAX_KT + i - KT] = swr[q];
+    }
+    for (int i = threadIdx.x + NSW * C::NT; i < NB * KT; i += C::NT) sws[i < KT ? i : LIN_MAX_KT + i - KT] = sw_at(i);
+  }
   const int swz = (ln >> 1) & 7;
   const int f0 = ln * 128 + ((lg ^ swz) << 4), f1 = ln * 128 + (((lg + 4) ^ swz) << 4);
   auto frag = [&](const uint8_t* base) {
@@ -571,7 +585,8 @@ __global__ __launch_bounds__(NW * 64) void k_lin_few(LinGemm p, const uint16_t* 
     const int at = kb * 128, left = p.kbytes - at;          // past the end: the block's first bytes (A has zeros)
     w[u][0] = *reinterpret_cast<const u32x4*>(wrow + at + (lg * 16 < left ? lg * 16 : 0));
     w[u][1] = *reinterpret_cast<const u32x4*>(wrow + at + (64 + lg * 16 < left ? 64 + lg * 16 : 0));
-    sw[u] = ws[kb];
+    // powers of two as the block-scaled MFMA of the tiles takes them: the exponent alone
+    sw[u] = P2 ? pow2_of_e8m0(e8m0_of_pow2(ws[kb])) : ws[kb];
   };
 #pragma unroll
   for (int u = 0; u < U; ++u) load_w(u, wave + u * NW);
@@ -641,10 +656,6 @@ __global__ __launch_bounds__(256) void k_lin_join(const float* __restrict__ part
   }
   const u32x2 o = {bf16x2_bits(s[0], s[1]), bf16x2_bits(s[2], s[3])};
   *reinterpret_cast<u32x2*>(out + i / n * ldo + i % n) = o;
-}
-
-__global__ __launch_bounds__(256) void k_lin_zero(uint32_t* __restrict__ p, int64_t n) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
 }
 
 // ---- host -------------------------------------------------------------------
@@ -914,11 +925,6 @@ void launch_linear_transpose(const uint8_t* w, const float* sc, int N, int K, ui
   hipLaunchKernelGGL(k_lin_transpose, dim3((K + 63) / 64, (N + 63) / 64), dim3(256), 0, s, w, N, K, wt);
   const int nb = (N + 127) / 128, kb = (K + 127) / 128;
   hipLaunchKernelGGL(k_lin_transpose_scales, dim3((nb * kb + 255) / 256), dim3(256), 0, s, sc, nb, kb, st);
-}
-
-void launch_linear_zero(void* p, int64_t bytes, hipStream_t s) {
-  const int64_t n = bytes / 4, b = (n + 255) / 256;
-  if (n > 0) hipLaunchKernelGGL(k_lin_zero, dim3((unsigned)(b < 4096 ? b : 4096)), dim3(256), 0, s, static_cast<uint32_t*>(p), n);
 }
 
 }  // namespace moe

@@ -1492,7 +1492,7 @@ moe_status moe_fp8_linear_backward(const moe_linear* lin, const void* d_y_bf16, 
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (M == 0) {
     if (d_w_bf16 == nullptr) return MOE_OK;
-    launch_linear_zero(d_w_bf16, (int64_t)N * K * 2, s);
+    launch_zero_f32(static_cast<float*>(d_w_bf16), (int64_t)N * K / 2, s);  // N K is even
     return launch_status();
   }
   const LinPlan p = linear_plan(lin, (d_x_bf16 ? MOE_LINEAR_D_X : 0) | (d_w_bf16 ? MOE_LINEAR_D_W : 0));
