@@ -366,7 +366,7 @@ __global__ __launch_bounds__(64) void k_gate(GateArgs p) {
     uint64_t k64 = 0;
     if (r < among && sure) {
       const float l = row[mine];
-      const double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)m);
+      const double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : l == m ? 1.0 : exp((double)l - (double)m);
       k64 = gate_key(p.bias ? s + (double)p.bias[mine] : s, false, mine);
     }
     int rank = 0, chosen = 0;
@@ -384,7 +384,7 @@ __global__ __launch_bounds__(64) void k_gate(GateArgs p) {
     double s = 0.0;
     if (r < p.k) {
       const float l = row[mine];
-      s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)m);
+      s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : l == m ? 1.0 : exp((double)l - (double)m);
     }
     const double tot = p.renorm ? gate_sum<16>(s) : (double)z;
     if (r < p.k) {

@@ -104,6 +104,18 @@ def test_far_logits(T):
     _check_forward(logits, big, 5, True, groups=4, top=2)
 
 
+@pytest.mark.parametrize("k", [1, 2, 3])
+def test_infinite_logits(k):
+    """One, two and three experts with all of a token's softmax, as many as are chosen or fewer."""
+    for E, groups in ((32, 1), (256, 4), (30, 3)):
+        logits = torch.randn(9, E, generator=torch.Generator().manual_seed(E + k))
+        for t, at in ((1, [3]), (2, [3, 9]), (4, [0, 1, E - 1])):
+            logits[t, at] = INF
+        for sigmoid in (True, False):
+            for renorm in (True, False):
+                _check_forward(logits, None, k, sigmoid, groups, groups, True, renorm)
+
+
 @pytest.mark.parametrize("T", [3, 260])
 @pytest.mark.parametrize("groups,top", [(1, 1), (4, 2), (3, 2)])
 def test_values_closer_than_fp32(T, groups, top):
