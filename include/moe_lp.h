@@ -538,7 +538,8 @@ moe_status moe_route_gated(const moe_layer* layer, const moe_gate* gate, const f
  *   softmax: d_logits[t][e] = s_e (ds_e - sum_j ds_j s_j)
  * (ds_e = 0 for experts not chosen).  Ids outside [0, E) have no part; an id that
  * a token has twice takes both gradients.  The bias has no gradient.  d_logits:
- * [T][E] fp32, written, or with accumulate != 0 added to what it holds. */
+ * [T][E] fp32 (over no input), written, or with accumulate != 0 added to what it
+ * holds. */
 moe_status moe_route_gated_backward(const moe_layer* layer, const moe_gate* gate, const float* logits,
                                     const float* bias, const int32_t* topk_ids, const float* d_topk_w,
                                     int32_t accumulate, float* d_logits, void* stream);
@@ -565,7 +566,9 @@ moe_status moe_expert_backward_gated(const moe_layer* layer, const moe_gate* gat
  * 128 x 128, [ceil(N/128)][ceil(K/128)] (the last blocks may be smaller), and
  * activations quantized per 128 columns of a row as moe_quantize_activations
  * does (MOE_W_FP8_E4M3_B128, or MOE_W_FP8_E4M3_B128_POW2 with powers of two on
- * both sides).  A workspace serves one call at a time. */
+ * both sides, of which the exponent alone is used).  A NaN or an infinity in x makes
+ * its whole row of y NaN, one in d_y its row of d_x and its column's row of d_w.
+ * Results lie over no input.  A workspace serves one call at a time. */
 typedef struct {
   int32_t num_tokens;   /* M: 0..2^20                                              */
   int32_t in_features;  /* K: multiple of 16, at most 2^17                         */
@@ -633,12 +636,12 @@ moe_status moe_grad_norm(const moe_tensor* tensors, int32_t n, float* norm, void
  * max_norm, else out = data (nothing is written in place).  A norm that is not
  * finite in fp32 clips nothing: the caller sees it and leaves the step out.
  * max_norm >= 0.
- * The tensors must not overlap. */
+ * The tensors, norm and ws must not overlap. */
 moe_status moe_grad_clip(const moe_tensor* tensors, int32_t n, float max_norm, float* norm, void* ws,
                          size_t ws_bytes, void* stream);
 
 /* The second half alone, for a norm [1] that the caller holds on the device (one
- * joined over ranks). */
+ * joined over ranks); norm lies outside the tensors. */
 moe_status moe_grad_scale(const moe_tensor* tensors, int32_t n, const float* norm, float max_norm, void* stream);
 
 /* ---- Allocation-free forward -------------------------------------------

@@ -817,6 +817,18 @@ def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
+def _apart(out, inputs):
+    """Refuses a result that lies over an input: workgroups still read the input while others write."""
+    first = out.data_ptr()
+    end = first + out.numel() * out.element_size()
+    for t in inputs:
+        if t.numel() and out.numel():
+            a = t.data_ptr()
+            last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+            if first < a + (last + 1) * t.element_size() and a < end:
+                raise ValueError("out: overlaps an input")
+
+
 def fp8_linear_workspace_bytes(M: int, K: int, N: int, grads: int = LINEAR_FORWARD) -> int:
     """Workspace of fp8_linear, or of fp8_linear_backward for LINEAR_D_X, LINEAR_D_W or both or-ed."""
     return lib().moe_fp8_linear_workspace_bytes(ctypes.byref(MoeLinear(M, K, N, FMT_FP8, 0, 0)), grads)
@@ -839,6 +851,8 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, fmt: int
     lin = MoeLinear(M, K, N, fmt, xs, 0)
     if out is None:
         out = x.new_empty((M, N))
+    else:
+        _apart(out, (x, w, w_scale))
     op = _typed(out, "out", torch.bfloat16, (M, N), dev)
     need = lib().moe_fp8_linear_workspace_bytes(ctypes.byref(lin), LINEAR_FORWARD) if ws is None else 0
     ws, wsp, nb = _workspace(need, ws, x)
@@ -974,4 +988,8 @@ def scale_grads(grads, norm: torch.Tensor, max_norm: float, out=None) -> None:
             return scale_grads(grads, norm, max_norm, out)
     if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != dev:
         raise ValueError(f"norm: one fp32 value on {dev} expected")
+    at = norm.data_ptr()
+    if n and any(size and to - 4 < at < to + size * (4 if kind == 0 else 2)
+                 for to, size, kind in zip(arr[1::4], arr[2::4], arr[3::4])):
+        raise ValueError("norm: lies in a tensor that is written")
     _check(lib().moe_grad_scale(arr, n, norm.data_ptr(), max_norm, _raw_stream(dev)), "moe_grad_scale")

@@ -43,8 +43,8 @@ MOE_DEV float lin_bf16(uint32_t w, int odd) { return odd ? __uint_as_float(w & 0
 // The quotient x / s, rounded once to fp32, by one multiplication and one
 // correction, q = x r, q + r (x - q s), with r = 1 / s: the same bits as the
 // division for all 16384 pairs of bf16 mantissas of x and the block's largest
-// (checked one by one; without the correction 1 code in 2750 differs).  Exact
-// remainders need s above 2^-90; below, it is divided.  |x| <= amax, so no quotient
+// (checked one by one; without the correction 1 code in 2750 differs).  With s below
+// 2^-90 the remainder would come near fp32's smallest numbers; there it is divided.  |x| <= amax, so no quotient
 // is past e4m3's largest.
 template <bool P2>
 struct LinBlock {

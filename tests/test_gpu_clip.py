@@ -112,6 +112,28 @@ def test_a_norm_that_is_not_finite_clips_nothing(bad):
     assert torch.equal(outs[0], before[0]) and torch.equal(outs[2], before[2])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_copies_of_what_is_not_clipped(dtype):
+    t = torch.randn(999, device="cuda").to(dtype)
+    t[::7] = math.nan
+    t[3], t[990] = math.inf, -math.inf
+    out = torch.zeros_like(t)
+    moe.clip_grads([t], 1.0, out=[out])
+    assert bool((out.isnan() == t.isnan()).all()) and torch.equal(out[~t.isnan()], t[~t.isnan()])
+
+
+def test_a_norm_among_the_tensors_is_refused():
+    flat = torch.ones(64, device="cuda")
+    with pytest.raises(ValueError):
+        moe.scale_grads([flat[:32]], flat[5:6], 1.0)
+    with pytest.raises(ValueError):
+        moe.scale_grads([flat[:32]], flat[40:41], 1.0, out=[flat[32:]])
+    moe.scale_grads([flat[:32]], flat[40:41], 0.5)
+    moe.scale_grads([], flat[40:41], 0.5)
+    moe.scale_grads([flat[40:40]], flat[40:41], 0.5)
+    assert bool((flat[:32] == 0.5).all()) and bool((flat[32:] == 1).all())
+
+
 def test_same_norm_in_every_run():
     grads = _grads([1_000_003, 77, 250_000], 6)
     norms = {float(moe.grad_norm(grads)) for _ in range(5)}

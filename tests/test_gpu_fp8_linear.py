@@ -130,6 +130,47 @@ def test_values_at_the_quantizers_borders():
         _near(moe.fp8_linear(xb, codes, s, FMT[pow2]), y, bound + 4 * 2.0 ** -126)
 
 
+@pytest.mark.parametrize("M", [3, 300])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_values_that_are_not_finite(M, pow2):
+    """A NaN or an infinity reaches its own row of the result (its own column's gradients) and no other."""
+    K, N = 400, 144
+    x, codes, s, d_y = _inputs(M, K, N, pow2, 8)
+    codes = codes.clamp_min(1)
+    wt, st = moe.fp8_linear_transpose(codes, s)
+    want = moe.fp8_linear(x, codes, s, FMT[pow2])
+    d_x, d_w = moe.fp8_linear_backward(d_y, wt, st, FMT[pow2], x=x, weight_grad=True)
+    x, d_y = x.clone(), d_y.clone()
+    x[1, 399] = float("nan")
+    x[2, 5] = float("inf")
+    d_y[1, 7] = -float("inf")
+    y = moe.fp8_linear(x, codes, s, FMT[pow2])
+    bad = torch.zeros(M, dtype=torch.bool, device="cuda")
+    bad[1:3] = True
+    assert not bool(y[bad].isfinite().any()) and torch.equal(y[~bad], want[~bad])
+    a, b = moe.fp8_linear_backward(d_y, wt, st, FMT[pow2], x=x, weight_grad=True)
+    bad[2] = False
+    assert not bool(a[bad].isfinite().any()) and torch.equal(a[~bad], d_x[~bad])
+    rows, cols = torch.ones(N, dtype=torch.bool, device="cuda"), torch.ones(K, dtype=torch.bool, device="cuda")
+    rows[7] = False
+    cols[[5, 399]] = False
+    assert torch.equal(b[rows][:, cols], d_w[rows][:, cols])
+    assert not bool(b[7].isfinite().any()) and not bool(b[:, ~cols].isfinite().any())
+
+
+def test_an_output_over_an_input_is_refused():
+    x, codes, s, _ = _inputs(40, 256, 256, False, 4)
+    flat = torch.empty(3 * 40 * 256, dtype=torch.bfloat16, device="cuda")
+    y, part = flat[:40 * 256].view(40, 256), flat[256:].view(torch.bfloat16)[:40 * 256].view(40, 256)
+    with pytest.raises(ValueError):
+        moe.fp8_linear(x, codes, s, out=x)
+    with pytest.raises(ValueError):
+        moe.fp8_linear(y.copy_(x), codes, s, out=part)
+    with pytest.raises(ValueError):
+        moe.fp8_linear(x, codes, s, out=codes.view(torch.bfloat16).reshape(-1)[:40 * 256].view(40, 256))
+    moe.fp8_linear(y, codes, s, out=flat[40 * 256:2 * 40 * 256].view(40, 256))      # side by side is fine
+
+
 def test_gradient_against_differences():
     """Where the quantizers are exact (codes times one power of two) the projection is linear."""
     M, K, N = 40, 256, 128

@@ -1,4 +1,6 @@
 """The 64-bit references against differences and against each other."""
+from fractions import Fraction
+
 import torch
 
 from tests import layer_ref as ref
@@ -58,3 +60,26 @@ def test_power_of_two_scale_is_the_smallest_at_or_above():
     s = ref.block_scale(a, True)
     assert s[0] == 1 and s[1] == 1 and s[2] == 2
     assert bool((s[1:].double() * 448 >= a[1:].double() * (1 - 1e-7)).all()) and bool((s[1:].double() * 224 < a[1:]).all())
+
+
+def _fp32(v):
+    """A positive fraction rounded to fp32 (nearest even)."""
+    e = v.numerator.bit_length() - v.denominator.bit_length() - 24
+    e += (v / Fraction(2) ** e >= 1 << 24) - (v / Fraction(2) ** e < 1 << 23)
+    return round(v / Fraction(2) ** e) * Fraction(2) ** e      # 24 bits kept; round() takes ties to even
+
+
+def test_a_product_and_a_correction_are_the_quotient():
+    """q = x r, q + r (x - q s) with r = 1 / s is x / s rounded once, for every pair of bf16 mantissas of x and of the
+    largest of its block (other exponents shift both alike)."""
+    wrong = 0
+    for top in range(128, 256):
+        s = _fp32(Fraction(top, 448))
+        r = _fp32(1 / s)
+        for x in range(128, 256):
+            q = _fp32(x * r)
+            e = x - q * s
+            e = _fp32(e) if e > 0 else -_fp32(-e) if e < 0 else 0     # one rounding, as of a fused operation
+            assert _fp32(q + r * e) == _fp32(x / s)
+            wrong += q != _fp32(x / s)
+    assert wrong > 0                                                  # the product alone is not
