@@ -643,6 +643,89 @@ __global__ __launch_bounds__(NW * 64) void k_lin_few(LinGemm p, const uint16_t* 
   }
 }
 
+// ---- rows of a batch of single tokens ----------------------------------------
+
+// Up to 16 MF rows, quantized before: a workgroup takes 16 NC columns, its NW waves
+// the K blocks in turn, every fragment straight from memory (the rows' codes from
+// the L2), U blocks requested ahead.  No barrier and no LDS but for the waves' sums:
+// what a tile's ring costs to fill is most of such a call (16 x 2048 x 7168: product
+// 4.5 us in place of 6; W alone 3).
+template <int NW, int MF, int NC, int U, bool P2>
+__global__ __launch_bounds__(NW * 64) void k_lin_batch(LinGemm p) {
+  __shared__ f32x4 sums[NW][MF * NC][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int ln = lane & 15, lg = lane >> 4;
+  const int n0 = blockIdx.x * 16 * NC, KT = p.kt;
+  const uint8_t *wrow[NC], *arow[MF];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) wrow[c] = p.b + (int64_t)min(n0 + c * 16 + ln, p.n - 1) * p.ldb;
+#pragma unroll
+  for (int i = 0; i < MF; ++i) arow[i] = p.a + (int64_t)min(i * 16 + ln, p.m - 1) * p.lda + lg * 16;
+  const float* ws = p.sb + (int64_t)(n0 / 128) * p.sb_ld;
+  u32x4 w[U][NC][2], a[U][MF][2];
+  float sw[U], sa[U][MF];
+  auto load = [&](int u, int kb) {
+    if (kb >= KT) return;                                   // the whole wave
+    const int at = kb * 128, left = p.kbytes - at;          // past the end: the block's first bytes (A has zeros)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      w[u][c][0] = *reinterpret_cast<const u32x4*>(wrow[c] + at + (lg * 16 < left ? lg * 16 : 0));
+      w[u][c][1] = *reinterpret_cast<const u32x4*>(wrow[c] + at + (64 + lg * 16 < left ? 64 + lg * 16 : 0));
+    }
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      a[u][i][0] = *reinterpret_cast<const u32x4*>(arow[i] + at);
+      a[u][i][1] = *reinterpret_cast<const u32x4*>(arow[i] + at + 64);
+      sa[u][i] = p.sa[(int64_t)kb * p.sa_ld + i * 16 + ln];              // rows past the last are not stored
+    }
+    sw[u] = P2 ? pow2_of_e8m0(e8m0_of_pow2(ws[kb])) : ws[kb];
+  };
+  auto whole = [](const u32x4 (&v)[2]) {
+    return (i32x8){(int)v[0].x, (int)v[0].y, (int)v[0].z, (int)v[0].w, (int)v[1].x, (int)v[1].y, (int)v[1].z, (int)v[1].w};
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u, wave + u * NW);
+  f32x4 acc[MF][NC];
+#pragma unroll
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[i][c] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k0 = wave; k0 < KT; k0 += NW * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = k0 + u * NW;
+      if (kb < KT) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          const float s = sw[u] * sa[u][i];
+          const i32x8 af = whole(a[u][i]);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const f32x4 part = mfma_fp8_16x16x128(whole(w[u][c]), af, (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[i][c][q] = fmaf(part[q], s, acc[i][c][q]);
+          }
+        }
+        load(u, kb + NW * U);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) sums[wave][i * NC + c][lane] = acc[i][c];
+  __syncthreads();
+  // the waves' sums in their order
+  for (int at = wave; at < MF * NC; at += NW) {
+    f32x4 s = sums[0][at][lane];
+#pragma unroll
+    for (int v = 1; v < NW; ++v) s += sums[v][at][lane];
+    const int m = at / NC * 16 + ln, n = n0 + at % NC * 16 + lg * 4;
+    if (m < p.m && n < p.n)
+      *reinterpret_cast<u32x2*>(p.out + (int64_t)m * p.ldo + n) = (u32x2){bf16x2_bits(s[0], s[1]), bf16x2_bits(s[2], s[3])};
+  }
+}
+
 // Sum of the splits' parts, in their order, rounded to bf16.
 __global__ __launch_bounds__(256) void k_lin_join(const float* __restrict__ part, int splits, int64_t mn, int n,
                                                   int64_t ldo, uint16_t* __restrict__ out) {
@@ -724,6 +807,20 @@ void lin_launch(const LinGemm& g, bool vec, bool pow2, hipStream_t s) {
   else hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, false, false>), grid, b, 0, s, g);
 }
 
+// Whether a product of quantized rows is k_lin_batch's, on top of lin_is_few's (16 rows
+// 2048 x 7168 8.9 us, in tiles 10.5; 7168 x 4096 13.8 and 16.9; 32 rows 4096 x 2048
+// 11.6 and 13.3, 1024 x 1024 6.4 and 8.1; 7168 x 576 15.2 and 13.4: long rows of
+// codes come from the L2 again for every 16 columns).
+constexpr int LIN_BATCH = kLinShapeCount;  // of LinChoice
+inline bool lin_is_batch(int64_t m, int kt) { return m <= 16 || (m <= 32 && kt <= 32); }
+
+template <int MF, int NC>
+void lin_batch(const LinGemm& g, bool pow2, hipStream_t s) {
+  const dim3 grid((g.n + 16 * NC - 1) / (16 * NC)), b(512);
+  if (pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin_batch<8, MF, NC, 2, true>), grid, b, 0, s, g);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin_batch<8, MF, NC, 2, false>), grid, b, 0, s, g);
+}
+
 void lin_product(LinGemm g, const LinChoice& c, bool vec, bool pow2, hipStream_t s) {
   g.splits = c.splits;
   g.halved = c.halved;
@@ -732,7 +829,12 @@ void lin_product(LinGemm g, const LinChoice& c, bool vec, bool pow2, hipStream_t
     case 1: lin_launch<LinT1>(g, vec, pow2, s); break;
     case 2: lin_launch<LinT2>(g, vec, pow2, s); break;
     case 3: lin_launch<LinT3>(g, vec, pow2, s); break;
-    default: lin_launch<LinT4>(g, vec, pow2, s); break;
+    case 4: lin_launch<LinT4>(g, vec, pow2, s); break;
+    default:  // LIN_BATCH; 32 columns where 16 would make more than a workgroup per CU
+      if (g.m <= 16 && g.n <= 16 * kLinCus) lin_batch<1, 1>(g, pow2, s);
+      else if (g.m <= 16) lin_batch<1, 2>(g, pow2, s);
+      else if (g.n <= 16 * kLinCus) lin_batch<2, 1>(g, pow2, s);
+      else lin_batch<2, 2>(g, pow2, s);
   }
   if (g.splits > 1) {
     const int64_t mn = (int64_t)g.m * g.n;
@@ -741,13 +843,13 @@ void lin_product(LinGemm g, const LinChoice& c, bool vec, bool pow2, hipStream_t
   }
 }
 
-// Whether a product is k_lin_few's: what it keeps of the rows has to fit 64 KB of LDS,
-// and at 13 to 16 rows it pays only for short ones (12 x 4096 x 2048 12.5 us, in tiles
-// 14.6; 16 rows 15.0 and 13.3; 16 x 1024 x 1024 4.8 and 7.6; 6 x 7168 x 4096 13.3 and
-// 16.4).
+// Whether a product is k_lin_few's, which quantizes the rows in every workgroup and so
+// pays for few and short ones (10 rows 2048 x 7168 9.1 us, with a launch that
+// quantizes them first 9.1, 12 rows 10.1 and 9.2; 4 and 8 rows 4096 x 2048 7.1 and 8.2,
+// 9.6 and 8.6; 3 and 6 rows 7168 x 4096 10.9 and 12.3, 12.5 and 11.8).
 inline int lin_few_waves(int kt) { return kt > 32 ? 16 : 8; }
 inline bool lin_is_few(int64_t m, int kt) {
-  return m * kt * 132 + lin_few_waves(kt) * 1024 <= 65536 && (m <= 12 || (m <= 16 && m * kt <= 128));
+  return m <= 16 && (m == 1 ? kt * 132 + 16384 <= 65536 : m * kt <= 176);
 }
 
 template <int NW>
@@ -817,7 +919,7 @@ LinPlan lin_plan(int M, int K, int N, bool backward, bool input_grad, bool weigh
     const int kt = (C + 127) / 128;
     p.q = take((size_t)M * kt * 128);
     p.s = take((size_t)kt * lin_scale_ld(M) * 4);
-    p.choice = lin_choose(M, out, kt);
+    p.choice = lin_is_batch(M, kt) ? LinChoice{LIN_BATCH, 1, 0} : lin_choose(M, out, kt);
     p.part = take(p.choice.splits > 1 ? (size_t)p.choice.splits * M * out * 4 : 0);
   }
   if (weight_grad) {

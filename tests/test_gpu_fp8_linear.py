@@ -77,6 +77,13 @@ def test_few_rows_of_any_length(M, K, N):
         _check(M, K, N, pow2, K, dw=K * N < 1 << 20)
 
 
+@pytest.mark.parametrize("M", [2, 3, 7, 11, 12, 16, 17, 32, 33])
+@pytest.mark.parametrize("K,N", [(2048, 1040), (1040, 4112), (4352, 272), (144, 128), (7168, 80)])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_batches_of_single_tokens(M, K, N, pow2):
+    _check(M, K, N, pow2, M + K, dw=M == 17)
+
+
 def test_one_gradient_alone():
     _check(70, 256, 144, False, 3, dx=True, dw=False)
     _check(70, 256, 144, False, 3, dx=False, dw=True)
