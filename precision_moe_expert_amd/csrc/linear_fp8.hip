@@ -210,11 +210,12 @@ __global__ __launch_bounds__(256) void k_lin_transpose_scales(const float* __res
 
 namespace {
 
-// BM x BN per workgroup of WM x WN waves, S stages of 128 K in LDS.
-template <int BM_, int BN_, int WM_, int WN_, int S_, int WPS_>
+// BM x BN per workgroup of G groups of WM x WN waves, which share the K blocks; S
+// stages of 128 K per group in LDS.
+template <int BM_, int BN_, int WM_, int WN_, int S_, int WPS_, int G_ = 1>
 struct LinTile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, WPS = WPS_;
-  static constexpr int NW = WM * WN, NT = NW * 64;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, WPS = WPS_, G = G_;
+  static constexpr int NW = WM * WN, NT = G * NW * 64;        // waves of a group, threads
   static constexpr int MI = BM / WM / 16, NJ = BN / WN / 16;
   static constexpr int NDA = BM / 8 / NW, NDB = BN / 8 / NW;  // DMAs per wave and stage, 8 rows each
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && NJ * 16 <= 128 && (MI == 2 || MI % 4 == 0), "tile");
@@ -224,7 +225,8 @@ struct LinTile {
   static constexpr int NPER = NDA + NDB + NDS;
   static constexpr int STAGE = (BM + BN) * 128 + (UA + UB) * 256;
   static constexpr int LS = BN * 2 + 16;                      // epilogue's row stride
-  static constexpr int SMEM = S * STAGE > BM * LS ? S * STAGE : BM * LS;
+  static constexpr int SUMS = (G - 1) * BM * BN * 4;          // the groups' sums but the first's
+  static constexpr int SMEM = G * S * STAGE > SUMS + BM * LS ? G * S * STAGE : SUMS + BM * LS;
   static_assert(SMEM <= 160 * 1024 && BN <= 256, "LDS; two blocks of scales at most");
   // what the tiles of a last round may be done with
   using Half = std::conditional_t<BM == 256, LinTile<BM_ / 2, BN_, WM_, WN_, 3, WPS_>, LinTile>;
@@ -283,12 +285,18 @@ template <class C, bool VEC, bool P2>
 MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, float* sws) {
   constexpr int MI = C::MI, NJ = C::NJ, S = C::S, NPER = C::NPER;
   constexpr int NB = (C::BN + 127) / 128;
-  const int k0 = (int)((int64_t)p.kt * split / p.splits), k1 = (int)((int64_t)p.kt * (split + 1) / p.splits);
-  const int KT = k1 - k0;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  constexpr bool PM = P2 && C::G == 1;  // powers of two inside the MFMA
+  const int ks = (int)((int64_t)p.kt * split / p.splits), k1 = (int)((int64_t)p.kt * (split + 1) / p.splits);
+  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int group = C::G > 1 ? all / C::NW : 0, wave = C::G > 1 ? all % C::NW : all;
+  // Every group takes KT blocks, so that all meet at the same barriers; those of a
+  // later group that an earlier one has too (`skip`) count 0.
+  const int KS = k1 - ks, KT = (KS + C::G - 1) / C::G;
+  const int k0 = ks + min(group * KT, KS - KT), skip = group * KT - (k0 - ks);
+  uint8_t* const ring = smem + group * S * C::STAGE;
   const int ln = lane & 15, lg = lane >> 4;
   const int wm = wave / C::WN, wn = wave % C::WN;
-  const uint32_t smem0 = lds_u32(smem);
+  const uint32_t smem0 = lds_u32(ring);
 
   // 16-byte part q of row r lies at slot q ^ (r >> 1 & 7): the 16 rows of a
   // fragment cover all banks
@@ -350,12 +358,15 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
   // requested and put into LDS after
   constexpr int NSW = NB * LIN_MAX_KT / C::NT > 4 ? 4 : NB * LIN_MAX_KT / C::NT;
   float swr[NSW];
-  const float* swp0 = VEC ? nullptr : p.sb + (int64_t)(n0 / 128) * p.sb_ld + k0;
+  const float* swp0 = VEC ? nullptr : p.sb + (int64_t)(n0 / 128) * p.sb_ld + ks;
   const int64_t sw_next = min(1, (p.n - 1) / 128 - n0 / 128) * (int64_t)p.sb_ld;  // to the second block's, if there is one
-  auto sw_at = [&](int i) { return i < KT ? swp0[i] : swp0[sw_next + i - KT]; };
+  auto sw_at = [&](int i) {
+    const float v = i < KS ? swp0[i] : swp0[sw_next + i - KS];
+    return P2 && !PM ? pow2_of_e8m0(e8m0_of_pow2(v)) : v;
+  };
   if constexpr (!VEC) {
 #pragma unroll
-    for (int q = 0; q < NSW; ++q) swr[q] = sw_at(min((int)threadIdx.x + q * C::NT, NB * KT - 1));
+    for (int q = 0; q < NSW; ++q) swr[q] = sw_at(min((int)threadIdx.x + q * C::NT, NB * KS - 1));
   }
   // of the stage that is S - 1 ahead, the first DMAs are requested as soon as its
   // place is free, the others with the row blocks that follow
@@ -371,9 +382,9 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
 #pragma unroll
     for (int q = 0; q < NSW; ++q) {
       const int i = threadIdx.x + q * C::NT;
-      if (i < NB * KT) sws[i < KT ? i : LIN_MAX_KT + i - KT] = swr[q];
+      if (i < NB * KS) sws[i < KS ? i : LIN_MAX_KT + i - KS] = swr[q];
     }
-    for (int i = threadIdx.x + NSW * C::NT; i < NB * KT; i += C::NT) sws[i < KT ? i : LIN_MAX_KT + i - KT] = sw_at(i);
+    for (int i = threadIdx.x + NSW * C::NT; i < NB * KS; i += C::NT) sws[i < KS ? i : LIN_MAX_KT + i - KS] = sw_at(i);
   }
   const int swz = (ln >> 1) & 7;
   const int f0 = ln * 128 + ((lg ^ swz) << 4), f1 = ln * 128 + (((lg + 4) ^ swz) << 4);
@@ -406,10 +417,10 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
   else wait_vmcnt_clamped<(S - 2) * NPER + FIRST>();
   lds_barrier();
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) read_b(smem, j);
-  read_sb(smem);
-  read_a(smem, 0, 0);
-  read_a(smem, 1, 1);
+  for (int j = 0; j < NJ; ++j) read_b(ring, j);
+  read_sb(ring);
+  read_a(ring, 0, 0);
+  read_a(ring, 1, 1);
   int slot = 0;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   f32x4 part[NJ];
@@ -420,7 +431,7 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
   // A row block's MFMAs run while the one before is scaled and added and the one
   // after the next is read.  The barrier that ends a stage stands before its last
   // two row blocks, whose MFMAs then cover the first reads of the next stage.
-  const float* swp = sws + (VEC ? 0 : (wn * NJ * 16) / 128 * LIN_MAX_KT);
+  const float* swp = sws + (VEC ? 0 : (wn * NJ * 16) / 128 * LIN_MAX_KT + k0 - ks);
   // REST: of stage kt + S - 1 to request: 0 it is not there, 1 its other DMAs, 2 the
   // same and it is the last; LOAD: the same of the first DMAs of stage kt + S
   auto step = [&](auto next_, auto rest_, auto load_, int kt) {
@@ -429,10 +440,10 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
     using RestLast = std::integral_constant<bool, rest == 2>;
     using LoadLast = std::integral_constant<bool, load == 2>;
     const int pslot = slot == 0 ? S - 1 : slot - 1;
-    const uint8_t* st = smem + slot * C::STAGE;
+    const uint8_t* st = ring + slot * C::STAGE;
     const int nslot = slot + 1 == S ? 0 : slot + 1;
-    const uint8_t* nst = smem + nslot * C::STAGE;
-    const float sw = VEC ? 1.0f : swp[kt];
+    const uint8_t* nst = ring + nslot * C::STAGE;
+    const float sw = VEC ? 1.0f : C::G > 1 && kt < skip ? 0.0f : swp[kt];
     const int esw = e8m0_of_pow2(sw);
     float fs = 0.0f;
 #pragma unroll
@@ -455,11 +466,11 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
         }
         if (MI > 2) read_a(nst, i + 2 - MI, i + 2 - MI);
       }
-      const float s = P2 ? 0.0f : VEC ? sa[i & 3] : sa[i & 3] * sw;
-      const int ea = P2 ? e8m0_of_pow2(sa[i & 3]) : 0;
+      const float s = PM ? 0.0f : VEC ? sa[i & 3] : sa[i & 3] * sw;
+      const int ea = PM ? e8m0_of_pow2(sa[i & 3]) : 0;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        if constexpr (P2) {
+        if constexpr (PM) {
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i & 3], acc[i][j], 0, 0, 0,
                                                                         VEC ? ebv[j] : esw, 0, ea);
         } else {
@@ -482,7 +493,7 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
       }
       fs = s;
     }
-    if constexpr (!P2) {
+    if constexpr (!PM) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) fold(MI - 1, j, fs);
     }
@@ -500,7 +511,26 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
 #pragma unroll 1
   for (; kt < KT - 1; ++kt) step(std::true_type(), I0(), I0(), kt);
   step(std::false_type(), I0(), I0(), kt);
+  if constexpr (C::G > 1) {  // the groups' sums in their order
+    static_assert(!VEC, "skipped blocks");
+    f32x4* sums = reinterpret_cast<f32x4*>(smem);
+    lds_barrier();  // the stages are free
+    if (group > 0)
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) sums[(((group - 1) * C::NW + wave) * MI * NJ + i * NJ + j) * 64 + lane] = acc[i][j];
+    lds_barrier();
+    if (group == 0)
+#pragma unroll
+      for (int g = 1; g < C::G; ++g)
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) acc[i][j] += sums[(((g - 1) * C::NW + wave) * MI * NJ + i * NJ + j) * 64 + lane];
+  }
   if (p.splits > 1) {
+    if (group > 0) return;
     float* o = p.part + (int64_t)split * p.m * p.n;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -513,13 +543,15 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
     }
     return;
   }
-  lds_barrier();  // the stages are free
+  uint8_t* const tile = smem + C::SUMS;
+  if constexpr (C::G == 1) lds_barrier();  // the stages are free
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
+      if (group > 0) continue;
       const u32x2 v = {bf16x2_bits(acc[i][j][0], acc[i][j][1]), bf16x2_bits(acc[i][j][2], acc[i][j][3])};
-      *reinterpret_cast<u32x2*>(smem + ((wm * MI + i) * 16 + ln) * C::LS + ((wn * NJ + j) * 16 + lg * 4) * 2) = v;
+      *reinterpret_cast<u32x2*>(tile + ((wm * MI + i) * 16 + ln) * C::LS + ((wn * NJ + j) * 16 + lg * 4) * 2) = v;
     }
   lds_barrier();
   constexpr int PPR = C::BN / 8;
@@ -528,7 +560,7 @@ MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, 
     const int r = c / PPR, q = c % PPR;
     if (m0 + r < p.m && n0 + q * 8 < p.n)
       *reinterpret_cast<u32x4*>(p.out + (int64_t)(m0 + r) * p.ldo + n0 + q * 8) =
-          *reinterpret_cast<const u32x4*>(smem + r * C::LS + q * 16);
+          *reinterpret_cast<const u32x4*>(tile + r * C::LS + q * 16);
   }
 }
 
@@ -743,6 +775,7 @@ __global__ __launch_bounds__(256) void k_lin_join(const float* __restrict__ part
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= mn) return;
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
   for (int q = 0; q < splits; ++q) {
     const f32x4 v = *reinterpret_cast<const f32x4*>(part + q * mn + i);
 #pragma unroll
@@ -764,14 +797,19 @@ using LinT1 = LinTile<128, 256, 2, 4, 3, 2>;
 using LinT2 = LinTile<128, 128, 2, 2, 2, 2>;
 using LinT3 = LinTile<64, 128, 1, 4, 3, 2>;
 using LinT4 = LinTile<32, 128, 1, 4, 3, 2>;
+// 17 to 256 rows by a few thousand columns: more workgroups, and half the K steps one
+// after the other (64 rows 2048 x 7168 9.7 us, 32 x 128 tiles 11.0; 256 rows 4096 x
+// 2048 12.9 and 18.5; four groups 3-6% slower, two groups of 64 x 64 4%)
+using LinT5 = LinTile<32, 64, 1, 4, 3, 4, 2>;
 struct LinShape {
   int bm, bn, per;
   float step, rest;
 };
 constexpr LinShape kLinShapes[] = {
     {256, 256, 1, 2500, 9000}, {128, 256, 1, 1400, 6000}, {128, 128, 2, 1700, 5000}, {64, 128, 2, 1000, 4000},
-    {32, 128, 2, 900, 4000}};
-constexpr int kLinShapeCount = 5;
+    {32, 128, 2, 900, 4000},  {32, 64, 2, 600, 4000}};
+constexpr int kLinShapeCount = 6;
+constexpr int kLinVecShapes = 5;  // without groups, for scales per row on both sides
 constexpr int kLinCus = 256;
 
 inline size_t lin_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -783,10 +821,10 @@ inline int lin_tiles(int64_t m, int64_t n, const LinShape& s) {
 // of workgroups cost, and of writing and joining the parts (fp32) where K is
 // split.  A last round of 256 x 256 tiles that would leave half of the CUs idle is
 // done in halves.
-LinChoice lin_choose(int64_t m, int64_t n, int kt) {
+LinChoice lin_choose(int64_t m, int64_t n, int kt, bool vec) {
   LinChoice best{0, 1, 0};
   float least = 0.0f;
-  for (int i = 0; i < kLinShapeCount; ++i) {
+  for (int i = 0; i < (vec ? kLinVecShapes : kLinShapeCount); ++i) {
     const LinShape& s = kLinShapes[i];
     const int tiles = lin_tiles(m, n, s), slots = kLinCus * s.per;
     for (int sp = 1; sp <= 16 && (sp == 1 || kt / sp >= 2); ++sp) {
@@ -812,9 +850,14 @@ template <class C>
 void lin_launch(const LinGemm& g, bool vec, bool pow2, hipStream_t s) {
   const int nt = ((g.m + C::BM - 1) / C::BM) * ((g.n + C::BN - 1) / C::BN);
   const dim3 grid(lin_grid(nt, g.halved) * g.splits), b(C::NT);
-  if (vec && pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, true, true>), grid, b, 0, s, g);
-  else if (vec) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, true, false>), grid, b, 0, s, g);
-  else if (pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, false, true>), grid, b, 0, s, g);
+  if constexpr (C::G == 1) {
+    if (vec) {
+      if (pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, true, true>), grid, b, 0, s, g);
+      else hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, true, false>), grid, b, 0, s, g);
+      return;
+    }
+  }
+  if (pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, false, true>), grid, b, 0, s, g);
   else hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, false, false>), grid, b, 0, s, g);
 }
 
@@ -841,6 +884,7 @@ void lin_product(LinGemm g, const LinChoice& c, bool vec, bool pow2, hipStream_t
     case 2: lin_launch<LinT2>(g, vec, pow2, s); break;
     case 3: lin_launch<LinT3>(g, vec, pow2, s); break;
     case 4: lin_launch<LinT4>(g, vec, pow2, s); break;
+    case 5: lin_launch<LinT5>(g, vec, pow2, s); break;
     default:  // LIN_BATCH; 32 columns where 16 would make more than a workgroup per CU
       if (g.m <= 16 && g.n <= 16 * kLinCus) lin_batch<1, 1>(g, pow2, s);
       else if (g.m <= 16) lin_batch<1, 2>(g, pow2, s);
@@ -930,7 +974,7 @@ LinPlan lin_plan(int M, int K, int N, bool backward, bool input_grad, bool weigh
     const int kt = (C + 127) / 128;
     p.q = take((size_t)M * kt * 128);
     p.s = take((size_t)kt * lin_scale_ld(M) * 4);
-    p.choice = lin_is_batch(M, kt) ? LinChoice{LIN_BATCH, 1, 0} : lin_choose(M, out, kt);
+    p.choice = lin_is_batch(M, kt) ? LinChoice{LIN_BATCH, 1, 0} : lin_choose(M, out, kt, false);
     p.part = take(p.choice.splits > 1 ? (size_t)p.choice.splits * M * out * 4 : 0);
   }
   if (weight_grad) {
@@ -939,7 +983,7 @@ LinPlan lin_plan(int M, int K, int N, bool backward, bool input_grad, bool weigh
     p.qb = take((size_t)K * kt * 128);
     p.sqa = take((size_t)kt * lin_scale_ld(N) * 4);
     p.sqb = take((size_t)kt * lin_scale_ld(K) * 4);
-    p.wchoice = lin_choose(N, K, kt);
+    p.wchoice = lin_choose(N, K, kt, true);
     p.wpart = take(p.wchoice.splits > 1 ? (size_t)p.wchoice.splits * N * K * 4 : 0);
   }
   p.total = o;

@@ -84,6 +84,14 @@ def test_batches_of_single_tokens(M, K, N, pow2):
     _check(M, K, N, pow2, M + K, dw=M == 17)
 
 
+@pytest.mark.parametrize("M,K,N", [(40, 2064, 4096), (64, 144, 2048), (100, 272, 1040), (256, 4096, 2048), (33, 1152, 80),
+                                   (200, 128, 512), (65, 656, 144)])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_a_few_dozen_rows(M, K, N, pow2):
+    """Odd numbers of blocks, one block, a last one that is not whole, columns that end inside a tile."""
+    _check(M, K, N, pow2, M, dw=M == 33)
+
+
 def test_one_gradient_alone():
     _check(70, 256, 144, False, 3, dx=True, dw=False)
     _check(70, 256, 144, False, 3, dx=False, dw=True)
