@@ -828,6 +828,8 @@ LinChoice lin_choose(int64_t m, int64_t n, int kt, bool vec) {
     const LinShape& s = kLinShapes[i];
     const int tiles = lin_tiles(m, n, s), slots = kLinCus * s.per;
     for (int sp = 1; sp <= 16 && (sp == 1 || kt / sp >= 2); ++sp) {
+      const float join = sp == 1 ? 0.0f : 6000.0f + (float)((double)sp * m * n * 8 / 2000.0);  // about 4 TB/s at 2 GHz
+      if (sp > 1 && join >= least) break;
       if (sp > 1 && ((int64_t)sp * m * n * 4 > (64 << 20) || (int64_t)tiles * (sp - 1) >= 2 * slots)) break;
       const int64_t wgs = (int64_t)tiles * sp, full = wgs / slots;
       const int rem = (int)(wgs - full * slots);
@@ -835,8 +837,7 @@ LinChoice lin_choose(int64_t m, int64_t n, int kt, bool vec) {
       const bool half = i == 0 && sp == 1 && rem > 0 && rem * 2 <= slots;
       // a round that leaves CUs to one workgroup instead of two costs less
       const float last = rem == 0 ? 0.0f : half ? 0.6f * one : s.per == 2 && rem * 2 <= slots ? 0.7f * one : one;
-      float cost = (float)full * one + last;
-      if (sp > 1) cost += 6000.0f + (float)((double)sp * m * n * 8 / 2000.0);  // about 4 TB/s at 2 GHz
+      const float cost = (float)full * one + last + join;
       if (i == 0 && sp == 1 ? true : cost < least) {
         least = cost;
         best = LinChoice{i, sp, half ? rem : 0};
