@@ -145,18 +145,18 @@ def test_values_at_the_quantizers_borders():
         _near(moe.fp8_linear(xb, codes, s, FMT[pow2]), y, bound + 4 * 2.0 ** -126)
 
 
-@pytest.mark.parametrize("M", [3, 300])
+@pytest.mark.parametrize("M,K", [(3, 400), (300, 400), (40, 272), (20, 656)])
 @pytest.mark.parametrize("pow2", [False, True])
-def test_values_that_are_not_finite(M, pow2):
+def test_values_that_are_not_finite(M, K, pow2):
     """A NaN or an infinity reaches its own row of the result (its own column's gradients) and no other."""
-    K, N = 400, 144
+    N = 144
     x, codes, s, d_y = _inputs(M, K, N, pow2, 8)
     codes = codes.clamp_min(1)
     wt, st = moe.fp8_linear_transpose(codes, s)
     want = moe.fp8_linear(x, codes, s, FMT[pow2])
     d_x, d_w = moe.fp8_linear_backward(d_y, wt, st, FMT[pow2], x=x, weight_grad=True)
     x, d_y = x.clone(), d_y.clone()
-    x[1, 399] = float("nan")
+    x[1, K - 1] = float("nan")
     x[2, 5] = float("inf")
     d_y[1, 7] = -float("inf")
     y = moe.fp8_linear(x, codes, s, FMT[pow2])
@@ -168,7 +168,7 @@ def test_values_that_are_not_finite(M, pow2):
     assert not bool(a[bad].isfinite().any()) and torch.equal(a[~bad], d_x[~bad])
     rows, cols = torch.ones(N, dtype=torch.bool, device="cuda"), torch.ones(K, dtype=torch.bool, device="cuda")
     rows[7] = False
-    cols[[5, 399]] = False
+    cols[[5, K - 1]] = False
     assert torch.equal(b[rows][:, cols], d_w[rows][:, cols])
     assert not bool(b[7].isfinite().any()) and not bool(b[:, ~cols].isfinite().any())
 
