@@ -536,7 +536,9 @@ moe_status moe_route_gated(const moe_layer* layer, const moe_gate* gate, const f
  * ds_j = (scale d_w_j - sum_i d_w_i w_i) / sum_i s_i,
  *   sigmoid: d_logits[t][ids_j] = ds_j s_j (1 - s_j), 0 elsewhere
  *   softmax: d_logits[t][e] = s_e (ds_e - sum_j ds_j s_j)
- * (ds_e = 0 for experts not chosen).  Ids outside [0, E) have no part; an id that
+ * (ds_e = 0 for experts not chosen).  Sigmoid scores are formed in 64 bits as in
+ * the forward, softmax's with renormalize against the largest chosen, so that far
+ * logits have their gradient too.  Ids outside [0, E) have no part; an id that
  * a token has twice takes both gradients.  The bias has no gradient.  d_logits:
  * [T][E] fp32 (over no input), written, or with accumulate != 0 added to what it
  * holds. */

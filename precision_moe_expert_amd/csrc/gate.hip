@@ -403,11 +403,15 @@ __global__ __launch_bounds__(64) void k_gate(GateArgs p) {
 }
 
 // What the gradients of one token's weights (16 lanes, r < k with a slot) come to:
-// with ds_j = scale dw_j, or with weights that sum to scale,
-// ds_j = (scale dw_j - sum_i dw_i w_i) / sum_i s_i,
+// with r_j = s_j / sum_i s_i and, where the weights sum to scale,
+// ds_j s_j = (scale dw_j - sum_i scale dw_i r_i) r_j, else scale dw_j s_j,
 //   sigmoid: dl_j = ds_j s_j (1 - s_j)
 //   softmax: dl_e = s_e (ds_e - sum_j ds_j s_j); where the weights were
 //            renormalised the last sum is 0.
+// Sigmoids are formed in 64 bits by the forward's own operations, so r_j is the
+// forward's also where every chosen score is below fp32's smallest number, and 0
+// where they are 0 in 64 bits too (logits below -709).  Softmax terms are taken
+// against the largest, their sum is 1 at least.
 // Ids outside [0, E) are left out, an id that is there twice gets both.
 struct GateSlot {
   int id;
@@ -427,24 +431,27 @@ MOE_DEV GateSlot gate_slot(const GateArgs& p, int64_t t, int r, const float* row
 // chosen, and any).  `add`: of the slot's own logit, without softmax's common sum
 // `dot`; sparse gradients are whole.  True: this lane writes for its id.
 MOE_DEV bool gate_slot_grad(const GateArgs& p, const GateSlot& s, int r, float m, float iz, float& add, float& dot) {
-  float sj = 0.0f, sp = 0.0f;
-  if (s.in) {
-    if (p.sigmoid) {
-      const float e = expf(-fabsf(s.l)), q = 1.0f / (1.0f + e);
-      sj = s.l >= 0.0f ? q : e * q;
-      sp = e * q * q;
-    } else {
-      sj = (s.l == m ? 1.0f : expf(s.l - m)) * iz;
-      sp = sj;
+  dot = 0.0f;
+  if (p.sigmoid) {
+    const double ex = exp(-(double)s.l), sj = s.in ? 1.0 / (1.0 + ex) : 0.0;
+    const double rest = ex < INFINITY ? ex * sj : 1.0;  // 1 - s_j
+    double g = (double)p.scale * (double)s.dw, part = sj;
+    if (p.renorm) {
+      const double tot = gate_sum<16>(sj);
+      part = tot > 0.0 ? sj / tot : 0.0;
+      g -= gate_sum<16>(s.in ? g * part : 0.0);
     }
+    add = s.in ? (float)(g * part * rest) : 0.0f;
+  } else {
+    const float sj = s.in ? (s.l == m ? 1.0f : expf(s.l - m)) * iz : 0.0f;
+    float g = p.scale * s.dw;
+    if (p.renorm) {
+      const float tot = gate_sum16(sj), it = tot > 0.0f ? 1.0f / tot : 0.0f;
+      g = (g - gate_sum16(g * sj) * it) * it;
+    }
+    dot = gate_sum16(s.in ? g * sj : 0.0f);
+    add = s.in ? g * sj : 0.0f;
   }
-  float g = p.scale * s.dw;
-  if (p.renorm) {
-    const float tot = gate_sum16(sj), it = tot > 0.0f ? 1.0f / tot : 0.0f;
-    g = (g - gate_sum16(g * sj) * it) * it;
-  }
-  dot = gate_sum16(s.in ? g * sj : 0.0f);
-  add = s.in ? g * sp : 0.0f;
   // one lane per id: the first with it takes what the others add
   bool first = s.there;
   const int base = threadIdx.x & 48;

@@ -254,6 +254,44 @@ def test_gradient_against_differences():
             assert abs(d - float((got * way).sum())) <= 1e-4 * float((got * way).abs().sum()) + 1e-9
 
 
+@pytest.mark.parametrize("E,k", [(24, 4), (26, 4), (64, 8), (67, 16), (16, 1), (18, 1)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradient_of_chosen_scores_near_zero(E, k, renorm):
+    """All chosen logits far below 0 (a bias chooses such experts): below fp32's smallest sigmoids the weights that sum
+    to `scale` are still those of the forward, and so is their gradient; from -745 on the forward's are 0."""
+    levels = [-60.0, -86.0, -90.0, -95.0, -101.0, -110.0, -690.0, -800.0]
+    g = torch.Generator().manual_seed(E + k)
+    T = 3 * len(levels)
+    logits = torch.randn(T, E, generator=g)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int()
+    far = torch.tensor(levels * 3)[:, None] - 1.5 * torch.rand(T, k, generator=g)
+    far[2 * len(levels):, 0] = 2.0                       # all but one
+    logits.scatter_(1, ids.long(), far)
+    dw = torch.randn(T, k, generator=g)
+    dw[:len(levels)] *= 0.01
+    dw[len(levels):2 * len(levels)] *= 200.0
+    got = _check_backward(logits, None, ids, dw, True, renorm)
+    _check_backward(logits, torch.zeros(E), ids, dw, True, renorm, start=torch.randn(T, E, generator=g))
+    if renorm and k > 1:                                 # not lost: of the size of d_w
+        part = got.abs().amax(1)[:len(levels) - 1]
+        assert bool((part > 1e-4).all()) and bool((part < 1.0).all())
+    assert bool((got[len(levels) - 1] == 0).all())
+
+
+def test_gradient_of_far_scores_against_differences():
+    l = torch.randn(6, 20, generator=torch.Generator().manual_seed(1)) - 95.0
+    ids = torch.arange(20).repeat(6, 1)[:, 3:8].int()
+    dw = torch.randn(6, 5, generator=torch.Generator().manual_seed(2))
+    got = _check_backward(l, None, ids, dw, True, True, 1.0)
+    h = 1e-5
+    for e in (3, 6):
+        d = torch.zeros(6, 20, dtype=torch.float64)
+        d[:, e] = h
+        up, dn = (ref.gate_weights(l.double() + s * d, None, ids, True, True, 1.0) for s in (1, -1))
+        # cubic term of the difference h^2, rounding of 64 bits 1e-16 / h
+        assert bool((((up - dn) * dw.double()).sum(1) / (2 * h) - got[:, e]).abs().max() < 1e-6)
+
+
 def _expert_inputs(T=96, H=256, I=256, E=16, seed=0):
     g = torch.Generator().manual_seed(seed)
     x = torch.randn(T, H, generator=g).bfloat16()
