@@ -292,6 +292,43 @@ def test_gradient_of_far_scores_against_differences():
         assert bool((((up - dn) * dw.double()).sum(1) / (2 * h) - got[:, e]).abs().max() < 1e-6)
 
 
+@pytest.mark.parametrize("T,E,k,groups", [(37, 384, 6, 1), (300, 256, 8, 8), (130, 1000, 16, 1), (40, 17, 5, 1),
+                                          (9, 1024, 4, 16), (33, 60, 5, 4), (21, 64, 16, 1)])
+def test_softmax_weights_are_rounded_once(T, E, k, groups):
+    """Weights that are not renormalised, in 64 bits up to their one rounding, whichever way a token's choice was made."""
+    logits, bias, g = _case(T, E, T + 3 * E, out=0.1)
+    logits *= 1.0 + 3.0 * torch.rand(T, 1, generator=g)
+    logits[1] = 0.25                        # equal terms: a sum of E
+    logits[3, ::2] = logits[3, 0]           # ties: the choice is made in 64 bits
+    logits[4] = -INF
+    logits[4, 5] = 1e30
+    for b in (None, bias * 0.5 / E):
+        want, w = ref.gate(logits, b, k, False, groups, max(1, groups // 2), False, False, 1.5)
+        r = moe.route_gated(_layer(T, E, k), _gate(False, groups, max(1, groups // 2), False, False, 1.5), logits.cuda(),
+                            None if b is None else b.cuda(), permute=False)
+        assert torch.equal(r["topk_ids"].cpu(), want)
+        off = (r["topk_w"].cpu().double() - w).abs()
+        # one rounding; of fp32's subnormal numbers half of the smallest
+        worst = float((off / (w.abs() * ref.F32 * (1 + 1e-6) + 2.0 ** -150 * (1 + 1e-6))).max())
+        assert worst <= 1.0
+
+
+def test_softmax_weights_of_large_logits():
+    """Far from 0 and far from each other: steps of fp32 between the logits from 2^-20 to more than exp's range."""
+    g = torch.Generator().manual_seed(7)
+    rows = [torch.randn(40, generator=g) * a + b for a in (1.0, 30.0, 300.0)
+            for b in (1e3, -5e5, 2.0 ** 24, -2.0 ** 29, 2.0 ** 30, 2.0 ** 31, -1e30, 3e38)]
+    rows += [torch.randn(40, generator=g) * 1e30, torch.randn(40, generator=g) * 3e9, torch.full((40,), 3.4e38)]
+    logits = torch.stack(rows)
+    for E in (40, 32, 16):
+        l = logits[:, :E].contiguous()
+        want, w = ref.gate(l, None, 6, False, 1, 1, True, False, 1.0)
+        r = moe.route_gated(_layer(len(rows), E, 6), _gate(False, 1, 1, True, False, 1.0), l.cuda(), permute=False)
+        assert torch.equal(r["topk_ids"].cpu(), want)
+        worst = float(((r["topk_w"].cpu().double() - w).abs() / (w * ref.F32 * (1 + 1e-6) + 2.0 ** -150 * (1 + 1e-6))).max())
+        assert worst <= 1.0
+
+
 def _expert_inputs(T=96, H=256, I=256, E=16, seed=0):
     g = torch.Generator().manual_seed(seed)
     x = torch.randn(T, H, generator=g).bfloat16()
