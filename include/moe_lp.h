@@ -554,8 +554,8 @@ moe_status moe_expert_forward_gated(const moe_layer* layer, const moe_gate* gate
                                     void* out_bf16, void* ws, size_t ws_bytes, void* stream);
 
 /* moe_expert_backward of moe_expert_forward_gated: d_logits through the gate
- * (moe_route_gated_backward of g_tj = <d_out_t, y_tj>), the rest and the
- * workspace as there; not timed. */
+ * (moe_route_gated_backward of g_tj = <d_out_t, y_tj>; over neither the logits nor
+ * the bias), the rest and the workspace as there; not timed. */
 moe_status moe_expert_backward_gated(const moe_layer* layer, const moe_gate* gate, const void* x_bf16,
                                      const float* logits, const float* bias, const moe_qweights* qweights,
                                      const moe_scales* scales, const void* bwd_weights, const void* adapter_bf16,

@@ -227,6 +227,18 @@ moe_status check_gate(const moe_gate* g, const float* bias, const Dims& d) {
   return g->num_groups > MOE_GATE_MAX_GROUPS ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
+// Whether d_logits lies over what the gate's gradient reads (waves write while others still read).
+bool gate_grad_overlaps(const Dims& d, const float* d_logits, const float* logits, const float* bias,
+                        const int32_t* ids, const float* d_w) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(d_logits), rows = (uintptr_t)d.T * d.E * 4;
+  auto over = [&](const void* p, uintptr_t bytes) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    return p != nullptr && a < b + bytes && b < a + rows;
+  };
+  const uintptr_t pairs = (uintptr_t)d.T * d.k * 4;
+  return over(logits, rows) || over(bias, (uintptr_t)d.E * 4) || over(ids, pairs) || over(d_w, pairs);
+}
+
 GateArgs gate_args(const Dims& d, const moe_gate* g, const float* logits, const float* bias) {
   GateArgs a{};
   a.logits = logits;
@@ -848,6 +860,8 @@ moe_status backward_impl(const moe_layer* layer, const void* x_bf16, const float
     return MOE_ERR_INVALID_ARGUMENT;
   const BwdLayout wl = bwd_layout(d);
   if (ws_bytes < wl.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (gate != nullptr && gate_grad_overlaps(d, d_logits, logits, gate->bias, nullptr, nullptr))
+    return MOE_ERR_INVALID_ARGUMENT;
   const BwdWeights bw = bwd_weights_layout(d);
 
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -1391,6 +1405,7 @@ moe_status moe_route_gated_backward(const moe_layer* layer, const moe_gate* gate
   const void* ptrs[] = {logits, topk_ids, d_topk_w, d_logits};
   for (const void* p : ptrs)
     if (p == nullptr || !aligned16(p)) return MOE_ERR_INVALID_ARGUMENT;
+  if (gate_grad_overlaps(d, d_logits, logits, bias, topk_ids, d_topk_w)) return MOE_ERR_INVALID_ARGUMENT;
   GateArgs a = gate_args(d, gate, logits, bias);
   a.ids = const_cast<int32_t*>(topk_ids);
   a.dw = d_topk_w;

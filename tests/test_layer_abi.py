@@ -69,6 +69,22 @@ def test_gate_limits_and_pointers():
     assert L.moe_route_gated(R(layer), R(g), FAKE, None, None, FAKE, BIG, None) == INV
 
 
+def test_gate_gradient_over_an_input_is_refused():
+    """d_logits of 64 x 64 floats: over an input's first bytes, its last ones, all of it."""
+    layer, gate, L = _layer(), binding.make_gate(), binding.lib()
+    big, small, bias = 64 * 64 * 4, 64 * 8 * 4, 64 * 4
+    at = dict(logits=1 << 24, bias=2 << 24, ids=3 << 24, w=4 << 24)
+    qw, sc = binding.MoeQWeights(FAKE, FAKE), binding.MoeScales(FAKE, FAKE, None, None)
+    for name, size in (("logits", big), ("bias", bias), ("ids", small), ("w", small)):
+        for d in (at[name], at[name] - big + 16, at[name] + size - 16):
+            for add in (0, 1):
+                assert L.moe_route_gated_backward(R(layer), R(gate), at["logits"], at["bias"], at["ids"], at["w"], add, d,
+                                                  None) == INV
+            if name in ("logits", "bias"):
+                assert L.moe_expert_backward_gated(R(layer), R(gate), FAKE, at["logits"], at["bias"], R(qw), R(sc), FAKE,
+                                                   None, FAKE, 1, FAKE, d, None, FAKE, BIG, None) == INV
+
+
 def _linear(M=64, K=256, N=512, fmt=binding.FMT_FP8, xs=0, ys=0):
     return binding.MoeLinear(M, K, N, fmt, xs, ys)
 
