@@ -910,10 +910,15 @@ def fp8_linear_backward(d_y: torch.Tensor, w_t: torch.Tensor, w_t_scale: torch.T
 
 # ---- clipping by the global norm ----
 
+def _lists(grads, out):
+    """What may be readable once only, as lists: a call on another device than the current one reads it twice."""
+    return (grads if isinstance(grads, list) else list(grads),
+            out if out is None or isinstance(out, list) else list(out))
+
+
 def _tensors(grads, out, write: bool = True):
     """(device, moe_tensor array, count) of a list of gradients; out: None (in place), or where the results go."""
-    grads = list(grads)
-    dest = grads if out is None else list(out)
+    dest = grads if out is None else out
     n = len(grads)
     if len(dest) != n:
         raise ValueError(f"out: {len(dest)} tensors for {n}")
@@ -955,6 +960,7 @@ def _tensors(grads, out, write: bool = True):
 
 
 def _norm_call(grads, out, ws, max_norm):
+    grads, out = _lists(grads, out)
     dev, arr, n = _tensors(grads, out, write=max_norm is not None)
     if _elsewhere(dev):
         with torch.cuda.device(dev):
@@ -982,6 +988,7 @@ def clip_grads(grads, max_norm: float, out=None, ws: torch.Tensor | None = None)
 
 def scale_grads(grads, norm: torch.Tensor, max_norm: float, out=None) -> None:
     """moe_grad_scale: the scaling of clip_grads for a norm [1] fp32 on the device (one joined over ranks)."""
+    grads, out = _lists(grads, out)
     dev, arr, n = _tensors(grads, out)
     if _elsewhere(dev):
         with torch.cuda.device(dev):

@@ -196,3 +196,47 @@ def test_wrappers_refuse_host_tensors():
         binding.clip_grads([torch.zeros(4)], 1.0)
     with pytest.raises(ValueError):
         binding.clip_grads([torch.zeros(4)], 1.0, out=[])
+
+
+@pytest.mark.parametrize("call", ["clip", "norm", "scale"])
+def test_lists_that_can_be_read_once(monkeypatch, call):
+    """Generators of tensors on a device that is not the current one: the call made again there has the same tensors."""
+    class Done(Exception):
+        pass
+
+    seen, turns = [], iter([True])
+
+    def tensors(grads, out, write=True):
+        seen.append((list(grads), None if out is None else list(out)))
+        return torch.device("cuda", 1), None, len(seen[-1][0])
+
+    def elsewhere(device):
+        if next(turns, False):
+            return True
+        raise Done
+
+    class On:
+        def __init__(self, device):
+            pass
+
+        def __enter__(self):
+            pass
+
+        def __exit__(self, *e):
+            pass
+
+    monkeypatch.setattr(binding, "_tensors", tensors)
+    monkeypatch.setattr(binding, "_elsewhere", elsewhere)
+    monkeypatch.setattr(torch.cuda, "device", On)
+    a, b = [torch.zeros(4), torch.ones(3)], [torch.zeros(4), torch.ones(3)]
+    with pytest.raises(Done):
+        if call == "clip":
+            binding.clip_grads((t for t in a), 1.0, out=(t for t in b))
+        elif call == "norm":
+            binding.grad_norm(t for t in a)
+        else:
+            binding.scale_grads((t for t in a), torch.ones(1), 1.0, out=(t for t in b))
+    assert len(seen) == 2
+    for grads, out in seen:
+        assert len(grads) == 2 and all(x is y for x, y in zip(grads, a))
+        assert call == "norm" or (len(out) == 2 and all(x is y for x, y in zip(out, b)))
