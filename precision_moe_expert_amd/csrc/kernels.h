@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "linear_choice.h"
+
 namespace moe {
 
 constexpr int MAX_EXPERTS = 1024;
@@ -300,9 +302,6 @@ struct LinGemm {
   int splits;             // ways K is split (1: not)
   float* part;            // [splits][m][n]
   int halved;             // last tiles that are done as two halves
-};
-struct LinChoice {
-  int shape, splits, halved;
 };
 struct LinPlan {
   LinChoice choice, wchoice;  // of y's or d_x's product, of d_w's

@@ -789,9 +789,7 @@ __global__ __launch_bounds__(256) void k_lin_join(const float* __restrict__ part
 
 namespace {
 
-// Tiles of a product, and what they cost (cycles of a CU, measured at 8192 x
-// 7168 x 4096 and smaller calls): a K block of one tile, the rest of a tile; `per`
-// workgroups share a CU.
+// The tiles of kLinShapes.
 using LinT0 = LinTile<256, 256, 2, 4, 2, 2>;
 using LinT1 = LinTile<128, 256, 2, 4, 3, 2>;
 using LinT2 = LinTile<128, 128, 2, 2, 2, 2>;
@@ -801,51 +799,10 @@ using LinT4 = LinTile<32, 128, 1, 4, 3, 2>;
 // after the other (64 rows 2048 x 7168 9.7 us, 32 x 128 tiles 11.0; 256 rows 4096 x
 // 2048 12.9 and 18.5; four groups 3-6% slower, two groups of 64 x 64 4%)
 using LinT5 = LinTile<32, 64, 1, 4, 3, 4, 2>;
-struct LinShape {
-  int bm, bn, per;
-  float step, rest;
-};
-constexpr LinShape kLinShapes[] = {
-    {256, 256, 1, 2500, 9000}, {128, 256, 1, 1400, 6000}, {128, 128, 2, 1700, 5000}, {64, 128, 2, 1000, 4000},
-    {32, 128, 2, 900, 4000},  {32, 64, 2, 600, 4000}};
-constexpr int kLinShapeCount = 6;
-constexpr int kLinVecShapes = 5;  // without groups, for scales per row on both sides
-constexpr int kLinCus = 256;
-
-inline size_t lin_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-inline int lin_tiles(int64_t m, int64_t n, const LinShape& s) {
-  return (int)((m + s.bm - 1) / s.bm * ((n + s.bn - 1) / s.bn));
-}
-
-// The tile and the ways K is split for a product: the least of what the rounds
-// of workgroups cost, and of writing and joining the parts (fp32) where K is
-// split.  A last round of 256 x 256 tiles that would leave half of the CUs idle is
-// done in halves.
-LinChoice lin_choose(int64_t m, int64_t n, int kt, bool vec) {
-  LinChoice best{0, 1, 0};
-  float least = 0.0f;
-  for (int i = 0; i < (vec ? kLinVecShapes : kLinShapeCount); ++i) {
-    const LinShape& s = kLinShapes[i];
-    const int tiles = lin_tiles(m, n, s), slots = kLinCus * s.per;
-    for (int sp = 1; sp <= 16 && (sp == 1 || kt / sp >= 2); ++sp) {
-      const float join = sp == 1 ? 0.0f : 6000.0f + (float)((double)sp * m * n * 8 / 2000.0);  // about 4 TB/s at 2 GHz
-      if (sp > 1 && join >= least) break;
-      if (sp > 1 && ((int64_t)sp * m * n * 4 > (64 << 20) || (int64_t)tiles * (sp - 1) >= 2 * slots)) break;
-      const int64_t wgs = (int64_t)tiles * sp, full = wgs / slots;
-      const int rem = (int)(wgs - full * slots);
-      const float one = (float)((kt + sp - 1) / sp) * s.step + s.rest;
-      const bool half = i == 0 && sp == 1 && rem > 0 && rem * 2 <= slots;
-      // a round that leaves CUs to one workgroup instead of two costs less
-      const float last = rem == 0 ? 0.0f : half ? 0.6f * one : s.per == 2 && rem * 2 <= slots ? 0.7f * one : one;
-      const float cost = (float)full * one + last + join;
-      if (i == 0 && sp == 1 ? true : cost < least) {
-        least = cost;
-        best = LinChoice{i, sp, half ? rem : 0};
-      }
-    }
-  }
-  return best;
-}
+template <class C>
+constexpr bool lin_is(int i) { return C::BM == kLinShapes[i].bm && C::BN == kLinShapes[i].bn; }
+static_assert(lin_is<LinT0>(0) && lin_is<LinT1>(1) && lin_is<LinT2>(2) && lin_is<LinT3>(3) && lin_is<LinT4>(4) &&
+                  lin_is<LinT5>(5), "the tiles that are chosen among");
 
 template <class C>
 void lin_launch(const LinGemm& g, bool vec, bool pow2, hipStream_t s) {
@@ -861,13 +818,6 @@ void lin_launch(const LinGemm& g, bool vec, bool pow2, hipStream_t s) {
   if (pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, false, true>), grid, b, 0, s, g);
   else hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin<C, false, false>), grid, b, 0, s, g);
 }
-
-// Whether a product of quantized rows is k_lin_batch's, on top of lin_is_few's (16 rows
-// 2048 x 7168 8.9 us, in tiles 10.5; 7168 x 4096 13.8 and 16.9; 32 rows 4096 x 2048
-// 11.6 and 13.3, 1024 x 1024 6.4 and 8.1; 7168 x 576 15.2 and 13.4: long rows of
-// codes come from the L2 again for every 16 columns).
-constexpr int LIN_BATCH = kLinShapeCount;  // of LinChoice
-inline bool lin_is_batch(int64_t m, int kt) { return m <= 16 || (m <= 32 && kt <= 32); }
 
 template <int MF, int NC>
 void lin_batch(const LinGemm& g, bool pow2, hipStream_t s) {
@@ -886,10 +836,10 @@ void lin_product(LinGemm g, const LinChoice& c, bool vec, bool pow2, hipStream_t
     case 3: lin_launch<LinT3>(g, vec, pow2, s); break;
     case 4: lin_launch<LinT4>(g, vec, pow2, s); break;
     case 5: lin_launch<LinT5>(g, vec, pow2, s); break;
-    default:  // LIN_BATCH; 32 columns where 16 would make more than a workgroup per CU
-      if (g.m <= 16 && g.n <= 16 * kLinCus) lin_batch<1, 1>(g, pow2, s);
+    default:  // LIN_BATCH
+      if (g.m <= 16 && lin_batch_cols(g.n) == 1) lin_batch<1, 1>(g, pow2, s);
       else if (g.m <= 16) lin_batch<1, 2>(g, pow2, s);
-      else if (g.n <= 16 * kLinCus) lin_batch<2, 1>(g, pow2, s);
+      else if (lin_batch_cols(g.n) == 1) lin_batch<2, 1>(g, pow2, s);
       else lin_batch<2, 2>(g, pow2, s);
   }
   if (g.splits > 1) {
@@ -897,15 +847,6 @@ void lin_product(LinGemm g, const LinChoice& c, bool vec, bool pow2, hipStream_t
     hipLaunchKernelGGL(k_lin_join, dim3((unsigned)((mn / 4 + 255) / 256)), dim3(256), 0, s, g.part, g.splits, mn, g.n,
                        g.ldo, g.out);
   }
-}
-
-// Whether a product is k_lin_few's, which quantizes the rows in every workgroup and so
-// pays for few and short ones (10 rows 2048 x 7168 9.1 us, with a launch that
-// quantizes them first 9.1, 12 rows 10.1 and 9.2; 4 and 8 rows 4096 x 2048 7.1 and 8.2,
-// 9.6 and 8.6; 3 and 6 rows 7168 x 4096 10.9 and 12.3, 12.5 and 11.8).
-inline int lin_few_waves(int kt) { return kt > 32 ? 16 : 8; }
-inline bool lin_is_few(int64_t m, int kt) {
-  return m <= 16 && (m == 1 ? kt * 132 + 16384 <= 65536 : m * kt <= 176);
 }
 
 template <int NW>
@@ -923,9 +864,7 @@ void lin_products(LinGemm dx, LinGemm dw, bool pow2, hipStream_t s) {
   const LinGemm &a = dw_first ? dw : dx, &b0 = dw_first ? dx : dw;
   LinGemm b = b0;
   const int na = lin_tiles(a.m, a.n, kLinShapes[0]), nb = lin_tiles(b.m, b.n, kLinShapes[0]);
-  // the last round of the shorter tiles, in halves if it would leave half of the CUs idle
-  const int rem = (int)(((int64_t)na * a.kt / b.kt + nb) % kLinCus);
-  b.halved = rem * 2 <= kLinCus && rem <= nb ? rem : 0;
+  b.halved = lin_joined_halves(na, a.kt, nb, b.kt);
   const int first = lin_grid(na, 0);
   const dim3 grid(first + lin_grid(nb, b.halved)), t(C::NT);
   if (dw_first && pow2) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_lin_both<C, true, true>), grid, t, 0, s, a, b, first);
@@ -1067,7 +1006,7 @@ void launch_linear_bwd(const LinPlan& pl, const uint16_t* dy, int64_t dy_stride,
   }
   const LinChoice &cx = pl.choice, &cw = pl.wchoice;
   if (both) {
-    if (cx.shape == 0 && cx.splits == 1 && cw.shape == 0 && cw.splits == 1) {
+    if (lin_joined(cx, cw)) {
       lin_products(gx, gw, pow2, s);
     } else {
       lin_product(gx, cx, false, pow2, s);

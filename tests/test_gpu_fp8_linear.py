@@ -5,6 +5,7 @@ import torch
 import precision_moe_expert_amd as moe
 from precision_moe_expert_amd import binding
 from tests import layer_ref as ref
+from tests.linear_choices import CHOICES
 
 pytestmark = pytest.mark.gpu
 FMT = {False: moe.FMT_FP8, True: moe.FMT_FP8_POW2}
@@ -90,6 +91,13 @@ def test_batches_of_single_tokens(M, K, N, pow2):
 def test_a_few_dozen_rows(M, K, N, pow2):
     """Odd numbers of blocks, one block, a last one that is not whole, columns that end inside a tile."""
     _check(M, K, N, pow2, M, dw=M == 33)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("M,K,N", [s for s, _ in CHOICES])
+def test_every_choice_of_kernel(M, K, N, pow2):
+    """Sizes of every tile, split, last round in halves and joined launch that a call may choose."""
+    _check(M, K, N, pow2, M)
 
 
 def test_one_gradient_alone():
