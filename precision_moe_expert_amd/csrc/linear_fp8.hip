@@ -276,11 +276,11 @@ constexpr int lin_sws() { return (C::BN + 127) / 128 * LIN_MAX_KT; }
 //
 // 256 x 256 by eight waves is what the L2 and LDS can feed: each byte staged meets
 // 256 others, and a wave's 128 x 64 reads a byte of LDS for 43 products.
-// Powers of two go into the MFMA: 4096 x 7168 x 4096 87 us, 2.8 PFLOP/s (the
+// Powers of two go into the MFMA: 4096 x 7168 x 4096 87-90 us, 2.7 PFLOP/s (the
 // library's product with one scale 83), MFMA busy 0.63 of the cycles, the rest
 // ring fill and epilogue in its one round of tiles.  fp32 scales take four VALU
 // operations per MFMA (d_w eight, as many cycles as the MFMA itself): 3001 x 4160 x
-// 7168 88 us, 2.0 PFLOP/s; d_x and d_w of 8192 x 7168 x 4096 412-464 us, 2.1-2.3.
+// 7168 91 us, 2.0 PFLOP/s; d_x and d_w of 8192 x 7168 x 4096 426-497 us, 1.9-2.3.
 template <class C, bool VEC, bool P2>
 MOE_DEV void lin_mm(const LinGemm& p, int m0, int n0, int split, uint8_t* smem, float* sws) {
   constexpr int MI = C::MI, NJ = C::NJ, S = C::S, NPER = C::NPER;
